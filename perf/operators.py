@@ -208,7 +208,7 @@ def prepare(case, seed):
         k = (torch.randn((rows, n, d), generator=g, device=dev) * ch * big).to(dt)
         v = (torch.randn((rows, n, d), generator=g, device=dev) * big).to(dt)
         return dict(op=op, k=k, v=v, k8=k8, v8=v8, ks=ks, vs=vs, table=table, len=i32(old + new),
-                    cu=cu(new), row_seq=i32(np.repeat(np.arange(len(new)), new)))
+                    cu=cu(new))
     (length,) = lens
     table, num = _pages(length, P, dev, g)
     k8, ks = _filled(num, n, P, d, ch, dev, g)
@@ -273,9 +273,10 @@ def _prompt_plain(s):
 def _append_plain(s):
     n_rows, N, D = s["k"].shape
     P = s["k8"].shape[2]
-    seq = s["row_seq"].long()
     cu, length = s["cu"].long(), s["len"].long()
-    pos = length[seq] - (cu[seq + 1] - torch.arange(n_rows, device=seq.device))
+    row = torch.arange(n_rows, device=cu.device)
+    seq = torch.searchsorted(cu[1:], row, right=True)
+    pos = length[seq] - (cu[seq + 1] - row)
     block, off = s["table"].long()[seq, pos // P], pos % P
     # the tokens that each page held before: none where this step begins it
     held = torch.full_like(s["ks"][:, 0], P, dtype=torch.long).index_reduce_(0, block, off, "amin")
@@ -323,7 +324,7 @@ def run(s):
             return rkv.prompt_attention(s["q"], s["k"], s["v"], s["cu_q"], s["cu_k"])
         if op == "append":
             rkv.page_append(s["k"], s["v"], s["k8"], s["v8"], s["ks"], s["vs"], s["table"], s["len"],
-                            s["cu"], s["row_seq"])
+                            s["cu"])
             return s["k8"].view(torch.float8_e4m3fn), s["v8"].view(torch.float8_e4m3fn), s["ks"], s["vs"]
         return rkv.page_attention(s["q"], s["k8"], s["v8"], s["ks"], s["vs"], s["table"], s["len"])
     if op == "plan":
