@@ -59,7 +59,8 @@ enum {
   RKV_FLAG_BAD_INDEX = 2,    /* a selected (seq, pos) was out of range        */
   RKV_FLAG_UNWRITTEN = 4,    /* a selected token was never written            */
   RKV_FLAG_FP16_SAT = 8,     /* a group extreme saturated at +-65504          */
-  RKV_FLAG_BAD_SLOT = 16     /* a pool slot outside [0, max_refs)             */
+  RKV_FLAG_BAD_SLOT = 16,    /* a pool slot outside [0, max_refs)             */
+  RKV_FLAG_NO_SPACE = 32     /* rkv_page_plan / rkv_page_release: refused     */
 };
 
 /*
@@ -348,6 +349,179 @@ rkv_status rkv_retrieve_noalloc(const void* queries, const int32_t* q_pos, int32
                                 const void* pool, const float* pool_norm2,
                                 const int32_t* pool_pos, int32_t R, int32_t d, int32_t topk,
                                 int32_t* out_idx, int32_t* flags, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Full-attention layers.  The deployment that the page describes keeps full attention in
+ * a few layers (ResidualKV notes §2.7: they pick the index set the sparse layers restore)
+ * and stores their K/V quantised.  These entry points serve such layers: a step's pages
+ * are planned on the GPU from the requests' lengths, the packed prompts are attended with
+ * their raw K/V, every new K/V row is stored in 8 bits, and a decode step attends the
+ * stored rows.  K arrives rotated (or with whatever position encoding the model uses).
+ *
+ * They need no context: every buffer is the caller's, nothing is allocated, kept from one
+ * call for the next or looked up by address, and calls whose buffers differ may run
+ * concurrently.  Every call may be captured into a CUDA graph; lengths are read on the
+ * device when the graph runs.
+ *   flags (device, int32) or NULL: RKV_FLAG_* bits are ORed into it (the caller clears it).
+ * What only the device can see never faults: lengths, offsets and block ids are checked
+ * there, and what is out of range is treated as absent.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * K/V rows of one layer in 8 bits, in pages of block_tokens positions (16, 32, 64 or 128):
+ *   k, v       (device) [num_blocks, N, block_tokens, D]  E4M3 codes; 16-byte aligned
+ *   k_scale, v_scale (device, fp32) [num_blocks, N]  one scale per page and head: a code c
+ *              stands for c * scale.  Scales are powers of two in [2^-64, 2^120], so a
+ *              stored value times its scale has no second rounding.
+ * N >= 1; head_dim 64 or 128; num_blocks * N * block_tokens < 2^31.  Needs no
+ * initialisation: rows that no append wrote are never used.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t block_tokens;
+  int32_t num_blocks;
+} rkv_pages;
+
+/*
+ * Where sequences' positions are: position p of sequence b lies in row p % block_tokens of
+ * page block_table[b][p / block_tokens].  One table serves all layers of a model.
+ *   block_table (device, int32) [batch, max_blocks]; entries past a sequence's pages are
+ *     ignored.
+ *   seq_len     (device, int32) [batch]  positions stored (after a step's appends).
+ * batch in [1, 8192]; max_blocks * block_tokens < 2^31.
+ */
+typedef struct {
+  int32_t* block_table;
+  int32_t* seq_len;
+  int32_t batch;
+  int32_t max_blocks;
+} rkv_page_table;
+
+/*
+ * Plan one step: sequence b appends new_tokens[b] >= 0 positions to the seq_len[b] that it
+ * has.  Pages that become needed are taken from the end of the free list, in order of
+ * sequence and position: the i-th is free_blocks[n_free - 1 - i].
+ *   table: block_table receives the new pages; seq_len is read.
+ *   free_blocks (device, int32) [num_blocks], n_free (device, int32) [1]: the free list.
+ *   seq_len_out (device) [batch], n_free_out (device) [1]: the lengths and the free count
+ *     after the step.  They may be table->seq_len and n_free themselves (update in place);
+ *     with others, the call can be repeated with the same result.
+ *   cu_rows (device, int32) [batch + 1]: first packed row of each sequence's new positions,
+ *     and their total.
+ *   row_seq, row_pos, row_slot (device, int32) [max_rows]: of each packed row, its sequence,
+ *     its position and its slot (page * block_tokens + row in the page); -1 past the total.
+ * All or nothing: where a length is negative or passes max_blocks * block_tokens
+ * (RKV_FLAG_BAD_INDEX), or the rows pass max_rows or the pages n_free (RKV_FLAG_NO_SPACE),
+ * no page is taken, lengths and free count stay, cu_rows is all 0 and the rows are all -1.
+ * Outputs must not overlap each other or the inputs, but for the two named.
+ * Errors (nothing launched): RKV_EINVAL.
+ */
+rkv_status rkv_page_plan(const rkv_page_table* table, const int32_t* new_tokens,
+                         const int32_t* free_blocks, const int32_t* n_free, int32_t num_blocks,
+                         int32_t block_tokens, int32_t max_rows, int32_t* seq_len_out,
+                         int32_t* n_free_out, int32_t* cu_rows, int32_t* row_seq,
+                         int32_t* row_pos, int32_t* row_slot, int32_t* flags, void* stream);
+
+/*
+ * Give finished sequences' pages back: for each b with finished[b] != 0 (device, int32
+ * [batch]), in order of sequence and position, its pages are put on the end of the free
+ * list, its table entries become -1 and its length 0.  If they do not fit the list (more
+ * than num_blocks), or a length is out of range, nothing changes and RKV_FLAG_NO_SPACE or
+ * RKV_FLAG_BAD_INDEX is raised.  Errors (nothing launched): RKV_EINVAL.
+ */
+rkv_status rkv_page_release(const rkv_page_table* table, const int32_t* finished,
+                            int32_t* free_blocks, int32_t* n_free, int32_t num_blocks,
+                            int32_t block_tokens, int32_t* flags, void* stream);
+
+/*
+ * Store a step's K/V rows in their pages (after rkv_page_plan, in stream order).
+ *   k, v (device, dtype RKV_BF16 or RKV_F32) [n_rows, N, D]: packed row r, head h at
+ *     k + r * k_strides[0] + h * k_strides[1] elements; 16-byte aligned rows.
+ *   cu_rows (device, int32) [batch + 1] and table->seq_len (after the step): rows
+ *     cu_rows[b] .. cu_rows[b + 1] - 1 are the last positions of sequence b.  Rows past
+ *     cu_rows[batch] are ignored.
+ * Scale of a page and head: the smallest power of two s >= 2^-64 with |x| <= 448 s for every
+ * finite x that the call brings to it, and no smaller than the page's present scale unless
+ * the call brings the page's row 0 (which begins the page anew).  Codes are E4M3(x / s),
+ * rounded to nearest even; infinities are stored as +-448 s, NaN stays NaN.  Where s grows,
+ * the rows that the page held before are rounded again at the new scale (exact but for
+ * values below 2^-6 s).
+ * Pages of different sequences must differ where they are written.
+ * A row whose position or page is out of range is left out (RKV_FLAG_BAD_INDEX).
+ * Errors (nothing launched): RKV_EINVAL, RKV_EALIGN, RKV_ECUDA.
+ */
+rkv_status rkv_page_append(const rkv_pages* pages, const rkv_page_table* table, const void* k,
+                           const int64_t k_strides[2], const void* v, const int64_t v_strides[2],
+                           int32_t dtype, int32_t n_rows, const int32_t* cu_rows, int32_t* flags,
+                           void* stream);
+
+/*
+ * Decode attention over the pages: o = softmax(scale q K^T) V over the seq_len[b] stored
+ * positions of each sequence, K and V as the codes and scales stand for them.
+ *   q (device, bf16) [batch, n_q_heads, D], row b, head h at q + b * q_strides[0] +
+ *     h * q_strides[1] elements (16-byte aligned); query head h reads key/value head
+ *     h / (n_q_heads / N).  n_q_heads: a multiple of N, at most 16 N.
+ *   scale: finite, > 0 (usually 1 / sqrt(D)).
+ *   out (device, bf16) [batch, n_q_heads, D], contiguous.
+ *   lse (device, fp32) [batch, n_q_heads] or NULL: log of the sum of exp(scale q.k).
+ *   workspace (device, 16-byte aligned): rkv_page_attention_workspace bytes, this call's
+ *     alone while it runs; its contents need no initialisation.
+ * A sequence of length 0 gives a zero row (lse -inf).  Positions whose page id is out of
+ * range are left out, and a length past the table is cut (RKV_FLAG_BAD_INDEX).  Bytes of a
+ * page behind the sequence's last position are never used, whatever they hold.
+ * The scores are exact products of bf16 q and the stored codes summed in fp32 (elements of
+ * q below 2^-21 of their row's largest are rounded to it); the weights enter the second
+ * product with 12 significant bits; sums are fp32.
+ * Errors (nothing launched): RKV_EINVAL, RKV_EALIGN, RKV_ECAPACITY (workspace), RKV_ECUDA.
+ */
+rkv_status rkv_page_attention(const rkv_pages* pages, const rkv_page_table* table, const void* q,
+                              const int64_t q_strides[2], int32_t n_q_heads, double scale,
+                              void* out, float* lse, void* workspace, size_t workspace_bytes,
+                              int32_t* flags, void* stream);
+
+/* Workspace of rkv_page_attention for these sizes, in *bytes (host).  No device work. */
+rkv_status rkv_page_attention_workspace(const rkv_pages* pages, const rkv_page_table* table,
+                                        int32_t n_q_heads, size_t* bytes);
+
+/*
+ * Causal attention of packed prompts with their raw K/V.
+ *   q (device, bf16) [total_q, n_q_heads, D], k, v (device, bf16) [total_k, N, D], out
+ *     (device, bf16) [total_q, n_q_heads, D]: row r, head h at r * strides[0] +
+ *     h * strides[1] elements; 16-byte aligned rows.  head_dim 64 or 128; n_q_heads a
+ *     multiple of N.
+ *   cu_q, cu_k (device, int32) [batch + 1]: first row of each sequence in q and in k / v,
+ *     non-decreasing from 0.  The queries are the last positions of their sequence: query i of
+ *     Lq sees keys 0 .. Lk - Lq + i (an earlier chunk's keys come first).  A query that sees
+ *     none (Lk < Lq) gives a zero row (lse -inf).
+ *   scale: finite, > 0 (usually 1 / sqrt(D)).
+ *   lse (device, fp32) [total_q, n_q_heads] or NULL: log of the sum of exp(scale q.k).
+ * Rows of out past cu_q[batch] are left as they are.  Rows of other sequences and rows past
+ * the last one have no effect, whatever they hold.  Within a sequence a NaN or infinity of V
+ * reaches rows that see it and may reach up to 255 rows before it (weights of 0 times NaN).
+ * Scores are exact bf16 products summed in fp32; the weights enter the second product as
+ * bf16; sums are fp32.  batch in [1, 8192].
+ * Offsets that decrease or pass total_q / total_k are cut (RKV_FLAG_BAD_INDEX).
+ * Errors (nothing launched): RKV_EINVAL, RKV_EALIGN, RKV_ECUDA.
+ */
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* out;
+  float* lse;
+  int64_t q_strides[2], k_strides[2], v_strides[2], out_strides[2];
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int32_t batch, total_q, total_k, n_q_heads, n_kv_heads, head_dim;
+  double scale;
+} rkv_prompt;
+
+rkv_status rkv_prompt_attention(const rkv_prompt* prompt, int32_t* flags, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Instrumentation (not part of the method).

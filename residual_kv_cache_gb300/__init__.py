@@ -16,12 +16,14 @@ import torch
 
 __all__ = ["RkvError", "RkvLibraryMissing", "Config", "Codec", "lib", "LIB_PATH", "retrieve_noalloc",
            "FLAG_TIMEOUT", "FLAG_BAD_INDEX", "FLAG_UNWRITTEN", "FLAG_FP16_SAT", "FLAG_BAD_SLOT",
-           "ABI_FUNCTIONS", "reconstruct_multi"]
+           "ABI_FUNCTIONS", "reconstruct_multi", "FLAG_NO_SPACE", "PagedCache", "PagePlan", "PageTable",
+           "page_plan", "page_release", "page_append", "page_attention", "prompt_attention"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "librkv.so")
 
 RKV_F32, RKV_BF16 = 0, 1
 FLAG_TIMEOUT, FLAG_BAD_INDEX, FLAG_UNWRITTEN, FLAG_FP16_SAT, FLAG_BAD_SLOT = 1, 2, 4, 8, 16
+FLAG_NO_SPACE = 32
 STATUS_NAMES = {0: "RKV_OK", -1: "RKV_EINVAL", -2: "RKV_EALIGN", -3: "RKV_ECAPACITY",
                 -4: "RKV_EEMPTYPOOL", -5: "RKV_ECUDA", -6: "RKV_EDEVICE", -7: "RKV_ETIMEOUT"}
 
@@ -84,6 +86,13 @@ ABI_FUNCTIONS = {
     "rkv_debug_scratch": (_I32, [_P, _I32, ctypes.POINTER(_P), ctypes.POINTER(ctypes.c_size_t)]),
     "rkv_debug_timeout_probe": (_I32, [_P, _P]),
     "rkv_retrieve_noalloc": (_I32, [_P, _P, _I32, _P, _P, _P, _I32, _I32, _I32, _P, _P, _P]),
+    "rkv_page_plan": (_I32, [_P, _P, _P, _P, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "rkv_page_release": (_I32, [_P, _P, _P, _P, _I32, _I32, _P, _P]),
+    "rkv_page_append": (_I32, [_P, _P, _P, _P, _P, _P, _I32, _I32, _P, _P, _P]),
+    "rkv_page_attention": (_I32, [_P, _P, _P, _P, _I32, ctypes.c_double, _P, _P, _P,
+                                  ctypes.c_size_t, _P, _P]),
+    "rkv_page_attention_workspace": (_I32, [_P, _P, _I32, ctypes.POINTER(ctypes.c_size_t)]),
+    "rkv_prompt_attention": (_I32, [_P, _P, _P]),
 }
 
 _lib = None
@@ -477,3 +486,7 @@ class Codec:
             self.free()
         except Exception:
             pass
+
+
+from .pages import (PagedCache, PagePlan, PageTable, page_append, page_attention,  # noqa: E402
+                    page_plan, page_release, prompt_attention)

@@ -14,6 +14,7 @@
 #include <string>
 #include <vector>
 
+#include "pages.h"
 #include "rkv_internal.h"
 
 using namespace rkv;
@@ -31,6 +32,21 @@ rkv_status fail(rkv_status s, const char* fmt, ...) {
   g_err = buf;
   return s;
 }
+
+}  // namespace
+
+namespace rkv {
+rkv_status fail_with(rkv_status s, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return fail(s, "%s", buf);
+}
+}  // namespace rkv
+
+namespace {
 
 #define CUDA_OK(call)                                                                    \
   do {                                                                                  \

@@ -1,0 +1,543 @@
+"""GPU parity of the full-attention layers' operators against their float64 definitions.
+
+Tolerances, per element, from the roundings (u = half a step, relative):
+* plan, release, codes and scales: equal (whole numbers, powers of two, one rounding each);
+* prompt attention: the output's bf16 rounding (u = 2^-8), each weight's bf16 rounding
+  (2^-8 of sum w |v| at most), and fp32 scores: a D-term sum is off by at most
+  D 2^-24 sum |q||k|, twice that (relative) in a weight over its normaliser, doubled
+  again for the scale, the subtraction and exp2, whose arguments are below 2^8;
+* page attention: the same with weights of 12 significant bits (2^-12) of the largest
+  weight's scale: 2^-11 of sum w |v| covers it and the range kept below the maximum;
+* lse: the fp32 score error and 2^-20 of its magnitude.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import residual_kv_cache_gb300 as rkv
+from oracle import pages as OP
+
+from _common import np64
+
+pytestmark = pytest.mark.gpu
+cuda = pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def randn(*shape, seed, dtype=torch.bfloat16):
+    return torch.randn(shape, generator=gen(seed)).to(dtype).cuda()
+
+
+def close(out, ref, a, big, D, weight_u, out_u=2.0 ** -8):
+    tol = out_u * np.abs(ref) + (weight_u + 4 * D * 2.0 ** -24 * big + 2.0 ** -14) * a + 1e-30
+    err = np.abs(np64(out) - ref)
+    assert np.all(err <= tol), float((err / tol).max())
+
+
+def close_lse(lse, ref, big, D):
+    got = np64(lse)
+    none = np.isneginf(ref)
+    assert np.array_equal(np.isneginf(got), none)
+    fin = ~none
+    assert np.all(np.abs(got[fin] - ref[fin]) <= 2 * D * 2.0 ** -24 * big + 2.0 ** -20 * (1 + np.abs(ref[fin])))
+
+
+# -------------------------------------------------------------------------------- plan
+def _plan_inputs(new, lens, P, M, spare, seed):
+    g = np.random.default_rng(seed)
+    have = [-(-x // P) for x in lens]
+    need = [max(0, -(-(x + y) // P) - h) for x, y, h in zip(lens, new, have)]
+    ids = g.permutation(sum(have) + sum(need) + spare)
+    table, at = np.full((len(lens), M), -1), 0
+    for b, h in enumerate(have):
+        table[b, :h] = ids[at:at + h]
+        at += h
+    free = ids[at:]
+    return table, np.concatenate([free, np.zeros(len(ids) - len(free), np.int64)]), len(free)
+
+
+PLANS = [  # lens, new, P
+    ([0], [1], 16), ([15, 16, 17, 0], [1, 1, 1, 0], 16), ([0, 0, 0], [0, 0, 0], 64),
+    ([5] * 33, [1] * 33, 64), ([0, 100, 127, 128, 0], [700, 0, 1, 0, 129], 128),
+    (list(range(0, 1200, 2)), [(7 * i) % 50 for i in range(600)], 32),
+    ([0], [40000], 16), ([3000, 0], [0, 20011], 64)]
+
+
+@cuda
+@pytest.mark.parametrize("case", range(len(PLANS)))
+@pytest.mark.parametrize("inplace", [False, True])
+def test_plan_matches_the_definition(case, inplace):
+    lens, new, P = PLANS[case]
+    M = max(1, max(-(-(a + b) // P) for a, b in zip(lens, new))) + 1
+    table, free, nf = _plan_inputs(new, lens, P, M, 2, case)
+    rows = sum(new) + 5
+    cu, ref_rows, lens2, left, table2 = OP.plan(new, lens, table, free, nf, P, rows)
+    t, ln, n = i32(table), i32(lens), i32([nf])
+    lo, no = (ln, n) if inplace else (torch.full_like(ln, -7), torch.full_like(n, -7))
+    flags = i32([0])
+    for _ in range(1 if inplace else 2):                    # repeatable when not in place
+        p = rkv.page_plan(i32(new), ln, t, i32(free), n, P, rows, lo, no, flags=flags)
+        assert p.cu_rows.tolist() == cu and lo.tolist() == lens2 and no.tolist() == [left]
+        assert np.array_equal(t.cpu().numpy(), table2)
+        got = torch.stack([p.row_seq, p.row_pos, p.row_slot]).cpu().numpy().T
+        assert np.array_equal(got[:len(ref_rows)], np.array(ref_rows).reshape(-1, 3))
+        assert np.all(got[len(ref_rows):] == -1)
+    assert flags.item() == 0
+    if not inplace:
+        assert ln.tolist() == lens and n.tolist() == [nf]
+
+
+@cuda
+@pytest.mark.parametrize("why", ["rows", "pages", "table", "negative", "negative_len", "free"])
+def test_plan_that_does_not_fit_changes_nothing(why):
+    lens, new, P, M = [10, 20, 0], [30, 0, 50], 16, 4
+    table, free, nf = _plan_inputs(new, lens, P, M, 0, 1)
+    rows, bit = 80, rkv.FLAG_NO_SPACE
+    if why == "rows":
+        rows = 79
+    elif why == "pages":
+        nf -= 1
+    else:
+        bit = rkv.FLAG_BAD_INDEX
+        if why == "table":
+            new[2] = 65
+        elif why == "negative":
+            new[1] = -1
+        elif why == "negative_len":
+            lens[1] = -3
+        else:
+            nf = len(free) + 1
+    for inplace in (False, True):
+        t, ln, n, flags = i32(table), i32(lens), i32([nf]), i32([0])
+        lo, no = (ln, n) if inplace else (torch.full_like(ln, -7), torch.full_like(n, -7))
+        p = rkv.page_plan(i32(new), ln, t, i32(free), n, P, rows, lo, no, flags=flags)
+        assert flags.item() == bit
+        assert p.cu_rows.tolist() == [0] * 4 and lo.tolist() == lens and no.tolist() == [nf]
+        assert np.array_equal(t.cpu().numpy(), table)
+        assert torch.all(p.row_seq == -1) and torch.all(p.row_pos == -1) and torch.all(p.row_slot == -1)
+
+
+@cuda
+def test_release_matches_the_definition_and_refuses_what_does_not_fit():
+    g = np.random.default_rng(5)
+    lens = [int(x) for x in g.integers(0, 300, size=700)]
+    fin = [int(x) for x in g.integers(0, 3, size=700)]
+    table, free, nf = _plan_inputs([0] * 700, lens, 16, 20, 9, 6)
+    l2, t2, f2, n2 = OP.release(fin, lens, table, free, nf, 16)
+    t, ln, f, n, flags = i32(table), i32(lens), i32(free), i32([nf]), i32([0])
+    rkv.page_release(i32(fin), ln, t, f, n, 16, flags=flags)
+    assert ln.tolist() == l2 and n.item() == n2 and flags.item() == 0
+    assert np.array_equal(t.cpu().numpy(), t2) and f[:n2].tolist() == [int(x) for x in f2[:n2]]
+    for bad in ("list", "length"):
+        t, ln, f, n, flags = i32(table), i32(lens), i32(free), i32([nf]), i32([0])
+        if bad == "list":
+            n.fill_(len(free) - n2 + nf + 1)
+        else:
+            ln[fin.index(1)] = 16 * 20 + 1
+        before = [x.clone() for x in (t, ln, f, n)]
+        rkv.page_release(i32(fin), ln, t, f, n, 16, flags=flags)
+        assert flags.item() == (rkv.FLAG_NO_SPACE if bad == "list" else rkv.FLAG_BAD_INDEX)
+        assert all(torch.equal(x, y) for x, y in zip(before, (t, ln, f, n)))
+
+
+# ------------------------------------------------------------------------------ append
+def _f8(codes):
+    return np64(codes.view(torch.float8_e4m3fn).float())
+
+
+def _cache(num, N, P, D, seed):
+    """Pages of random codes (no NaN) and small scales."""
+    g = gen(seed)
+    c = torch.randn((2, num, N, P, D), generator=g).to(torch.float8_e4m3fn).view(torch.uint8).cuda()
+    s = torch.exp2(torch.randint(-9, -5, (2, num, N), generator=g).float()).cuda()
+    return c[0], c[1], s[0], s[1]
+
+
+@cuda
+@pytest.mark.parametrize("P,D,dtype", [(16, 64, torch.bfloat16), (16, 128, torch.float32), (32, 128, torch.bfloat16),
+                                       (64, 128, torch.bfloat16), (64, 64, torch.float32), (128, 128, torch.float32),
+                                       (128, 64, torch.bfloat16)])
+@pytest.mark.parametrize("what", ["decode", "mixed", "prompt"])
+def test_append_matches_the_definition(P, D, dtype, what):
+    N = 3
+    old = {"decode": [0, 5, P - 1, P, 3 * P + 7], "mixed": [0, 5, P, 0, 2 * P - 1, 9], "prompt": [0]}[what]
+    new = {"decode": [1] * 5, "mixed": [3 * P + 1, 1, 0, P, 2 * P + 2, 0], "prompt": [5 * P + 3]}[what]
+    lens, cu = [a + b for a, b in zip(old, new)], [0] + np.cumsum(new).tolist()
+    M = max(-(-x // P) for x in lens) + 1
+    table, _, _ = _plan_inputs([0] * len(lens), lens, P, M, 3, 11)
+    num = int(table.max()) + 4
+    k8, v8, ks, vs = _cache(num, N, P, D, 12)
+    ref = [(_f8(k8), np64(ks)), (_f8(v8), np64(vs))]
+    n = sum(new)
+    kv = torch.randn((n + 2, 2 * N + 1, D), generator=gen(13)) * torch.exp2(
+        torch.randint(-8, 4, (n + 2, 2 * N + 1, 1), generator=gen(14)).float())
+    kv = kv.to(dtype).cuda()
+    k, v = kv[:, :N], kv[:, N + 1:]                         # strided views; two rows too many
+    flags = i32([0])
+    rkv.page_append(k, v, k8, v8, ks, vs, i32(table), i32(lens), i32(cu), flags=flags)
+    for x, codes, scale, (rc, rs) in ((k, k8, ks, ref[0]), (v, v8, vs, ref[1])):
+        OP.append(np64(x), rc, rs, table.tolist(), lens, cu, P)
+        assert np.array_equal(np64(scale), rs)
+        assert np.array_equal(_f8(codes), rc)
+    assert flags.item() == 0
+
+
+@cuda
+def test_append_of_zeros_infinities_and_nan():
+    P, N, D = 16, 2, 64
+    x = torch.zeros((3, N, D))
+    x[1, 0, 5], x[1, 0, 6], x[2, 0, 7], x[2, 0, 8] = math.inf, -math.inf, math.nan, 3.0
+    x[0, 1, 0] = 1e-30                                       # below the smallest scale's codes
+    for dt in (torch.float32, torch.bfloat16):
+        xx = x.to(dt).cuda()
+        k8, v8, ks, vs = _cache(2, N, P, D, 15)
+        rc, rs = _f8(k8), np64(ks)
+        rkv.page_append(xx, xx, k8, v8, ks, vs, i32([[1]]), i32([3]), i32([0, 3]))
+        OP.append(np64(xx), rc, rs, [[1]], [3], [0, 3], P)
+        assert np.array_equal(np64(ks), rs) and np.array_equal(_f8(k8), rc, equal_nan=True)
+        assert _f8(k8)[1, 0, 1, 5] == 448 and np.isnan(_f8(k8)[1, 0, 2, 7]) and rs[1, 1] == 2.0 ** -64
+
+
+@cuda
+def test_append_leaves_out_what_is_out_of_range():
+    """Bad page ids, lengths past the table and offsets past the rows: those rows are left
+    out and flagged, the others stored."""
+    P, N, D = 16, 2, 64
+    x = randn(6, N, D, seed=16)
+    for case in ("id", "negative_id", "length", "rows", "offset"):
+        k8, v8, ks, vs = _cache(4, N, P, D, 17)
+        rc, rs = _f8(k8), np64(ks)
+        table, lens, cu = [[0, 1], [2, 3], [1, 0]], [3, 18, 0], [0, 3, 6, 6]
+        flags = i32([0])
+        t2, l2, c2 = [list(r) for r in table], list(lens), list(cu)
+        if case == "id":
+            t2[0][0] = 4
+        elif case == "negative_id":
+            t2[0][0] = -1
+        elif case == "length":
+            l2[0] = 33
+        elif case == "rows":
+            c2[3] = 7                                       # more rows than the third length holds
+        else:
+            c2[0] = -2
+        rkv.page_append(x, x, k8, v8, ks, vs, i32(t2), i32(l2), i32(c2), flags=flags)
+        keep = [0, 0, 3, 3] if case != "rows" else cu[:2] + [6, 6]
+        if case == "rows":
+            OP.append(np64(x), rc, rs, table, lens, cu, P)
+        else:
+            OP.append(np64(x), rc, rs, table, [0, 18, 0], [3, 3, 6, 6], P)
+        assert np.array_equal(np64(ks), rs) and np.array_equal(_f8(k8), rc), (case, keep)
+        assert flags.item() == rkv.FLAG_BAD_INDEX
+
+
+# --------------------------------------------------------------------- page attention
+def _paged(lens, N, P, D, seed, poison=True, spread=0):
+    """Pages holding random K/V for sequences of these lengths; NaN codes and scales
+    everywhere else.  Returns the library's tensors and the stored values in float64."""
+    M = max(1, max(-(-x // P) for x in lens)) + 1
+    table, _, _ = _plan_inputs([0] * len(lens), lens, P, M, 3, seed)
+    num = int(table.max()) + 4
+    k8, v8, ks, vs = _cache(num, N, P, D, seed + 1)
+    if spread:
+        ks *= torch.exp2(torch.randint(0, 3, ks.shape, generator=gen(seed + 2)).float()).cuda()
+        vs *= torch.exp2(torch.randint(-spread, spread + 1, vs.shape, generator=gen(seed + 3)).float()).cuda()
+    ks *= 8
+    val = [_f8(c) * np64(s)[:, :, None, None] for c, s in ((k8, ks), (v8, vs))]
+    if poison:
+        used = torch.zeros((num, P), dtype=torch.bool, device="cuda")
+        for b, n in enumerate(lens):
+            for t in range(-(-n // P)):
+                used[table[b, t], :min(P, n - t * P)] = True
+        for c in (k8, v8):
+            c.masked_fill_(~used[:, None, :, None], 0x7F)
+        empty = ~used.any(1)
+        ks[empty], vs[empty] = math.nan, math.inf
+    return (k8, v8, ks, vs), i32(table), table, val
+
+
+ATTEND = [  # lens, Hq, N, P, D
+    ([1], 1, 1, 16, 128), ([0, 1, 2, 15, 16, 17], 8, 2, 16, 64), ([127, 128, 129, 0, 255], 28, 4, 64, 128),
+    ([1000], 32, 8, 64, 128), ([300, 5, 77], 32, 2, 32, 128), ([513, 1, 64], 9, 1, 128, 128),
+    ([700, 650], 12, 1, 16, 64), ([40] * 70, 5, 5, 32, 64), ([5000, 3, 2047], 14, 2, 64, 64),
+    ([130] * 3, 24, 2, 128, 128)]
+
+
+@cuda
+@pytest.mark.parametrize("case", range(len(ATTEND)))
+def test_page_attention_matches_the_definition(case):
+    lens, Hq, N, P, D = ATTEND[case]
+    cache, table, tb, (kv, vv) = _paged(lens, N, P, D, 100 + case)
+    q = randn(len(lens), Hq + 1, D, seed=200 + case)[:, 1:]             # a strided view
+    lse = torch.empty((len(lens), Hq), device="cuda")
+    flags = i32([0])
+    sc = 1 / math.sqrt(D)
+    out = rkv.page_attention(q, *cache, table, i32(lens), lse=lse, flags=flags)
+    ref, rl, a, big = OP.page_attention(np64(q), kv, vv, tb, lens, P, sc)
+    close(out, ref, a, big, D, 2.0 ** -11)
+    close_lse(lse, rl, big, D)
+    assert flags.item() == 0
+    again = rkv.page_attention(q, *cache, table, i32(lens))
+    assert torch.equal(again, out)                                       # no order of atomics
+
+
+@cuda
+@pytest.mark.parametrize("spread", [0, 10])
+def test_page_attention_peaked_and_wide_scales(spread):
+    """Large scores (one key takes nearly all), a growing maximum, and value scales that
+    differ by 2^20 between pages."""
+    lens, Hq, N, P, D = [900, 260], 16, 2, 16, 128
+    cache, table, tb, (kv, vv) = _paged(lens, N, P, D, 300, spread=spread)
+    for mult in (0.01, 6.0):
+        q = randn(2, Hq, D, seed=301) * mult
+        out = rkv.page_attention(q, *cache, table, i32(lens), scale=0.09)
+        ref, _, a, big = OP.page_attention(np64(q), kv, vv, tb, lens, P, 0.09)
+        # weights are held to 12 bits of the largest weight times page scale seen: the error of
+        # an element is relative to the largest of its head and dimension's sums
+        close(out, ref, a.max(axis=-1, keepdims=True) + 0 * a, big, D, 2.0 ** -11)
+
+
+@cuda
+def test_page_attention_leaves_out_bad_pages_and_cuts_lengths():
+    lens, Hq, N, P, D = [100, 64, 40], 8, 2, 16, 128
+    cache, table, tb, (kv, vv) = _paged(lens, N, P, D, 400, poison=False)
+    q = randn(3, Hq, D, seed=401)
+    t2, flags = table.clone(), i32([0])
+    t2[0, 2], t2[1, 1], t2[2, 0] = -1, 10 ** 6, -5
+    out = rkv.page_attention(q, *cache, t2, i32([100, 64, 10 ** 9]), flags=flags)
+    assert flags.item() == rkv.FLAG_BAD_INDEX
+    keep = [[0, 1, 3, 4, 5, 6], [0, 2, 3], list(range(1, t2.shape[1]))]
+    for b, pages in enumerate(keep):
+        ids = [int(t2[b, j]) for j in pages if 0 <= int(t2[b, j]) < kv.shape[0]]
+        n = {0: 84, 1: 48, 2: 16 * len(ids)}[b]
+        ref, _, a, big = OP.page_attention(np64(q[b:b + 1]), kv, vv, [ids], [n], P, 1 / math.sqrt(D))
+        close(out[b:b + 1], ref, a, big, D, 2.0 ** -11)
+    out = rkv.page_attention(q, *cache, table, i32([-4, 0, 40]), flags=flags)
+    assert not out[:2].any() and out[2].any()
+
+
+@cuda
+def test_page_attention_nan_stays_with_its_head_and_sequence():
+    lens, Hq, N, P, D = [140, 140], 8, 2, 64, 128
+    cache, table, tb, (kv, vv) = _paged(lens, N, P, D, 500)
+    q = randn(2, Hq, D, seed=501)
+    clean = rkv.page_attention(q, *cache, table, i32(lens))
+    q2 = q.clone()
+    q2[0, 5, 3], q2[0, 1, 0] = math.nan, math.inf
+    out = rkv.page_attention(q2, *cache, table, i32(lens))
+    assert torch.isnan(out[0, 5]).all() and torch.isnan(out[0, 1]).all()
+    same = torch.ones((2, Hq), dtype=torch.bool, device="cuda")
+    same[0, 5] = same[0, 1] = False
+    assert torch.equal(out[same], clean[same])
+    cache[1][int(tb[1, 1]), 1, 7, 9] = 0x7F                              # a stored NaN of V, head 1
+    out = rkv.page_attention(q, *cache, table, i32(lens))
+    bad = torch.isnan(out)
+    want = torch.zeros_like(bad)
+    want[1, 4:, 9] = True
+    assert torch.equal(bad, want) and torch.equal(out[~bad], clean[~bad])
+
+
+# ------------------------------------------------------------------- prompt attention
+PROMPT = [  # lq, lk, Hq, N, D
+    ([1], [1], 1, 1, 128), ([1, 2, 3], [1, 2, 3], 4, 2, 64), ([77], [77], 32, 8, 128),
+    ([128, 0, 129, 1, 127], [128, 0, 129, 1, 127], 14, 2, 128), ([300, 45], [300, 45], 3, 3, 64),
+    ([260], [700], 8, 2, 128), ([5, 1, 130], [400, 257, 130], 7, 1, 64), ([200, 10], [60, 0], 4, 1, 128),
+    ([33] * 9, [33] * 9, 5, 1, 128), ([513], [513], 2, 1, 128), ([100, 20], [0, 300], 4, 2, 64)]
+
+
+def _cu(lens):
+    return [0] + np.cumsum(lens).tolist()
+
+
+@cuda
+@pytest.mark.parametrize("case", range(len(PROMPT)))
+def test_prompt_attention_matches_the_definition(case):
+    lq, lk, Hq, N, D = PROMPT[case]
+    cq, ck = _cu(lq), _cu(lk)
+    pad = 7                                                  # rows behind the last sequence
+    q = randn(cq[-1] + pad, Hq, D, seed=600 + case)
+    kv = randn(ck[-1] + pad, 2 * N, D, seed=700 + case) * 2
+    kv[ck[-1]:] = math.nan
+    q[cq[-1]:] = math.inf
+    k, v = kv[:, :N], kv[:, N:]
+    out = torch.full((cq[-1] + pad, Hq, D), 5.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((cq[-1] + pad, Hq), 5.0, device="cuda")
+    flags = i32([0])
+    got = rkv.prompt_attention(q, k, v, i32(cq), i32(ck), out=out, lse=lse, flags=flags)
+    assert got is out and flags.item() == 0
+    ref, rl, a, big = OP.prompt_attention(np64(q[:cq[-1]]), np64(k[:ck[-1]]), np64(v[:ck[-1]]), cq, ck,
+                                          1 / math.sqrt(D))
+    close(out[:cq[-1]], ref, a, big, D, 2.0 ** -8)
+    close_lse(lse[:cq[-1]], rl, big, D)
+    assert torch.all(out[cq[-1]:] == 5.0) and torch.all(lse[cq[-1]:] == 5.0)
+
+
+@cuda
+@pytest.mark.parametrize("layout", ["packed", "heads_first", "fused"])
+def test_prompt_attention_layouts(layout):
+    T, Hq, N, D = 200, 6, 2, 128
+    q, k, v = randn(T, Hq, D, seed=801), randn(T, N, D, seed=802), randn(T, N, D, seed=803)
+    base = rkv.prompt_attention(q, k, v, i32([0, 150, T]))
+    out = None
+    if layout == "heads_first":
+        q, k, v = (x.transpose(0, 1).contiguous().transpose(0, 1) for x in (q, k, v))
+        out = torch.empty((Hq, T, D), dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    elif layout == "fused":
+        x = torch.cat([q, k, v, q[:, :1]], dim=1)
+        q, k, v = x[:, :Hq], x[:, Hq:Hq + N], x[:, Hq + N:Hq + 2 * N]
+    assert torch.equal(rkv.prompt_attention(q, k, v, i32([0, 150, T]), out=out), base)
+    # a batch of the same rows, one head's keys for all heads of a group
+    one = rkv.prompt_attention(q, k[:, :1], v[:, :1], i32([0, 150, T]))
+    assert torch.equal(one[:, :3], base[:, :3])
+
+
+@cuda
+def test_prompt_attention_keeps_sequences_apart():
+    """NaN and infinities in one sequence leave the others' bits as they are, and large
+    scores neither overflow nor lose rows."""
+    lens, Hq, N, D = [70, 100, 150], 4, 2, 128
+    cu = _cu(lens)
+    q, k, v = randn(320, Hq, D, seed=811), randn(320, N, D, seed=812), randn(320, N, D, seed=813)
+    base = rkv.prompt_attention(q, k, v, i32(cu))
+    for t in (q, k, v):
+        bad = t.clone()
+        bad[70:170:7] = math.nan
+        bad[75:170:9] = math.inf
+        args = [bad if x is t else x for x in (q, k, v)]
+        out = rkv.prompt_attention(*args, i32(cu))
+        assert torch.equal(out[:70], base[:70]) and torch.equal(out[170:], base[170:])
+    k2 = k.clone()
+    k2[40:] = math.nan                                       # keys that no earlier row sees
+    assert torch.equal(rkv.prompt_attention(q, k2, v, i32(cu))[:40], base[:40])
+    big = rkv.prompt_attention(q * 64, k * 16, v, i32(cu))
+    ref, _, a, s = OP.prompt_attention(np64(q * 64), np64(k * 16), np64(v), cu, cu, 1 / math.sqrt(D))
+    close(big, ref, a, s, D, 2.0 ** -8)
+
+
+@cuda
+def test_prompt_attention_cuts_bad_offsets():
+    T, Hq, N, D = 40, 2, 1, 64
+    q, k, v = randn(T, Hq, D, seed=821), randn(T, N, D, seed=822), randn(T, N, D, seed=823)
+    for cu in ([0, 30, 10 ** 6], [-5, 20, 40], [0, 30, 20]):
+        flags, out = i32([0]), torch.zeros((T, Hq, D), dtype=torch.bfloat16, device="cuda")
+        rkv.prompt_attention(q, k, v, i32(cu), out=out, flags=flags)
+        assert flags.item() == rkv.FLAG_BAD_INDEX
+    assert torch.equal(out[:30], rkv.prompt_attention(q, k, v, i32([0, 30]))[:30])
+
+
+# --------------------------------------------------------------------- the run together
+@cuda
+def test_serving_loop_with_graph_replay():
+    """Prompts planned, attended and stored, decode steps captured once and replayed, a
+    request released and its slot reused: every step against the definition over all rows
+    that the requests have had."""
+    B, Hq, N, D, P = 3, 8, 2, 128, 16
+    table = rkv.PageTable(B, 12, 24, P)
+    cache = rkv.PagedCache(N, D, 24, P)
+    for t in (cache.k8, cache.v8):
+        t.fill_(0x7F)
+    hist = [[] for _ in range(B)]                            # (k, v) rows of each sequence
+    step_new = [40, 0, 33]
+
+    def check(o, q):
+        kv = [np.concatenate(h) if h else np.zeros((0, 2, N, D)) for h in hist]
+        ks = np64(cache.k_scale)
+        for b in range(B):
+            n = len(kv[b])
+            assert n == table.seq_len[b].item()
+            if n == 0:
+                assert not o[b].any()
+                continue
+            ids = table.block_table[b, :-(-n // P)].cpu().numpy()
+            val = [_f8(c)[ids] * np64(s)[ids][:, :, None, None] for c, s in
+                   ((cache.k8, cache.k_scale), (cache.v8, cache.v_scale))]
+            rows = [x.transpose(0, 2, 1, 3).reshape(-1, N, D)[:n] for x in val]
+            for i in range(2):                               # stored rows: two roundings at most
+                s = (ks if i == 0 else np64(cache.v_scale))[ids].repeat(P, axis=0)[:n, :, None]
+                assert np.all(np.abs(rows[i] - kv[b][:, i]) <=
+                              2 * np.maximum(np.abs(kv[b][:, i]) * 1.07 * 2.0 ** -4, s * 2.0 ** -10))
+            vals = [x for x in val]
+            ref, _, a, big = OP.page_attention(np64(q[b:b + 1]), vals[0], vals[1], [list(range(len(ids)))], [n], P,
+                                               1 / math.sqrt(D))
+            close(o[b:b + 1], ref, a, big, D, 2.0 ** -11)
+
+    def remember(k, v, cu):
+        for b in range(B):
+            a, c = cu[b], cu[b + 1]
+            if c > a:
+                hist[b].append(np.stack([np64(k[a:c]), np64(v[a:c])], axis=1))
+
+    # prompts of sequences 0 and 2
+    q, k, v = randn(80, Hq, D, seed=901), randn(80, N, D, seed=902), randn(80, N, D, seed=903)
+    plan = table.plan(i32(step_new), 80)
+    o = rkv.prompt_attention(q, k, v, plan.cu_rows, flags=table.flags)
+    cache.append(k, v, table, plan)
+    cu = plan.cu_rows.tolist()
+    assert cu == [0, 40, 40, 73]
+    ref, _, a, big = OP.prompt_attention(np64(q[:73]), np64(k[:73]), np64(v[:73]), cu, cu, 1 / math.sqrt(D))
+    close(o[:73], ref, a, big, D, 2.0 ** -8)
+    remember(k, v, cu)
+    qd = randn(B, Hq, D, seed=904)
+    check(cache.attend(qd, table), qd)
+
+    # decode: captured once, replayed with new rows and lengths
+    new, kd, vd = i32([1, 1, 1]), randn(B, N, D, seed=905), randn(B, N, D, seed=906)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        p = table.plan(new, B)
+        cache.append(kd, vd, table, p)
+        od = cache.attend(qd, table)
+    for step in range(20):
+        kd.copy_(randn(B, N, D, seed=1000 + step) * (1 + step % 3))
+        vd.copy_(randn(B, N, D, seed=1100 + step))
+        qd.copy_(randn(B, Hq, D, seed=1200 + step))
+        new.copy_(i32([1, step % 2, 1]))
+        graph.replay()
+        remember(kd, vd, p.cu_rows.tolist())
+        if step % 6 == 5:
+            check(od, qd)
+
+    # the first request ends; its slot takes another
+    before = table.n_free.item()
+    pages = -(-len(np.concatenate(hist[0])) // P)
+    table.release(i32([1, 0, 0]))
+    hist[0] = []
+    assert table.n_free.item() == before + pages
+    q, k, v = randn(50, Hq, D, seed=911), randn(50, N, D, seed=912), randn(50, N, D, seed=913)
+    plan = table.plan(i32([50, 0, 0]), 64)
+    cache.append(k, v, table, plan)
+    remember(k, v, plan.cu_rows.tolist())
+    check(cache.attend(qd, table), qd)
+    assert table.flags.item() == 0
+
+
+@cuda
+def test_streams_and_calls_at_once():
+    """Calls on two streams at once and a side stream's call: the results of calls alone."""
+    lens = [3000, 17, 900]
+    cache, table, _, _ = _paged(lens, 4, 64, 128, 1300)
+    qs = [randn(3, 16, 128, seed=1301 + i) for i in range(6)]
+    x = [randn(700, 8, 128, seed=1310 + i) for i in range(6)]
+    cu, ln = i32([0, 300, 700]), i32(lens)
+    alone = [(rkv.page_attention(q, *cache, table, ln), rkv.prompt_attention(t, t[:, :2], t[:, 2:4], cu))
+             for q, t in zip(qs, x)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for i, (q, t) in enumerate(zip(qs, x)):
+        s = streams[i % 2]
+        got.append((rkv.page_attention(q, *cache, table, ln, stream=s),
+                    rkv.prompt_attention(t, t[:, :2], t[:, 2:4], cu, stream=s)))
+    torch.cuda.synchronize()
+    for (a, b), (c, d) in zip(alone, got):
+        assert torch.equal(a, c) and torch.equal(b, d)
