@@ -1,14 +1,64 @@
-// k_page_attention.cu - decode attention over 8-bit pages: o = softmax(scale q K^T) V.
+// k_page_attention.cu - decode attention over 8-bit pages: o = softmax(scale q K^T) V for one
+// query row a sequence, K and V as E4M3 codes with a power-of-two scale per page and head.
+//
+// The read is bound by HBM: every stored byte is needed once, and the G query heads that
+// share a key/value head are too few for the work to be more than a few operations a byte.
+// So the bytes go from HBM to shared memory by TMA and from there straight into the tensor
+// core: no code is ever decoded by a thread.
+//
+//   Tile = 128 positions of one (sequence, key/value head); its pages are 1 to 8 boxes of
+//   [P rows x D bytes], stacked into a K tile and a V tile (rows swizzled by TMA).
+//   Scores:   S[token, n]  = K_tile Q^T       M = 128 tokens, N = 16 or 32, K = D
+//   Values:   O[d, n]     += V_tile^T P       M = D (128 lanes), N = 32 or 48, K = 128 tokens
+//   both tcgen05.mma kind::f8f6f4 with fp32 accumulation in TMEM; V enters as an MN-major A.
+//   The operands that are not stored in 8 bits are split into E4M3 parts, one column each:
+//   a bf16 q (scaled to its row's largest) is exactly hi + lo / 16 where it is within 2^-14
+//   of that largest, and within 2^-21 of it everywhere; a weight is hi + mid / 16 + lo / 256,
+//   12 significant bits for weights down to 2^-6 and an absolute 2^-18 below.  The products
+//   are exact and the parts are joined in fp32.
+//   Softmax: thread t owns token t (TMEM lane t).  Scores s are kept in base 2, and a page's
+//   value scale 2^e is folded into the weights: the second product takes 2^(s + e - m), the
+//   sum 2^(s - m).  The reference m of a head is the maximum of s + e over some earlier
+//   tiles, so the parts hold the terms that weigh most, whatever the pages' scales.  It is
+//   raised (sums and accumulators rescaled) only when an s + e exceeds it by 8, which one
+//   vote a tile finds: the usual tile has no reduction across tokens.
+//
+// Work split: all tiles of the call in the order (sequence, head, tile) are cut into equal
+// contiguous shares, one a CTA (one CTA an SM), whatever the lengths.  A (sequence, head)
+// that lies inside one share is written to `out` directly; others leave fp32 partials (m, l,
+// o), at most two a CTA, which the second kernel joins in tile order: no atomics, the same
+// bits on every run.
+//
+// Warps: 0 TMA producer, 1 MMA issuer, 2 queries and segment list, 3 idle, 4-7 softmax.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
+#include <cuda_fp16.h>
+#include <cudaTypedefs.h>
+
+#include <cfloat>
 
 #include "pages.h"
+#include "tc_common.cuh"
 
 namespace rkv {
 namespace {
 
-struct PageAttnArgs {
-  const uint8_t *k, *v;
+constexpr int kTile = 128;                 // positions per tile
+constexpr int kPaThreads = 256;
+constexpr int kSoftWarp0 = 4;
+constexpr int kSlots = 4;                  // segments whose queries are held ahead
+constexpr int kMaxCtas = 256;              // shares of a call (partials in the workspace)
+constexpr int kMaxTilePages = kTile / 16;
+constexpr uint32_t kPaTmemCols = 256;
+constexpr uint32_t kSCol = 0, kSStride = 32;      // two score buffers
+constexpr uint32_t kOCol = 64, kOStride = 64;     // two accumulators
+constexpr float kRaise = 8.f;              // weights stay below 2^8
+
+// A run of tiles of one (sequence, head) inside a CTA's share.
+struct Segment {
+  int b, h, tile0, tiles, len, slot;       // slot: workspace partial, or -1 for the whole
+};
+
+struct PaArgs {
   const float *ks, *vs;
   const int32_t *table, *seq_len;
   const __nv_bfloat16* q;
@@ -16,56 +66,651 @@ struct PageAttnArgs {
   __nv_bfloat16* out;
   float* lse;
   int32_t* flags;
-  int N, Hq, shift, num_blocks, max_blocks;
-  float scale;
+  int* status;
+  float *pm, *pl, *po;                     // partials [2 kMaxCtas][G], [..][G], [..][G][D]
+  int batch, N, G, shift, num_blocks, max_blocks;
+  float scale_log2;
 };
 
-// One warp per (sequence, query head): a running maximum and sum over the positions.
 template <int D>
-__global__ void page_attention_kernel(PageAttnArgs p) {
-  const int b = blockIdx.x, hq = blockIdx.y, lane = threadIdx.x;
-  const int h = hq / (p.Hq / p.N);
-  constexpr int kE = D / 32;
-  float q[kE], o[kE], m = -INFINITY, l = 0.f;
-  for (int e = 0; e < kE; ++e) {
-    q[e] = __bfloat162float(p.q[b * p.qst.row + hq * p.qst.head + lane * kE + e]) * p.scale;
-    o[e] = 0.f;
-  }
-  int len = p.seq_len[b];
-  const int cap = p.max_blocks << p.shift;
-  if (len < 0 || len > cap) {
-    raise_flag(p.flags, RKV_FLAG_BAD_INDEX);
-    len = len < 0 ? 0 : cap;
-  }
-  for (int t = 0; t < len; ++t) {
-    const int id = p.table[(int64_t)b * p.max_blocks + (t >> p.shift)];
-    if (id < 0 || id >= p.num_blocks) {
-      raise_flag(p.flags, RKV_FLAG_BAD_INDEX);
-      continue;
+struct PaCfg {
+  static constexpr uint32_t kHalf = kTile * D;               // bytes of a K or V tile
+  static constexpr uint32_t kStage = 2 * kHalf;
+  static constexpr int kStages = D == 128 ? 6 : 12;
+  static constexpr uint32_t kQBytes = 32 * D;                // one segment's query tile
+  static constexpr uint32_t kPBytes = 48 * kTile;            // one weight tile
+  static constexpr uint32_t kMetaOff = kStages * kStage + kSlots * kQBytes + 2 * kPBytes;
+  static constexpr uint32_t kMeta = kStages * kMaxTilePages * 8;   // (k scale, v scale)
+  static constexpr uint32_t kSmem = 1024 + kMetaOff + kMeta + 1024;
+};
+
+__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+
+// The stored length of sequence b, cut to what the table can hold.
+__device__ __forceinline__ int length_of(const PaArgs& a, int b, bool& bad) {
+  const int len = a.seq_len[b];
+  const int64_t cap = (int64_t)a.max_blocks << a.shift;
+  bad = len < 0 || len > cap;
+  return len < 0 ? 0 : (int)(len > cap ? cap : len);
+}
+
+// First tile of share c of C.
+__device__ __forceinline__ int64_t share_start(int64_t total, int c, int C) {
+  return total / C * c + total % C * c / C;
+}
+
+// tcgen05.mma kind::f8f6f4, E4M3 operands in shared memory, fp32 accumulation.
+__device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "setp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+      "}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// Instruction descriptor: fp32 D, E4M3 A and B; kTransA: A is MN-major.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, bool trans_a) {
+  return (1u << 4) | (trans_a ? 1u << 15 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Descriptor of a tile with D-byte rows (128- or 64-byte swizzle, groups of 8 rows).
+template <int D>
+__device__ __forceinline__ uint64_t sdesc_rows(uint32_t saddr, uint32_t lbo) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)((8 * D) >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)(D == 128 ? 2 : 4) << 61;
+}
+
+// Byte offset of 16-byte chunk c of row r in such a tile.
+template <int D>
+__device__ __forceinline__ uint32_t chunk_off(int r, int c) {
+  return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// Lane 0 waits; the whole warp is ordered after it.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
+  const bool ok = warp_wait(bar, parity, abort, status);
+  __syncwarp();
+  return ok;
+}
+
+__device__ __forceinline__ bool vote_or(bool pred) { return !bar_red_and(1, 128, !pred); }
+
+// kH: query heads computed (G rounded up to 2, 4, 8 or 16).
+template <int D, int kH>
+__global__ void __launch_bounds__(kPaThreads, 1)
+    page_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                          PaArgs a) {
+  using C = PaCfg<D>;
+  constexpr int kST = C::kStages;
+  constexpr int kGP = kH <= 8 ? 8 : 16;              // rows of one part
+  constexpr int kNQ = 2 * kGP;                       // score columns: hi, lo
+  constexpr int kNP = kGP == 8 ? 32 : 48;            // weight columns: hi, mid, lo (+ padding)
+  extern __shared__ uint8_t raw[];
+  uint8_t* sm = align1024(raw);
+  uint8_t* s_q = sm + kST * C::kStage;
+  uint8_t* s_p = s_q + kSlots * C::kQBytes;
+  float2* s_meta = reinterpret_cast<float2*>(sm + C::kMetaOff);
+  __shared__ __align__(8) uint64_t full[kST], empty[kST], s_full[2], s_empty[2], p_full[2], p_empty[2],
+      o_full[2], o_empty[2], q_full[kSlots], q_empty[kSlots], drain;
+  __shared__ Segment seg[kSlots];
+  __shared__ float s_qf[kSlots][16];
+  __shared__ float s_red[4][16];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort, s_b0;
+  __shared__ int64_t s_pref;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort = &s_abort;
+
+  if (tid == 0) {
+    tma_prefetch(&tm_k);
+    tma_prefetch(&tm_v);
+    for (int i = 0; i < kST; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1), mbar_init(&s_empty[i], 4);
+      mbar_init(&p_full[i], 128), mbar_init(&p_empty[i], 1);
+      mbar_init(&o_full[i], 1), mbar_init(&o_empty[i], 4);
     }
-    const int64_t head = (int64_t)id * p.N + h;
-    const int64_t row = ((head << p.shift) + (t & ((1 << p.shift) - 1))) * D + lane * kE;
-    float s = 0.f;
-    for (int e = 0; e < kE; ++e) {
-      __nv_fp8_e4m3 c;
-      c.__x = p.k[row + e];
-      s += q[e] * (float)c;
-    }
-    for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-    s *= p.ks[head];
-    const float mn = fmaxf(m, s);
-    const float f = m == -INFINITY ? 0.f : expf(m - mn), w = expf(s - mn);
-    l = l * f + w;
-    for (int e = 0; e < kE; ++e) {
-      __nv_fp8_e4m3 c;
-      c.__x = p.v[row + e];
-      o[e] = o[e] * f + w * (float)c * p.vs[head];
-    }
-    m = mn;
+    for (int i = 0; i < kSlots; ++i) mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 6);
+    mbar_init(&drain, 1);
+    s_abort = 0;
+    s_b0 = a.batch;
+    fence_barrier_init();
   }
-  for (int e = 0; e < kE; ++e)
-    p.out[((int64_t)b * p.Hq + hq) * D + lane * kE + e] = __float2bfloat16(l != 0.f ? o[e] / l : 0.f);
-  if (p.lse && lane == 0) p.lse[(int64_t)b * p.Hq + hq] = l != 0.f ? m + logf(l) : -INFINITY;
+  if (warp == 1) {
+    tmem_alloc(&s_tmem, kPaTmemCols);
+    tmem_relinquish();
+  }
+
+  // the call's tiles, and the sequence in which this CTA's share begins
+  int64_t total = 0;
+  bool any_bad = false;
+  for (int b0 = 0; b0 < a.batch; b0 += kPaThreads) {
+    bool bad = false;
+    const int b = b0 + tid;
+    int64_t n = b < a.batch ? tiles_of(length_of(a, b, bad)) : 0, t;
+    any_bad |= bad;
+    int x = 0, tx;
+    block_scan<kPaThreads>(n, x, t, tx);
+    total += t;
+  }
+  if (any_bad && blockIdx.x == 0) raise_flag(a.flags, RKV_FLAG_BAD_INDEX);
+  total *= a.N;
+  const int n_cta = (int)min((int64_t)gridDim.x, total), cta = blockIdx.x;
+  const int64_t f0 = cta < n_cta ? share_start(total, cta, n_cta) : 0;
+  const int64_t f1 = cta < n_cta ? share_start(total, cta + 1, n_cta) : 0;
+  int64_t pref = 0;
+  for (int b0 = 0; b0 < a.batch && pref * a.N <= f0; b0 += kPaThreads) {
+    bool bad;
+    const int b = b0 + tid;
+    const int64_t mine = b < a.batch ? tiles_of(length_of(a, b, bad)) : 0;
+    int64_t n = mine, t;
+    int x = 0, tx;
+    block_scan<kPaThreads>(n, x, t, tx);
+    if (mine > 0 && (pref + n - mine) * a.N <= f0 && f0 < (pref + n) * a.N) s_b0 = b, s_pref = pref + n - mine;
+    pref += t;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_launch_dependents();
+  const uint32_t tmem = s_tmem;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA producer
+    const int P = 1 << a.shift, ppt = kTile >> a.shift;      // pages per tile
+    Ring ring;
+    int64_t issued = 0;
+    bool ok = true;
+    for (int s = 0, ph = 0; ok; s == kSlots - 1 ? (s = 0, ph ^= 1) : ++s) {
+      if (!(ok = wait_warp(&q_full[s], ph, abort, a.status))) break;
+      const Segment g = seg[s];
+      if (g.b < 0) break;
+      const int pages = (g.len + P - 1) >> a.shift;          // of the whole sequence
+      const int end = min((g.tile0 + g.tiles) * ppt, pages);
+      const int32_t* row = a.table + (int64_t)g.b * a.max_blocks;
+      // lane i holds page p0 + i: 32 pages, a whole number of tiles
+      int p0 = g.tile0 * ppt;
+      int id = p0 + lane < end ? __ldg(row + p0 + lane) : -1;
+      for (int t = 0; t < g.tiles && ok; p0 += 32) {
+        const bool here = p0 + lane < end, good = here && id >= 0 && id < a.num_blocks;
+        if (here && !good) raise_flag(a.flags, RKV_FLAG_BAD_INDEX);
+        const int64_t head = (int64_t)id * a.N + g.h;
+        // a page that is not there has a negative scale
+        float2 sc = make_float2(0.f, -1.f);
+        if (good) sc = make_float2(__ldg(a.ks + head), __ldg(a.vs + head));
+        const int next = p0 + 32 + lane;
+        const int id_next = next < end ? __ldg(row + next) : -1;
+        for (int i = 0; i < 32 && t < g.tiles; i += ppt, ++t) {
+          if (!(ok = wait_warp(&empty[ring.stage], ring.phase ^ 1u, abort, a.status))) break;
+          uint8_t* st = sm + ring.stage * C::kStage;
+          const bool mine = lane >= i && lane < i + ppt;
+          if (mine) s_meta[ring.stage * kMaxTilePages + lane - i] = sc;
+          const uint32_t n = __popc(__ballot_sync(0xffffffffu, mine && good));
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(&full[ring.stage], n * 2u * (uint32_t)(P * D));
+          __syncwarp();
+          if (mine && good) {
+            const uint32_t off = (uint32_t)(lane - i) * (uint32_t)(P * D);
+            tma_load_2d(st + off, &tm_v, &full[ring.stage], 0, (int32_t)(head << a.shift));
+            tma_load_2d(st + C::kHalf + off, &tm_k, &full[ring.stage], 0, (int32_t)(head << a.shift));
+          }
+          ring.next(kST);
+          ++issued;
+        }
+        id = id_next;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_empty[s]);
+    }
+    if (*abort && lane == 0)                                 // no copy may outlive the CTA
+      for (int i = 0; i < kST && i < issued; ++i) {
+        ring.stage = ring.stage == 0 ? (ring.phase ^= 1u, kST - 1) : ring.stage - 1;
+        drain_wait(&full[ring.stage], ring.phase);
+      }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer
+    constexpr uint32_t id_s = idesc_f8(128, kNQ, false), id_o = idesc_f8(128, kNP, true);
+    Ring ring, prev;                                         // this tile's stage, the last one's
+    int64_t k = 0;
+    uint32_t n_seg = 0;
+    bool ok = true;
+    for (int s = 0, ph = 0; ok; s == kSlots - 1 ? (s = 0, ph ^= 1) : ++s, ++n_seg) {
+      if (!(ok = wait_warp(&q_full[s], ph, abort, a.status))) break;
+      if (seg[s].b < 0) break;
+      const int tiles = seg[s].tiles;
+      const uint32_t o_tm = tmem + kOCol + (n_seg & 1u) * kOStride;
+      // the accumulator of the segment before the last has been read
+      if (!(ok = wait_warp(&o_empty[n_seg & 1u], ((n_seg >> 1) & 1u) ^ 1u, abort, a.status))) break;
+      for (int t = 0; t <= tiles; ++t) {
+        if (t < tiles) {
+          const uint32_t sb = (uint32_t)k & 1u, sp = (uint32_t)(k >> 1) & 1u;
+          if (!(ok = wait_warp(&full[ring.stage], ring.phase, abort, a.status))) break;
+          if (!(ok = wait_warp(&s_empty[sb], sp ^ 1u, abort, a.status))) break;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t kt = smem_u32(sm + ring.stage * C::kStage + C::kHalf);
+            const uint32_t qt = smem_u32(s_q + s * C::kQBytes);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+              umma_f8(tmem + kSCol + sb * kSStride, sdesc_rows<D>(kt + i * 32, 16), sdesc_rows<D>(qt + i * 32, 16),
+                      id_s, i > 0);
+            umma_commit(&s_full[sb]);
+            if (t == tiles - 1) umma_commit(&q_empty[s]);
+          }
+          __syncwarp();
+        }
+        if (t > 0) {                                         // the tile before: O += V^T P
+          const int64_t kp = k - 1;
+          const uint32_t pb = (uint32_t)kp & 1u, pp = (uint32_t)(kp >> 1) & 1u;
+          if (!(ok = wait_warp(&p_full[pb], pp, abort, a.status))) break;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t vt = smem_u32(sm + prev.stage * C::kStage);
+            const uint32_t pt = smem_u32(s_p + pb * C::kPBytes);
+            // M = 128 lanes; for D = 64 the upper 64 read the K tile behind V and are unused
+#pragma unroll
+            for (int i = 0; i < kTile / 32; ++i)
+              umma_f8(o_tm, sdesc_rows<D>(vt + i * 32 * D, C::kHalf), sdesc_rows<128>(pt + i * 32, 16), id_o,
+                      t > 1 || i > 0);
+            umma_commit(&empty[prev.stage]);
+            umma_commit(&p_empty[pb]);
+            if (t == tiles) umma_commit(&o_full[n_seg & 1u]);
+          }
+          __syncwarp();
+        }
+        if (t < tiles) {
+          prev = ring;
+          ring.next(kST);
+          ++k;
+        }
+      }
+    }
+    if (*abort && lane == 0) {
+      umma_commit(&drain);
+      drain_wait(&drain, 0);
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------- segments and their query tiles
+    int64_t f = f0, pre = f0 < f1 ? s_pref : 0;
+    int b = s_b0, chunk = -1, len_l = 0;                     // lane i: length of sequence chunk + i
+    bool first = true, ok = true;
+    for (int s = 0, ph = 1; ok; s == kSlots - 1 ? (s = 0, ph ^= 1) : ++s) {
+      Segment g{-1, 0, 0, 0, 0, -1};
+      while (f < f1 && g.b < 0 && b < a.batch) {
+        if (chunk != (b & ~31)) {
+          chunk = b & ~31;
+          bool bad;
+          len_l = chunk + lane < a.batch ? length_of(a, chunk + lane, bad) : 0;
+        }
+        const int len = __shfl_sync(0xffffffffu, len_l, b & 31);
+        const int nb = tiles_of(len);
+        const int64_t rel = f - pre * a.N;
+        if (rel >= (int64_t)nb * a.N) {
+          pre += nb;
+          ++b;
+          continue;
+        }
+        g.b = b, g.len = len;
+        g.h = (int)(rel / nb), g.tile0 = (int)(rel % nb);
+        g.tiles = (int)min((int64_t)(nb - g.tile0), f1 - f);
+        g.slot = g.tiles == nb ? -1 : 2 * cta + (first ? 0 : 1);
+        f += g.tiles;
+        first = false;
+      }
+      if (!(ok = wait_warp(&q_empty[s], ph, abort, a.status))) break;
+      if (g.b >= 0) {
+        const __nv_bfloat16* q = a.q + g.b * a.qst.row + (int64_t)g.h * a.G * a.qst.head;
+        uint8_t* qt = s_q + s * C::kQBytes;
+        constexpr int kE = D / 32;                           // values per lane
+#pragma unroll 4
+        for (int h = 0; h < kH; ++h) {
+          float v[kE];
+          float amax = 0.f;
+#pragma unroll
+          for (int e = 0; e < kE; e += 2) {
+            uint32_t u = 0;
+            if (h < a.G) u = *reinterpret_cast<const uint32_t*>(q + h * a.qst.head + lane * kE + e);
+            v[e] = __uint_as_float(u << 16), v[e + 1] = __uint_as_float(u & 0xFFFF0000u);
+          }
+#pragma unroll
+          for (int e = 0; e < kE; ++e) {
+            if (!(fabsf(v[e]) < INFINITY)) v[e] = NAN;       // an infinity has no product either
+            amax = fmaxf(amax, fabsf(v[e]));
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          // 2^7 <= amax 2^-ex < 2^8
+          const int ex = max((int)(__float_as_uint(amax) >> 23) - 127, -100) - 7;
+          const float mul = __uint_as_float((uint32_t)(127 - ex) << 23);
+          uint32_t hi = 0, lo = 0;
+#pragma unroll
+          for (int e = 0; e < kE; e += 2) {
+            const float x = v[e] * mul, y = v[e + 1] * mul;
+            const uint32_t c = e4m3x2(x, y);
+            const float2 r = from_e4m3x2(c);
+            hi |= c << (8 * e);
+            lo |= e4m3x2((x - r.x) * 16.f, (y - r.y) * 16.f) << (8 * e);
+          }
+          const int col = lane * kE;
+          const uint32_t oh = chunk_off<D>(h, col >> 4) + (col & 15);
+          const uint32_t ol = chunk_off<D>(kGP + h, col >> 4) + (col & 15);
+          if (kE == 4) {
+            *reinterpret_cast<uint32_t*>(qt + oh) = hi;
+            *reinterpret_cast<uint32_t*>(qt + ol) = lo;
+          } else {
+            *reinterpret_cast<uint16_t*>(qt + oh) = (uint16_t)hi;
+            *reinterpret_cast<uint16_t*>(qt + ol) = (uint16_t)lo;
+          }
+          if (lane == 0) s_qf[s][h] = __uint_as_float((uint32_t)(127 + ex) << 23) * a.scale_log2;
+        }
+      }
+      if (lane == 0) seg[s] = g;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[s]);
+      if (g.b < 0) break;
+    }
+  } else if (warp >= kSoftWarp0) {
+    // ---------------------------------------------------------------------- softmax
+    const int tok = tid - kSoftWarp0 * 32, w = warp - kSoftWarp0;
+    const uint32_t tm = tmem + ((uint32_t)(w * 32) << 16);
+    Ring ring;
+    int64_t k = 0;
+    uint32_t n_seg = 0;
+    bool ok = true;
+    for (int s = 0, ph = 0; ok; s == kSlots - 1 ? (s = 0, ph ^= 1) : ++s, ++n_seg) {
+      ok = wait_warp(&q_full[s], ph, abort, a.status);
+      if (vote_or(!ok)) break;
+      const Segment g = seg[s];
+      if (g.b < 0) break;
+      float m[kH], l[kH], qf[kH];
+#pragma unroll
+      for (int h = 0; h < kH; ++h) m[h] = -FLT_MAX, l[h] = 0.f, qf[h] = s_qf[s][h];
+      const uint32_t o_tm = tm + kOCol + (n_seg & 1u) * kOStride;
+      for (int t = 0; t < g.tiles; ++t, ++k) {
+        const uint32_t sb = (uint32_t)k & 1u, sp = (uint32_t)(k >> 1) & 1u;
+        ok = ok && wait_warp(&full[ring.stage], ring.phase, abort, a.status) &&
+             wait_warp(&s_full[sb], sp, abort, a.status);
+        float x[kH];
+        const float2 sc = s_meta[ring.stage * kMaxTilePages + (tok >> a.shift)];
+        const bool valid = (g.tile0 + t) * kTile + tok < g.len && !(sc.y < 0.f);
+        if (ok) {
+          tc_fence_after();
+          uint32_t r[kNQ];
+          if (kNQ == 16) tmem_ld16(tm + kSCol + sb * kSStride, r);
+          else tmem_ld32(tm + kSCol + sb * kSStride, r);
+          tmem_ld_wait();
+          tc_fence_before();
+          if (lane == 0) mbar_arrive(&s_empty[sb]);
+#pragma unroll
+          for (int h = 0; h < kH; ++h) {
+            const float d = fmaf(__uint_as_float(r[kGP + h]), 0.0625f, __uint_as_float(r[h]));
+            x[h] = valid ? d * (sc.x * qf[h]) : -INFINITY;
+          }
+        }
+        // log2 of the value scale: the weights times it are what has to stay in range
+        const float ev = (float)((int)(__float_as_uint(sc.y) >> 23) - 127);
+        bool raise = !ok || t == 0;
+        if (ok) {
+#pragma unroll
+          for (int h = 0; h < kH; ++h) raise |= x[h] + ev > m[h] + kRaise;
+        }
+        if (vote_or(raise)) {
+          if (vote_or(!ok)) {
+            ok = false;
+            break;
+          }
+          // the reference becomes the maximum so far
+          float y[kH];
+#pragma unroll
+          for (int h = 0; h < kH; ++h) y[h] = x[h] + ev;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+#pragma unroll
+            for (int h = 0; h < kH; ++h) y[h] = fmaxf(y[h], __shfl_xor_sync(0xffffffffu, y[h], o));
+          }
+          if (lane == 0) {
+#pragma unroll
+            for (int h = 0; h < kH; ++h) s_red[w][h] = y[h];
+          }
+          bar_sync(1, 128);
+          float f[kH];
+#pragma unroll
+          for (int h = 0; h < kH; ++h) {
+            const float mn = fmaxf(m[h], fmaxf(fmaxf(s_red[0][h], s_red[1][h]), fmaxf(s_red[2][h], s_red[3][h])));
+            const float c = ex2_approx(m[h] - mn);
+            l[h] *= c;
+            f[h] = c;
+            m[h] = mn;
+          }
+          if (t > 0) {
+            // every product issued so far has been added
+            const int64_t kp = k - 1;
+            ok = wait_warp(&p_empty[kp & 1], (uint32_t)(kp >> 1) & 1u, abort, a.status);
+            if (ok) {
+              tc_fence_after();
+#pragma unroll
+              for (int part = 0; part < 3; ++part) {
+                uint32_t r[kGP];
+                if (kGP == 8) tmem_ld8(o_tm + part * kGP, r);
+                else tmem_ld16(o_tm + part * kGP, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int h = 0; h < kH; ++h) r[h] = __float_as_uint(__uint_as_float(r[h]) * f[h]);
+                if (kGP == 8) tmem_st8(o_tm + part * kGP, r);
+                else tmem_st16(o_tm + part * kGP, r);
+              }
+              tmem_st_wait();
+            }
+          }
+          if (vote_or(!ok)) {                                // also: s_red has been read
+            ok = false;
+            break;
+          }
+        }
+        // the weights, their sum, and their parts for the second product
+        if (k >= 2) {
+          const int64_t kp = k - 2;
+          ok = ok && wait_warp(&p_empty[kp & 1], (uint32_t)(kp >> 1) & 1u, abort, a.status);
+        }
+        if (ok) {
+          uint8_t* pt = s_p + sb * C::kPBytes;
+          const uint32_t c16 = (uint32_t)tok >> 4, c0 = (uint32_t)tok & 15u;
+#pragma unroll
+          for (int h = 0; h < kH; h += 2) {
+            const float p0 = ex2_approx(x[h] - m[h]), p1 = ex2_approx(x[h + 1] - m[h + 1]);
+            l[h] += p0;
+            l[h + 1] += p1;
+            float u0 = valid ? p0 * sc.y : 0.f, u1 = valid ? p1 * sc.y : 0.f;
+#pragma unroll
+            for (int part = 0; part < 3; ++part) {
+              const uint32_t c = e4m3x2(u0, u1);
+              const int n0 = part * kGP + h, n1 = n0 + 1;
+              pt[n0 * 128 + ((c16 ^ (n0 & 7)) << 4) + c0] = (uint8_t)c;
+              pt[n1 * 128 + ((c16 ^ (n1 & 7)) << 4) + c0] = (uint8_t)(c >> 8);
+              if (part < 2) {
+                const float2 e = from_e4m3x2(c);
+                u0 = (u0 - e.x) * 16.f;
+                u1 = (u1 - e.y) * 16.f;
+              }
+            }
+          }
+          if (!valid) {                                      // 0 x what the row holds must be 0
+            uint8_t* vt = sm + ring.stage * C::kStage + tok * D;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) *reinterpret_cast<uint4*>(vt + i * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          tc_fence_before();
+          mbar_arrive(&p_full[sb]);
+        }
+        ring.next(kST);
+      }
+      // the segment's sums and accumulators
+      if (ok) ok = wait_warp(&o_full[n_seg & 1u], (n_seg >> 1) & 1u, abort, a.status);
+      if (vote_or(!ok)) break;
+      tc_fence_after();
+      float o[kH];
+#pragma unroll
+      for (int h = 0; h < kH; ++h) o[h] = 0.f;
+#pragma unroll
+      for (int part = 2; part >= 0; --part) {
+        uint32_t r[kGP];
+        if (kGP == 8) tmem_ld8(o_tm + part * kGP, r);
+        else tmem_ld16(o_tm + part * kGP, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int h = 0; h < kH; ++h) o[h] = fmaf(o[h], 0.0625f, __uint_as_float(r[h]));
+      }
+      tc_fence_before();
+#pragma unroll
+      for (int h = 0; h < kH; ++h) {
+#pragma unroll
+        for (int i = 16; i > 0; i >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], i);
+      }
+      if (lane == 0) {
+        mbar_arrive(&o_empty[n_seg & 1u]);
+        mbar_arrive(&q_empty[s]);
+#pragma unroll
+        for (int h = 0; h < kH; ++h) s_red[w][h] = l[h];
+      }
+      bar_sync(1, 128);
+#pragma unroll
+      for (int h = 0; h < kH; ++h) l[h] = s_red[0][h] + s_red[1][h] + s_red[2][h] + s_red[3][h];
+      bar_sync(1, 128);                                      // s_red may be written again
+      if (g.slot < 0) {
+        const int64_t row = ((int64_t)g.b * a.N + g.h) * a.G;
+#pragma unroll
+        for (int h = 0; h < kH; ++h) {
+          if (h < a.G) {
+            if (tok < D) a.out[(row + h) * D + tok] = __float2bfloat16(l[h] != 0.f ? o[h] / l[h] : 0.f);
+            if (a.lse && tok == 0)
+              a.lse[row + h] = l[h] != 0.f ? (m[h] + log2f(l[h])) * 0.6931471805599453f : -INFINITY;
+          }
+        }
+      } else {
+        const int64_t row = (int64_t)g.slot * a.G;
+#pragma unroll
+        for (int h = 0; h < kH; ++h) {
+          if (h < a.G) {
+            if (tok < D) a.po[(row + h) * D + tok] = o[h];
+            if (tok == 0) a.pm[row + h] = m[h], a.pl[row + h] = l[h];
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, kPaTmemCols);
+}
+
+// Joins the partials of each (sequence, head) that several shares hold, in their order, and
+// zeroes the rows of empty sequences.  Grid (batch, N), D threads.
+template <int D>
+__global__ void __launch_bounds__(D) page_attention_join_kernel(PaArgs a, int grid) {
+  const int b = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
+  int64_t before = 0, all = 0;
+  for (int i = tid; i < a.batch; i += D) {
+    bool bad;
+    const int n = tiles_of(length_of(a, i, bad));
+    all += n;
+    if (i < b) before += n;
+  }
+  __shared__ int64_t s_all[D / 32], s_before[D / 32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  if ((tid & 31) == 0) s_all[tid >> 5] = all, s_before[tid >> 5] = before;
+  __syncthreads();
+  all = before = 0;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) all += s_all[i], before += s_before[i];
+  bool bad;
+  const int nb = tiles_of(length_of(a, b, bad));
+  const int64_t row = ((int64_t)b * a.N + h) * a.G;
+  pdl_wait_previous_grid();
+  if (nb == 0) {
+    for (int g = 0; g < a.G; ++g) {
+      a.out[(row + g) * D + tid] = __float2bfloat16(0.f);
+      if (a.lse && tid == 0) a.lse[row + g] = -INFINITY;
+    }
+    return;
+  }
+  const int64_t total = all * a.N, f0 = before * a.N + (int64_t)h * nb, f1 = f0 + nb;
+  const int C = (int)min((int64_t)grid, total);
+  int c0 = (int)(f0 * C / total), c1;
+  while (c0 > 0 && share_start(total, c0, C) > f0) --c0;
+  while (c0 + 1 < C && share_start(total, c0 + 1, C) <= f0) ++c0;
+  c1 = c0;
+  while (c1 + 1 < C && share_start(total, c1 + 1, C) < f1) ++c1;
+  if (c0 == c1) return;
+  const int first = 2 * c0 + (share_start(total, c0, C) == f0 ? 0 : 1);
+  for (int g = 0; g < a.G; ++g) {
+    float m = -FLT_MAX, l = 0.f, o = 0.f;
+    for (int c = c0; c <= c1; ++c) {
+      const int64_t i = (int64_t)(c == c0 ? first : 2 * c) * a.G + g;
+      const float pm = __ldcg(a.pm + i), pl = __ldcg(a.pl + i), po = __ldcg(a.po + i * D + tid);
+      const float mn = fmaxf(m, pm), fa = ex2_approx(m - mn), fb = ex2_approx(pm - mn);
+      l = l * fa + pl * fb;
+      o = o * fa + po * fb;
+      m = mn;
+    }
+    a.out[(row + g) * D + tid] = __float2bfloat16(l != 0.f ? o / l : 0.f);
+    if (a.lse && tid == 0) a.lse[row + g] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  }
+}
+
+rkv_status check_heads(const rkv_pages* pages, int n_q_heads) {
+  if (n_q_heads < 1 || n_q_heads % pages->n_kv_heads || n_q_heads / pages->n_kv_heads > kPageMaxGroup)
+    return fail_with(RKV_EINVAL, "n_q_heads must be a multiple of n_kv_heads, at most %d times it", kPageMaxGroup);
+  return RKV_OK;
+}
+
+template <int D, int kH>
+cudaError_t launch_main(const CUtensorMap& mk, const CUtensorMap& mv, const PaArgs& a, int grid, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(page_attention_kernel<D, kH>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, PaCfg<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  page_attention_kernel<D, kH><<<grid, kPaThreads, PaCfg<D>::kSmem, s>>>(mk, mv, a);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_all(const CUtensorMap& mk, const CUtensorMap& mv, const PaArgs& a, int grid, cudaStream_t s) {
+  cudaError_t e = a.G <= 2   ? launch_main<D, 2>(mk, mv, a, grid, s)
+                  : a.G <= 4 ? launch_main<D, 4>(mk, mv, a, grid, s)
+                  : a.G <= 8 ? launch_main<D, 8>(mk, mv, a, grid, s)
+                             : launch_main<D, 16>(mk, mv, a, grid, s);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(a.batch, a.N);
+  lc.blockDim = dim3(D);
+  lc.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  e = cudaLaunchKernelEx(&lc, page_attention_join_kernel<D>, a, grid);
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 }  // namespace
@@ -73,19 +718,14 @@ __global__ void page_attention_kernel(PageAttnArgs p) {
 
 using namespace rkv;
 
-static rkv_status check_heads(const rkv_pages* pages, int n_q_heads) {
-  if (n_q_heads < 1 || n_q_heads % pages->n_kv_heads || n_q_heads / pages->n_kv_heads > kPageMaxGroup)
-    return fail_with(RKV_EINVAL, "n_q_heads must be a multiple of n_kv_heads, at most %d times it", kPageMaxGroup);
-  return RKV_OK;
-}
-
 extern "C" rkv_status rkv_page_attention_workspace(const rkv_pages* pages, const rkv_page_table* table,
                                                    int32_t n_q_heads, size_t* bytes) {
   if (!bytes) return fail_with(RKV_EINVAL, "bytes is NULL");
   if (rkv_status st = check_pages(pages)) return st;
   if (rkv_status st = check_table(table, pages->block_tokens)) return st;
   if (rkv_status st = check_heads(pages, n_q_heads)) return st;
-  *bytes = 16;
+  const size_t G = n_q_heads / pages->n_kv_heads;
+  *bytes = 16 + sizeof(float) * 2 * kMaxCtas * G * (2 + (size_t)pages->head_dim);
   return RKV_OK;
 }
 
@@ -101,23 +741,36 @@ extern "C" rkv_status rkv_page_attention(const rkv_pages* pages, const rkv_page_
   if (!is_aligned(q, 16) || !is_aligned(out, 16) || !is_aligned(workspace, 16) || q_strides[0] < 0 ||
       q_strides[1] < 0 || q_strides[0] % 8 || q_strides[1] % 8)
     return fail_with(RKV_EALIGN, "q, out, workspace and q's strides must be whole 16 bytes");
-  PageAttnArgs a;
-  a.k = static_cast<const uint8_t*>(pages->k), a.v = static_cast<const uint8_t*>(pages->v);
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+    return fail_with(RKV_ECUDA, "no usable current device");
+  const int D = pages->head_dim;
+  const uint64_t rows = (uint64_t)pages->num_blocks * pages->n_kv_heads * pages->block_tokens;
+  CUtensorMap mk, mv;
+  if (!encode_map_bytes(&mk, pages->k, D, rows, pages->block_tokens) ||
+      !encode_map_bytes(&mv, pages->v, D, rows, pages->block_tokens))
+    return fail_with(RKV_ECUDA, "cuTensorMapEncodeTiled is unavailable or rejected the pages");
+  PaArgs a;
   a.ks = pages->k_scale, a.vs = pages->v_scale;
   a.table = table->block_table, a.seq_len = table->seq_len;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.qst = {q_strides[0], q_strides[1]};
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse, a.flags = flags;
-  a.N = pages->n_kv_heads, a.Hq = n_q_heads;
+  a.batch = table->batch;
+  a.N = pages->n_kv_heads, a.G = n_q_heads / a.N;
+  // a wait that gives up reports to the caller's flags, or to a word of the workspace
+  a.status = flags ? flags : static_cast<int*>(workspace);
+  a.pm = static_cast<float*>(workspace) + 4;
+  a.pl = a.pm + 2 * kMaxCtas * a.G;
+  a.po = a.pl + 2 * kMaxCtas * a.G;
   a.shift = 4;
   while ((1 << a.shift) < pages->block_tokens) ++a.shift;
   a.num_blocks = pages->num_blocks, a.max_blocks = table->max_blocks;
-  a.scale = (float)scale;
-  const dim3 grid(table->batch, n_q_heads);
+  a.scale_log2 = (float)(scale * 1.4426950408889634);
+  const int grid = sms < kMaxCtas ? sms : kMaxCtas;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (pages->head_dim == 128) page_attention_kernel<128><<<grid, 32, 0, s>>>(a);
-  else page_attention_kernel<64><<<grid, 32, 0, s>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = D == 128 ? launch_all<128>(mk, mv, a, grid, s) : launch_all<64>(mk, mv, a, grid, s);
   return e == cudaSuccess ? RKV_OK : fail_with(RKV_ECUDA, "page attention launch failed: %s", cudaGetErrorString(e));
 }

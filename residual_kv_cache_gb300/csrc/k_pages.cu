@@ -29,32 +29,6 @@ namespace {
 constexpr int kPlanThreads = 512;
 constexpr int kMaxPlanCtas = 8;      // portable cluster size
 
-// Inclusive prefix sums of (a, b) over the block, and the block's totals.
-template <int kThreads>
-__device__ __forceinline__ void block_scan(int64_t& a, int& b, int64_t& total_a, int& total_b) {
-  __shared__ int64_t wa[kThreads / 32];
-  __shared__ int wb[kThreads / 32];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t xa = __shfl_up_sync(0xffffffffu, a, o);
-    const int xb = __shfl_up_sync(0xffffffffu, b, o);
-    if (lane >= o) a += xa, b += xb;
-  }
-  __syncthreads();                    // an earlier scan's totals have been read
-  if (lane == 31) wa[w] = a, wb[w] = b;
-  __syncthreads();
-  total_a = 0, total_b = 0;
-  int64_t pa = 0;
-  int pb = 0;
-#pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) {
-    if (i == w) pa = total_a, pb = total_b;
-    total_a += wa[i], total_b += wb[i];
-  }
-  a += pa, b += pb;
-}
-
 // Largest index i in [0, n) with v[i] <= x (v non-decreasing, v[0] <= x).
 __device__ __forceinline__ int last_not_above(const int* v, int n, int x) {
   int lo = 0, hi = n;

@@ -1,6 +1,7 @@
 // pages.h - what the full-attention layers' kernels share: limits, argument checks and the
 // launchers behind the rkv_page_* and rkv_prompt_* entry points.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -29,8 +30,42 @@ struct Strides {
 rkv_status check_pages(const rkv_pages* pg);
 rkv_status check_table(const rkv_page_table* t, int block_tokens);
 
+// 2-D tensor map of byte rows of `inner` (64 or 128) bytes, swizzled by their width, box =
+// {inner, box_rows}; false where the driver's encoder is missing or refuses (rkv_api.cu).
+bool encode_map_bytes(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows);
+// 3-D tensor map of a strided bf16 [rows, heads, D] tensor, 128-byte swizzle, box =
+// {64 elements, 1 head, box_rows}.
+bool encode_map_heads(CUtensorMap* m, const void* base, uint64_t D, uint64_t heads, uint64_t rows,
+                      const int64_t strides[2], uint32_t box_rows);
+
 __device__ __forceinline__ void raise_flag(int32_t* flags, int32_t bit) {
   if (flags) atomicOr(flags, bit);
+}
+
+// Inclusive prefix sums of (a, b) over the block, and the block's totals.
+template <int kThreads>
+__device__ __forceinline__ void block_scan(int64_t& a, int& b, int64_t& total_a, int& total_b) {
+  __shared__ int64_t wa[kThreads / 32];
+  __shared__ int wb[kThreads / 32];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t xa = __shfl_up_sync(0xffffffffu, a, o);
+    const int xb = __shfl_up_sync(0xffffffffu, b, o);
+    if (lane >= o) a += xa, b += xb;
+  }
+  __syncthreads();                    // an earlier scan's totals have been read
+  if (lane == 31) wa[w] = a, wb[w] = b;
+  __syncthreads();
+  total_a = 0, total_b = 0;
+  int64_t pa = 0;
+  int pb = 0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i == w) pa = total_a, pb = total_b;
+    total_a += wa[i], total_b += wb[i];
+  }
+  a += pa, b += pb;
 }
 
 }  // namespace rkv

@@ -85,6 +85,37 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows,
   return r == CUDA_SUCCESS;
 }
 
+}  // namespace
+
+namespace rkv {
+bool encode_map_bytes(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows) {
+  if (!get_encoder()) return false;
+  cuuint64_t dims[2] = {inner, rows};
+  cuuint64_t strides[1] = {inner};
+  cuuint32_t box[2] = {(cuuint32_t)inner, box_rows};
+  cuuint32_t es[2] = {1u, 1u};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  inner == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_map_heads(CUtensorMap* m, const void* base, uint64_t D, uint64_t heads, uint64_t rows,
+                      const int64_t strides[2], uint32_t box_rows) {
+  if (!get_encoder()) return false;
+  cuuint64_t dims[3] = {D, heads, rows};
+  // the stride of a dimension of one is never used
+  cuuint64_t st[2] = {heads > 1 ? (cuuint64_t)strides[1] * 2 : D * 2, rows > 1 ? (cuuint64_t)strides[0] * 2 : D * 2};
+  cuuint32_t box[3] = {64u, 1u, box_rows};
+  cuuint32_t es[3] = {1u, 1u, 1u};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, st, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace rkv
+
+namespace {
+
 // Calls fn(p) for every reference position p < T, in increasing order, and returns
 // their number (ResidualKV notes §2.6): the sink tokens 0 .. sink-1, then p_0 = sink,
 // p_{m+1} = p_m + s0 + floor(alpha * (p_m - sink)), the product taken in binary64.
