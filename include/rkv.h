@@ -504,7 +504,7 @@ rkv_status rkv_page_attention_workspace(const rkv_pages* pages, const rkv_page_t
  * the last one have no effect, whatever they hold.  Within a sequence a NaN or infinity of V
  * reaches rows that see it and may reach up to 255 rows before it (weights of 0 times NaN).
  * Scores are exact bf16 products summed in fp32; the weights enter the second product as
- * bf16; sums are fp32.  batch in [1, 8192].
+ * bf16; sums are fp32.  batch in [1, 8192]; total_q and total_k at most 2^30.
  * Offsets that decrease or pass total_q / total_k are cut (RKV_FLAG_BAD_INDEX).
  * Errors (nothing launched): RKV_EINVAL, RKV_EALIGN, RKV_ECUDA.
  */

@@ -66,7 +66,6 @@ struct PaArgs {
   __nv_bfloat16* out;
   float* lse;
   int32_t* flags;
-  int* status;
   float *pm, *pl, *po;                     // partials [2 kMaxCtas][G], [..][G], [..][G][D]
   int batch, N, G, shift, num_blocks, max_blocks;
   float scale_log2;
@@ -170,10 +169,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   __shared__ float s_qf[kSlots][16];
   __shared__ float s_red[4][16];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_b0;
+  __shared__ int s_abort, s_status, s_b0;
   __shared__ int64_t s_pref;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* abort = &s_abort;
+  int* status = a.flags ? a.flags : &s_status;               // where a wait that gives up reports
 
   if (tid == 0) {
     tma_prefetch(&tm_k);
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     int64_t issued = 0;
     bool ok = true;
     for (int s = 0, ph = 0; ok; s == kSlots - 1 ? (s = 0, ph ^= 1) : ++s) {
-      if (!(ok = wait_warp(&q_full[s], ph, abort, a.status))) break;
+      if (!(ok = wait_warp(&q_full[s], ph, abort, status))) break;
       const Segment g = seg[s];
       if (g.b < 0) break;
       const int pages = (g.len + P - 1) >> a.shift;          // of the whole sequence
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         const int next = p0 + 32 + lane;
         const int id_next = next < end ? __ldg(row + next) : -1;
         for (int i = 0; i < 32 && t < g.tiles; i += ppt, ++t) {
-          if (!(ok = wait_warp(&empty[ring.stage], ring.phase ^ 1u, abort, a.status))) break;
+          if (!(ok = wait_warp(&empty[ring.stage], ring.phase ^ 1u, abort, status))) break;
           uint8_t* st = sm + ring.stage * C::kStage;
           const bool mine = lane >= i && lane < i + ppt;
           if (mine) s_meta[ring.stage * kMaxTilePages + lane - i] = sc;
@@ -289,17 +289,17 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     uint32_t n_seg = 0;
     bool ok = true;
     for (int s = 0, ph = 0; ok; s == kSlots - 1 ? (s = 0, ph ^= 1) : ++s, ++n_seg) {
-      if (!(ok = wait_warp(&q_full[s], ph, abort, a.status))) break;
+      if (!(ok = wait_warp(&q_full[s], ph, abort, status))) break;
       if (seg[s].b < 0) break;
       const int tiles = seg[s].tiles;
       const uint32_t o_tm = tmem + kOCol + (n_seg & 1u) * kOStride;
       // the accumulator of the segment before the last has been read
-      if (!(ok = wait_warp(&o_empty[n_seg & 1u], ((n_seg >> 1) & 1u) ^ 1u, abort, a.status))) break;
+      if (!(ok = wait_warp(&o_empty[n_seg & 1u], ((n_seg >> 1) & 1u) ^ 1u, abort, status))) break;
       for (int t = 0; t <= tiles; ++t) {
         if (t < tiles) {
           const uint32_t sb = (uint32_t)k & 1u, sp = (uint32_t)(k >> 1) & 1u;
-          if (!(ok = wait_warp(&full[ring.stage], ring.phase, abort, a.status))) break;
-          if (!(ok = wait_warp(&s_empty[sb], sp ^ 1u, abort, a.status))) break;
+          if (!(ok = wait_warp(&full[ring.stage], ring.phase, abort, status))) break;
+          if (!(ok = wait_warp(&s_empty[sb], sp ^ 1u, abort, status))) break;
           tc_fence_after();
           if (lane == 0) {
             const uint32_t kt = smem_u32(sm + ring.stage * C::kStage + C::kHalf);
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         if (t > 0) {                                         // the tile before: O += V^T P
           const int64_t kp = k - 1;
           const uint32_t pb = (uint32_t)kp & 1u, pp = (uint32_t)(kp >> 1) & 1u;
-          if (!(ok = wait_warp(&p_full[pb], pp, abort, a.status))) break;
+          if (!(ok = wait_warp(&p_full[pb], pp, abort, status))) break;
           tc_fence_after();
           if (lane == 0) {
             const uint32_t vt = smem_u32(sm + prev.stage * C::kStage);
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         f += g.tiles;
         first = false;
       }
-      if (!(ok = wait_warp(&q_empty[s], ph, abort, a.status))) break;
+      if (!(ok = wait_warp(&q_empty[s], ph, abort, status))) break;
       if (g.b >= 0) {
         const __nv_bfloat16* q = a.q + g.b * a.qst.row + (int64_t)g.h * a.G * a.qst.head;
         uint8_t* qt = s_q + s * C::kQBytes;
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     uint32_t n_seg = 0;
     bool ok = true;
     for (int s = 0, ph = 0; ok; s == kSlots - 1 ? (s = 0, ph ^= 1) : ++s, ++n_seg) {
-      ok = wait_warp(&q_full[s], ph, abort, a.status);
+      ok = wait_warp(&q_full[s], ph, abort, status);
       if (vote_or(!ok)) break;
       const Segment g = seg[s];
       if (g.b < 0) break;
@@ -443,8 +443,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       const uint32_t o_tm = tm + kOCol + (n_seg & 1u) * kOStride;
       for (int t = 0; t < g.tiles; ++t, ++k) {
         const uint32_t sb = (uint32_t)k & 1u, sp = (uint32_t)(k >> 1) & 1u;
-        ok = ok && wait_warp(&full[ring.stage], ring.phase, abort, a.status) &&
-             wait_warp(&s_full[sb], sp, abort, a.status);
+        ok = ok && wait_warp(&full[ring.stage], ring.phase, abort, status) &&
+             wait_warp(&s_full[sb], sp, abort, status);
         float x[kH];
         const float2 sc = s_meta[ring.stage * kMaxTilePages + (tok >> a.shift)];
         const bool valid = (g.tile0 + t) * kTile + tok < g.len && !(sc.y < 0.f);
@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           if (t > 0) {
             // every product issued so far has been added
             const int64_t kp = k - 1;
-            ok = wait_warp(&p_empty[kp & 1], (uint32_t)(kp >> 1) & 1u, abort, a.status);
+            ok = wait_warp(&p_empty[kp & 1], (uint32_t)(kp >> 1) & 1u, abort, status);
             if (ok) {
               tc_fence_after();
 #pragma unroll
@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         // the weights, their sum, and their parts for the second product
         if (k >= 2) {
           const int64_t kp = k - 2;
-          ok = ok && wait_warp(&p_empty[kp & 1], (uint32_t)(kp >> 1) & 1u, abort, a.status);
+          ok = ok && wait_warp(&p_empty[kp & 1], (uint32_t)(kp >> 1) & 1u, abort, status);
         }
         if (ok) {
           uint8_t* pt = s_p + sb * C::kPBytes;
@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         ring.next(kST);
       }
       // the segment's sums and accumulators
-      if (ok) ok = wait_warp(&o_full[n_seg & 1u], (n_seg >> 1) & 1u, abort, a.status);
+      if (ok) ok = wait_warp(&o_full[n_seg & 1u], (n_seg >> 1) & 1u, abort, status);
       if (vote_or(!ok)) break;
       tc_fence_after();
       float o[kH];
@@ -725,7 +725,7 @@ extern "C" rkv_status rkv_page_attention_workspace(const rkv_pages* pages, const
   if (rkv_status st = check_table(table, pages->block_tokens)) return st;
   if (rkv_status st = check_heads(pages, n_q_heads)) return st;
   const size_t G = n_q_heads / pages->n_kv_heads;
-  *bytes = 16 + sizeof(float) * 2 * kMaxCtas * G * (2 + (size_t)pages->head_dim);
+  *bytes = sizeof(float) * 2 * kMaxCtas * G * (2 + (size_t)pages->head_dim);
   return RKV_OK;
 }
 
@@ -760,9 +760,7 @@ extern "C" rkv_status rkv_page_attention(const rkv_pages* pages, const rkv_page_
   a.lse = lse, a.flags = flags;
   a.batch = table->batch;
   a.N = pages->n_kv_heads, a.G = n_q_heads / a.N;
-  // a wait that gives up reports to the caller's flags, or to a word of the workspace
-  a.status = flags ? flags : static_cast<int*>(workspace);
-  a.pm = static_cast<float*>(workspace) + 4;
+  a.pm = static_cast<float*>(workspace);
   a.pl = a.pm + 2 * kMaxCtas * a.G;
   a.po = a.pl + 2 * kMaxCtas * a.G;
   a.shift = 4;
