@@ -685,20 +685,22 @@ rkv_status check_heads(const rkv_pages* pages, int n_q_heads) {
 }
 
 template <int D, int kH>
-cudaError_t launch_main(const CUtensorMap& mk, const CUtensorMap& mv, const PaArgs& a, int grid, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(page_attention_kernel<D, kH>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, PaCfg<D>::kSmem);
+cudaError_t launch_main(const CUtensorMap& mk, const CUtensorMap& mv, const PaArgs& a, int grid, int dev,
+                        cudaStream_t s) {
+  static SmemOptIn opt_in;
+  const cudaError_t e = opt_in(page_attention_kernel<D, kH>, PaCfg<D>::kSmem, dev);
   if (e != cudaSuccess) return e;
   page_attention_kernel<D, kH><<<grid, kPaThreads, PaCfg<D>::kSmem, s>>>(mk, mv, a);
   return cudaGetLastError();
 }
 
 template <int D>
-cudaError_t launch_all(const CUtensorMap& mk, const CUtensorMap& mv, const PaArgs& a, int grid, cudaStream_t s) {
-  cudaError_t e = a.G <= 2   ? launch_main<D, 2>(mk, mv, a, grid, s)
-                  : a.G <= 4 ? launch_main<D, 4>(mk, mv, a, grid, s)
-                  : a.G <= 8 ? launch_main<D, 8>(mk, mv, a, grid, s)
-                             : launch_main<D, 16>(mk, mv, a, grid, s);
+cudaError_t launch_all(const CUtensorMap& mk, const CUtensorMap& mv, const PaArgs& a, int grid, int dev,
+                        cudaStream_t s) {
+  cudaError_t e = a.G <= 2   ? launch_main<D, 2>(mk, mv, a, grid, dev, s)
+                  : a.G <= 4 ? launch_main<D, 4>(mk, mv, a, grid, dev, s)
+                  : a.G <= 8 ? launch_main<D, 8>(mk, mv, a, grid, dev, s)
+                             : launch_main<D, 16>(mk, mv, a, grid, dev, s);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(a.batch, a.N);
@@ -769,6 +771,6 @@ extern "C" rkv_status rkv_page_attention(const rkv_pages* pages, const rkv_page_
   a.scale_log2 = (float)(scale * 1.4426950408889634);
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = D == 128 ? launch_all<128>(mk, mv, a, grid, s) : launch_all<64>(mk, mv, a, grid, s);
+  const cudaError_t e = D == 128 ? launch_all<128>(mk, mv, a, grid, dev, s) : launch_all<64>(mk, mv, a, grid, dev, s);
   return e == cudaSuccess ? RKV_OK : fail_with(RKV_ECUDA, "page attention launch failed: %s", cudaGetErrorString(e));
 }

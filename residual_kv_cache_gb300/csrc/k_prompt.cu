@@ -477,9 +477,9 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 
 template <int D>
 cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PrArgs& a, int grid,
-                   cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(prompt_attention_kernel<D>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, PrCfg<D>::kSmem);
+                   int dev, cudaStream_t s) {
+  static SmemOptIn opt_in;
+  const cudaError_t e = opt_in(prompt_attention_kernel<D>, PrCfg<D>::kSmem, dev);
   if (e != cudaSuccess) return e;
   prompt_attention_kernel<D><<<grid, kPrThreads, PrCfg<D>::kSmem, s>>>(q, k, v, a);
   return cudaGetLastError();
@@ -537,6 +537,6 @@ extern "C" rkv_status rkv_prompt_attention(const rkv_prompt* pr, int32_t* flags,
   const int64_t tiles = ((int64_t)p.total_q / kRows + p.batch) * p.n_q_heads;
   const int grid = (int)(tiles < sms ? tiles : sms);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = D == 128 ? launch<128>(mq, mk, mv, a, grid, s) : launch<64>(mq, mk, mv, a, grid, s);
+  const cudaError_t e = D == 128 ? launch<128>(mq, mk, mv, a, grid, dev, s) : launch<64>(mq, mk, mv, a, grid, dev, s);
   return e == cudaSuccess ? RKV_OK : fail_with(RKV_ECUDA, "prompt attention launch failed: %s", cudaGetErrorString(e));
 }

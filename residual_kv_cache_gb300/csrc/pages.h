@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/rkv.h"
 
 namespace rkv {
@@ -37,6 +39,25 @@ bool encode_map_bytes(CUtensorMap* m, const void* base, uint64_t inner, uint64_t
 // {64 elements, 1 head, box_rows}.
 bool encode_map_heads(CUtensorMap* m, const void* base, uint64_t D, uint64_t heads, uint64_t rows,
                       const int64_t strides[2], uint32_t box_rows);
+
+// Opts a kernel into `smem` bytes of dynamic shared memory on the current device, once per
+// device (the attribute belongs to the device's copy of the function).  One instance per
+// kernel; concurrent first calls set the same value twice.
+class SmemOptIn {
+ public:
+  template <typename F>
+  cudaError_t operator()(F* fn, size_t smem, int dev) {
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev < 64 && (done_.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess && dev < 64) done_.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+
+ private:
+  std::atomic<uint64_t> done_{0};
+};
 
 __device__ __forceinline__ void raise_flag(int32_t* flags, int32_t bit) {
   if (flags) atomicOr(flags, bit);

@@ -149,7 +149,7 @@ def test_binding_refuses_what_the_library_cannot_see():
         rkv.page_append(bf(4, 2, 64), bf(4, 2, 64), u8, u8, f32, f32, i32(2, 4), i32(2), i32(3))
     with pytest.raises(ValueError, match="k8"):
         rkv.page_attention(bf(2, 4, 64), u8, u8, f32, f32, i32(2, 4), i32(2))
-    with pytest.raises(ValueError, match="q must be"):
+    with pytest.raises(ValueError, match="q must be a CUDA"):
         rkv.prompt_attention(bf(4, 4, 64), bf(4, 2, 64), bf(4, 2, 64), i32(2))
     for s in (0.0, -1.0, math.inf, math.nan):
         with pytest.raises(ValueError, match="scale"):
@@ -159,25 +159,25 @@ def test_binding_refuses_what_the_library_cannot_see():
 
 def test_rows_strides():
     """Rows may be strided views of a projection's output; strides of dimensions of one are
-    not looked at, others must be whole 16 bytes."""
-    class Cuda(torch.Tensor):
-        @property
-        def is_cuda(self):
-            return True
-    mk = lambda t: t.as_subclass(Cuda)  # noqa: E731
-    bf = (torch.bfloat16,)
-    x = mk(torch.zeros((6, 10, 64), dtype=torch.bfloat16))
-    assert list(RP._rows(x[:, 2:5], "x", (None, 3, 64), None, bf)) == [640, 64]
-    assert list(RP._rows(x.transpose(0, 1), "x", (10, 6, 64), None, bf)) == [64, 640]
-    assert list(RP._rows(x[:0], "x", (None, None, 64), None, bf)) == [0, 0]
-    odd = mk(torch.zeros((6, 10, 67), dtype=torch.bfloat16))[:, :, :64]
+    not looked at, others must be whole 16 bytes.  (Device -1 stands for the CPU here.)"""
+    bf = torch.bfloat16
+    x = torch.zeros((6, 10, 64), dtype=bf)
+    assert list(RP._rows(x[:, 2:5], "x", (6, 3, 64), -1, bf)) == [640, 64]
+    assert list(RP._rows(x.transpose(0, 1), "x", (10, 6, 64), -1, bf)) == [64, 640]
+    assert list(RP._rows(x[:0], "x", (0, 10, 64), -1, bf)) == [0, 64]
+    odd = torch.zeros((6, 10, 67), dtype=bf)[:, :, :64]
     with pytest.raises(ValueError, match="16 bytes"):
-        RP._rows(odd, "x", (6, 10, 64), None, bf)
-    assert RP._rows(odd[:1, :1], "x", (1, 1, 64), None, bf) is not None
-    with pytest.raises(ValueError):
-        RP._rows(x.transpose(1, 2), "x", (6, 64, 10), None, bf)
-    with pytest.raises(ValueError):
-        RP._rows(x.float(), "x", (6, 10, 64), None, bf)
+        RP._rows(odd, "x", (6, 10, 64), -1, bf)
+    assert list(RP._rows(odd[:1, :1], "x", (1, 1, 64), -1, bf)) == [0, 0]
+    assert list(RP._rows(odd[:0], "x", (0, 10, 64), -1, bf)) == [0, 0]
+    with pytest.raises(ValueError, match="x must be"):
+        RP._rows(x.transpose(1, 2), "x", (6, 10, 64), -1, bf)
+    with pytest.raises(ValueError, match="16 bytes"):
+        RP._rows(x.transpose(1, 2), "x", (6, 64, 10), -1, bf)
+    with pytest.raises(ValueError, match="x must be"):
+        RP._rows(x.float(), "x", (6, 10, 64), -1, bf)
+    with pytest.raises(ValueError, match="x must be"):
+        RP._rows(x, "x", (6, 10, 64), 0, bf)
 
 
 # ------------------------------------------------------------- pins of the definitions
