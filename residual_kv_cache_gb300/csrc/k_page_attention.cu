@@ -283,25 +283,25 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
-    constexpr uint32_t id_s = idesc_f8(128, kNQ, false), id_o = idesc_f8(128, kNP, true);
-    Ring ring, prev;                                         // this tile's stage, the last one's
-    int64_t k = 0;
-    uint32_t n_seg = 0;
-    bool ok = true;
-    for (int s = 0, ph = 0; ok; s == kSlots - 1 ? (s = 0, ph ^= 1) : ++s, ++n_seg) {
-      if (!(ok = wait_warp(&q_full[s], ph, abort, status))) break;
-      if (seg[s].b < 0) break;
-      const int tiles = seg[s].tiles;
-      const uint32_t o_tm = tmem + kOCol + (n_seg & 1u) * kOStride;
-      // the accumulator of the segment before the last has been read
-      if (!(ok = wait_warp(&o_empty[n_seg & 1u], ((n_seg >> 1) & 1u) ^ 1u, abort, status))) break;
-      for (int t = 0; t <= tiles; ++t) {
-        if (t < tiles) {
-          const uint32_t sb = (uint32_t)k & 1u, sp = (uint32_t)(k >> 1) & 1u;
-          if (!(ok = wait_warp(&full[ring.stage], ring.phase, abort, status))) break;
-          if (!(ok = wait_warp(&s_empty[sb], sp ^ 1u, abort, status))) break;
-          tc_fence_after();
-          if (lane == 0) {
+    if (elect_one()) {
+      constexpr uint32_t id_s = idesc_f8(128, kNQ, false), id_o = idesc_f8(128, kNP, true);
+      Ring ring, prev;                                       // this tile's stage, the last one's
+      int64_t k = 0;
+      uint32_t n_seg = 0;
+      bool ok = true;
+      for (int s = 0, ph = 0; ok; s == kSlots - 1 ? (s = 0, ph ^= 1) : ++s, ++n_seg) {
+        if (!(ok = mbar_wait(&q_full[s], ph, abort, status))) break;
+        if (seg[s].b < 0) break;
+        const int tiles = seg[s].tiles;
+        const uint32_t o_tm = tmem + kOCol + (n_seg & 1u) * kOStride;
+        // the accumulator of the segment before the last has been read
+        if (!(ok = mbar_wait(&o_empty[n_seg & 1u], ((n_seg >> 1) & 1u) ^ 1u, abort, status))) break;
+        for (int t = 0; t <= tiles; ++t) {
+          if (t < tiles) {
+            const uint32_t sb = (uint32_t)k & 1u, sp = (uint32_t)(k >> 1) & 1u;
+            if (!(ok = mbar_wait(&full[ring.stage], ring.phase, abort, status))) break;
+            if (!(ok = mbar_wait(&s_empty[sb], sp ^ 1u, abort, status))) break;
+            tc_fence_after();
             const uint32_t kt = smem_u32(sm + ring.stage * C::kStage + C::kHalf);
             const uint32_t qt = smem_u32(s_q + s * C::kQBytes);
 #pragma unroll
@@ -311,14 +311,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             umma_commit(&s_full[sb]);
             if (t == tiles - 1) umma_commit(&q_empty[s]);
           }
-          __syncwarp();
-        }
-        if (t > 0) {                                         // the tile before: O += V^T P
-          const int64_t kp = k - 1;
-          const uint32_t pb = (uint32_t)kp & 1u, pp = (uint32_t)(kp >> 1) & 1u;
-          if (!(ok = wait_warp(&p_full[pb], pp, abort, status))) break;
-          tc_fence_after();
-          if (lane == 0) {
+          if (t > 0) {                                       // the tile before: O += V^T P
+            const int64_t kp = k - 1;
+            const uint32_t pb = (uint32_t)kp & 1u, pp = (uint32_t)(kp >> 1) & 1u;
+            if (!(ok = mbar_wait(&p_full[pb], pp, abort, status))) break;
+            tc_fence_after();
             const uint32_t vt = smem_u32(sm + prev.stage * C::kStage);
             const uint32_t pt = smem_u32(s_p + pb * C::kPBytes);
             // M = 128 lanes; for D = 64 the upper 64 read the K tile behind V and are unused
@@ -330,18 +327,17 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             umma_commit(&p_empty[pb]);
             if (t == tiles) umma_commit(&o_full[n_seg & 1u]);
           }
-          __syncwarp();
-        }
-        if (t < tiles) {
-          prev = ring;
-          ring.next(kST);
-          ++k;
+          if (t < tiles) {
+            prev = ring;
+            ring.next(kST);
+            ++k;
+          }
         }
       }
-    }
-    if (*abort && lane == 0) {
-      umma_commit(&drain);
-      drain_wait(&drain, 0);
+      if (*abort) {
+        umma_commit(&drain);
+        drain_wait(&drain, 0);
+      }
     }
   } else if (warp == 2) {
     // ------------------------------------------------- segments and their query tiles
