@@ -16,7 +16,10 @@
 //   of that largest, and within 2^-21 of it everywhere; a weight is hi + mid / 16 + lo / 256,
 //   12 significant bits for weights down to 2^-6 and an absolute 2^-18 below.  The products
 //   are exact and the parts are joined in fp32.
-//   Softmax: thread t owns token t (TMEM lane t).  Scores s are kept in base 2, and a page's
+//   Softmax: two groups of 128 threads take a segment's tiles in turn, each with its own
+//   score buffer, weights, sums and accumulator (joined at the segment's end), so that one
+//   group's chain of dependent steps runs beside the other's.  Thread t of a group owns
+//   token t (TMEM lane t).  Scores s are kept in base 2, and a page's
 //   value scale 2^e is folded into the weights: the second product takes 2^(s + e - m), the
 //   sum 2^(s - m).  The reference m of a head is the maximum of s + e over some earlier
 //   tiles, so the parts hold the terms that weigh most, whatever the pages' scales.  It is
@@ -29,7 +32,8 @@
 // o), at most two a CTA, which the second kernel joins in tile order: no atomics, the same
 // bits on every run.
 //
-// Warps: 0 TMA producer, 1 MMA issuer, 2 queries and segment list, 3 idle, 4-7 softmax.
+// Warps: 0 TMA producer, 1 MMA issuer, 2 queries and segment list, 3 idle, 4-7 and 8-11
+// softmax.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
@@ -43,14 +47,14 @@ namespace rkv {
 namespace {
 
 constexpr int kTile = 128;                 // positions per tile
-constexpr int kPaThreads = 256;
+constexpr int kPaThreads = 384;
 constexpr int kSoftWarp0 = 4;
 constexpr int kSlots = 4;                  // segments whose queries are held ahead
 constexpr int kMaxCtas = 256;              // shares of a call (partials in the workspace)
 constexpr int kMaxTilePages = kTile / 16;
-constexpr uint32_t kPaTmemCols = 256;
-constexpr uint32_t kSCol = 0, kSStride = 32;      // two score buffers
-constexpr uint32_t kOCol = 64, kOStride = 64;     // two accumulators
+constexpr uint32_t kPaTmemCols = 512;
+constexpr uint32_t kSCol = 0, kSStride = 32;      // a score buffer for each group
+constexpr uint32_t kOCol = 64, kOStride = 64;     // accumulators: [segment parity][group]
 constexpr float kRaise = 8.f;              // weights stay below 2^8
 
 // A run of tiles of one (sequence, head) inside a CTA's share.
@@ -75,12 +79,14 @@ template <int D>
 struct PaCfg {
   static constexpr uint32_t kHalf = kTile * D;               // bytes of a K or V tile
   static constexpr uint32_t kStage = 2 * kHalf;
-  static constexpr int kStages = D == 128 ? 6 : 12;
+  static constexpr int kStages = D == 128 ? 5 : 10;
   static constexpr uint32_t kQBytes = 32 * D;                // one segment's query tile
   static constexpr uint32_t kPBytes = 48 * kTile;            // one weight tile
   static constexpr uint32_t kMetaOff = kStages * kStage + kSlots * kQBytes + 2 * kPBytes;
   static constexpr uint32_t kMeta = kStages * kMaxTilePages * 8;   // (k scale, v scale)
-  static constexpr uint32_t kSmem = 1024 + kMetaOff + kMeta + 1024;
+  static constexpr uint32_t kJoinOff = kMetaOff + kMeta;           // second group's o, m, l
+  static constexpr uint32_t kJoin = (16 * kTile + 32) * 4;
+  static constexpr uint32_t kSmem = 1024 + kJoinOff + kJoin;
 };
 
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
@@ -93,10 +99,24 @@ __device__ __forceinline__ int length_of(const PaArgs& a, int b, bool& bad) {
   return len < 0 ? 0 : (int)(len > cap ? cap : len);
 }
 
-// First tile of share c of C.
-__device__ __forceinline__ int64_t share_start(int64_t total, int c, int C) {
-  return total / C * c + total % C * c / C;
-}
+// Equal contiguous shares of `total` tiles: share c begins at start(c).
+struct Shares {
+  int64_t q;
+  int r, C;
+  __device__ __forceinline__ Shares(int64_t total, int max_c) {
+    C = (int)min((int64_t)max_c, total);
+    if (C == 0) {
+      q = 0, r = 0;
+    } else if (total <= INT32_MAX) {
+      q = (int)total / C;
+      r = (int)total % C;
+    } else {
+      q = total / C;
+      r = (int)(total % C);
+    }
+  }
+  __device__ __forceinline__ int64_t start(int c) const { return q * c + r * c / C; }
+};
 
 // tcgen05.mma kind::f8f6f4, E4M3 operands in shared memory, fp32 accumulation.
 __device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -146,7 +166,9 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
   return ok;
 }
 
-__device__ __forceinline__ bool vote_or(bool pred) { return !bar_red_and(1, 128, !pred); }
+// Whether pred holds in any thread of softmax group g, or of both groups.
+__device__ __forceinline__ bool vote_group(int g, bool pred) { return !bar_red_and(1 + g, 128, !pred); }
+__device__ __forceinline__ bool vote_both(bool pred) { return !bar_red_and(3, 256, !pred); }
 
 // kH: query heads computed (G rounded up to 2, 4, 8 or 16).
 template <int D, int kH>
@@ -163,11 +185,12 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   uint8_t* s_q = sm + kST * C::kStage;
   uint8_t* s_p = s_q + kSlots * C::kQBytes;
   float2* s_meta = reinterpret_cast<float2*>(sm + C::kMetaOff);
+  float* s_join = reinterpret_cast<float*>(sm + C::kJoinOff);
   __shared__ __align__(8) uint64_t full[kST], empty[kST], s_full[2], s_empty[2], p_full[2], p_empty[2],
-      o_full[2], o_empty[2], q_full[kSlots], q_empty[kSlots], drain;
+      o_full[2], o_empty[2], d_full[kSlots], q_full[kSlots], q_empty[kSlots], drain;
   __shared__ Segment seg[kSlots];
   __shared__ float s_qf[kSlots][16];
-  __shared__ float s_red[4][16];
+  __shared__ float s_red[2][4][16];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_status, s_b0;
   __shared__ int64_t s_pref;
@@ -178,13 +201,13 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   if (tid == 0) {
     tma_prefetch(&tm_k);
     tma_prefetch(&tm_v);
-    for (int i = 0; i < kST; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+    for (int i = 0; i < kST; ++i) mbar_init(&full[i], 2), mbar_init(&empty[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1), mbar_init(&s_empty[i], 4);
       mbar_init(&p_full[i], 128), mbar_init(&p_empty[i], 1);
-      mbar_init(&o_full[i], 1), mbar_init(&o_empty[i], 4);
+      mbar_init(&o_full[i], 1), mbar_init(&o_empty[i], 8);
     }
-    for (int i = 0; i < kSlots; ++i) mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 6);
+    for (int i = 0; i < kSlots; ++i) mbar_init(&d_full[i], 1), mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 10);
     mbar_init(&drain, 1);
     s_abort = 0;
     s_b0 = a.batch;
@@ -196,32 +219,37 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   }
 
   // the call's tiles, and the sequence in which this CTA's share begins
-  int64_t total = 0;
+  int64_t total = 0, incl = 0, mine = 0;
   bool any_bad = false;
   for (int b0 = 0; b0 < a.batch; b0 += kPaThreads) {
     bool bad = false;
     const int b = b0 + tid;
-    int64_t n = b < a.batch ? tiles_of(length_of(a, b, bad)) : 0, t;
+    mine = b < a.batch ? tiles_of(length_of(a, b, bad)) : 0;
     any_bad |= bad;
-    int x = 0, tx;
-    block_scan<kPaThreads>(n, x, t, tx);
-    total += t;
-  }
-  if (any_bad && blockIdx.x == 0) raise_flag(a.flags, RKV_FLAG_BAD_INDEX);
-  total *= a.N;
-  const int n_cta = (int)min((int64_t)gridDim.x, total), cta = blockIdx.x;
-  const int64_t f0 = cta < n_cta ? share_start(total, cta, n_cta) : 0;
-  const int64_t f1 = cta < n_cta ? share_start(total, cta + 1, n_cta) : 0;
-  int64_t pref = 0;
-  for (int b0 = 0; b0 < a.batch && pref * a.N <= f0; b0 += kPaThreads) {
-    bool bad;
-    const int b = b0 + tid;
-    const int64_t mine = b < a.batch ? tiles_of(length_of(a, b, bad)) : 0;
     int64_t n = mine, t;
     int x = 0, tx;
     block_scan<kPaThreads>(n, x, t, tx);
-    if (mine > 0 && (pref + n - mine) * a.N <= f0 && f0 < (pref + n) * a.N) s_b0 = b, s_pref = pref + n - mine;
-    pref += t;
+    incl = total + n;
+    total += t;
+  }
+  if (any_bad && blockIdx.x == 0) raise_flag(a.flags, RKV_FLAG_BAD_INDEX);
+  const Shares shares(total * a.N, gridDim.x);
+  const int cta = blockIdx.x;
+  const int64_t f0 = cta < shares.C ? shares.start(cta) : 0, f1 = cta < shares.C ? shares.start(cta + 1) : 0;
+  if (a.batch <= kPaThreads) {
+    if (mine > 0 && (incl - mine) * a.N <= f0 && f0 < incl * a.N) s_b0 = tid, s_pref = incl - mine;
+  } else {
+    int64_t pref = 0;
+    for (int b0 = 0; b0 < a.batch && pref * a.N <= f0; b0 += kPaThreads) {
+      bool bad;
+      const int b = b0 + tid;
+      mine = b < a.batch ? tiles_of(length_of(a, b, bad)) : 0;
+      int64_t n = mine, t;
+      int x = 0, tx;
+      block_scan<kPaThreads>(n, x, t, tx);
+      if (mine > 0 && (pref + n - mine) * a.N <= f0 && f0 < (pref + n) * a.N) s_b0 = b, s_pref = pref + n - mine;
+      pref += t;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -236,7 +264,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     int64_t issued = 0;
     bool ok = true;
     for (int s = 0, ph = 0; ok; s == kSlots - 1 ? (s = 0, ph ^= 1) : ++s) {
-      if (!(ok = wait_warp(&q_full[s], ph, abort, status))) break;
+      if (!(ok = wait_warp(&d_full[s], ph, abort, status))) break;
       const Segment g = seg[s];
       if (g.b < 0) break;
       const int pages = (g.len + P - 1) >> a.shift;          // of the whole sequence
@@ -246,8 +274,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       int p0 = g.tile0 * ppt;
       int id = p0 + lane < end ? __ldg(row + p0 + lane) : -1;
       for (int t = 0; t < g.tiles && ok; p0 += 32) {
-        const bool here = p0 + lane < end, good = here && id >= 0 && id < a.num_blocks;
-        if (here && !good) raise_flag(a.flags, RKV_FLAG_BAD_INDEX);
+        const bool stored = p0 + lane < end, good = stored && id >= 0 && id < a.num_blocks;
+        if (stored && !good) raise_flag(a.flags, RKV_FLAG_BAD_INDEX);
         const int64_t head = (int64_t)id * a.N + g.h;
         // a page that is not there has a negative scale
         float2 sc = make_float2(0.f, -1.f);
@@ -257,17 +285,19 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         for (int i = 0; i < 32 && t < g.tiles; i += ppt, ++t) {
           if (!(ok = wait_warp(&empty[ring.stage], ring.phase ^ 1u, abort, status))) break;
           uint8_t* st = sm + ring.stage * C::kStage;
-          const bool mine = lane >= i && lane < i + ppt;
-          if (mine) s_meta[ring.stage * kMaxTilePages + lane - i] = sc;
-          const uint32_t n = __popc(__ballot_sync(0xffffffffu, mine && good));
-          __syncwarp();
+          const bool here = lane >= i && lane < i + ppt;
+          const uint32_t n = __popc(__ballot_sync(0xffffffffu, here && good));
           if (lane == 0) mbar_arrive_expect_tx(&full[ring.stage], n * 2u * (uint32_t)(P * D));
           __syncwarp();
-          if (mine && good) {
+          if (here && good) {
             const uint32_t off = (uint32_t)(lane - i) * (uint32_t)(P * D);
             tma_load_2d(st + off, &tm_v, &full[ring.stage], 0, (int32_t)(head << a.shift));
             tma_load_2d(st + C::kHalf + off, &tm_k, &full[ring.stage], 0, (int32_t)(head << a.shift));
           }
+          // the scales arrive while the copies are under way
+          if (here) s_meta[ring.stage * kMaxTilePages + lane - i] = sc;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[ring.stage]);
           ring.next(kST);
           ++issued;
         }
@@ -285,22 +315,24 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     // ------------------------------------------------------------------ MMA issuer
     if (elect_one()) {
       constexpr uint32_t id_s = idesc_f8(128, kNQ, false), id_o = idesc_f8(128, kNP, true);
-      Ring ring, prev;                                       // this tile's stage, the last one's
-      int64_t k = 0;
-      uint32_t n_seg = 0;
+      Ring ring, done;                                       // stages of the next S and V products
+      uint32_t s_ph[2] = {1, 1}, p_ph[2] = {0, 0}, n_seg = 0;
       bool ok = true;
       for (int s = 0, ph = 0; ok; s == kSlots - 1 ? (s = 0, ph ^= 1) : ++s, ++n_seg) {
         if (!(ok = mbar_wait(&q_full[s], ph, abort, status))) break;
         if (seg[s].b < 0) break;
         const int tiles = seg[s].tiles;
-        const uint32_t o_tm = tmem + kOCol + (n_seg & 1u) * kOStride;
+        const uint32_t o_tm = tmem + kOCol + (n_seg & 1u) * 2 * kOStride;
         // the accumulator of the segment before the last has been read
         if (!(ok = mbar_wait(&o_empty[n_seg & 1u], ((n_seg >> 1) & 1u) ^ 1u, abort, status))) break;
-        for (int t = 0; t <= tiles; ++t) {
+        // a tile's scores are issued as soon as its group has read its last ones, two tiles
+        // ahead of the second product
+        for (int t = 0; t < tiles + 2; ++t) {
           if (t < tiles) {
-            const uint32_t sb = (uint32_t)k & 1u, sp = (uint32_t)(k >> 1) & 1u;
+            const uint32_t sb = (uint32_t)t & 1u;
             if (!(ok = mbar_wait(&full[ring.stage], ring.phase, abort, status))) break;
-            if (!(ok = mbar_wait(&s_empty[sb], sp ^ 1u, abort, status))) break;
+            if (!(ok = mbar_wait(&s_empty[sb], s_ph[sb], abort, status))) break;
+            s_ph[sb] ^= 1u;
             tc_fence_after();
             const uint32_t kt = smem_u32(sm + ring.stage * C::kStage + C::kHalf);
             const uint32_t qt = smem_u32(s_q + s * C::kQBytes);
@@ -310,27 +342,24 @@ __global__ void __launch_bounds__(kPaThreads, 1)
                       id_s, i > 0);
             umma_commit(&s_full[sb]);
             if (t == tiles - 1) umma_commit(&q_empty[s]);
+            ring.next(kST);
           }
-          if (t > 0) {                                       // the tile before: O += V^T P
-            const int64_t kp = k - 1;
-            const uint32_t pb = (uint32_t)kp & 1u, pp = (uint32_t)(kp >> 1) & 1u;
-            if (!(ok = mbar_wait(&p_full[pb], pp, abort, status))) break;
+          if (t >= 2) {                                      // O += V^T P of tile t - 2
+            const uint32_t pb = (uint32_t)t & 1u;
+            if (!(ok = mbar_wait(&p_full[pb], p_ph[pb], abort, status))) break;
+            p_ph[pb] ^= 1u;
             tc_fence_after();
-            const uint32_t vt = smem_u32(sm + prev.stage * C::kStage);
+            const uint32_t vt = smem_u32(sm + done.stage * C::kStage);
             const uint32_t pt = smem_u32(s_p + pb * C::kPBytes);
             // M = 128 lanes; for D = 64 the upper 64 read the K tile behind V and are unused
 #pragma unroll
             for (int i = 0; i < kTile / 32; ++i)
-              umma_f8(o_tm, sdesc_rows<D>(vt + i * 32 * D, C::kHalf), sdesc_rows<128>(pt + i * 32, 16), id_o,
-                      t > 1 || i > 0);
-            umma_commit(&empty[prev.stage]);
+              umma_f8(o_tm + pb * kOStride, sdesc_rows<D>(vt + i * 32 * D, C::kHalf), sdesc_rows<128>(pt + i * 32, 16), id_o,
+                      t >= 4 || i > 0);
+            umma_commit(&empty[done.stage]);
             umma_commit(&p_empty[pb]);
-            if (t == tiles) umma_commit(&o_full[n_seg & 1u]);
-          }
-          if (t < tiles) {
-            prev = ring;
-            ring.next(kST);
-            ++k;
+            if (t == tiles + 1) umma_commit(&o_full[n_seg & 1u]);
+            done.next(kST);
           }
         }
       }
@@ -368,6 +397,10 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         first = false;
       }
       if (!(ok = wait_warp(&q_empty[s], ph, abort, status))) break;
+      if (lane == 0) {
+        seg[s] = g;
+        mbar_arrive(&d_full[s]);                             // the copies need no more
+      }
       if (g.b >= 0) {
         const __nv_bfloat16* q = a.q + g.b * a.qst.row + (int64_t)g.h * a.G * a.qst.head;
         uint8_t* qt = s_q + s * C::kQBytes;
@@ -414,7 +447,6 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           if (lane == 0) s_qf[s][h] = __uint_as_float((uint32_t)(127 + ex) << 23) * a.scale_log2;
         }
       }
-      if (lane == 0) seg[s] = g;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[s]);
@@ -422,36 +454,40 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     }
   } else if (warp >= kSoftWarp0) {
     // ---------------------------------------------------------------------- softmax
-    const int tok = tid - kSoftWarp0 * 32, w = warp - kSoftWarp0;
+    const int wg = (warp - kSoftWarp0) >> 2, tok = tid & 127, w = warp & 3;
     const uint32_t tm = tmem + ((uint32_t)(w * 32) << 16);
-    Ring ring;
-    int64_t k = 0;
-    uint32_t n_seg = 0;
+    const uint32_t s_tm = tm + kSCol + wg * kSStride;
+    uint8_t* pt = s_p + wg * C::kPBytes;
+    Ring ring;                                               // stage of the segment's tile t
+    uint32_t n_seg = 0, s_ph = 0, p_ph = 1;                  // p_ph: of the group's last product
     bool ok = true;
     for (int s = 0, ph = 0; ok; s == kSlots - 1 ? (s = 0, ph ^= 1) : ++s, ++n_seg) {
       ok = wait_warp(&q_full[s], ph, abort, status);
-      if (vote_or(!ok)) break;
+      if (vote_both(!ok)) break;
       const Segment g = seg[s];
       if (g.b < 0) break;
       float m[kH], l[kH], qf[kH];
 #pragma unroll
       for (int h = 0; h < kH; ++h) m[h] = -FLT_MAX, l[h] = 0.f, qf[h] = s_qf[s][h];
-      const uint32_t o_tm = tm + kOCol + (n_seg & 1u) * kOStride;
-      for (int t = 0; t < g.tiles; ++t, ++k) {
-        const uint32_t sb = (uint32_t)k & 1u, sp = (uint32_t)(k >> 1) & 1u;
-        ok = ok && wait_warp(&full[ring.stage], ring.phase, abort, status) &&
-             wait_warp(&s_full[sb], sp, abort, status);
+      const uint32_t o_tm = tm + kOCol + ((n_seg & 1u) * 2 + wg) * kOStride;
+      for (int t = 0; t < g.tiles; ++t) {
+        const int stage = ring.stage;
+        const uint32_t st_ph = ring.phase;
+        ring.next(kST);
+        if ((t & 1) != wg) continue;
+        ok = ok && wait_warp(&full[stage], st_ph, abort, status) && wait_warp(&s_full[wg], s_ph, abort, status);
+        s_ph ^= 1u;
         float x[kH];
-        const float2 sc = s_meta[ring.stage * kMaxTilePages + (tok >> a.shift)];
+        const float2 sc = s_meta[stage * kMaxTilePages + (tok >> a.shift)];
         const bool valid = (g.tile0 + t) * kTile + tok < g.len && !(sc.y < 0.f);
         if (ok) {
           tc_fence_after();
           uint32_t r[kNQ];
-          if (kNQ == 16) tmem_ld16(tm + kSCol + sb * kSStride, r);
-          else tmem_ld32(tm + kSCol + sb * kSStride, r);
+          if (kNQ == 16) tmem_ld16(s_tm, r);
+          else tmem_ld32(s_tm, r);
           tmem_ld_wait();
           tc_fence_before();
-          if (lane == 0) mbar_arrive(&s_empty[sb]);
+          if (lane == 0) mbar_arrive(&s_empty[wg]);
 #pragma unroll
           for (int h = 0; h < kH; ++h) {
             const float d = fmaf(__uint_as_float(r[kGP + h]), 0.0625f, __uint_as_float(r[h]));
@@ -460,13 +496,16 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         }
         // log2 of the value scale: the weights times it are what has to stay in range
         const float ev = (float)((int)(__float_as_uint(sc.y) >> 23) - 127);
-        bool raise = !ok || t == 0;
+        bool raise = !ok || t < 2;
         if (ok) {
 #pragma unroll
           for (int h = 0; h < kH; ++h) raise |= x[h] + ev > m[h] + kRaise;
         }
-        if (vote_or(raise)) {
-          if (vote_or(!ok)) {
+        // the products of the group's last tile have been added, its weights can go
+        ok = ok && wait_warp(&p_empty[wg], p_ph, abort, status);
+        p_ph ^= 1u;
+        if (vote_group(wg, raise || !ok)) {
+          if (vote_group(wg, !ok)) {
             ok = false;
             break;
           }
@@ -481,130 +520,137 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           }
           if (lane == 0) {
 #pragma unroll
-            for (int h = 0; h < kH; ++h) s_red[w][h] = y[h];
+            for (int h = 0; h < kH; ++h) s_red[wg][w][h] = y[h];
           }
-          bar_sync(1, 128);
+          bar_sync(1 + wg, 128);
           float f[kH];
 #pragma unroll
           for (int h = 0; h < kH; ++h) {
-            const float mn = fmaxf(m[h], fmaxf(fmaxf(s_red[0][h], s_red[1][h]), fmaxf(s_red[2][h], s_red[3][h])));
-            const float c = ex2_approx(m[h] - mn);
-            l[h] *= c;
-            f[h] = c;
+            const float mn = fmaxf(m[h], fmaxf(fmaxf(s_red[wg][0][h], s_red[wg][1][h]),
+                                               fmaxf(s_red[wg][2][h], s_red[wg][3][h])));
+            f[h] = ex2_approx(m[h] - mn);
+            l[h] *= f[h];
             m[h] = mn;
           }
-          if (t > 0) {
-            // every product issued so far has been added
-            const int64_t kp = k - 1;
-            ok = wait_warp(&p_empty[kp & 1], (uint32_t)(kp >> 1) & 1u, abort, status);
-            if (ok) {
-              tc_fence_after();
-#pragma unroll
-              for (int part = 0; part < 3; ++part) {
-                uint32_t r[kGP];
-                if (kGP == 8) tmem_ld8(o_tm + part * kGP, r);
-                else tmem_ld16(o_tm + part * kGP, r);
-                tmem_ld_wait();
-#pragma unroll
-                for (int h = 0; h < kH; ++h) r[h] = __float_as_uint(__uint_as_float(r[h]) * f[h]);
-                if (kGP == 8) tmem_st8(o_tm + part * kGP, r);
-                else tmem_st16(o_tm + part * kGP, r);
-              }
-              tmem_st_wait();
-            }
-          }
-          if (vote_or(!ok)) {                                // also: s_red has been read
-            ok = false;
-            break;
-          }
-        }
-        // the weights, their sum, and their parts for the second product
-        if (k >= 2) {
-          const int64_t kp = k - 2;
-          ok = ok && wait_warp(&p_empty[kp & 1], (uint32_t)(kp >> 1) & 1u, abort, status);
-        }
-        if (ok) {
-          uint8_t* pt = s_p + sb * C::kPBytes;
-          const uint32_t c16 = (uint32_t)tok >> 4, c0 = (uint32_t)tok & 15u;
-#pragma unroll
-          for (int h = 0; h < kH; h += 2) {
-            const float p0 = ex2_approx(x[h] - m[h]), p1 = ex2_approx(x[h + 1] - m[h + 1]);
-            l[h] += p0;
-            l[h + 1] += p1;
-            float u0 = valid ? p0 * sc.y : 0.f, u1 = valid ? p1 * sc.y : 0.f;
+          if (t >= 2) {
+            tc_fence_after();
 #pragma unroll
             for (int part = 0; part < 3; ++part) {
-              const uint32_t c = e4m3x2(u0, u1);
-              const int n0 = part * kGP + h, n1 = n0 + 1;
-              pt[n0 * 128 + ((c16 ^ (n0 & 7)) << 4) + c0] = (uint8_t)c;
-              pt[n1 * 128 + ((c16 ^ (n1 & 7)) << 4) + c0] = (uint8_t)(c >> 8);
-              if (part < 2) {
-                const float2 e = from_e4m3x2(c);
-                u0 = (u0 - e.x) * 16.f;
-                u1 = (u1 - e.y) * 16.f;
-              }
+              uint32_t r[kGP];
+              if (kGP == 8) tmem_ld8(o_tm + part * kGP, r);
+              else tmem_ld16(o_tm + part * kGP, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int h = 0; h < kH; ++h) r[h] = __float_as_uint(__uint_as_float(r[h]) * f[h]);
+              if (kGP == 8) tmem_st8(o_tm + part * kGP, r);
+              else tmem_st16(o_tm + part * kGP, r);
+            }
+            tmem_st_wait();
+          }
+          bar_sync(1 + wg, 128);                             // s_red has been read
+        }
+        // the weights, their sum, and their parts for the second product
+        const uint32_t c16 = (uint32_t)tok >> 4, c0 = (uint32_t)tok & 15u;
+#pragma unroll
+        for (int h = 0; h < kH; h += 2) {
+          const float p0 = ex2_approx(x[h] - m[h]), p1 = ex2_approx(x[h + 1] - m[h + 1]);
+          l[h] += p0;
+          l[h + 1] += p1;
+          float u0 = valid ? p0 * sc.y : 0.f, u1 = valid ? p1 * sc.y : 0.f;
+#pragma unroll
+          for (int part = 0; part < 3; ++part) {
+            const uint32_t c = e4m3x2(u0, u1);
+            const int n0 = part * kGP + h, n1 = n0 + 1;
+            pt[n0 * 128 + ((c16 ^ (n0 & 7)) << 4) + c0] = (uint8_t)c;
+            pt[n1 * 128 + ((c16 ^ (n1 & 7)) << 4) + c0] = (uint8_t)(c >> 8);
+            if (part < 2) {
+              const float2 e = from_e4m3x2(c);
+              u0 = (u0 - e.x) * 16.f;
+              u1 = (u1 - e.y) * 16.f;
             }
           }
-          if (!valid) {                                      // 0 x what the row holds must be 0
-            uint8_t* vt = sm + ring.stage * C::kStage + tok * D;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) *reinterpret_cast<uint4*>(vt + i * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          tc_fence_before();
-          mbar_arrive(&p_full[sb]);
         }
-        ring.next(kST);
+        if (!valid) {                                        // 0 x what the row holds must be 0
+          uint8_t* vt = sm + stage * C::kStage + tok * D;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) *reinterpret_cast<uint4*>(vt + i * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(&p_full[wg]);
       }
-      // the segment's sums and accumulators
+      // the group's sums and accumulator
       if (ok) ok = wait_warp(&o_full[n_seg & 1u], (n_seg >> 1) & 1u, abort, status);
-      if (vote_or(!ok)) break;
+      if (vote_both(!ok)) {                                  // also: s_join and s_red are free
+        ok = false;
+        break;
+      }
       tc_fence_after();
       float o[kH];
 #pragma unroll
       for (int h = 0; h < kH; ++h) o[h] = 0.f;
+      if (wg < g.tiles) {
 #pragma unroll
-      for (int part = 2; part >= 0; --part) {
-        uint32_t r[kGP];
-        if (kGP == 8) tmem_ld8(o_tm + part * kGP, r);
-        else tmem_ld16(o_tm + part * kGP, r);
-        tmem_ld_wait();
+        for (int part = 2; part >= 0; --part) {
+          uint32_t r[kGP];
+          if (kGP == 8) tmem_ld8(o_tm + part * kGP, r);
+          else tmem_ld16(o_tm + part * kGP, r);
+          tmem_ld_wait();
 #pragma unroll
-        for (int h = 0; h < kH; ++h) o[h] = fmaf(o[h], 0.0625f, __uint_as_float(r[h]));
-      }
-      tc_fence_before();
+          for (int h = 0; h < kH; ++h) o[h] = fmaf(o[h], 0.0625f, __uint_as_float(r[h]));
+        }
+        tc_fence_before();
 #pragma unroll
-      for (int h = 0; h < kH; ++h) {
+        for (int h = 0; h < kH; ++h) {
 #pragma unroll
-        for (int i = 16; i > 0; i >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], i);
+          for (int i = 16; i > 0; i >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], i);
+        }
+        if (lane == 0) {
+#pragma unroll
+          for (int h = 0; h < kH; ++h) s_red[wg][w][h] = l[h];
+        }
+        bar_sync(1 + wg, 128);
+#pragma unroll
+        for (int h = 0; h < kH; ++h)
+          l[h] = s_red[wg][0][h] + s_red[wg][1][h] + s_red[wg][2][h] + s_red[wg][3][h];
       }
       if (lane == 0) {
         mbar_arrive(&o_empty[n_seg & 1u]);
         mbar_arrive(&q_empty[s]);
-#pragma unroll
-        for (int h = 0; h < kH; ++h) s_red[w][h] = l[h];
       }
-      bar_sync(1, 128);
+      if (g.tiles > 1) {                                     // the second group's tiles
+        if (wg == 1) {
 #pragma unroll
-      for (int h = 0; h < kH; ++h) l[h] = s_red[0][h] + s_red[1][h] + s_red[2][h] + s_red[3][h];
-      bar_sync(1, 128);                                      // s_red may be written again
-      if (g.slot < 0) {
-        const int64_t row = ((int64_t)g.b * a.N + g.h) * a.G;
-#pragma unroll
-        for (int h = 0; h < kH; ++h) {
-          if (h < a.G) {
-            if (tok < D) a.out[(row + h) * D + tok] = __float2bfloat16(l[h] != 0.f ? o[h] / l[h] : 0.f);
-            if (a.lse && tok == 0)
-              a.lse[row + h] = l[h] != 0.f ? (m[h] + log2f(l[h])) * 0.6931471805599453f : -INFINITY;
+          for (int h = 0; h < kH; ++h) {
+            s_join[h * kTile + tok] = o[h];
+            if (tok == 0) s_join[16 * kTile + h] = m[h], s_join[16 * kTile + 16 + h] = l[h];
           }
         }
-      } else {
-        const int64_t row = (int64_t)g.slot * a.G;
+        bar_sync(3, 256);
+        if (wg == 0) {
+#pragma unroll
+          for (int h = 0; h < kH; ++h) {
+            const float m1 = s_join[16 * kTile + h], mn = fmaxf(m[h], m1);
+            const float fa = ex2_approx(m[h] - mn), fb = ex2_approx(m1 - mn);
+            o[h] = o[h] * fa + s_join[h * kTile + tok] * fb;
+            l[h] = l[h] * fa + s_join[16 * kTile + 16 + h] * fb;
+            m[h] = mn;
+          }
+        }
+      }
+      if (wg == 0) {
+        const int64_t row = g.slot < 0 ? ((int64_t)g.b * a.N + g.h) * a.G : (int64_t)g.slot * a.G;
 #pragma unroll
         for (int h = 0; h < kH; ++h) {
           if (h < a.G) {
-            if (tok < D) a.po[(row + h) * D + tok] = o[h];
-            if (tok == 0) a.pm[row + h] = m[h], a.pl[row + h] = l[h];
+            if (g.slot < 0) {
+              if (tok < D) a.out[(row + h) * D + tok] = __float2bfloat16(l[h] != 0.f ? o[h] / l[h] : 0.f);
+              if (a.lse && tok == 0)
+                a.lse[row + h] = l[h] != 0.f ? (m[h] + log2f(l[h])) * 0.6931471805599453f : -INFINITY;
+            } else {
+              if (tok < D) a.po[(row + h) * D + tok] = o[h];
+              if (tok == 0) a.pm[row + h] = m[h], a.pl[row + h] = l[h];
+            }
           }
         }
       }
@@ -617,18 +663,20 @@ __global__ void __launch_bounds__(kPaThreads, 1)
 }
 
 // Joins the partials of each (sequence, head) that several shares hold, in their order, and
-// zeroes the rows of empty sequences.  Grid (batch, N), D threads.
+// zeroes the rows of empty sequences.  Grid (batch, N, G), D threads.
 template <int D>
 __global__ void __launch_bounds__(D) page_attention_join_kernel(PaArgs a, int grid) {
-  const int b = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
+  const int b = blockIdx.x, h = blockIdx.y, g = blockIdx.z, tid = threadIdx.x;
+  __shared__ int64_t s_all[D / 32], s_before[D / 32];
+  __shared__ float s_m[kMaxCtas], s_l[kMaxCtas], s_red[2][D / 32];
+  bool bad;
+  const int nb = tiles_of(length_of(a, b, bad));
   int64_t before = 0, all = 0;
   for (int i = tid; i < a.batch; i += D) {
-    bool bad;
     const int n = tiles_of(length_of(a, i, bad));
     all += n;
     if (i < b) before += n;
   }
-  __shared__ int64_t s_all[D / 32], s_before[D / 32];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     all += __shfl_xor_sync(0xffffffffu, all, o);
@@ -639,39 +687,56 @@ __global__ void __launch_bounds__(D) page_attention_join_kernel(PaArgs a, int gr
   all = before = 0;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) all += s_all[i], before += s_before[i];
-  bool bad;
-  const int nb = tiles_of(length_of(a, b, bad));
-  const int64_t row = ((int64_t)b * a.N + h) * a.G;
+  const int64_t row = (((int64_t)b * a.N + h) * a.G + g);
+  const int64_t total = all * a.N, f0 = before * a.N + (int64_t)h * nb, f1 = f0 + nb;
+  const Shares shares(total, grid);
+  // the share in which the head's tiles begin, and the last one that has any of them
+  int c0 = total > 0 ? min(shares.C - 1, (int)((float)f0 / (float)total * shares.C)) : 0, c1;
+  while (c0 > 0 && shares.start(c0) > f0) --c0;
+  while (c0 + 1 < shares.C && shares.start(c0 + 1) <= f0) ++c0;
+  c1 = c0;
+  while (c1 + 1 < shares.C && shares.start(c1 + 1) < f1) ++c1;
   pdl_wait_previous_grid();
   if (nb == 0) {
-    for (int g = 0; g < a.G; ++g) {
-      a.out[(row + g) * D + tid] = __float2bfloat16(0.f);
-      if (a.lse && tid == 0) a.lse[row + g] = -INFINITY;
-    }
+    a.out[row * D + tid] = __float2bfloat16(0.f);
+    if (a.lse && tid == 0) a.lse[row] = -INFINITY;
     return;
   }
-  const int64_t total = all * a.N, f0 = before * a.N + (int64_t)h * nb, f1 = f0 + nb;
-  const int C = (int)min((int64_t)grid, total);
-  int c0 = (int)(f0 * C / total), c1;
-  while (c0 > 0 && share_start(total, c0, C) > f0) --c0;
-  while (c0 + 1 < C && share_start(total, c0 + 1, C) <= f0) ++c0;
-  c1 = c0;
-  while (c1 + 1 < C && share_start(total, c1 + 1, C) < f1) ++c1;
-  if (c0 == c1) return;
-  const int first = 2 * c0 + (share_start(total, c0, C) == f0 ? 0 : 1);
-  for (int g = 0; g < a.G; ++g) {
-    float m = -FLT_MAX, l = 0.f, o = 0.f;
-    for (int c = c0; c <= c1; ++c) {
-      const int64_t i = (int64_t)(c == c0 ? first : 2 * c) * a.G + g;
-      const float pm = __ldcg(a.pm + i), pl = __ldcg(a.pl + i), po = __ldcg(a.po + i * D + tid);
-      const float mn = fmaxf(m, pm), fa = ex2_approx(m - mn), fb = ex2_approx(pm - mn);
-      l = l * fa + pl * fb;
-      o = o * fa + po * fb;
-      m = mn;
-    }
-    a.out[(row + g) * D + tid] = __float2bfloat16(l != 0.f ? o / l : 0.f);
-    if (a.lse && tid == 0) a.lse[row + g] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  if (c0 == c1) return;                      // written by its one share
+  // partial i: the first segment of share c0 + i, but for c0's unless it begins there
+  const int n = c1 - c0 + 1, first = shares.start(c0) == f0 ? 2 * c0 : 2 * c0 + 1;
+  float m = -FLT_MAX;
+  for (int i = tid; i < n; i += D) {
+    const int64_t at = (int64_t)(i == 0 ? first : 2 * (c0 + i)) * a.G + g;
+    s_m[i] = __ldcg(a.pm + at);
+    s_l[i] = __ldcg(a.pl + at);
+    m = fmaxf(m, s_m[i]);
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((tid & 31) == 0) s_red[0][tid >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) m = fmaxf(m, s_red[0][i]);
+  float l = 0.f;
+  for (int i = tid; i < n; i += D) {
+    const float f = ex2_approx(s_m[i] - m);
+    l += s_l[i] * f;
+    s_m[i] = f;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if ((tid & 31) == 0) s_red[1][tid >> 5] = l;
+  __syncthreads();
+  l = 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) l += s_red[1][i];
+  float o = 0.f;
+#pragma unroll 8
+  for (int i = 0; i < n; ++i)
+    o = fmaf(__ldcg(a.po + ((int64_t)(i == 0 ? first : 2 * (c0 + i)) * a.G + g) * D + tid), s_m[i], o);
+  a.out[row * D + tid] = __float2bfloat16(l != 0.f ? o / l : 0.f);
+  if (a.lse && tid == 0) a.lse[row] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 rkv_status check_heads(const rkv_pages* pages, int n_q_heads) {
@@ -699,7 +764,7 @@ cudaError_t launch_all(const CUtensorMap& mk, const CUtensorMap& mv, const PaArg
                              : launch_main<D, 16>(mk, mv, a, grid, dev, s);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(a.batch, a.N);
+  lc.gridDim = dim3(a.batch, a.N, a.G);
   lc.blockDim = dim3(D);
   lc.stream = s;
   cudaLaunchAttribute attr[1];
