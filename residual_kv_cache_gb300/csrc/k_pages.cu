@@ -7,27 +7,28 @@
 // page have + i of a sequence is free[n_free - 1 - (first + i)], and packed row r lies in
 // the sequence with cu_b <= r < cu_{b+1}, at position len_b + r - cu_b.  Every CTA scans the
 // lengths itself (they fit in shared memory), so pages and rows are independent items found
-// by bisection, and no CTA waits for another's prefix.  Nothing a CTA reads may change
-// before all have read it (lengths and the free count can be updated in place): the CTAs
-// form one cluster and meet once after their scans.  The call is a handful of dependent
-// loads: latency bounds it up to some 10^4 rows, the row maps' stores beyond.
+// by bisection, and no CTA waits for another's prefix.  No CTA may change what another still
+// reads: where several CTAs share the rows and the lengths or the free count are updated in
+// place, a second kernel does that from the offsets.  The call is a handful of dependent
+// loads and latency bounds it: a thread takes kPlanRows rows whose loads overlap (65 000
+// rows of 256 sequences: 14.6 us on one cluster of 8 CTAs, one row at a time).
 //
-// Append.  One CTA takes the rows that a step brings to one (page, head) of K or of V: it
-// holds them in registers between finding their largest magnitude and storing their codes,
-// so each row is read once, and no other CTA touches the page's scale.  Bandwidth bounds
-// long appends, latency single tokens.
-#include <cooperative_groups.h>
+// Append.  A CTA takes the rows that a step brings to one page, of K or of V, and one or
+// more of its heads in turn: it holds a head's rows in registers between finding their
+// largest magnitude and storing their codes, so each row is read once, and no other CTA
+// touches the page and head's scale.  Bandwidth bounds long appends, latency single tokens:
+// finding the page takes about as long as a head's rows, so a CTA takes several heads where
+// there are CTAs enough (32768 rows of 8 heads of 128: 64 us with a head a CTA).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
 #include "pages.h"
 
 namespace rkv {
-namespace cg = cooperative_groups;
 namespace {
 
 constexpr int kPlanThreads = 512;
-constexpr int kMaxPlanCtas = 8;      // portable cluster size
+constexpr int kPlanRows = 4;         // rows of one thread at a time
 
 // Largest index i in [0, n) with v[i] <= x (v non-decreasing, v[0] <= x).
 __device__ __forceinline__ int last_not_above(const int* v, int n, int x) {
@@ -53,6 +54,7 @@ struct PlanArgs {
   int32_t* row_slot;
   int32_t* flags;
   int batch, max_blocks, num_blocks, shift, max_rows;   // page size = 1 << shift
+  int state;                         // this kernel also writes the new lengths and free count
 };
 
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanArgs p) {
@@ -60,7 +62,6 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanArgs p) {
   int* s_cu = psm;                   // [batch] first row of each sequence
   int* s_first = s_cu + p.batch;     // [batch] first taken page of each sequence
   int* s_len = s_first + p.batch;    // [batch] stored positions
-  cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x;
   const int P1 = (1 << p.shift) - 1;
   const int64_t cap = (int64_t)p.max_blocks << p.shift;
@@ -86,32 +87,39 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanArgs p) {
     rows += ta;
     pages += tc;
   }
-  bad = __syncthreads_or(bad);
+  bad = __syncthreads_or(bad);     // and: everyone's sums are in shared memory
   const bool full = !bad && (rows > p.max_rows || pages > n_free);
   const bool ok = !bad && !full;
   const int total = ok ? (int)rows : 0;
-  // The old lengths of a refused step are still to be copied: read them before the barrier.
-  cluster.sync();                    // every CTA has read the lengths and the free count
-
   const int step = gridDim.x * kPlanThreads, first = blockIdx.x * kPlanThreads + tid;
-  for (int r = first; r < p.max_rows; r += step) {
-    int seq = -1, pos = -1, slot = -1;
-    if (r < total) {
-      // empty sequences share their first row with the next: the last one is the owner
-      seq = last_not_above(s_cu, p.batch, r);
-      pos = s_len[seq] + r - s_cu[seq];
-      const int page = pos >> p.shift, have = (s_len[seq] + P1) >> p.shift;
-      const int64_t at = (int64_t)seq * p.max_blocks + page;
-      const int id = page < have ? p.table[at]
-                                 : p.free_blocks[n_free - 1 - (s_first[seq] + page - have)];
-      if (id >= 0 && id < p.num_blocks)
-        slot = (id << p.shift) + (pos & P1);
-      else
-        raise_flag(p.flags, RKV_FLAG_BAD_INDEX);
+  for (int r0 = first; r0 < p.max_rows; r0 += step * kPlanRows) {
+    int seq[kPlanRows], pos[kPlanRows], id[kPlanRows];
+#pragma unroll
+    for (int i = 0; i < kPlanRows; ++i) {
+      const int r = r0 + i * step;
+      seq[i] = pos[i] = id[i] = -1;
+      if (r < total) {
+        // empty sequences share their first row with the next: the last one is the owner
+        const int b = last_not_above(s_cu, p.batch, r);
+        seq[i] = b;
+        pos[i] = s_len[b] + r - s_cu[b];
+        const int page = pos[i] >> p.shift, have = (s_len[b] + P1) >> p.shift;
+        const int32_t* at = page < have ? p.table + (int64_t)b * p.max_blocks + page
+                                        : p.free_blocks + (n_free - 1 - (s_first[b] + page - have));
+        id[i] = *at;
+      }
     }
-    p.row_seq[r] = seq;
-    p.row_pos[r] = pos;
-    p.row_slot[r] = slot;
+#pragma unroll
+    for (int i = 0; i < kPlanRows; ++i) {
+      const int r = r0 + i * step;
+      if (r < p.max_rows) {
+        const bool fine = id[i] >= 0 && id[i] < p.num_blocks;
+        if (r < total && !fine) raise_flag(p.flags, RKV_FLAG_BAD_INDEX);
+        p.row_seq[r] = seq[i];
+        p.row_pos[r] = pos[i];
+        p.row_slot[r] = fine ? (id[i] << p.shift) + (pos[i] & P1) : -1;
+      }
+    }
   }
   if (ok) {
     for (int i = first; i < pages; i += step) {
@@ -122,18 +130,35 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanArgs p) {
   }
   for (int b = first; b < p.batch; b += step) {
     p.cu_rows[b] = ok ? s_cu[b] : 0;
-    const int next = b + 1 < p.batch ? s_cu[b + 1] : total;
-    if (ok)
-      p.seq_len_out[b] = s_len[b] + next - s_cu[b];
-    else if (p.seq_len_out != p.seq_len)
-      p.seq_len_out[b] = p.seq_len[b];
+    if (p.state) {
+      const int next = b + 1 < p.batch ? s_cu[b + 1] : total;
+      p.seq_len_out[b] = ok ? s_len[b] + next - s_cu[b] : p.seq_len[b];
+    }
   }
   if (first == 0) {
     p.cu_rows[p.batch] = total;
-    *p.n_free_out = ok ? n_free - pages : n_free;
+    if (p.state) *p.n_free_out = ok ? n_free - pages : n_free;
     if (bad) raise_flag(p.flags, RKV_FLAG_BAD_INDEX);
     if (full) raise_flag(p.flags, RKV_FLAG_NO_SPACE);
   }
+}
+
+// The lengths and the free count after a planned step, from its offsets (all 0 where it was
+// refused).  One CTA.
+__global__ void __launch_bounds__(kPlanThreads) page_plan_state_kernel(PlanArgs p) {
+  const int tid = threadIdx.x;
+  const int64_t P1 = (1 << p.shift) - 1;
+  const int n_free = *p.n_free;
+  int taken = 0;
+  for (int b = tid; b < p.batch; b += kPlanThreads) {
+    const int len = p.seq_len[b], nw = p.cu_rows[b + 1] - p.cu_rows[b];
+    if (nw > 0) taken += (int)((len + nw + P1) >> p.shift) - (int)((len + P1) >> p.shift);
+    p.seq_len_out[b] = len + nw;
+  }
+  int64_t none = 0, total_none;
+  int total;
+  block_scan<kPlanThreads>(none, taken, total_none, total);
+  if (tid == 0) *p.n_free_out = n_free - total;
 }
 
 // One CTA: a release moves a few thousand ids at a request's end.
@@ -178,6 +203,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 
 // ------------------------------------------------------------------------------ append
 constexpr int kAppendThreads = 256;
+constexpr int kAppendCtas = 10;
 
 struct AppendArgs {
   const void* x[2];                  // k, v
@@ -200,42 +226,117 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// Eight consecutive values of a row as floats.
-__device__ __forceinline__ void load_row8(const __nv_bfloat16* p, float* f) {
-  const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
-__device__ __forceinline__ void load_row8(const float* p, float* f) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-}
-
 // Two floats to E4M3, nearest even, saturating (NaN stays NaN).
 __device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
-// Grid (units, N, 2): unit u = the u-th (sequence, page) that the step touches, in order;
-// z: K or V.  D / 8 threads share a row; a thread holds kHold chunks of eight values.
-template <typename T, int D, int kPage>
-__global__ void __launch_bounds__(kAppendThreads) page_append_kernel(AppendArgs p) {
-  constexpr int kLanes = D / 8;                              // threads of one row
-  constexpr int kRows = kAppendThreads / kLanes;             // rows of one pass
-  constexpr int kHold = (kPage + kRows - 1) / kRows;         // passes over a page
+// Eight codes of a stored row, rounded again at a scale grown by 1 / ratio (powers of two:
+// the products are exact).
+__device__ __forceinline__ void rescale8(uint8_t* codes, float ratio) {
+  uint2* q = reinterpret_cast<uint2*>(codes);
+  const uint2 old = *q;
+  const uint32_t in[2] = {old.x, old.y};
+  uint32_t w[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    uint32_t half[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((uint16_t)(in[e] >> (16 * j)), __NV_E4M3);
+      const float2 v = __half22float2(__half2(hr));
+      half[j] = to_e4m3x2(v.x * ratio, v.y * ratio);
+    }
+    w[e] = half[0] | half[1] << 16;
+  }
+  *q = make_uint2(w[0], w[1]);
+}
+
+// Largest magnitude of eight values, infinities and NaN left out; their codes at 1 / scale.
+__device__ __forceinline__ float finite_max8(const float* f) {
+  float a = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float m = fabsf(f[e]);
+    if (m < INFINITY) a = fmaxf(a, m);
+  }
+  return a;
+}
+__device__ __forceinline__ uint2 codes8(const float* f, float inv) {
+  uint32_t w[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    w[e] = to_e4m3x2(f[4 * e] * inv, f[4 * e + 1] * inv) |
+           to_e4m3x2(f[4 * e + 2] * inv, f[4 * e + 3] * inv) << 16;
+  return make_uint2(w[0], w[1]);
+}
+
+// Eight consecutive values of a row, as loaded and as floats.
+template <typename T>
+struct Chunk;
+template <>
+struct Chunk<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ float finite_max() const {
+    float f[8];
+    get(f);
+    return finite_max8(f);
+  }
+  __device__ __forceinline__ uint2 codes(float inv) const {
+    float f[8];
+    get(f);
+    return codes8(f, inv);
+  }
+  __device__ __forceinline__ void get(float* f) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+};
+template <>
+struct Chunk<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldg(reinterpret_cast<const float4*>(p));
+    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ float finite_max() const {
+    float f[8];
+    get(f);
+    return finite_max8(f);
+  }
+  __device__ __forceinline__ uint2 codes(float inv) const {
+    float f[8];
+    get(f);
+    return codes8(f, inv);
+  }
+  __device__ __forceinline__ void get(float* f) const {
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  }
+};
+
+// The rows that a step brings to one page.
+struct PageRows {
+  int page;                          // the page's id
+  int off, n;                        // rows [off, off + n) of the page
+  int row;                           // packed row of the first
+};
+
+// The rows of unit blockIdx.x: the u-th (sequence, page) that the step touches, in order.
+// False for units past the last and for pages out of range.
+__device__ __forceinline__ bool find_page(const AppendArgs& p, PageRows& out) {
   __shared__ int s_seq, s_page, s_lo, s_hi, s_row0;
-  __shared__ float s_max[kAppendThreads / 32];
-  const int tid = threadIdx.x, u = blockIdx.x, h = blockIdx.y, z = blockIdx.z;
+  const int tid = threadIdx.x, u = blockIdx.x;
 
   // the unit's sequence and page
   if (tid == 0) s_seq = -1;
   int64_t base = 0;
-  for (int b0 = 0; b0 < p.batch && base <= u; b0 += kAppendThreads) {
+  const bool checks = u == 0 && blockIdx.y == 0 && blockIdx.z == 0;    // looks at every sequence
+  for (int b0 = 0; b0 < p.batch && (base <= u || checks); b0 += kAppendThreads) {
     const int b = b0 + tid;
     int lo = 0, hi = 0, r0 = 0;      // the step's positions [lo, hi) of sequence b
     if (b < p.batch) {
@@ -245,7 +346,7 @@ __global__ void __launch_bounds__(kAppendThreads) page_append_kernel(AppendArgs 
         if (rows > 0 && r0 >= 0 && rows <= len && len <= (int64_t)p.max_blocks << p.shift) {
           lo = (int)(len - rows);
           hi = lo + (int)max((int64_t)0, min(rows, (int64_t)p.n_rows - r0));
-        } else if (u == 0 && h == 0 && z == 0) {
+        } else if (checks) {
           raise_flag(p.flags, RKV_FLAG_BAD_INDEX);
         }
       }
@@ -265,7 +366,7 @@ __global__ void __launch_bounds__(kAppendThreads) page_append_kernel(AppendArgs 
   }
   __syncthreads();
   const int seq = s_seq;
-  if (seq < 0) return;               // fewer pages than the grid's bound
+  if (seq < 0) return false;               // fewer pages than the grid's bound
   const int page = s_page, P = 1 << p.shift;
   const int lo = max(s_lo, page << p.shift), hi = min(s_hi, (page + 1) << p.shift);
   const int off0 = lo & (P - 1), n = hi - lo;                // rows of the page, from off0
@@ -273,72 +374,109 @@ __global__ void __launch_bounds__(kAppendThreads) page_append_kernel(AppendArgs 
   const int id = p.table[(int64_t)seq * p.max_blocks + page];
   if (id < 0 || id >= p.num_blocks) {
     if (tid == 0) raise_flag(p.flags, RKV_FLAG_BAD_INDEX);
-    return;
+    return false;
   }
-  const int64_t head = (int64_t)id * p.N + h;
-  float* scale_p = p.scale[z] + head;
-  uint8_t* codes = p.codes[z] + (head << p.shift) * D;
-  const T* x = static_cast<const T*>(p.x[z]) + (int64_t)row0 * p.st[z].row + (int64_t)h * p.st[z].head;
-  const int lane = tid % kLanes, r_in = tid / kLanes;
-  const float held = off0 > 0 ? *scale_p : 0.f;
+  out.page = id;
+  out.off = off0, out.n = n;
+  out.row = row0;
+  return true;
+}
 
-  float f[kHold][8];
-  float amax = 0.f;
+// Grid (units, head groups, 2): unit u = the u-th (sequence, page) that the step touches, in
+// order; kPar heads at a time, every gridDim.y-th such set; z: K or V.  D / 8 threads share a
+// row; a thread holds kHold chunks of eight values of each head.
+template <typename T, int D, int kPage>
+__global__ void __launch_bounds__(kAppendThreads) page_append_kernel(AppendArgs p) {
+  constexpr int kLanes = D / 8;                              // threads of one row
+  constexpr int kRows = kAppendThreads / kLanes;             // rows of one pass
+  constexpr int kHold = (kPage + kRows - 1) / kRows;         // passes over a page
+  constexpr int kPar = kHold >= 4 ? 1 : 4 / kHold;           // heads held at a time
+  __shared__ float s_max[kPar][kAppendThreads / 32];
+  const int tid = threadIdx.x, z = blockIdx.z;
+  PageRows u;
+  if (!find_page(p, u)) return;
+  const int off0 = u.off, n = u.n;
+  const int lane = tid % kLanes, r_in = tid / kLanes;
+  const T* rows = static_cast<const T*>(p.x[z]) + (int64_t)u.row * p.st[z].row + lane * 8;
+  for (int h0 = blockIdx.y * kPar; h0 < p.N; h0 += gridDim.y * kPar) {
+    const int64_t head = (int64_t)u.page * p.N + h0;
+    float held[kPar], amax[kPar];
+    Chunk<T> c[kPar][kHold];
 #pragma unroll
-  for (int i = 0; i < kHold; ++i) {
-    const int r = i * kRows + r_in;
-    if (r < n) {
-      load_row8(x + (int64_t)r * p.st[z].row + lane * 8, f[i]);
+    for (int g = 0; g < kPar; ++g) {
+      held[g] = off0 > 0 && h0 + g < p.N ? p.scale[z][head + g] : 0.f;
+      const T* x = rows + (int64_t)(h0 + g) * p.st[z].head;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float m = fabsf(f[i][e]);
-        if (m < INFINITY) amax = fmaxf(amax, m);             // finite values only
-      }
+      for (int i = 0; i < kHold; ++i)
+        if (h0 + g < p.N && i * kRows + r_in < n) c[g][i].load(x + (int64_t)(i * kRows + r_in) * p.st[z].row);
     }
+#pragma unroll
+    for (int g = 0; g < kPar; ++g) {
+      amax[g] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kHold; ++i)
+        if (h0 + g < p.N && i * kRows + r_in < n) amax[g] = fmaxf(amax[g], c[g][i].finite_max());
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) amax[g] = fmaxf(amax[g], __shfl_xor_sync(0xffffffffu, amax[g], o));
+    }
+    __syncthreads();                 // the last heads' maxima have been read
+    if ((tid & 31) == 0) {
+#pragma unroll
+      for (int g = 0; g < kPar; ++g) s_max[g][tid >> 5] = amax[g];
+    }
+    __syncthreads();                 // every thread has read the held scales
+#pragma unroll
+    for (int g = 0; g < kPar; ++g) {
+      if (h0 + g >= p.N) break;
+#pragma unroll
+      for (int i = 0; i < kAppendThreads / 32; ++i) amax[g] = fmaxf(amax[g], s_max[g][i]);
+      const float need = pow2i(scale_exponent(amax[g]));
+      const float s = held[g] > need ? held[g] : need;
+      const float inv = 1.f / s;     // a power of two: exact
+      uint8_t* codes = p.codes[z] + ((head + g) << p.shift) * D + lane * 8;
+      if (tid == 0) p.scale[z][head + g] = s;
+#pragma unroll
+      for (int i = 0; i < kHold; ++i)
+        if (i * kRows + r_in < n)
+          *reinterpret_cast<uint2*>(codes + (int64_t)(off0 + i * kRows + r_in) * D) = c[g][i].codes(inv);
+      if (held[g] > 0.f && held[g] < s)
+        for (int r = r_in; r < off0; r += kRows) rescale8(codes + (int64_t)r * D, held[g] / s);
+    }
+  }
+}
+
+// The same for calls of few rows a sequence: a warp takes one head of a page, D / 32 values a
+// lane, and reads its rows twice where there are several.  Grid (units, ceil(N / 8), 2).
+template <typename T, int D>
+__global__ void __launch_bounds__(kAppendThreads) page_append_narrow_kernel(AppendArgs p) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes;         // rows of one pass of a warp
+  const int tid = threadIdx.x, z = blockIdx.z, h = blockIdx.y * (kAppendThreads / 32) + (tid >> 5);
+  PageRows u;
+  if (!find_page(p, u) || h >= p.N) return;
+  const int lane = tid % kLanes, r_in = (tid & 31) / kLanes;
+  const int64_t head = (int64_t)u.page * p.N + h;
+  const T* x = static_cast<const T*>(p.x[z]) + (int64_t)u.row * p.st[z].row + (int64_t)h * p.st[z].head + lane * 8;
+  const float held = u.off > 0 ? p.scale[z][head] : 0.f;
+  Chunk<T> c;
+  float amax = 0.f;
+  for (int r = r_in; r < u.n; r += kRows) {
+    c.load(x + (int64_t)r * p.st[z].row);
+    amax = fmaxf(amax, c.finite_max());
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if ((tid & 31) == 0) s_max[tid >> 5] = amax;
-  __syncthreads();                   // every thread has read the held scale
-#pragma unroll
-  for (int i = 0; i < kAppendThreads / 32; ++i) amax = fmaxf(amax, s_max[i]);
   const float need = pow2i(scale_exponent(amax));
   const float s = held > need ? held : need;
-  const float inv = 1.f / s;         // a power of two: exact
-  if (tid == 0) *scale_p = s;
-#pragma unroll
-  for (int i = 0; i < kHold; ++i) {
-    const int r = i * kRows + r_in;
-    if (r < n) {
-      uint32_t w[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        w[e] = to_e4m3x2(f[i][4 * e] * inv, f[i][4 * e + 1] * inv) |
-               to_e4m3x2(f[i][4 * e + 2] * inv, f[i][4 * e + 3] * inv) << 16;
-      *reinterpret_cast<uint2*>(codes + (int64_t)(off0 + r) * D + lane * 8) = make_uint2(w[0], w[1]);
-    }
+  const float inv = 1.f / s;
+  uint8_t* codes = p.codes[z] + (head << p.shift) * D + lane * 8;
+  __syncwarp();                      // every lane has read the held scale
+  if ((tid & 31) == 0) p.scale[z][head] = s;
+  for (int r = r_in; r < u.n; r += kRows) {
+    if (u.n > kRows) c.load(x + (int64_t)r * p.st[z].row);   // else still held
+    *reinterpret_cast<uint2*>(codes + (int64_t)(u.off + r) * D) = c.codes(inv);
   }
-  if (held > 0.f && held < s) {      // the page's earlier rows at the grown scale
-    const float ratio = held / s;    // a power of two: exact
-    for (int r = r_in; r < off0; r += kRows) {
-      uint2* q = reinterpret_cast<uint2*>(codes + (int64_t)r * D + lane * 8);
-      const uint2 c = *q;
-      const uint32_t in[2] = {c.x, c.y};
-      uint32_t w[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        uint32_t half[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((uint16_t)(in[e] >> (16 * j)), __NV_E4M3);
-          const float2 v = __half22float2(__half2(hr));
-          half[j] = to_e4m3x2(v.x * ratio, v.y * ratio);
-        }
-        w[e] = half[0] | half[1] << 16;
-      }
-      *q = make_uint2(w[0], w[1]);
-    }
-  }
+  if (held > 0.f && held < s)
+    for (int r = r_in; r < u.off; r += kRows) rescale8(codes + (int64_t)r * D, held / s);
 }
 
 int log2_block(int block_tokens) {
@@ -349,21 +487,28 @@ int log2_block(int block_tokens) {
 
 bool block_ok(int b) { return b == 16 || b == 32 || b == 64 || b == 128; }
 
-// The kernels' shared memory beyond 48 KB is opted into on every call that needs it: the
-// attribute belongs to the current device's copy of the function.
-template <typename F>
-bool opt_in(F* fn, size_t smem) {
-  return smem <= 48 * 1024 ||
-         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess;
+template <typename T, int D, int kPage>
+void launch_page(const AppendArgs& a, int64_t units, int sms, cudaStream_t s) {
+  constexpr int kHold = (kPage * D / 8 + kAppendThreads - 1) / kAppendThreads, kPar = kHold >= 4 ? 1 : 4 / kHold;
+  // head groups: as few heads a CTA as make kAppendCtas CTAs an SM
+  const int64_t groups = (int64_t)kAppendCtas * sms / (2 * units) + 1, most = ceil_div(a.N, kPar);
+  page_append_kernel<T, D, kPage><<<dim3((unsigned)units, (unsigned)(groups < most ? groups : most), 2),
+                                    kAppendThreads, 0, s>>>(a);
 }
 
 template <typename T, int D>
-void launch_append(const AppendArgs& a, int block_tokens, dim3 grid, cudaStream_t s) {
+void launch_append(const AppendArgs& a, int block_tokens, int64_t units, int sms, cudaStream_t s) {
+  // up to two rows a sequence on average: a warp a head
+  if (a.n_rows <= 2 * a.batch) {
+    const dim3 grid((unsigned)units, (unsigned)ceil_div(a.N, kAppendThreads / 32), 2);
+    page_append_narrow_kernel<T, D><<<grid, kAppendThreads, 0, s>>>(a);
+    return;
+  }
   switch (block_tokens) {
-    case 16: page_append_kernel<T, D, 16><<<grid, kAppendThreads, 0, s>>>(a); break;
-    case 32: page_append_kernel<T, D, 32><<<grid, kAppendThreads, 0, s>>>(a); break;
-    case 64: page_append_kernel<T, D, 64><<<grid, kAppendThreads, 0, s>>>(a); break;
-    default: page_append_kernel<T, D, 128><<<grid, kAppendThreads, 0, s>>>(a); break;
+    case 16: launch_page<T, D, 16>(a, units, sms, s); break;
+    case 32: launch_page<T, D, 32>(a, units, sms, s); break;
+    case 64: launch_page<T, D, 64>(a, units, sms, s); break;
+    default: launch_page<T, D, 128>(a, units, sms, s); break;
   }
 }
 
@@ -427,24 +572,25 @@ extern "C" rkv_status rkv_page_plan(const rkv_page_table* table, const int32_t* 
   a.num_blocks = num_blocks;
   a.shift = log2_block(block_tokens);
   a.max_rows = max_rows;
-  // CTAs of one cluster, doubled while each still has a few thousand rows to fill
+  // one CTA for up to four rows a thread twice over; then as many as that takes
   int ctas = 1;
-  while (ctas < kMaxPlanCtas && max_rows > ctas * 4 * kPlanThreads) ctas *= 2;
+  if (max_rows > 2 * kPlanRows * kPlanThreads) ctas = ceil_div(max_rows, kPlanRows * kPlanThreads);
+  ctas = ctas < 512 ? ctas : 512;
+  const bool in_place = seq_len_out == a.seq_len || n_free_out == n_free;
+  a.state = ctas == 1 || !in_place;
   const size_t smem = sizeof(int) * 3 * (size_t)a.batch;
-  if (!opt_in(page_plan_kernel, smem)) return fail_with(RKV_ECUDA, "cudaFuncSetAttribute failed");
-  cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(ctas);
-  lc.blockDim = dim3(kPlanThreads);
-  lc.dynamicSmemBytes = smem;
-  lc.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&lc, page_plan_kernel, a);
-  if (e == cudaSuccess) e = cudaGetLastError();
+  static SmemOptIn opt_in;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      opt_in(page_plan_kernel, sizeof(int) * 3 * (size_t)kMaxBatch, dev) != cudaSuccess)
+    return fail_with(RKV_ECUDA, "no usable current device");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  page_plan_kernel<<<ctas, kPlanThreads, smem, s>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess && !a.state) {
+    page_plan_state_kernel<<<1, kPlanThreads, 0, s>>>(a);
+    e = cudaGetLastError();
+  }
   return e == cudaSuccess ? RKV_OK : fail_with(RKV_ECUDA, "page plan launch failed: %s", cudaGetErrorString(e));
 }
 
@@ -498,14 +644,19 @@ extern "C" rkv_status rkv_page_append(const rkv_pages* pages, const rkv_page_tab
   // pages a step can touch: a sequence's rows touch at most (rows - 2) / P + 2, and no more
   // than its rows
   const int64_t bound = (int64_t)n_rows / pages->block_tokens + 2 * (int64_t)a.batch;
-  const dim3 grid((unsigned)(bound < n_rows ? bound : n_rows), a.N, 2);
+  const int64_t units = bound < n_rows ? bound : n_rows;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return fail_with(RKV_ECUDA, "no usable current device");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int P = pages->block_tokens;
   if (dtype == RKV_F32)
-    pages->head_dim == 128 ? launch_append<float, 128>(a, pages->block_tokens, grid, s)
-                           : launch_append<float, 64>(a, pages->block_tokens, grid, s);
+    pages->head_dim == 128 ? launch_append<float, 128>(a, P, units, sms, s)
+                           : launch_append<float, 64>(a, P, units, sms, s);
   else
-    pages->head_dim == 128 ? launch_append<__nv_bfloat16, 128>(a, pages->block_tokens, grid, s)
-                           : launch_append<__nv_bfloat16, 64>(a, pages->block_tokens, grid, s);
+    pages->head_dim == 128 ? launch_append<__nv_bfloat16, 128>(a, P, units, sms, s)
+                           : launch_append<__nv_bfloat16, 64>(a, P, units, sms, s);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? RKV_OK : fail_with(RKV_ECUDA, "page append launch failed: %s", cudaGetErrorString(e));
 }

@@ -69,7 +69,8 @@ PLANS = [  # lens, new, P
     ([0], [1], 16), ([15, 16, 17, 0], [1, 1, 1, 0], 16), ([0, 0, 0], [0, 0, 0], 64),
     ([5] * 33, [1] * 33, 64), ([0, 100, 127, 128, 0], [700, 0, 1, 0, 129], 128),
     (list(range(0, 1200, 2)), [(7 * i) % 50 for i in range(600)], 32),
-    ([0], [40000], 16), ([3000, 0], [0, 20011], 64)]
+    ([0], [40000], 16), ([3000, 0], [0, 20011], 64), ([i % 33 for i in range(5000)], [1] * 5000, 16),
+    ([0] * 8192, [0] * 8000 + [1] * 192, 16)]
 
 
 @cuda
@@ -166,11 +167,13 @@ def _cache(num, N, P, D, seed):
 @pytest.mark.parametrize("P,D,dtype", [(16, 64, torch.bfloat16), (16, 128, torch.float32), (32, 128, torch.bfloat16),
                                        (64, 128, torch.bfloat16), (64, 64, torch.float32), (128, 128, torch.float32),
                                        (128, 64, torch.bfloat16)])
-@pytest.mark.parametrize("what", ["decode", "mixed", "prompt"])
+@pytest.mark.parametrize("what", ["decode", "mixed", "prompt", "few"])
 def test_append_matches_the_definition(P, D, dtype, what):
-    N = 3
-    old = {"decode": [0, 5, P - 1, P, 3 * P + 7], "mixed": [0, 5, P, 0, 2 * P - 1, 9], "prompt": [0]}[what]
-    new = {"decode": [1] * 5, "mixed": [3 * P + 1, 1, 0, P, 2 * P + 2, 0], "prompt": [5 * P + 3]}[what]
+    N = 9 if what == "few" else 3
+    old = {"decode": [0, 5, P - 1, P, 3 * P + 7], "mixed": [0, 5, P, 0, 2 * P - 1, 9], "prompt": [0],
+           "few": [0, 7, P - 3, 2 * P, 1] + [P] * 20}[what]
+    new = {"decode": [1] * 5, "mixed": [3 * P + 1, 1, 0, P, 2 * P + 2, 0], "prompt": [5 * P + 3],
+           "few": [2 * P // 3, 0, 9, 3, 1] + [0] * 20}[what]
     lens, cu = [a + b for a, b in zip(old, new)], [0] + np.cumsum(new).tolist()
     M = max(-(-x // P) for x in lens) + 1
     table, _, _ = _plan_inputs([0] * len(lens), lens, P, M, 3, 11)
