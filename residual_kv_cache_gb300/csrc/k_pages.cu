@@ -13,12 +13,13 @@
 // loads and latency bounds it: a thread takes kPlanRows rows whose loads overlap (65 000
 // rows of 256 sequences: 14.6 us on one cluster of 8 CTAs, one row at a time).
 //
-// Append.  A CTA takes the rows that a step brings to one page, of K or of V, and one or
-// more of its heads in turn: it holds a head's rows in registers between finding their
-// largest magnitude and storing their codes, so each row is read once, and no other CTA
-// touches the page and head's scale.  Bandwidth bounds long appends, latency single tokens:
-// finding the page takes about as long as a head's rows, so a CTA takes several heads where
-// there are CTAs enough (32768 rows of 8 heads of 128: 64 us with a head a CTA).
+// Append.  A CTA takes the rows that a step brings to a run of 64 positions (whole pages; one
+// page of 128), of K or of V, and one or more heads in turn: it holds a head's rows in
+// registers between finding their pages' largest magnitudes and storing their codes, so each
+// row is read once, and no other CTA touches the pages' scales.  Bandwidth bounds long
+// appends, latency single tokens: finding the run takes about as long as a head's rows, so a
+// CTA takes several heads where there are CTAs enough (32768 rows of 8 heads of 128: 64 us
+// with a head a CTA, 38 us so; pages of 16 a page a CTA 62 us).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -217,9 +218,9 @@ struct AppendArgs {
   int batch, max_blocks, num_blocks, N, shift, n_rows;
 };
 
-// Exponent e of the smallest scale 2^e with amax <= 448 2^e (448 = 1.75 2^8), in [-64, 120].
-__device__ __forceinline__ int scale_exponent(float amax) {
-  const uint32_t u = __float_as_uint(amax);
+// Exponent e of the smallest scale 2^e with amax <= 448 2^e (448 = 1.75 2^8), in [-64, 120],
+// from amax's bits.
+__device__ __forceinline__ int scale_exponent(uint32_t u) {
   const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   return max(-64, min(120, e));      // zero and subnormals: exponent field 0
 }
@@ -252,13 +253,14 @@ __device__ __forceinline__ void rescale8(uint8_t* codes, float ratio) {
   *q = make_uint2(w[0], w[1]);
 }
 
-// Largest magnitude of eight values, infinities and NaN left out; their codes at 1 / scale.
-__device__ __forceinline__ float finite_max8(const float* f) {
-  float a = 0.f;
+// Bits of the largest finite magnitude of eight values (of floats of one sign, larger values
+// have larger bits).
+__device__ __forceinline__ uint32_t finite_max8(const float* f) {
+  uint32_t a = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float m = fabsf(f[e]);
-    if (m < INFINITY) a = fmaxf(a, m);
+    const uint32_t m = __float_as_uint(f[e]) & 0x7FFFFFFFu;
+    if (m < 0x7F800000u) a = max(a, m);
   }
   return a;
 }
@@ -278,8 +280,12 @@ template <>
 struct Chunk<__nv_bfloat16> {
   uint4 u;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ float finite_max() const {
-    float f[8];
+  __device__ __forceinline__ uint32_t finite_max() const {
+    const uint32_t m2 = __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu),
+                                 __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu));
+    const uint32_t m = max(m2 << 16, m2 & 0xFFFF0000u);
+    if (m < 0x7F800000u) return m;
+    float f[8];                      // an infinity or NaN among them
     get(f);
     return finite_max8(f);
   }
@@ -304,7 +310,7 @@ struct Chunk<float> {
     a = __ldg(reinterpret_cast<const float4*>(p));
     b = __ldg(reinterpret_cast<const float4*>(p) + 1);
   }
-  __device__ __forceinline__ float finite_max() const {
+  __device__ __forceinline__ uint32_t finite_max() const {
     float f[8];
     get(f);
     return finite_max8(f);
@@ -319,23 +325,21 @@ struct Chunk<float> {
   }
 };
 
-// The rows that a step brings to one page.
-struct PageRows {
-  int page;                          // the page's id
-  int off, n;                        // rows [off, off + n) of the page
+// The rows that a step brings to one run of 2^shift positions of a sequence.
+struct Run {
+  int seq, run;                      // positions run 2^shift ..
+  int lo, hi;                        // rows [lo, hi) of the run are new
   int row;                           // packed row of the first
 };
 
-// The rows of unit blockIdx.x: the u-th (sequence, page) that the step touches, in order.
-// False for units past the last and for pages out of range.
-__device__ __forceinline__ bool find_page(const AppendArgs& p, PageRows& out) {
-  __shared__ int s_seq, s_page, s_lo, s_hi, s_row0;
-  const int tid = threadIdx.x, u = blockIdx.x;
-
-  // the unit's sequence and page
-  if (tid == 0) s_seq = -1;
-  int64_t base = 0;
+// Unit blockIdx.x: the u-th (sequence, run) that the step touches, in order.  False for units
+// past the last.
+__device__ __forceinline__ bool find_run(const AppendArgs& p, int shift, Run& out) {
+  __shared__ Run s_run;
+  const int tid = threadIdx.x, u = blockIdx.x, P1 = (1 << shift) - 1;
   const bool checks = u == 0 && blockIdx.y == 0 && blockIdx.z == 0;    // looks at every sequence
+  if (tid == 0) s_run.seq = -1;
+  int64_t base = 0;
   for (int b0 = 0; b0 < p.batch && (base <= u || checks); b0 += kAppendThreads) {
     const int b = b0 + tid;
     int lo = 0, hi = 0, r0 = 0;      // the step's positions [lo, hi) of sequence b
@@ -351,96 +355,131 @@ __device__ __forceinline__ bool find_page(const AppendArgs& p, PageRows& out) {
         }
       }
     }
-    const int P1 = (1 << p.shift) - 1;
-    const int touched = hi > lo ? ((hi + P1) >> p.shift) - (lo >> p.shift) : 0;
+    const int touched = hi > lo ? (int)(((int64_t)hi + P1) >> shift) - (lo >> shift) : 0;
     int64_t a = touched, ta;
     int c = 0, tc;
     block_scan<kAppendThreads>(a, c, ta, tc);
     const int64_t mine = base + a - touched;
     if (u >= mine && u < base + a) {
-      s_seq = b;
-      s_page = (lo >> p.shift) + (int)(u - mine);
-      s_lo = lo, s_hi = hi, s_row0 = r0;
+      Run r;
+      r.seq = b;
+      r.run = (lo >> shift) + (int)(u - mine);
+      const int64_t at = (int64_t)r.run << shift;
+      r.lo = (int)max((int64_t)0, lo - at);
+      r.hi = (int)min((int64_t)P1 + 1, hi - at);
+      r.row = r0 + (int)(at + r.lo - lo);
+      s_run = r;
     }
     base += ta;
   }
   __syncthreads();
-  const int seq = s_seq;
-  if (seq < 0) return false;               // fewer pages than the grid's bound
-  const int page = s_page, P = 1 << p.shift;
-  const int lo = max(s_lo, page << p.shift), hi = min(s_hi, (page + 1) << p.shift);
-  const int off0 = lo & (P - 1), n = hi - lo;                // rows of the page, from off0
-  const int row0 = s_row0 + (lo - s_lo);
-  const int id = p.table[(int64_t)seq * p.max_blocks + page];
-  if (id < 0 || id >= p.num_blocks) {
-    if (tid == 0) raise_flag(p.flags, RKV_FLAG_BAD_INDEX);
-    return false;
-  }
-  out.page = id;
-  out.off = off0, out.n = n;
-  out.row = row0;
-  return true;
+  out = s_run;
+  return out.seq >= 0;
 }
 
-// Grid (units, head groups, 2): unit u = the u-th (sequence, page) that the step touches, in
+// Id of page `page` of a sequence, -1 (and a flag) where it is out of range.
+__device__ __forceinline__ int page_id(const AppendArgs& p, int seq, int page) {
+  const int id = p.table[(int64_t)seq * p.max_blocks + page];
+  if (id >= 0 && id < p.num_blocks) return id;
+  raise_flag(p.flags, RKV_FLAG_BAD_INDEX);
+  return -1;
+}
+
+constexpr int kRunTokens = 64;       // positions of a run, or a page where that is longer
+
+// Grid (units, head groups, 2): unit u = the u-th (sequence, run) that the step touches, in
 // order; kPar heads at a time, every gridDim.y-th such set; z: K or V.  D / 8 threads share a
-// row; a thread holds kHold chunks of eight values of each head.
+// row; a thread holds kHold chunks of eight values of each head: those of rows r_in,
+// r_in + kRows, ... of the run.  A warp's rows of one chunk lie in one page.
 template <typename T, int D, int kPage>
 __global__ void __launch_bounds__(kAppendThreads) page_append_kernel(AppendArgs p) {
+  constexpr int kRun = kPage > kRunTokens ? kPage : kRunTokens;
   constexpr int kLanes = D / 8;                              // threads of one row
-  constexpr int kRows = kAppendThreads / kLanes;             // rows of one pass
-  constexpr int kHold = (kPage + kRows - 1) / kRows;         // passes over a page
+  constexpr int kRows = kAppendThreads / kLanes;             // rows of one pass: 16 or 32
+  constexpr int kHold = kRun / kRows;                        // passes over a run
   constexpr int kPar = kHold >= 4 ? 1 : 4 / kHold;           // heads held at a time
-  __shared__ float s_max[kPar][kAppendThreads / 32];
-  const int tid = threadIdx.x, z = blockIdx.z;
-  PageRows u;
-  if (!find_page(p, u)) return;
-  const int off0 = u.off, n = u.n;
+  constexpr int kMerge = kPage > kRows ? kPage / kRows : 1;  // passes of one page
+  constexpr int kMax = kHold / kMerge;                       // maxima of a thread
+  constexpr int kWarps = kPage < kRows ? kAppendThreads / 32 * kPage / kRows : kAppendThreads / 32;   // of a page
+  __shared__ __align__(16) uint32_t s_max[kPar][kMax][kAppendThreads / 32];
+  __shared__ int s_id[kRun / kPage];
+  const int tid = threadIdx.x, z = blockIdx.z, warp = tid >> 5;
+  Run u;
+  if (!find_run(p, __builtin_ctz(kRun), u)) return;
+  if (tid < kRun / kPage) {
+    const bool touched = tid * kPage < u.hi && (tid + 1) * kPage > u.lo;
+    s_id[tid] = touched ? page_id(p, u.seq, u.run * (kRun / kPage) + tid) : -1;
+  }
+  __syncthreads();
   const int lane = tid % kLanes, r_in = tid / kLanes;
-  const T* rows = static_cast<const T*>(p.x[z]) + (int64_t)u.row * p.st[z].row + lane * 8;
+  // of chunk i: its row of the run, its page of the run, whether it is new and its page there
+  auto row_of = [&](int i) { return i * kRows + r_in; };
+  auto page_of = [&](int i) { return row_of(i) / kPage; };
+  int id[kHold];
+#pragma unroll
+  for (int i = 0; i < kHold; ++i) id[i] = row_of(i) >= u.lo && row_of(i) < u.hi ? s_id[page_of(i)] : -1;
+  // only the first page can hold earlier rows
+  const int first = u.lo / kPage, before = u.lo % kPage, first_id = s_id[first];
+  const T* rows = static_cast<const T*>(p.x[z]) + ((int64_t)u.row - u.lo) * p.st[z].row + lane * 8;
   for (int h0 = blockIdx.y * kPar; h0 < p.N; h0 += gridDim.y * kPar) {
-    const int64_t head = (int64_t)u.page * p.N + h0;
-    float held[kPar], amax[kPar];
+    float held[kPar];
+    uint32_t amax[kPar][kMax];
     Chunk<T> c[kPar][kHold];
 #pragma unroll
     for (int g = 0; g < kPar; ++g) {
-      held[g] = off0 > 0 && h0 + g < p.N ? p.scale[z][head + g] : 0.f;
+      held[g] = before > 0 && first_id >= 0 && h0 + g < p.N ? p.scale[z][(int64_t)first_id * p.N + h0 + g] : 0.f;
       const T* x = rows + (int64_t)(h0 + g) * p.st[z].head;
 #pragma unroll
       for (int i = 0; i < kHold; ++i)
-        if (h0 + g < p.N && i * kRows + r_in < n) c[g][i].load(x + (int64_t)(i * kRows + r_in) * p.st[z].row);
+        if (h0 + g < p.N && id[i] >= 0) c[g][i].load(x + (int64_t)row_of(i) * p.st[z].row);
     }
 #pragma unroll
     for (int g = 0; g < kPar; ++g) {
-      amax[g] = 0.f;
 #pragma unroll
-      for (int i = 0; i < kHold; ++i)
-        if (h0 + g < p.N && i * kRows + r_in < n) amax[g] = fmaxf(amax[g], c[g][i].finite_max());
+      for (int m = 0; m < kMax; ++m) {
+        uint32_t x = 0;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) amax[g] = fmaxf(amax[g], __shfl_xor_sync(0xffffffffu, amax[g], o));
+        for (int i = m * kMerge; i < (m + 1) * kMerge; ++i)
+          if (h0 + g < p.N && id[i] >= 0) x = max(x, c[g][i].finite_max());
+        amax[g][m] = __reduce_max_sync(0xffffffffu, x);
+      }
     }
     __syncthreads();                 // the last heads' maxima have been read
     if ((tid & 31) == 0) {
 #pragma unroll
-      for (int g = 0; g < kPar; ++g) s_max[g][tid >> 5] = amax[g];
+      for (int g = 0; g < kPar; ++g)
+#pragma unroll
+        for (int m = 0; m < kMax; ++m) s_max[g][m][warp] = amax[g][m];
     }
     __syncthreads();                 // every thread has read the held scales
 #pragma unroll
     for (int g = 0; g < kPar; ++g) {
       if (h0 + g >= p.N) break;
 #pragma unroll
-      for (int i = 0; i < kAppendThreads / 32; ++i) amax[g] = fmaxf(amax[g], s_max[g][i]);
-      const float need = pow2i(scale_exponent(amax[g]));
-      const float s = held[g] > need ? held[g] : need;
-      const float inv = 1.f / s;     // a power of two: exact
-      uint8_t* codes = p.codes[z] + ((head + g) << p.shift) * D + lane * 8;
-      if (tid == 0) p.scale[z][head + g] = s;
+      for (int m = 0; m < kMax; ++m) {
+        uint32_t x = 0;
 #pragma unroll
-      for (int i = 0; i < kHold; ++i)
-        if (i * kRows + r_in < n)
-          *reinterpret_cast<uint2*>(codes + (int64_t)(off0 + i * kRows + r_in) * D) = c[g][i].codes(inv);
-      if (held[g] > 0.f && held[g] < s)
-        for (int r = r_in; r < off0; r += kRows) rescale8(codes + (int64_t)r * D, held[g] / s);
+        for (int w = 0; w < kWarps; w += 4) {
+          const uint4 y = *reinterpret_cast<const uint4*>(&s_max[g][m][warp / kWarps * kWarps + w]);
+          x = max(max(max(x, y.x), max(y.y, y.z)), y.w);
+        }
+        const int page = page_of(m * kMerge), pid = s_id[page];
+        if (pid < 0) continue;
+        const bool grows = page == first && before > 0;
+        const float need = pow2i(scale_exponent(x));
+        const float s = grows && held[g] > need ? held[g] : need;
+        const float inv = 1.f / s;   // a power of two: exact
+        const int64_t head = (int64_t)pid * p.N + h0 + g;
+        uint8_t* codes = p.codes[z] + (head * kPage) * D + lane * 8;
+        if (row_of(m * kMerge) % kPage == 0 && lane == 0) p.scale[z][head] = s;
+#pragma unroll
+        for (int i = m * kMerge; i < (m + 1) * kMerge; ++i)
+          if (id[i] >= 0)
+            *reinterpret_cast<uint2*>(codes + (int64_t)(row_of(i) % kPage) * D) = c[g][i].codes(inv);
+        if (grows && held[g] > 0.f && held[g] < s)
+          for (int r = row_of(m * kMerge) % kPage; r < before; r += kRows < kPage ? kRows : kPage)
+            rescale8(codes + (int64_t)r * D, held[g] / s);
+      }
     }
   }
 }
@@ -451,32 +490,33 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kAppendThreads) page_append_narrow_kernel(AppendArgs p) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;         // rows of one pass of a warp
   const int tid = threadIdx.x, z = blockIdx.z, h = blockIdx.y * (kAppendThreads / 32) + (tid >> 5);
-  PageRows u;
-  if (!find_page(p, u) || h >= p.N) return;
-  const int lane = tid % kLanes, r_in = (tid & 31) / kLanes;
-  const int64_t head = (int64_t)u.page * p.N + h;
+  Run u;
+  if (!find_run(p, p.shift, u) || h >= p.N) return;
+  const int id = page_id(p, u.seq, u.run);
+  if (id < 0) return;
+  const int lane = tid % kLanes, r_in = (tid & 31) / kLanes, n = u.hi - u.lo;
+  const int64_t head = (int64_t)id * p.N + h;
   const T* x = static_cast<const T*>(p.x[z]) + (int64_t)u.row * p.st[z].row + (int64_t)h * p.st[z].head + lane * 8;
-  const float held = u.off > 0 ? p.scale[z][head] : 0.f;
+  const float held = u.lo > 0 ? p.scale[z][head] : 0.f;
   Chunk<T> c;
-  float amax = 0.f;
-  for (int r = r_in; r < u.n; r += kRows) {
+  uint32_t amax = 0;
+  for (int r = r_in; r < n; r += kRows) {
     c.load(x + (int64_t)r * p.st[z].row);
-    amax = fmaxf(amax, c.finite_max());
+    amax = max(amax, c.finite_max());
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  amax = __reduce_max_sync(0xffffffffu, amax);
   const float need = pow2i(scale_exponent(amax));
   const float s = held > need ? held : need;
   const float inv = 1.f / s;
   uint8_t* codes = p.codes[z] + (head << p.shift) * D + lane * 8;
   __syncwarp();                      // every lane has read the held scale
   if ((tid & 31) == 0) p.scale[z][head] = s;
-  for (int r = r_in; r < u.n; r += kRows) {
-    if (u.n > kRows) c.load(x + (int64_t)r * p.st[z].row);   // else still held
-    *reinterpret_cast<uint2*>(codes + (int64_t)(u.off + r) * D) = c.codes(inv);
+  for (int r = r_in; r < n; r += kRows) {
+    if (n > kRows) c.load(x + (int64_t)r * p.st[z].row);   // else still held
+    *reinterpret_cast<uint2*>(codes + (int64_t)(u.lo + r) * D) = c.codes(inv);
   }
   if (held > 0.f && held < s)
-    for (int r = r_in; r < u.off; r += kRows) rescale8(codes + (int64_t)r * D, held / s);
+    for (int r = r_in; r < u.lo; r += kRows) rescale8(codes + (int64_t)r * D, held / s);
 }
 
 int log2_block(int block_tokens) {
@@ -487,9 +527,18 @@ int log2_block(int block_tokens) {
 
 bool block_ok(int b) { return b == 16 || b == 32 || b == 64 || b == 128; }
 
+// Runs that a step can touch: a sequence's rows touch at most (rows - 2) / length + 2, and no
+// more than its rows.
+int64_t touched_runs(const AppendArgs& a, int length) {
+  const int64_t bound = (int64_t)a.n_rows / length + 2 * (int64_t)a.batch;
+  return bound < a.n_rows ? bound : a.n_rows;
+}
+
 template <typename T, int D, int kPage>
-void launch_page(const AppendArgs& a, int64_t units, int sms, cudaStream_t s) {
-  constexpr int kHold = (kPage * D / 8 + kAppendThreads - 1) / kAppendThreads, kPar = kHold >= 4 ? 1 : 4 / kHold;
+void launch_page(const AppendArgs& a, int sms, cudaStream_t s) {
+  constexpr int kRun = kPage > kRunTokens ? kPage : kRunTokens;
+  constexpr int kHold = kRun * D / 8 / kAppendThreads, kPar = kHold >= 4 ? 1 : 4 / kHold;
+  const int64_t units = touched_runs(a, kRun);
   // head groups: as few heads a CTA as make kAppendCtas CTAs an SM
   const int64_t groups = (int64_t)kAppendCtas * sms / (2 * units) + 1, most = ceil_div(a.N, kPar);
   page_append_kernel<T, D, kPage><<<dim3((unsigned)units, (unsigned)(groups < most ? groups : most), 2),
@@ -497,18 +546,18 @@ void launch_page(const AppendArgs& a, int64_t units, int sms, cudaStream_t s) {
 }
 
 template <typename T, int D>
-void launch_append(const AppendArgs& a, int block_tokens, int64_t units, int sms, cudaStream_t s) {
+void launch_append(const AppendArgs& a, int block_tokens, int sms, cudaStream_t s) {
   // up to two rows a sequence on average: a warp a head
   if (a.n_rows <= 2 * a.batch) {
-    const dim3 grid((unsigned)units, (unsigned)ceil_div(a.N, kAppendThreads / 32), 2);
+    const dim3 grid((unsigned)touched_runs(a, block_tokens), (unsigned)ceil_div(a.N, kAppendThreads / 32), 2);
     page_append_narrow_kernel<T, D><<<grid, kAppendThreads, 0, s>>>(a);
     return;
   }
   switch (block_tokens) {
-    case 16: launch_page<T, D, 16>(a, units, sms, s); break;
-    case 32: launch_page<T, D, 32>(a, units, sms, s); break;
-    case 64: launch_page<T, D, 64>(a, units, sms, s); break;
-    default: launch_page<T, D, 128>(a, units, sms, s); break;
+    case 16: launch_page<T, D, 16>(a, sms, s); break;
+    case 32: launch_page<T, D, 32>(a, sms, s); break;
+    case 64: launch_page<T, D, 64>(a, sms, s); break;
+    default: launch_page<T, D, 128>(a, sms, s); break;
   }
 }
 
@@ -641,10 +690,6 @@ extern "C" rkv_status rkv_page_append(const rkv_pages* pages, const rkv_page_tab
   a.N = pages->n_kv_heads;
   a.shift = log2_block(pages->block_tokens);
   a.n_rows = n_rows;
-  // pages a step can touch: a sequence's rows touch at most (rows - 2) / P + 2, and no more
-  // than its rows
-  const int64_t bound = (int64_t)n_rows / pages->block_tokens + 2 * (int64_t)a.batch;
-  const int64_t units = bound < n_rows ? bound : n_rows;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -652,11 +697,11 @@ extern "C" rkv_status rkv_page_append(const rkv_pages* pages, const rkv_page_tab
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int P = pages->block_tokens;
   if (dtype == RKV_F32)
-    pages->head_dim == 128 ? launch_append<float, 128>(a, P, units, sms, s)
-                           : launch_append<float, 64>(a, P, units, sms, s);
+    pages->head_dim == 128 ? launch_append<float, 128>(a, P, sms, s)
+                           : launch_append<float, 64>(a, P, sms, s);
   else
-    pages->head_dim == 128 ? launch_append<__nv_bfloat16, 128>(a, P, units, sms, s)
-                           : launch_append<__nv_bfloat16, 64>(a, P, units, sms, s);
+    pages->head_dim == 128 ? launch_append<__nv_bfloat16, 128>(a, P, sms, s)
+                           : launch_append<__nv_bfloat16, 64>(a, P, sms, s);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? RKV_OK : fail_with(RKV_ECUDA, "page append launch failed: %s", cudaGetErrorString(e));
 }
