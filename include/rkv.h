@@ -500,13 +500,15 @@ rkv_status rkv_page_attention_workspace(const rkv_pages* pages, const rkv_page_t
  *     none (Lk < Lq) gives a zero row (lse -inf).
  *   scale: finite, > 0 (usually 1 / sqrt(D)).
  *   lse (device, fp32) [total_q, n_q_heads] or NULL: log of the sum of exp(scale q.k).
+ *   workspace (device, 16-byte aligned): rkv_prompt_attention_workspace bytes, this call's
+ *     alone while it runs (NULL where that is 0); needs no initialisation.
  * Rows of out past cu_q[batch] are left as they are.  Rows of other sequences and rows past
  * the last one have no effect, whatever they hold.  Within a sequence a NaN or infinity of V
  * reaches rows that see it and may reach up to 255 rows before it (weights of 0 times NaN).
  * Scores are exact bf16 products summed in fp32; the weights enter the second product as
  * bf16; sums are fp32.  batch in [1, 8192]; total_q and total_k at most 2^30.
  * Offsets that decrease or pass total_q / total_k are cut (RKV_FLAG_BAD_INDEX).
- * Errors (nothing launched): RKV_EINVAL, RKV_EALIGN, RKV_ECUDA.
+ * Errors (nothing launched): RKV_EINVAL, RKV_EALIGN, RKV_ECAPACITY (workspace), RKV_ECUDA.
  */
 typedef struct {
   const void* q;
@@ -519,9 +521,17 @@ typedef struct {
   const int32_t* cu_k;
   int32_t batch, total_q, total_k, n_q_heads, n_kv_heads, head_dim;
   double scale;
+  void* workspace;
+  size_t workspace_bytes;
 } rkv_prompt;
 
 rkv_status rkv_prompt_attention(const rkv_prompt* prompt, int32_t* flags, void* stream);
+
+/*
+ * Workspace of rkv_prompt_attention for these sizes (pointers are not looked at), in *bytes
+ * (host); 0 for calls that need none.  No device work.
+ */
+rkv_status rkv_prompt_attention_workspace(const rkv_prompt* prompt, size_t* bytes);
 
 /* ---------------------------------------------------------------------------
  * Instrumentation (not part of the method).

@@ -93,6 +93,7 @@ ABI_FUNCTIONS = {
                                   ctypes.c_size_t, _P, _P]),
     "rkv_page_attention_workspace": (_I32, [_P, _P, _I32, ctypes.POINTER(ctypes.c_size_t)]),
     "rkv_prompt_attention": (_I32, [_P, _P, _P]),
+    "rkv_prompt_attention_workspace": (_I32, [_P, ctypes.POINTER(ctypes.c_size_t)]),
 }
 
 _lib = None

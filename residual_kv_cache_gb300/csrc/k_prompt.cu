@@ -4,19 +4,33 @@
 // works on two tiles of 128 query rows that read the same key/value head, so that the tensor
 // core always has one tile's products while the other tile's softmax runs:
 //   S_t = Q_t K^T   [128 rows x 128 keys] in TMEM, thread r of softmax group t owns row r
-//   P_t = 2^(c s - c m) as bf16 over S_t in TMEM
+//   P_t = 2^(c s - m) as bf16 in TMEM, m per row
 //   O_t += P_t V    A = P_t from TMEM, V an MN-major B; accumulated in TMEM
 // tcgen05 products execute in issue order, and a commit covers everything issued before it:
-// S_t of key tile j is complete only when P_t V of tile j - 1 is, so one barrier a tile
-// tells its group both.  No reduction crosses threads.  m is the row's maximum over some
-// earlier tiles: it is raised (sum and accumulator rescaled) only when a score exceeds it
-// by 2^8, so most tiles rescale nothing.  Sums are fp32 over the unrounded weights.
+// with P_t over S_t (D = 128), S_t of key tile j is complete only when P_t V of tile j - 1
+// is, so one barrier a tile tells its group both.  With D = 64 there is room for P_t beside
+// S_t, and the next S_t is computed as soon as this one has been read.
+//
+// What bounds the loop is the chain from S_t over P_t to the next S_t (with D = 128: softmax,
+// P V, Q K^T and two hand-overs of some 350 cycles, where the two tiles' products take 2048
+// cycles a key tile).  So the softmax is short: no reduction crosses threads, and no maximum
+// is taken in the usual tile.  m is the maximum over the first tile's keys; a bf16 weight has
+// the range of an fp32, and nothing is lost while weights grow past 1.  Only when a row's
+// weights of 64 keys sum to more than 2^24 is m raised to the scores' maximum, the sum and the
+// accumulator rescaled and the half tile done again.  P_t is handed over in halves of 64
+// keys, so that its product starts on the first.  Sums are fp32 over the unrounded weights.
 //
 // Row tiles of one sequence and key/value head are numbered r = q_tile G + head and taken
 // in consecutive pairs, so that both need the same keys (or one tile more): with an even G
-// two heads of one query tile, with G = 1 two neighbouring query tiles.  One CTA an SM walks
-// the pairs of all sequences, longest rows of a sequence first, in alternating directions,
-// so that its shares of long and short pairs even out.
+// two heads of one query tile, with G = 1 two neighbouring query tiles.  One CTA an SM works
+// through pairs:
+//   * where there are several for each CTA, it takes every gridDim-th pair of the list
+//     (longest rows of a sequence first, heads fastest) in alternating directions, so that
+//     shares of long and short pairs even out and the CTAs at work read the same keys;
+//   * where there are few, all key tiles of all pairs are cut into equal contiguous shares,
+//     and a pair that lies in several shares is joined from fp32 partials (m, l, O) by a
+//     second kernel, in their order (three chunks of up to 500 queries over up to 4100 keys,
+//     16 heads of 64: 37 us whole, @@ us in shares).
 //
 // Packed rows: a tile's rows behind its sequence are other sequences' rows.  Their queries
 // fill lanes whose results are not stored; their keys are masked by position; their values
@@ -34,8 +48,8 @@ namespace {
 constexpr int kRows = 128;                 // query rows of a tile
 constexpr int kKeys = 128;                 // keys of a tile
 constexpr int kPrThreads = 384;
-constexpr int kItems = 2;                  // work items held ahead
-constexpr float kPrRaise = 8.f;
+constexpr int kItems = 3;                  // work items held ahead
+constexpr float kPrRaise = 16777216.f;     // 2^24: a row's weights of 64 keys may sum to it
 
 // Two row tiles of one sequence and key/value head.
 struct Item {
@@ -44,7 +58,18 @@ struct Item {
   int row[2], rows[2];                     // first row of q / out, rows of the tile (0: none)
   int head[2];                             // query head
   int lim[2];                              // keys that the tile's row 0 sees (may be <= 0)
-  int n[2];                                // key tiles; n[0] <= n[1]
+  int j0, n[2];                            // key tiles [j0, n[t]); n[0] <= n[1]
+  int slot;                                // partial in the workspace, or -1: all keys
+};
+
+constexpr int kPrMaxCtas = 160;            // CTAs of a launch (two partials each)
+constexpr int kFewPairs = 4;               // fewer pairs a CTA than this: equal shares
+constexpr int kMinShare = 8;               // key tiles (of one row tile) that are worth a CTA
+
+// What the joining kernel has to know of a partial.
+struct Partial {
+  int valid, last;                         // last: it ends its pair
+  int row[2], rows[2], head[2];
 };
 
 struct PrArgs {
@@ -55,13 +80,195 @@ struct PrArgs {
   int32_t* flags;
   int batch, total_q, total_k, Hq, N, G;
   float scale_log2;
+  int split;                               // equal shares; else whole pairs
+  Partial* info;                           // [2 grid]: a CTA's continued pair, its unfinished one
+  float *pm, *pl, *po;                     // [2 grid][2][128], .., [2 grid][2][128][D]
 };
+
+// The key tiles of one sequence's row tiles, in closed form.
+struct Seq {
+  int q0, lq, k0, lk, nq, c, G;
+  __device__ __forceinline__ Seq(int q0_, int lq_, int k0_, int lk_, int G_)
+      : q0(q0_), lq(lq_), k0(k0_), lk(lk_), G(G_) {
+    nq = (lq + kRows - 1) / kRows;
+    const int off = lk - lq;               // ceil(off / 128)
+    c = off > 0 ? (off + kKeys - 1) / kKeys : -(-off / kKeys);
+  }
+  __device__ __forceinline__ int tiles() const { return nq * G; }
+  __device__ __forceinline__ int pairs() const { return (nq * G + 1) / 2; }
+  // key tiles that query tile qt sees
+  __device__ __forceinline__ int n(int qt) const {
+    return qt == nq - 1 ? (lk + kKeys - 1) / kKeys : max(0, qt + 1 + c);
+  }
+  // sum of n over the query tiles before q, q < nq
+  __device__ __forceinline__ int before(int q) const {
+    const int m = c >= 0 ? q : max(0, q + c);
+    return m * (m + 1) / 2 + (c >= 0 ? q * c : 0);
+  }
+  // sum of n over the row tiles before r
+  __device__ __forceinline__ int prefix(int r) const {
+    if (nq == 0) return 0;
+    const int q = min(r / G, nq - 1);
+    return G * before(q) + (r - q * G) * n(q);
+  }
+  // the pair of row tiles r1 - 1 (where it is >= 0) and r1, of key/value head h
+  __device__ __forceinline__ void item(Item& it, int r0, int r1, int h) const {
+    it.kvh = h;
+    it.k0 = k0, it.lk = lk;
+    it.j0 = 0, it.slot = -1;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int r = t ? r1 : r0, qt = r >= 0 ? r / G : 0;
+      it.row[t] = q0 + qt * kRows;
+      it.rows[t] = r >= 0 ? min(kRows, lq - qt * kRows) : 0;
+      it.head[t] = h * G + (r >= 0 ? r % G : 0);
+      it.lim[t] = lk - lq + qt * kRows + 1;
+      it.n[t] = r >= 0 ? n(qt) : 0;
+    }
+  }
+};
+
+// The sequence of lane i's index (none past the batch): its rows and keys, cut to what there is.
+__device__ __forceinline__ void load_seq(const PrArgs& a, int b, int& q0, int& lq, int& k0, int& lk) {
+  q0 = lq = k0 = lk = 0;
+  if (b >= a.batch) return;
+  const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1], d0 = a.cu_k[b], d1 = a.cu_k[b + 1];
+  q0 = min(max(c0, 0), a.total_q), k0 = min(max(d0, 0), a.total_k);
+  const int q1 = min(max(c1, q0), a.total_q), k1 = min(max(d1, k0), a.total_k);
+  lq = q1 - q0, lk = k1 - k0;
+  if (blockIdx.x == 0 && (q0 != c0 || q1 != c1 || k0 != d0 || k1 != d1)) raise_flag(a.flags, RKV_FLAG_BAD_INDEX);
+}
+
+// Calls emit(item) for CTA blockIdx.x's items in order, until there are no more or it returns
+// false; run by a whole warp.
+template <typename F>
+__device__ __forceinline__ void walk_pairs(const PrArgs& a, F emit) {
+  const int lane = threadIdx.x & 31;
+  int64_t base = 0, round = 0;             // items before sequence b
+  int b = 0, chunk = -1, q0 = 0, lq = 0, k0 = 0, lk = 0;     // lane i: sequence chunk + i
+  while (true) {
+    const int64_t i = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    Item it;
+    it.kvh = -1;
+    while (b < a.batch) {
+      if (chunk != (b & ~31)) {
+        chunk = b & ~31;
+        load_seq(a, chunk + lane, q0, lq, k0, lk);
+      }
+      const int my_pairs = Seq(q0, lq, k0, lk, a.G).pairs();
+      if (b == chunk) {                    // skip the chunk if it ends before i
+        int64_t sum = (int64_t)my_pairs * a.N;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (i >= base + sum) {
+          base += sum;
+          b += 32;
+          continue;
+        }
+      }
+      const int64_t here = (int64_t)__shfl_sync(0xffffffffu, my_pairs, b & 31) * a.N;
+      if (i >= base + here) {
+        base += here;
+        ++b;
+        continue;
+      }
+      const Seq q(__shfl_sync(0xffffffffu, q0, b & 31), __shfl_sync(0xffffffffu, lq, b & 31),
+                  __shfl_sync(0xffffffffu, k0, b & 31), __shfl_sync(0xffffffffu, lk, b & 31), a.G);
+      const int rel = (int)(i - base), r1 = q.tiles() - 1 - 2 * (rel / a.N);   // longest first
+      q.item(it, r1 - 1, r1, rel % a.N);
+      break;
+    }
+    if (!emit(it) || it.kvh < 0) return;
+    ++round;
+  }
+}
+
+template <typename F>
+__device__ __forceinline__ void walk_shares(const PrArgs& a, F emit) {
+  const int lane = threadIdx.x & 31, cta = blockIdx.x;
+  int q0, lq, k0, lk;
+  int total = 0;                           // key tiles of all row tiles (few_pairs: in 32 bits)
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    load_seq(a, b0 + lane, q0, lq, k0, lk);
+    const Seq q(q0, lq, k0, lk, a.G);
+    total += q.prefix(q.tiles()) * a.N;
+  }
+  total = __reduce_add_sync(0xffffffffu, total);
+  const int C = max(1, min((int)gridDim.x, total / kMinShare)), quot = total / C, rest = total % C;
+  const int f0 = cta < C ? quot * cta + rest * cta / C : total;
+  // pairs without keys have no tiles: they belong to the share they begin in, the last
+  // share's end included
+  const int f1 = cta + 1 < C ? quot * (cta + 1) + rest * (cta + 1) / C : total + (cta + 1 == C ? 1 : 0);
+  Partial part[2];
+  part[0].valid = part[1].valid = 0;
+  int base = 0;                            // tiles before sequence b
+  int b = 0, chunk = -1;
+  bool go = f0 < f1;
+  while (go && b < a.batch && base < f1) {
+    if (chunk != (b & ~31)) {
+      chunk = b & ~31;
+      load_seq(a, chunk + lane, q0, lq, k0, lk);
+    }
+    const Seq q(__shfl_sync(0xffffffffu, q0, b & 31), __shfl_sync(0xffffffffu, lq, b & 31),
+                __shfl_sync(0xffffffffu, k0, b & 31), __shfl_sync(0xffffffffu, lk, b & 31), a.G);
+    const int head = q.prefix(q.tiles());
+    // every head's first pair that ends behind f0 or begins at or behind it
+    for (int h = 0; h < a.N && go; ++h, base += head) {
+      if (base + head < f0 || base >= f1) continue;
+      int lo = 0, hi = q.pairs();
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (base + q.prefix(min(2 * mid + 2, q.tiles())) > f0 || base + q.prefix(2 * mid) >= f0) hi = mid;
+        else lo = mid + 1;
+      }
+      for (int p = lo; p < q.pairs() && go; ++p) {
+        const bool two = 2 * p + 1 < q.tiles();
+        const int s = base + q.prefix(2 * p), e = base + q.prefix(min(2 * p + 2, q.tiles()));
+        if (s >= f1) break;
+        Item it;
+        q.item(it, two ? 2 * p : -1, two ? 2 * p + 1 : 2 * p, h);
+        const int n1 = it.n[1];
+        // tiles [f0, f1) of the pair's as a range of its key tiles
+        // (cost = n1 for one tile, else 2 n1 or 2 n1 - 1: x n1 / cost rounded up)
+        const int cost = e - s, x0 = max(f0 - s, 0), x1 = min(f1 - s, cost);
+        const int j0 = two ? (x0 + 1) / 2 : x0, j1 = two ? (x1 + 1) / 2 : x1;
+        if (cost > 0 && j1 <= j0) continue;                  // its few tiles are a neighbour's
+        it.j0 = j0;
+        it.n[0] = min(it.n[0], j1), it.n[1] = j1;
+        if (j0 > 0 || j1 < n1) {
+          const int w = j0 > 0 ? 0 : 1;
+          it.slot = 2 * cta + w;
+          part[w].valid = 1, part[w].last = j1 == n1;
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            part[w].row[t] = it.row[t], part[w].rows[t] = it.rows[t], part[w].head[t] = it.head[t];
+        }
+        go = emit(it);
+      }
+    }
+    ++b;
+  }
+  if (lane == 0) {
+    a.info[2 * cta] = part[0];
+    a.info[2 * cta + 1] = part[1];
+  }
+  if (go || !(f0 < f1)) {
+    Item it;
+    it.kvh = -1;
+    emit(it);
+  }
+}
 
 template <int D>
 struct PrCfg {
   static constexpr uint32_t kTileB = kKeys * D * 2;          // bytes of a Q, K or V tile
-  static constexpr int kSlots = D == 128 ? 5 : 10;           // ring of K and V tiles
-  static constexpr uint32_t kSmem = 1024 + (2 + kSlots) * kTileB;
+  static constexpr int kSlots = D == 128 ? 4 : 8;            // ring of K and V tiles
+  // TMEM columns: S_t at 128 t; O_t at 256 + D t; P_t over S_t, or, where there is room, at
+  // 384 + 64 t, so that the next S_t can be computed while P_t is still in use
+  static constexpr bool kApart = D == 64;
+  static constexpr uint32_t kO = 256, kP = kApart ? 384 : 0, kPStride = kApart ? 64 : 128;
+  static constexpr uint32_t kStage = 32 * 128;               // a warp's rows on their way out
+  static constexpr uint32_t kSmem = 1024 + (2 + kSlots) * kTileB + 8 * kStage;
 };
 
 // A tile of 128 rows x D bf16 as D / 64 blocks of [128 rows x 128 bytes].
@@ -83,10 +290,10 @@ __device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t lbo) {
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
+// Every lane waits (a lane's wait handed on by a shuffle costs some 200 cycles more); the
+// verdict is the warp's.
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
-  const bool ok = warp_wait(bar, parity, abort, status);
-  __syncwarp();
-  return ok;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
 }
 
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
@@ -95,10 +302,36 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
   return r;
+}
+
+// 128 bytes of each of a warp's 32 rows, lane = row, to rows `dst`[r] of `live` rows: through
+// the warp's shared memory, so that a store writes whole 128-byte lines (a lane writing its
+// own row touches 32 lines a store: an item's results took 5000 cycles so).
+template <typename F>
+__device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t* w, int live, F dst) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();                                              // the last rows have been read
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+        make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int r = 4 * k + (lane >> 3), c = lane & 7;
+    const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
+    if (r < live) *reinterpret_cast<uint4*>(dst(r) + c * 16) = v;
+  }
 }
 
 template <int D>
@@ -110,8 +343,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   extern __shared__ uint8_t raw[];
   uint8_t* s_q = align1024(raw);
   uint8_t* s_kv = s_q + 2 * C::kTileB;
-  __shared__ __align__(8) uint64_t kv_full[kSlots], kv_empty[kSlots], q_full, q_empty, s_full[2], p_full[2],
-      o_full[2], i_full[kItems], i_empty[kItems], drain;
+  __shared__ __align__(8) uint64_t kv_full[kSlots], kv_empty[kSlots], q_full, q_empty, s_full[2], s_empty[2],
+      p_half[2], p_full[2], p_empty[2], p_mid[2], o_full[2], i_full[kItems], i_empty[kItems], drain;
   __shared__ Item items[kItems];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_status;
@@ -125,7 +358,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     tma_prefetch(&tm_v);
     for (int i = 0; i < kSlots; ++i) mbar_init(&kv_full[i], 1), mbar_init(&kv_empty[i], 1);
     mbar_init(&q_full, 1), mbar_init(&q_empty, 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_full[i], 128), mbar_init(&o_full[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1), mbar_init(&s_empty[i], 4), mbar_init(&p_half[i], 128);
+      mbar_init(&p_full[i], 128), mbar_init(&p_empty[i], 1), mbar_init(&p_mid[i], 1);
+      mbar_init(&o_full[i], 1);
+    }
     for (int i = 0; i < kItems; ++i) mbar_init(&i_full[i], 1), mbar_init(&i_empty[i], 10);
     mbar_init(&drain, 1);
     s_abort = 0;
@@ -155,12 +392,13 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           mbar_arrive(&i_empty[s]);
           if (it.kvh < 0) break;
           if (it.n[1] == 0) continue;
+          const bool both = it.n[0] > it.j0;
           if (!(ok = mbar_wait(&q_empty, q_ph, abort, status))) break;
           q_ph ^= 1u;
-          mbar_arrive_expect_tx(&q_full, (it.n[0] > 0 ? 2 : 1) * C::kTileB);
-          if (it.n[0] > 0) load_tile<D>(s_q, &tm_q, &q_full, it.head[0], it.row[0]);
+          mbar_arrive_expect_tx(&q_full, (both ? 2 : 1) * C::kTileB);
+          if (both) load_tile<D>(s_q, &tm_q, &q_full, it.head[0], it.row[0]);
           load_tile<D>(s_q + C::kTileB, &tm_q, &q_full, it.head[1], it.row[1]);
-          for (int j = 0; j < 2 * it.n[1]; ++j) {            // K 0, V 0, K 1, V 1, ...
+          for (int j = 2 * it.j0; j < 2 * it.n[1]; ++j) {            // K 0, V 0, K 1, V 1, ...
             if (!(ok = mbar_wait(&kv_empty[kv.stage], kv.phase ^ 1u, abort, status))) break;
             mbar_arrive_expect_tx(&kv_full[kv.stage], C::kTileB);
             load_tile<D>(s_kv + kv.stage * C::kTileB, (j & 1) ? &tm_v : &tm_k, &kv_full[kv.stage], it.kvh,
@@ -185,11 +423,17 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         constexpr uint32_t id_s = idesc_bf16_f32(128, kKeys);
         constexpr uint32_t id_o = idesc_bf16_f32(128, D) | (1u << 16);
         Ring kv;                                             // the next slot to be used
-        uint32_t q_ph = 0, p_ph[2] = {0, 0};
+        uint32_t q_ph = 0, p_ph[2] = {0, 0}, s_ph[2] = {1, 1};
         bool ok = true;
         const uint32_t q_sm = smem_u32(s_q), kv_sm = smem_u32(s_kv);
         // S_t = Q_t K^T
         auto qk = [&](int t, int slot) {
+          if (C::kApart) {                                   // the last S_t has been read
+            ok = ok && mbar_wait(&s_empty[t], s_ph[t], abort, status);
+            s_ph[t] ^= 1u;
+            if (!ok) return;
+            tc_fence_after();
+          }
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
             const uint32_t off = (uint32_t)(i >> 2) * (kKeys * 128) + (uint32_t)(i & 3) * 32;
@@ -198,16 +442,25 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           }
           umma_commit(&s_full[t]);
         };
-        // O_t (+)= P_t V
+        // O_t (+)= P_t V, half the keys at a time as P_t comes
         auto pv = [&](int t, int slot, bool acc) {
 #pragma unroll
-          for (int i = 0; i < kKeys / 16; ++i)
-            umma_bf16_ta(tmem + 256 + t * 128, tmem + t * 128 + i * 8,
-                         sdesc_mn(kv_sm + slot * C::kTileB + i * 2048, kKeys * 128), id_o, acc || i > 0);
+          for (int h = 0; h < 2; ++h) {
+            ok = ok && mbar_wait(h ? &p_full[t] : &p_half[t], p_ph[t], abort, status);
+            if (!ok) return;
+            tc_fence_after();
+#pragma unroll
+            for (int i = 4 * h; i < 4 * h + 4; ++i)
+              umma_bf16_ta(tmem + C::kO + t * D, tmem + C::kP + t * C::kPStride + i * 8,
+                           sdesc_mn(kv_sm + slot * C::kTileB + i * 2048, kKeys * 128), id_o, acc || i > 0);
+            if (h == 0) umma_commit(&p_mid[t]);
+          }
+          p_ph[t] ^= 1u;
+          if (C::kApart) umma_commit(&p_empty[t]);
         };
         for (int s = 0, ph = 0; ok; s == kItems - 1 ? (s = 0, ph ^= 1) : ++s) {
           if (!(ok = mbar_wait(&i_full[s], ph, abort, status))) break;
-          const int kvh = items[s].kvh, n0 = items[s].n[0], n1 = items[s].n[1];
+          const int kvh = items[s].kvh, n0 = items[s].n[0], n1 = items[s].n[1], j0 = items[s].j0;
           mbar_arrive(&i_empty[s]);
           if (kvh < 0) break;
           if (n1 == 0) continue;
@@ -215,30 +468,51 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           q_ph ^= 1u;
           if (!(ok = mbar_wait(&kv_full[kv.stage], kv.phase, abort, status))) break;
           tc_fence_after();
-          if (n0 > 0) qk(0, kv.stage);
+          if (n0 > j0) qk(0, kv.stage);
           qk(1, kv.stage);
           umma_commit(&kv_empty[kv.stage]);
-          if (n1 == 1) umma_commit(&q_empty);
+          if (n1 == j0 + 1) umma_commit(&q_empty);
           kv.next(kSlots);
-          for (int j = 0; j < n1 && ok; ++j) {
+          for (int j = j0; j < n1 && ok; ++j) {
             const Ring v = kv;                               // V j, then K j + 1
             kv.next(kSlots);
-            if (!(ok = mbar_wait(&kv_full[v.stage], v.phase, abort, status))) break;
-            if (j + 1 < n1 && !(ok = mbar_wait(&kv_full[kv.stage], kv.phase, abort, status))) break;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              const int n = t ? n1 : n0;
-              if (j < n) {
-                if (!(ok = mbar_wait(&p_full[t], p_ph[t], abort, status))) break;
-                p_ph[t] ^= 1u;
+            // K j + 1 is done with once the second tile's scores are computed
+            auto next_qk = [&](int t) {
+              if (j + 1 < (t ? n1 : n0)) qk(t, kv.stage);
+              if (t == 1 && j + 1 < n1) {
+                umma_commit(&kv_empty[kv.stage]);
+                if (j + 2 == n1) umma_commit(&q_empty);
+              }
+            };
+            if (C::kApart) {
+              if (j + 1 < n1) {
+                if (!(ok = ok && mbar_wait(&kv_full[kv.stage], kv.phase, abort, status))) break;
                 tc_fence_after();
-                pv(t, v.stage, j > 0);
-                if (t == 1) umma_commit(&kv_empty[v.stage]);
-                if (j + 1 < n) qk(t, kv.stage);
-                else umma_commit(&o_full[t]);
-                if (t == 1 && j + 1 < n1) {
-                  umma_commit(&kv_empty[kv.stage]);
-                  if (j + 2 == n1) umma_commit(&q_empty);
+                next_qk(0);
+                next_qk(1);
+              }
+              if (!(ok = ok && mbar_wait(&kv_full[v.stage], v.phase, abort, status))) break;
+#pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                if (j < (t ? n1 : n0)) {
+                  pv(t, v.stage, j > j0);
+                  if (j + 1 == (t ? n1 : n0)) umma_commit(&o_full[t]);
+                }
+              }
+              umma_commit(&kv_empty[v.stage]);
+            } else {
+              if (!(ok = ok && mbar_wait(&kv_full[v.stage], v.phase, abort, status))) break;
+#pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                if (j < (t ? n1 : n0)) {
+                  pv(t, v.stage, j > j0);
+                  if (t == 1) umma_commit(&kv_empty[v.stage]);
+                  if (t == 0 && j + 1 < n1) ok = ok && mbar_wait(&kv_full[kv.stage], kv.phase, abort, status);
+                  if (t == 1 && j + 1 < n1 && j >= n0)       // tile 0 has not waited for it
+                    ok = ok && mbar_wait(&kv_full[kv.stage], kv.phase, abort, status);
+                  if (!ok) break;
+                  next_qk(t);
+                  if (j + 1 == (t ? n1 : n0)) umma_commit(&o_full[t]);
                 }
               }
             }
@@ -252,131 +526,96 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       }
     } else if (warp == 10) {
       // ------------------------------------------------------------------ work list
-      int64_t base = 0;                                      // items before sequence b
-      int b = 0, chunk = -1;
-      int q0 = 0, lq = 0, k0 = 0, lk = 0;                    // lane i: sequence chunk + i
-      bool ok = true;
-      const int64_t C0 = gridDim.x;
-      int64_t round = 0;
-      for (int s = 0, ph = 1; ok; s == kItems - 1 ? (s = 0, ph ^= 1) : ++s, ++round) {
-        const int64_t i = round * C0 + ((round & 1) ? C0 - 1 - blockIdx.x : blockIdx.x);
-        Item it;
-        it.kvh = -1;
-        while (b < a.batch) {
-          if (chunk != (b & ~31)) {
-            chunk = b & ~31;
-            const int sb = chunk + lane;
-            q0 = lq = k0 = lk = 0;
-            if (sb < a.batch) {
-              const int c0 = a.cu_q[sb], c1 = a.cu_q[sb + 1], d0 = a.cu_k[sb], d1 = a.cu_k[sb + 1];
-              q0 = min(max(c0, 0), a.total_q), k0 = min(max(d0, 0), a.total_k);
-              const int q1 = min(max(c1, q0), a.total_q), k1 = min(max(d1, k0), a.total_k);
-              lq = q1 - q0, lk = k1 - k0;
-              if (blockIdx.x == 0 && (q0 != c0 || q1 != c1 || k0 != d0 || k1 != d1))
-                raise_flag(a.flags, RKV_FLAG_BAD_INDEX);
-            }
-          }
-          const int my_pairs = ((lq + kRows - 1) / kRows * a.G + 1) / 2;
-          if (b == chunk) {                                  // skip the chunk if it ends before i
-            int64_t sum = (int64_t)my_pairs * a.N;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (i >= base + sum) {
-              base += sum;
-              b += 32;
-              continue;
-            }
-          }
-          const int pairs = __shfl_sync(0xffffffffu, my_pairs, b & 31);
-          if (i >= base + (int64_t)pairs * a.N) {
-            base += (int64_t)pairs * a.N;
-            ++b;
-            continue;
-          }
-          const int rel = (int)(i - base);
-          const int LQ = __shfl_sync(0xffffffffu, lq, b & 31), Q0 = __shfl_sync(0xffffffffu, q0, b & 31);
-          it.lk = __shfl_sync(0xffffffffu, lk, b & 31);
-          it.k0 = __shfl_sync(0xffffffffu, k0, b & 31);
-          it.kvh = rel % a.N;
-          const int top = (LQ + kRows - 1) / kRows * a.G - 1 - 2 * (rel / a.N);   // longest first
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const int r = top - 1 + t;
-            const int qt = r >= 0 ? r / a.G : 0;
-            it.row[t] = Q0 + qt * kRows;
-            it.rows[t] = r >= 0 ? min(kRows, LQ - qt * kRows) : 0;
-            it.head[t] = it.kvh * a.G + (r >= 0 ? r % a.G : 0);
-            it.lim[t] = it.lk - LQ + qt * kRows + 1;
-            const int seen = it.lim[t] + it.rows[t] - 1;     // by the tile's last row
-            it.n[t] = it.rows[t] > 0 && seen > 0 ? (seen + kKeys - 1) / kKeys : 0;
-          }
-          break;
-        }
-        if (!(ok = wait_all(&i_empty[s], ph, abort, status))) break;
+      int s = 0;
+      uint32_t ph = 1;
+      auto emit = [&](const Item& it) {
+        if (!wait_all(&i_empty[s], ph, abort, status)) return false;
         if (lane == 0) {
           items[s] = it;
           mbar_arrive(&i_full[s]);
         }
         __syncwarp();
-        if (it.kvh < 0) break;
-      }
+        if (++s == kItems) s = 0, ph ^= 1u;
+        return true;
+      };
+      if (a.split) walk_shares(a, emit);
+      else walk_pairs(a, emit);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // -------------------------------------------------------------------------- softmax
     const int t = warp >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_tm = tmem + t * 128 + lanes, o_tm = tmem + 256 + t * 128 + lanes;
-    uint32_t s_ph = 0, o_ph = 0;
+    const uint32_t s_tm = tmem + t * 128 + lanes, o_tm = tmem + C::kO + t * D + lanes;
+    const uint32_t p_tm = tmem + C::kP + t * C::kPStride + lanes;
+    uint32_t s_ph = 0, o_ph = 0, p_ph = 1, mid_ph = 0;
     Ring kv;                                                 // slot of K j
     const float c = a.scale_log2;
     bool ok = true;
     for (int si = 0, ph = 0; ok; si == kItems - 1 ? (si = 0, ph ^= 1) : ++si) {
       if (!(ok = wait_all(&i_full[si], ph, abort, status))) break;
       const int kvh = items[si].kvh, n = items[si].n[t], n1 = items[si].n[1], lk = items[si].lk;
-      const int row = items[si].row[t], rows = items[si].rows[t], head = items[si].head[t];
+      const int j0 = items[si].j0;
       // keys that this row sees
       const int see = min(items[si].lim[t] + r, lk);
       const int see0 = items[si].lim[t];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&i_empty[si]);
       if (kvh < 0) break;
-      float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < n1; ++j) {
+      float m = -INFINITY, l = 0.f;                          // m in base 2
+      const uint64_t cc = f32x2_pack(c, c);
+      for (int j = j0; j < n1; ++j) {
         kv.next(kSlots);                                     // now V j
         if (j < n) {
           if (!(ok = wait_all(&s_full[t], s_ph, abort, status))) break;
           s_ph ^= 1u;
           tc_fence_after();
-          uint32_t x[128];
+          const bool masked = (j + 1) * kKeys > see0;        // some row does not see every key
+          const int vis = see - j * kKeys;
+          uint32_t xa[32], xb[32], w[32];
+          // scores of keys k .. k + 31 that the row does not see
+          auto mask = [&](uint32_t* x, int k) {
+            if (masked) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_ld32(s_tm + 32 * i, x + 32 * i);
-          tmem_ld_wait();
-          if ((j + 1) * kKeys > see0) {                      // some row does not see every key
-            const int vis = see - j * kKeys;
-#pragma unroll
-            for (int i = 0; i < 128; ++i) x[i] = i < vis ? x[i] : 0xFF800000u;
-          }
-          float mx[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(x[i]);
-#pragma unroll
-          for (int i = 4; i < 128; i += 8) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              mx[e] = fmaxf(mx[e], __uint_as_float(x[i + e]));
-              if (i + 4 + e < 128) mx[e] = fmaxf(mx[e], __uint_as_float(x[i + 4 + e]));
+              for (int e = 0; e < 32; ++e) x[e] = k + e < vis ? x[e] : 0xFF800000u;
             }
-          }
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          const bool raise = top * c > m * c + kPrRaise;     // also from -inf
-          if (__any_sync(0xffffffffu, raise)) {
-            const float mn = raise ? top : m;
-            const float f = raise ? ex2_approx((m - mn) * c) : 1.f;
+          };
+          auto top_of = [&](const uint32_t* x) {
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                mx[u] = max3(mx[u], __uint_as_float(x[e + 2 * u]), __uint_as_float(x[e + 2 * u + 1]));
+            }
+            return max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+          };
+          // weights of 32 keys, and their sum added to two pairs
+          auto weigh = [&](const uint32_t* x, uint32_t* out, uint64_t* sum) {
+            const float z = m == -INFINITY ? 0.f : -m;
+            const uint64_t nm = f32x2_pack(z, z);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float y0, y1;
+              f32x2_unpack(fma2(f32x2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), cc, nm), y0, y1);
+              y0 = ex2_approx(y0);
+              y1 = ex2_approx(y1);
+              sum[i & 1] = f32x2_add(sum[i & 1], f32x2_pack(y0, y1));
+              out[i] = bf16x2(y0, y1);
+            }
+          };
+          auto total = [&](const uint64_t* sum) {
+            float a0, a1;
+            f32x2_unpack(f32x2_add(sum[0], sum[1]), a0, a1);
+            return a0 + a1;
+          };
+          // m becomes the maximum with `top`; what was summed so far is rescaled (`acc`: an
+          // accumulator among it, whose products are complete)
+          auto raise_to = [&](float top, bool acc) {
+            const float mn = fmaxf(m, top * c);
+            const float f = m == mn ? 1.f : ex2_approx(m - mn);
             l *= f;
             m = mn;
-            if (j > 0) {                                     // P V of tile j - 1 is complete
-#pragma unroll
+            if (acc) {
+#pragma unroll 1
               for (int i = 0; i < D / 16; ++i) {
                 uint32_t o[16];
                 tmem_ld16(o_tm + 16 * i, o);
@@ -386,29 +625,51 @@ __global__ void __launch_bounds__(kPrThreads, 1)
                 tmem_st16(o_tm + 16 * i, o);
               }
             }
+          };
+          bool again = j == j0;                              // the first tile's maximum
+          float part;
+          if (!again) {
+            uint64_t sum[2] = {0, 0};
+            tmem_ld32(s_tm, xa);
+            tmem_ld_wait();
+            tmem_ld32(s_tm + 32, xb);
+            mask(xa, 0);
+            weigh(xa, w, sum);
+            tmem_ld_wait();
+            tmem_ld32(s_tm + 64, xa);
+            mask(xb, 32);
+            weigh(xb, w + 16, sum);
+            part = total(sum);
+            again = __any_sync(0xffffffffu, part > kPrRaise);
           }
-          const float mc = m == -INFINITY ? 0.f : m * c;
-          const uint64_t cc = f32x2_pack(c, c), nm = f32x2_pack(-mc, -mc);
-          uint64_t sum[2] = {0, 0};
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t w[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const uint64_t y = fma2(f32x2_pack(__uint_as_float(x[64 * h + 2 * i]),
-                                                 __uint_as_float(x[64 * h + 2 * i + 1])), cc, nm);
-              float y0, y1;
-              f32x2_unpack(y, y0, y1);
-              y0 = ex2_approx(y0);
-              y1 = ex2_approx(y1);
-              sum[i & 1] = f32x2_add(sum[i & 1], f32x2_pack(y0, y1));
-              w[i] = bf16x2(y0, y1);
+          if (C::kApart) {                                   // P V of tile j - 1 is complete
+            if (!(ok = wait_all(&p_empty[t], p_ph, abort, status))) break;
+            p_ph ^= 1u;
+            tc_fence_after();
+          }
+          if (again) {
+            float top = -INFINITY;
+            tmem_ld_wait();
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              tmem_ld32(s_tm + 32 * i, xa);
+              tmem_ld_wait();
+              mask(xa, 32 * i);
+              top = fmaxf(top, top_of(xa));
             }
-            tmem_st32(s_tm + 32 * h, w);
+            raise_to(top, j > j0);
+            uint64_t sum[2] = {0, 0};
+            tmem_ld32(s_tm, xa);
+            tmem_ld32(s_tm + 32, xb);
+            tmem_ld_wait();
+            mask(xa, 0);
+            mask(xb, 32);
+            weigh(xa, w, sum);
+            weigh(xb, w + 16, sum);
+            part = total(sum);
+            tmem_ld32(s_tm + 64, xa);
           }
-          float a0, a1;
-          f32x2_unpack(f32x2_add(sum[0], sum[1]), a0, a1);
-          l += a0 + a1;
+          l += part;
           if ((j + 1) * kKeys > lk) {                        // values behind the sequence
             if (!(ok = wait_all(&kv_full[kv.stage], kv.phase, abort, status))) break;
             if (j * kKeys + r >= lk) {
@@ -421,6 +682,38 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             }
             fence_proxy_async_smem();
           }
+          tmem_st32(p_tm, w);
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&p_half[t]);                           // the product starts on 64 keys
+          {
+            uint64_t sum[2] = {0, 0};
+            tmem_ld_wait();
+            tmem_ld32(s_tm + 96, xb);
+            mask(xa, 64);
+            weigh(xa, w, sum);
+            tmem_ld_wait();
+            if (C::kApart) {
+              tc_fence_before();
+              if (lane == 0) mbar_arrive(&s_empty[t]);
+            }
+            mask(xb, 96);
+            weigh(xb, w + 16, sum);
+            part = total(sum);
+            if (__any_sync(0xffffffffu, part > kPrRaise)) {
+              // the first half's product has to be complete
+              if (!(ok = wait_all(&p_mid[t], mid_ph, abort, status))) break;
+              tc_fence_after();
+              raise_to(fmaxf(top_of(xa), top_of(xb)), true);
+              uint64_t sum2[2] = {0, 0};
+              weigh(xa, w, sum2);
+              weigh(xb, w + 16, sum2);
+              part = total(sum2);
+            }
+          }
+          mid_ph ^= 1u;
+          l += part;
+          tmem_st32(p_tm + 32, w);
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(&p_full[t]);
@@ -429,37 +722,58 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       }
       if (!ok) break;
       // the rows' results
-      const bool live = r < rows;
-      const int64_t at = row + r;
-      __nv_bfloat16* o = a.out + at * a.ost.row + head * a.ost.head;
-      if (n > 0) {
+      const int w0 = (warp & 3) * 32, live = items[si].rows[t] - w0;       // of the warp's rows
+      const int64_t at = items[si].row[t] + w0;
+      const int head = items[si].head[t], slot = items[si].slot;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&i_empty[si]);
+      if (n > j0) {
         if (!(ok = wait_all(&o_full[t], o_ph, abort, status))) break;
         o_ph ^= 1u;
         tc_fence_after();
       }
-      const float inv = l != 0.f ? 1.f / l : 0.f;
+      uint8_t* stage = s_kv + kSlots * C::kTileB + warp * C::kStage;
+      if (slot >= 0) {
+        // a partial: relative to m
+        const int64_t prow = ((int64_t)slot * 2 + t) * kRows + w0;
+#pragma unroll 1
+        for (int i = 0; i < D / 32; ++i) {
+          uint32_t x[32];
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        uint32_t x[32];
-        if (n > 0) {
-          tmem_ld32(o_tm + 32 * i, x);
-          tmem_ld_wait();
-        }
-        if (live) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t w[4];
-#pragma unroll
-            for (int d = 0; d < 4; ++d)
-              w[d] = l != 0.f ? bf16x2(__uint_as_float(x[8 * e + 2 * d]) * inv, __uint_as_float(x[8 * e + 2 * d + 1]) * inv)
-                              : 0u;
-            *reinterpret_cast<uint4*>(o + 32 * i + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int e = 0; e < 32; ++e) x[e] = 0;
+          if (n > j0) {
+            tmem_ld32(o_tm + 32 * i, x);
+            tmem_ld_wait();
           }
+          store_rows(stage, x, live, [&](int row) {
+            return reinterpret_cast<uint8_t*>(a.po + (prow + row) * D + 32 * i);
+          });
         }
+        if (lane < live) a.pm[prow + lane] = m, a.pl[prow + lane] = l;
+      } else {
+        const float inv = l != 0.f ? 1.f / l : 0.f;
+#pragma unroll 1
+        for (int i = 0; i < D / 64; ++i) {
+          uint32_t w[32];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t x[32];
+            if (n > j0) {
+              tmem_ld32(o_tm + 64 * i + 32 * h, x);
+              tmem_ld_wait();
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              w[16 * h + e] = l != 0.f ? bf16x2(__uint_as_float(x[2 * e]) * inv, __uint_as_float(x[2 * e + 1]) * inv) : 0u;
+          }
+          store_rows(stage, w, live, [&](int row) {
+            return reinterpret_cast<uint8_t*>(a.out + (at + row) * a.ost.row + head * a.ost.head + 64 * i);
+          });
+        }
+        if (lane < live && a.lse)
+          a.lse[(at + lane) * a.Hq + head] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
       }
       tc_fence_before();
-      if (live && a.lse)
-        a.lse[at * a.Hq + head] = l != 0.f ? (m * c + log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
   }
   tc_fence_before();
@@ -468,22 +782,85 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   if (warp == 11) tmem_dealloc(tmem, 512);
 }
 
+// Joins the partials of the pair that CTA blockIdx.x began and did not finish: its own, then
+// those of the CTAs after it until one that ends the pair.  Grid (grid, 2 tiles, 4), a warp a
+// row at a time.
+constexpr int kJoinThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PrArgs a, int grid) {
+  constexpr int kE = D / 32;
+  const int c = blockIdx.x, t = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_wait_previous_grid();
+  const Partial own = a.info[2 * c + 1];
+  if (!own.valid || own.last) return;
+  int end = c + 1;
+  while (end < grid && a.info[2 * end].valid && !a.info[2 * end].last) ++end;
+  end = min(end, grid - 1);
+  for (int r = blockIdx.z * kJoinThreads / 32 + warp; r < own.rows[t]; r += gridDim.z * kJoinThreads / 32) {
+    float m = -INFINITY, l = 0.f, o[kE];
+#pragma unroll
+    for (int e = 0; e < kE; ++e) o[e] = 0.f;
+    for (int d = c; d <= end; ++d) {
+      const int64_t i = ((int64_t)(d == c ? 2 * c + 1 : 2 * d) * 2 + t) * kRows + r;
+      const float pm = __ldcg(a.pm + i), pl = __ldcg(a.pl + i);
+      float po[kE];
+      const float* src = a.po + i * D + lane * kE;
+      if (kE == 4) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+        po[0] = v.x, po[1] = v.y, po[kE - 2] = v.z, po[kE - 1] = v.w;
+      } else {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+        po[0] = v.x, po[1] = v.y;
+      }
+      const float mn = fmaxf(m, pm);
+      // a part without keys weighs nothing; NaN stays
+      const float fa = m == -INFINITY ? 0.f : ex2_approx(m - mn), fb = pm == -INFINITY && pl == 0.f ? 0.f : ex2_approx(pm - mn);
+      l = l * fa + pl * fb;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) o[e] = o[e] * fa + po[e] * fb;
+      m = mn;
+    }
+    const int64_t at = own.row[t] + r;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    __nv_bfloat16* dst = a.out + at * a.ost.row + own.head[t] * a.ost.head + lane * kE;
+#pragma unroll
+    for (int e = 0; e < kE; e += 2)
+      *reinterpret_cast<uint32_t*>(dst + e) = l != 0.f ? bf16x2(o[e] * inv, o[e + 1] * inv) : 0u;
+    if (a.lse && lane == 0)
+      a.lse[at * a.Hq + own.head[t]] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  }
+}
+
 template <int D>
 cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PrArgs& a, int grid,
                    int dev, cudaStream_t s) {
   static SmemOptIn opt_in;
-  const cudaError_t e = opt_in(prompt_attention_kernel<D>, PrCfg<D>::kSmem, dev);
+  cudaError_t e = opt_in(prompt_attention_kernel<D>, PrCfg<D>::kSmem, dev);
   if (e != cudaSuccess) return e;
   prompt_attention_kernel<D><<<grid, kPrThreads, PrCfg<D>::kSmem, s>>>(q, k, v, a);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !a.split) return e;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(grid, 2, 4);
+  lc.blockDim = dim3(kJoinThreads);
+  lc.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  e = cudaLaunchKernelEx(&lc, prompt_join_kernel<D>, a, grid);
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-}  // namespace
-}  // namespace rkv
+// Whether the call's pairs are so few that its key tiles are shared out instead.
+bool few_pairs(const rkv_prompt& p) {
+  const int64_t tiles = ((int64_t)p.total_q / kRows + p.batch) * p.n_q_heads;   // at most
+  return p.total_k > 4 * kKeys && p.total_k <= 1 << 26 && tiles < 2 * kFewPairs * kPrMaxCtas;
+}
 
-using namespace rkv;
-
-extern "C" rkv_status rkv_prompt_attention(const rkv_prompt* pr, int32_t* flags, void* stream) {
+rkv_status check_prompt(const rkv_prompt* pr) {
   if (!pr) return fail_with(RKV_EINVAL, "prompt is NULL");
   const rkv_prompt& p = *pr;
   if (p.head_dim != 64 && p.head_dim != 128) return fail_with(RKV_EINVAL, "head_dim must be 64 or 128");
@@ -494,6 +871,27 @@ extern "C" rkv_status rkv_prompt_attention(const rkv_prompt* pr, int32_t* flags,
       (int64_t)p.total_q * p.n_q_heads > (int64_t)1 << 38)
     return fail_with(RKV_EINVAL, "total_q and total_k must be in 0..2^30, total_q * n_q_heads at most 2^38");
   if (!(p.scale > 0.0 && p.scale < 1e30)) return fail_with(RKV_EINVAL, "scale must be finite and > 0");
+  return RKV_OK;
+}
+
+}  // namespace
+}  // namespace rkv
+
+using namespace rkv;
+
+extern "C" rkv_status rkv_prompt_attention_workspace(const rkv_prompt* prompt, size_t* bytes) {
+  if (!bytes) return fail_with(RKV_EINVAL, "bytes is NULL");
+  if (rkv_status st = check_prompt(prompt)) return st;
+  const size_t slots = 2 * kPrMaxCtas, rows = 2 * kRows;
+  *bytes = few_pairs(*prompt)
+               ? slots * (sizeof(Partial) + sizeof(float) * rows * (2 + (size_t)prompt->head_dim))
+               : 0;
+  return RKV_OK;
+}
+
+extern "C" rkv_status rkv_prompt_attention(const rkv_prompt* pr, int32_t* flags, void* stream) {
+  if (rkv_status st = check_prompt(pr)) return st;
+  const rkv_prompt& p = *pr;
   if (p.total_q == 0) return RKV_OK;
   if (!p.q || !p.out || !p.cu_q || !p.cu_k || (p.total_k > 0 && (!p.k || !p.v)))
     return fail_with(RKV_EINVAL, "NULL pointer");
@@ -503,6 +901,11 @@ extern "C" rkv_status rkv_prompt_attention(const rkv_prompt* pr, int32_t* flags,
       return fail_with(RKV_EALIGN, "strides must be >= 0 and multiples of 16 bytes");
   if (!is_aligned(p.q, 16) || !is_aligned(p.k, 16) || !is_aligned(p.v, 16) || !is_aligned(p.out, 16))
     return fail_with(RKV_EALIGN, "q, k, v and out must be 16-byte aligned");
+  size_t need = 0;
+  if (rkv_status st = rkv_prompt_attention_workspace(pr, &need)) return st;
+  if (p.workspace_bytes < need || (need > 0 && !p.workspace))
+    return fail_with(RKV_ECAPACITY, "workspace has %zu of %zu bytes", p.workspace ? p.workspace_bytes : (size_t)0, need);
+  if (!is_aligned(p.workspace, 16)) return fail_with(RKV_EALIGN, "workspace must be 16-byte aligned");
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
@@ -526,9 +929,18 @@ extern "C" rkv_status rkv_prompt_attention(const rkv_prompt* pr, int32_t* flags,
   a.batch = p.batch, a.total_q = p.total_q, a.total_k = p.total_k;
   a.Hq = p.n_q_heads, a.N = p.n_kv_heads, a.G = a.Hq / a.N;
   a.scale_log2 = (float)(p.scale * 1.4426950408889634);
-  // no more CTAs than row tiles there can be
-  const int64_t tiles = ((int64_t)p.total_q / kRows + p.batch) * p.n_q_heads;
-  const int grid = (int)(tiles < sms ? tiles : sms);
+  a.split = need > 0;
+  int grid = sms < kPrMaxCtas ? sms : kPrMaxCtas;
+  if (a.split) {
+    a.po = static_cast<float*>(p.workspace);
+    a.pm = a.po + (size_t)2 * kPrMaxCtas * 2 * kRows * p.head_dim;
+    a.pl = a.pm + 2 * kPrMaxCtas * 2 * kRows;
+    a.info = reinterpret_cast<Partial*>(a.pl + 2 * kPrMaxCtas * 2 * kRows);
+  } else {
+    // no more CTAs than row tiles there can be
+    const int64_t tiles = ((int64_t)p.total_q / kRows + p.batch) * p.n_q_heads;
+    if (tiles < grid) grid = (int)tiles;
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = D == 128 ? launch<128>(mq, mk, mv, a, grid, dev, s) : launch<64>(mq, mk, mv, a, grid, dev, s);
   return e == cudaSuccess ? RKV_OK : fail_with(RKV_ECUDA, "prompt attention launch failed: %s", cudaGetErrorString(e));

@@ -49,7 +49,8 @@ class _Prompt(ctypes.Structure):
                 ("q_strides", _Strides), ("k_strides", _Strides), ("v_strides", _Strides),
                 ("out_strides", _Strides), ("cu_q", _P), ("cu_k", _P), ("batch", _I32),
                 ("total_q", _I32), ("total_k", _I32), ("n_q_heads", _I32), ("n_kv_heads", _I32),
-                ("head_dim", _I32), ("scale", ctypes.c_double)]
+                ("head_dim", _I32), ("scale", ctypes.c_double), ("workspace", _P),
+                ("workspace_bytes", ctypes.c_size_t)]
 
 
 # ------------------------------------------------------------------------------ checks
@@ -283,8 +284,14 @@ def prompt_attention(q, k, v, cu_q, cu_k=None, scale=None, out=None, lse=None, f
     else:
         os_ = _rows(out, "out", q_shape, dev, _BF16)
     a = _Prompt(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse_p, qs, ks, vs, os_, cq, ck,
-                n_cu[0] - 1, Tq, Tk, Hq, N, D, sc)
-    _call(_rkv.lib().rkv_prompt_attention, dev, stream, ctypes.byref(a), _flags(flags, dev))
+                n_cu[0] - 1, Tq, Tk, Hq, N, D, sc, None, 0)
+    lib, nbytes = _rkv.lib(), ctypes.c_size_t()
+    _rkv._check(lib.rkv_prompt_attention_workspace(ctypes.byref(a), ctypes.byref(nbytes)))
+    ws = None
+    if nbytes.value:
+        ws = _new(nbytes.value, _U8, dev, stream)
+        a.workspace, a.workspace_bytes = ws.data_ptr(), nbytes.value
+    _call(lib.rkv_prompt_attention, dev, stream, ctypes.byref(a), _flags(flags, dev))
     return out
 
 

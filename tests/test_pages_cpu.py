@@ -118,7 +118,8 @@ def test_prompt_refusals(lib):
     def call(**kw):
         d = dict(q=A, k=A, v=A, out=A, lse=None, q_strides=S(4096, 128), k_strides=S(1024, 128),
                  v_strides=S(1024, 128), out_strides=S(4096, 128), cu_q=A, cu_k=A, batch=2, total_q=10,
-                 total_k=10, n_q_heads=32, n_kv_heads=8, head_dim=128, scale=0.1)
+                 total_k=10, n_q_heads=32, n_kv_heads=8, head_dim=128, scale=0.1, workspace=None,
+                 workspace_bytes=0)
         d.update(kw)
         p = RP._Prompt(*(d[n] for n, _ in RP._Prompt._fields_))
         return lib.rkv_prompt_attention(ctypes.byref(p), None, None)
@@ -132,6 +133,19 @@ def test_prompt_refusals(lib):
                 dict(v_strides=S(1024, -128)), dict(out_strides=S(4096, 4))):
         assert call(**bad) == -2, bad
     assert call(total_q=0) == 0
+
+    def workspace(**kw):
+        d = dict(total_q=500, total_k=500, n_q_heads=32, n_kv_heads=8, head_dim=128, batch=2, scale=0.1)
+        d.update(kw)
+        p, n = RP._Prompt(**d), ctypes.c_size_t(7)
+        st = lib.rkv_prompt_attention_workspace(ctypes.byref(p), ctypes.byref(n))
+        return n.value if st == 0 else st
+    assert workspace() == 0 and workspace(total_k=5000) > 0 and workspace(head_dim=96) == -1
+    assert lib.rkv_prompt_attention_workspace(None, None) == -1
+    n = workspace(total_q=10, total_k=5000)
+    assert call(total_k=5000) == -3 and call(total_k=5000, workspace=A, workspace_bytes=n - 1) == -3
+    assert call(total_k=5000, workspace=None, workspace_bytes=n) == -3
+    assert call(total_k=5000, workspace=A + 4, workspace_bytes=n) == -2
 
 
 def test_binding_refuses_what_the_library_cannot_see():
