@@ -27,10 +27,9 @@
 //   * where there are several for each CTA, it takes every gridDim-th pair of the list
 //     (longest rows of a sequence first, heads fastest) in alternating directions, so that
 //     shares of long and short pairs even out and the CTAs at work read the same keys;
-//   * where there are few, all key tiles of all pairs are cut into equal contiguous shares,
-//     and a pair that lies in several shares is joined from fp32 partials (m, l, O) by a
-//     second kernel, in their order (three chunks of up to 500 queries over up to 4100 keys,
-//     16 heads of 64: 37 us whole, @@ us in shares).
+//   * where there are fewer pairs than CTAs, and many keys, all key tiles of all pairs are
+//     cut into equal contiguous shares, and a pair that lies in several shares is joined from
+//     fp32 partials (m, l, O) by a second kernel, in their order.
 //
 // Packed rows: a tile's rows behind its sequence are other sequences' rows.  Their queries
 // fill lanes whose results are not stored; their keys are masked by position; their values
@@ -63,7 +62,7 @@ struct Item {
 };
 
 constexpr int kPrMaxCtas = 160;            // CTAs of a launch (two partials each)
-constexpr int kFewPairs = 4;               // fewer pairs a CTA than this: equal shares
+constexpr int kFewCtas = 152, kFewGain = 10;   // (few_pairs)
 constexpr int kMinShare = 8;               // key tiles (of one row tile) that are worth a CTA
 
 // What the joining kernel has to know of a partial.
@@ -141,11 +140,12 @@ __device__ __forceinline__ void load_seq(const PrArgs& a, int b, int& q0, int& l
 
 // Calls emit(item) for CTA blockIdx.x's items in order, until there are no more or it returns
 // false; run by a whole warp.
+// (q0, lq, k0, lk: lane i's sequence i.)
 template <typename F>
-__device__ __forceinline__ void walk_pairs(const PrArgs& a, F emit) {
+__device__ __forceinline__ void walk_pairs(const PrArgs& a, int q0, int lq, int k0, int lk, F emit) {
   const int lane = threadIdx.x & 31;
   int64_t base = 0, round = 0;             // items before sequence b
-  int b = 0, chunk = -1, q0 = 0, lq = 0, k0 = 0, lk = 0;     // lane i: sequence chunk + i
+  int b = 0, chunk = 0;                    // lane i: sequence chunk + i
   while (true) {
     const int64_t i = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     Item it;
@@ -184,12 +184,11 @@ __device__ __forceinline__ void walk_pairs(const PrArgs& a, F emit) {
 }
 
 template <typename F>
-__device__ __forceinline__ void walk_shares(const PrArgs& a, F emit) {
+__device__ __forceinline__ void walk_shares(const PrArgs& a, int q0, int lq, int k0, int lk, F emit) {
   const int lane = threadIdx.x & 31, cta = blockIdx.x;
-  int q0, lq, k0, lk;
   int total = 0;                           // key tiles of all row tiles (few_pairs: in 32 bits)
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    load_seq(a, b0 + lane, q0, lq, k0, lk);
+    if (b0 > 0) load_seq(a, b0 + lane, q0, lq, k0, lk);
     const Seq q(q0, lq, k0, lk, a.G);
     total += q.prefix(q.tiles()) * a.N;
   }
@@ -202,7 +201,7 @@ __device__ __forceinline__ void walk_shares(const PrArgs& a, F emit) {
   Partial part[2];
   part[0].valid = part[1].valid = 0;
   int base = 0;                            // tiles before sequence b
-  int b = 0, chunk = -1;
+  int b = 0, chunk = a.batch <= 32 ? 0 : -1;
   bool go = f0 < f1;
   while (go && b < a.batch && base < f1) {
     if (chunk != (b & ~31)) {
@@ -215,15 +214,21 @@ __device__ __forceinline__ void walk_shares(const PrArgs& a, F emit) {
     // every head's first pair that ends behind f0 or begins at or behind it
     for (int h = 0; h < a.N && go; ++h, base += head) {
       if (base + head < f0 || base >= f1) continue;
-      int lo = 0, hi = q.pairs();
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (base + q.prefix(min(2 * mid + 2, q.tiles())) > f0 || base + q.prefix(2 * mid) >= f0) hi = mid;
-        else lo = mid + 1;
+      int lo = 0, hi = q.pairs();          // 32 places at a time
+      while (lo < hi && base < f0) {
+        const int at = lo + (int)((int64_t)(hi - lo) * lane / 32), r = 2 * at;
+        const uint32_t found = __ballot_sync(0xffffffffu, base + q.prefix(min(r + 2, q.tiles())) > f0 ||
+                                                              base + q.prefix(r) >= f0);
+        const int k = found ? __ffs(found) - 1 : 32;
+        const int above = k > 0 ? __shfl_sync(0xffffffffu, at, k - 1) + 1 : lo;
+        hi = k < 32 ? __shfl_sync(0xffffffffu, at, k & 31) : hi;
+        lo = above;
       }
+      int e = base + q.prefix(2 * lo);
       for (int p = lo; p < q.pairs() && go; ++p) {
         const bool two = 2 * p + 1 < q.tiles();
-        const int s = base + q.prefix(2 * p), e = base + q.prefix(min(2 * p + 2, q.tiles()));
+        const int s = e;
+        e += q.n(2 * p / q.G) + (two ? q.n((2 * p + 1) / q.G) : 0);
         if (s >= f1) break;
         Item it;
         q.item(it, two ? 2 * p : -1, two ? 2 * p + 1 : 2 * p, h);
@@ -314,11 +319,10 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return r;
 }
 
-// 128 bytes of each of a warp's 32 rows, lane = row, to rows `dst`[r] of `live` rows: through
+// 128 bytes of each of a warp's 32 rows, lane = row, to dst + row stride (`live` rows): through
 // the warp's shared memory, so that a store writes whole 128-byte lines (a lane writing its
 // own row touches 32 lines a store: an item's results took 5000 cycles so).
-template <typename F>
-__device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t* w, int live, F dst) {
+__device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t* w, int live, uint8_t* dst, int64_t stride) {
   const int lane = threadIdx.x & 31;
   __syncwarp();                                              // the last rows have been read
 #pragma unroll
@@ -326,11 +330,13 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t* w, in
     *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) =
         make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
   __syncwarp();
+  const int c = lane & 7;
+  dst += (lane >> 3) * stride + c * 16;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int r = 4 * k + (lane >> 3), c = lane & 7;
+  for (int k = 0; k < 8; ++k, dst += 4 * stride) {
+    const int r = 4 * k + (lane >> 3);
     const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
-    if (r < live) *reinterpret_cast<uint4*>(dst(r) + c * 16) = v;
+    if (r < live) *reinterpret_cast<uint4*>(dst) = v;
   }
 }
 
@@ -485,15 +491,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
               }
             };
             if (C::kApart) {
-              if (j + 1 < n1) {
-                if (!(ok = ok && mbar_wait(&kv_full[kv.stage], kv.phase, abort, status))) break;
-                tc_fence_after();
-                next_qk(0);
-                next_qk(1);
-              }
-              if (!(ok = ok && mbar_wait(&kv_full[v.stage], v.phase, abort, status))) break;
+              if (j + 1 < n1 && !(ok = ok && mbar_wait(&kv_full[kv.stage], kv.phase, abort, status))) break;
 #pragma unroll
               for (int t = 0; t < 2; ++t) {
+                next_qk(t);
+                if (t == 0 && !(ok = ok && mbar_wait(&kv_full[v.stage], v.phase, abort, status))) break;
                 if (j < (t ? n1 : n0)) {
                   pv(t, v.stage, j > j0);
                   if (j + 1 == (t ? n1 : n0)) umma_commit(&o_full[t]);
@@ -526,8 +528,9 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       }
     } else if (warp == 10) {
       // ------------------------------------------------------------------ work list
-      int s = 0;
+      int s = 0, q0, lq, k0, lk;
       uint32_t ph = 1;
+      load_seq(a, lane, q0, lq, k0, lk);
       auto emit = [&](const Item& it) {
         if (!wait_all(&i_empty[s], ph, abort, status)) return false;
         if (lane == 0) {
@@ -538,8 +541,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         if (++s == kItems) s = 0, ph ^= 1u;
         return true;
       };
-      if (a.split) walk_shares(a, emit);
-      else walk_pairs(a, emit);
+      if (a.split) walk_shares(a, q0, lq, k0, lk, emit);
+      else walk_pairs(a, q0, lq, k0, lk, emit);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
@@ -626,48 +629,39 @@ __global__ void __launch_bounds__(kPrThreads, 1)
               }
             }
           };
-          bool again = j == j0;                              // the first tile's maximum
           float part;
-          if (!again) {
-            uint64_t sum[2] = {0, 0};
-            tmem_ld32(s_tm, xa);
-            tmem_ld_wait();
-            tmem_ld32(s_tm + 32, xb);
-            mask(xa, 0);
-            weigh(xa, w, sum);
-            tmem_ld_wait();
-            tmem_ld32(s_tm + 64, xa);
-            mask(xb, 32);
-            weigh(xb, w + 16, sum);
-            part = total(sum);
-            again = __any_sync(0xffffffffu, part > kPrRaise);
-          }
           if (C::kApart) {                                   // P V of tile j - 1 is complete
             if (!(ok = wait_all(&p_empty[t], p_ph, abort, status))) break;
             p_ph ^= 1u;
             tc_fence_after();
           }
-          if (again) {
-            float top = -INFINITY;
-            tmem_ld_wait();
+          bool again = j == j0;                              // the first tile's maximum
+          while (true) {
+            if (again) {
+              float top = -INFINITY;
 #pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-              tmem_ld32(s_tm + 32 * i, xa);
-              tmem_ld_wait();
-              mask(xa, 32 * i);
-              top = fmaxf(top, top_of(xa));
+              for (int i = 0; i < 4; ++i) {
+                tmem_ld32(s_tm + 32 * i, xa);
+                tmem_ld_wait();
+                mask(xa, 32 * i);
+                top = fmaxf(top, top_of(xa));
+              }
+              raise_to(top, j > j0);
             }
-            raise_to(top, j > j0);
             uint64_t sum[2] = {0, 0};
             tmem_ld32(s_tm, xa);
-            tmem_ld32(s_tm + 32, xb);
             tmem_ld_wait();
+            tmem_ld32(s_tm + 32, xb);
             mask(xa, 0);
-            mask(xb, 32);
             weigh(xa, w, sum);
+            tmem_ld_wait();
+            tmem_ld32(s_tm + 64, xa);
+            mask(xb, 32);
             weigh(xb, w + 16, sum);
             part = total(sum);
-            tmem_ld32(s_tm + 64, xa);
+            if (again || !__any_sync(0xffffffffu, part > kPrRaise)) break;
+            again = true;
+            tmem_ld_wait();
           }
           l += part;
           if ((j + 1) * kKeys > lk) {                        // values behind the sequence
@@ -686,31 +680,29 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(&p_half[t]);                           // the product starts on 64 keys
-          {
+          tmem_ld_wait();
+          tmem_ld32(s_tm + 96, xb);
+          mask(xa, 64);
+          again = false;
+          while (true) {
             uint64_t sum[2] = {0, 0};
-            tmem_ld_wait();
-            tmem_ld32(s_tm + 96, xb);
-            mask(xa, 64);
             weigh(xa, w, sum);
             tmem_ld_wait();
-            if (C::kApart) {
+            if (C::kApart && !again) {
               tc_fence_before();
-              if (lane == 0) mbar_arrive(&s_empty[t]);
+              if (lane == 0) mbar_arrive(&s_empty[t]);       // S_t is in registers
             }
-            mask(xb, 96);
+            if (!again) mask(xb, 96);
             weigh(xb, w + 16, sum);
             part = total(sum);
-            if (__any_sync(0xffffffffu, part > kPrRaise)) {
-              // the first half's product has to be complete
-              if (!(ok = wait_all(&p_mid[t], mid_ph, abort, status))) break;
-              tc_fence_after();
-              raise_to(fmaxf(top_of(xa), top_of(xb)), true);
-              uint64_t sum2[2] = {0, 0};
-              weigh(xa, w, sum2);
-              weigh(xb, w + 16, sum2);
-              part = total(sum2);
-            }
+            if (again || !__any_sync(0xffffffffu, part > kPrRaise)) break;
+            // the first half's product has to be complete
+            if (!(ok = wait_all(&p_mid[t], mid_ph, abort, status))) break;
+            tc_fence_after();
+            raise_to(fmaxf(top_of(xa), top_of(xb)), true);
+            again = true;
           }
+          if (!ok) break;
           mid_ph ^= 1u;
           l += part;
           tmem_st32(p_tm + 32, w);
@@ -745,30 +737,24 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             tmem_ld32(o_tm + 32 * i, x);
             tmem_ld_wait();
           }
-          store_rows(stage, x, live, [&](int row) {
-            return reinterpret_cast<uint8_t*>(a.po + (prow + row) * D + 32 * i);
-          });
+          store_rows(stage, x, live, reinterpret_cast<uint8_t*>(a.po + prow * D + 32 * i), D * 4);
         }
         if (lane < live) a.pm[prow + lane] = m, a.pl[prow + lane] = l;
       } else {
         const float inv = l != 0.f ? 1.f / l : 0.f;
-#pragma unroll 1
+        uint8_t* dst = reinterpret_cast<uint8_t*>(a.out + at * a.ost.row + head * a.ost.head);
+#pragma unroll
         for (int i = 0; i < D / 64; ++i) {
-          uint32_t w[32];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t x[32];
-            if (n > j0) {
-              tmem_ld32(o_tm + 64 * i + 32 * h, x);
-              tmem_ld_wait();
-            }
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              w[16 * h + e] = l != 0.f ? bf16x2(__uint_as_float(x[2 * e]) * inv, __uint_as_float(x[2 * e + 1]) * inv) : 0u;
+          uint32_t x[64], w[32];
+          if (n > j0) {
+            tmem_ld32(o_tm + 64 * i, x);
+            tmem_ld32(o_tm + 64 * i + 32, x + 32);
+            tmem_ld_wait();
           }
-          store_rows(stage, w, live, [&](int row) {
-            return reinterpret_cast<uint8_t*>(a.out + (at + row) * a.ost.row + head * a.ost.head + 64 * i);
-          });
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            w[e] = l != 0.f ? bf16x2(__uint_as_float(x[2 * e]) * inv, __uint_as_float(x[2 * e + 1]) * inv) : 0u;
+          store_rows(stage, w, live, dst + 128 * i, a.ost.row * 2);
         }
         if (lane < live && a.lse)
           a.lse[(at + lane) * a.Hq + head] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
@@ -783,8 +769,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 }
 
 // Joins the partials of the pair that CTA blockIdx.x began and did not finish: its own, then
-// those of the CTAs after it until one that ends the pair.  Grid (grid, 2 tiles, 4), a warp a
-// row at a time.
+// those of the CTAs after it until one that ends the pair.  Grid (grid, 2 tiles, 8), a warp
+// two rows.
 constexpr int kJoinThreads = 256;
 
 template <int D>
@@ -797,29 +783,46 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PrArgs a, int
   int end = c + 1;
   while (end < grid && a.info[2 * end].valid && !a.info[2 * end].last) ++end;
   end = min(end, grid - 1);
-  for (int r = blockIdx.z * kJoinThreads / 32 + warp; r < own.rows[t]; r += gridDim.z * kJoinThreads / 32) {
+  const int n = end - c + 1;
+  auto slot_of = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
+  for (int r = blockIdx.z * (kJoinThreads / 32) + warp; r < own.rows[t]; r += gridDim.z * (kJoinThreads / 32)) {
     float m = -INFINITY, l = 0.f, o[kE];
 #pragma unroll
     for (int e = 0; e < kE; ++e) o[e] = 0.f;
-    for (int d = c; d <= end; ++d) {
-      const int64_t i = ((int64_t)(d == c ? 2 * c + 1 : 2 * d) * 2 + t) * kRows + r;
-      const float pm = __ldcg(a.pm + i), pl = __ldcg(a.pl + i);
-      float po[kE];
-      const float* src = a.po + i * D + lane * kE;
-      if (kE == 4) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-        po[0] = v.x, po[1] = v.y, po[kE - 2] = v.z, po[kE - 1] = v.w;
-      } else {
-        const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-        po[0] = v.x, po[1] = v.y;
+    for (int i0 = 0; i0 < n; i0 += 32) {                     // lane i: partial i0 + i
+      float pm = -INFINITY, pl = 0.f;
+      if (i0 + lane < n) {
+        const int64_t at = ((int64_t)slot_of(i0 + lane) * 2 + t) * kRows + r;
+        pm = __ldcg(a.pm + at), pl = __ldcg(a.pl + at);
       }
-      const float mn = fmaxf(m, pm);
-      // a part without keys weighs nothing; NaN stays
-      const float fa = m == -INFINITY ? 0.f : ex2_approx(m - mn), fb = pm == -INFINITY && pl == 0.f ? 0.f : ex2_approx(pm - mn);
-      l = l * fa + pl * fb;
+      float top = fmaxf(m, pm);
 #pragma unroll
-      for (int e = 0; e < kE; ++e) o[e] = o[e] * fa + po[e] * fb;
-      m = mn;
+      for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+      // a part without keys weighs nothing; NaN stays
+      const float f = pm == -INFINITY && pl == 0.f ? 0.f : ex2_approx(pm - top);
+      const float fm = m == -INFINITY ? 0.f : ex2_approx(m - top);
+      float add = pl * f;
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1) add += __shfl_xor_sync(0xffffffffu, add, k);
+      l = l * fm + add;
+      m = top;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) o[e] *= fm;
+#pragma unroll 4
+      for (int i = i0; i < min(n, i0 + 32); ++i) {
+        const float w = __shfl_sync(0xffffffffu, f, i - i0);
+        const float* src = a.po + (((int64_t)slot_of(i) * 2 + t) * kRows + r) * D + lane * kE;
+        float po[kE];
+        if (kE == 4) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+          po[0] = v.x, po[1] = v.y, po[kE - 2] = v.z, po[kE - 1] = v.w;
+        } else {
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+          po[0] = v.x, po[1] = v.y;
+        }
+#pragma unroll
+        for (int e = 0; e < kE; ++e) o[e] = fmaf(po[e], w, o[e]);
+      }
     }
     const int64_t at = own.row[t] + r;
     const float inv = l != 0.f ? 1.f / l : 0.f;
@@ -842,7 +845,7 @@ cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap
   e = cudaGetLastError();
   if (e != cudaSuccess || !a.split) return e;
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(grid, 2, 4);
+  lc.gridDim = dim3(grid, 2, kRows / (kJoinThreads / 32) / 2);
   lc.blockDim = dim3(kJoinThreads);
   lc.stream = s;
   cudaLaunchAttribute attr[1];
@@ -855,9 +858,14 @@ cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap
 }
 
 // Whether the call's pairs are so few that its key tiles are shared out instead.
+// Whole pairs take as long as the longest, shares the mean and a join that costs about
+// kFewGain key tiles of a pair (512 queries over 16384 keys, 32 heads: 202 us whole, 108 in
+// shares; one query over 8192 keys 101 and 28; 1024
+// over 1024, 144 pairs, 20 and 32).
 bool few_pairs(const rkv_prompt& p) {
-  const int64_t tiles = ((int64_t)p.total_q / kRows + p.batch) * p.n_q_heads;   // at most
-  return p.total_k > 4 * kKeys && p.total_k <= 1 << 26 && tiles < 2 * kFewPairs * kPrMaxCtas;
+  const int64_t pairs = ((int64_t)p.total_q / kRows + p.batch) * p.n_q_heads / 2;   // at most
+  const int64_t keys = p.total_k / kKeys / p.batch;                                // key tiles, mean
+  return p.total_k <= 1 << 26 && pairs < kFewCtas && (kFewCtas - pairs) * keys > kFewGain * kFewCtas;
 }
 
 rkv_status check_prompt(const rkv_prompt* pr) {
