@@ -355,7 +355,8 @@ PROMPT = [  # lq, lk, Hq, N, D
     ([260], [700], 8, 2, 128), ([5, 1, 130], [400, 257, 130], 7, 1, 64), ([200, 10], [60, 0], 4, 1, 128),
     ([33] * 9, [33] * 9, 5, 1, 128), ([513], [513], 2, 1, 128), ([100, 20], [0, 300], 4, 2, 64),
     ([300], [5000], 2, 1, 128), ([1], [9001], 7, 1, 64), ([100, 0, 64, 300], [0, 90, 3000, 700], 6, 2, 128),
-    ([129, 1, 1, 1], [640, 2000, 1, 300], 3, 1, 64), ([1000], [1000], 5, 1, 64)]
+    ([129, 1, 1, 1], [640, 2000, 1, 300], 3, 1, 64), ([1000], [1000], 5, 1, 64),
+    ([100, 0, 64, 200], [0, 90, 9000, 7000], 6, 2, 128), ([128, 0, 257], [9128, 300, 5000], 2, 2, 64)]
 
 
 def _cu(lens):

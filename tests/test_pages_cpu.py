@@ -140,10 +140,10 @@ def test_prompt_refusals(lib):
         p, n = RP._Prompt(**d), ctypes.c_size_t(7)
         st = lib.rkv_prompt_attention_workspace(ctypes.byref(p), ctypes.byref(n))
         return n.value if st == 0 else st
-    assert workspace() == 0 and workspace(total_k=5000) > 0 and workspace(head_dim=96) == -1
+    assert workspace() == 0 and workspace(total_q=10, total_k=5000) > 0 and workspace(head_dim=96) == -1
     assert lib.rkv_prompt_attention_workspace(None, None) == -1
     n = workspace(total_q=10, total_k=5000)
-    assert call(total_k=5000) == -3 and call(total_k=5000, workspace=A, workspace_bytes=n - 1) == -3
+    assert call(total_k=5000, total_q=10) == -3 and call(total_k=5000, workspace=A, workspace_bytes=n - 1) == -3
     assert call(total_k=5000, workspace=None, workspace_bytes=n) == -3
     assert call(total_k=5000, workspace=A + 4, workspace_bytes=n) == -2
 
