@@ -159,11 +159,9 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// Lane 0 waits; the whole warp is ordered after it.
+// Every lane waits; the verdict is the warp's.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
-  const bool ok = warp_wait(bar, parity, abort, status);
-  __syncwarp();
-  return ok;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
 }
 
 // Whether pred holds in any thread of softmax group g, or of both groups.
