@@ -16,10 +16,10 @@
 //   of that largest, and within 2^-21 of it everywhere; a weight is hi + mid / 16 + lo / 256,
 //   12 significant bits for weights down to 2^-6 and an absolute 2^-18 below.  The products
 //   are exact and the parts are joined in fp32.
-//   Softmax: two groups of 128 threads take a segment's tiles in turn, each with its own
-//   score buffer, weights, sums and accumulator (joined at the segment's end), so that one
-//   group's chain of dependent steps runs beside the other's.  Thread t of a group owns
-//   token t (TMEM lane t).  Scores s are kept in base 2, and a page's
+//   Softmax: two groups of 128 threads take a CTA's tiles in turn, each with its own score
+//   buffer, weights, sums and accumulator, so that one group's chain of dependent steps runs
+//   beside the other's, across the ends of sequences too.  The group of a segment's last tile
+//   joins the other's part to its own.  Thread t of a group owns token t (TMEM lane t).  Scores s are kept in base 2, and a page's
 //   value scale 2^e is folded into the weights: the second product takes 2^(s + e - m), the
 //   sum 2^(s - m).  The reference m of a head is the maximum of s + e over some earlier
 //   tiles, so the parts hold the terms that weigh most, whatever the pages' scales.  It is
@@ -32,16 +32,15 @@
 // o), at most two a CTA, which the second kernel joins in tile order: no atomics, the same
 // bits on every run.
 //
-// Warps: 0 TMA producer, 1 MMA issuer, 2 queries and segment list, 3 idle, 4-7 and 8-11
-// softmax.
+// Warps: 0 TMA producer, 1 MMA issuer, 2 queries and segment list, 3 page scales, 4-7 and
+// 8-11 softmax.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 
 #include <cfloat>
 
-#include "pages.h"
-#include "tc_common.cuh"
+#include "pages.cuh"
 
 namespace rkv {
 namespace {
@@ -52,9 +51,9 @@ constexpr int kSoftWarp0 = 4;
 constexpr int kSlots = 4;                  // segments whose queries are held ahead
 constexpr int kMaxCtas = 256;              // shares of a call (partials in the workspace)
 constexpr int kMaxTilePages = kTile / 16;
-constexpr uint32_t kPaTmemCols = 512;
+constexpr uint32_t kPaTmemCols = 256;
 constexpr uint32_t kSCol = 0, kSStride = 32;      // a score buffer for each group
-constexpr uint32_t kOCol = 64, kOStride = 64;     // accumulators: [segment parity][group]
+constexpr uint32_t kOCol = 64, kOStride = 64;     // an accumulator for each group
 constexpr float kRaise = 8.f;              // weights stay below 2^8
 
 // A run of tiles of one (sequence, head) inside a CTA's share.
@@ -84,9 +83,9 @@ struct PaCfg {
   static constexpr uint32_t kPBytes = 48 * kTile;            // one weight tile
   static constexpr uint32_t kMetaOff = kStages * kStage + kSlots * kQBytes + 2 * kPBytes;
   static constexpr uint32_t kMeta = kStages * kMaxTilePages * 8;   // (k scale, v scale)
-  static constexpr uint32_t kJoinOff = kMetaOff + kMeta;           // second group's o, m, l
+  static constexpr uint32_t kJoinOff = kMetaOff + kMeta;           // a group's o, m, l
   static constexpr uint32_t kJoin = (16 * kTile + 32) * 4;
-  static constexpr uint32_t kSmem = 1024 + kJoinOff + kJoin;
+  static constexpr uint32_t kSmem = 1024 + kJoinOff + 2 * kJoin;
 };
 
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
@@ -117,6 +116,14 @@ struct Shares {
   }
   __device__ __forceinline__ int64_t start(int c) const { return q * c + r * c / C; }
 };
+
+// Pages of a segment's sequence that its tiles reach, and the id of one (-1 past them).
+__device__ __forceinline__ int page_end(const PaArgs& a, const Segment& g) {
+  return min((int)(((int64_t)g.len + (1 << a.shift) - 1) >> a.shift), (g.tile0 + g.tiles) * (kTile >> a.shift));
+}
+__device__ __forceinline__ int page_at(const PaArgs& a, const Segment& g, int page, int end) {
+  return page < end ? __ldg(a.table + (int64_t)g.b * a.max_blocks + page) : -1;
+}
 
 // tcgen05.mma kind::f8f6f4, E4M3 operands in shared memory, fp32 accumulation.
 __device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -159,14 +166,8 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// Every lane waits; the verdict is the warp's.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
-}
-
-// Whether pred holds in any thread of softmax group g, or of both groups.
+// Whether pred holds in any thread of softmax group g.
 __device__ __forceinline__ bool vote_group(int g, bool pred) { return !bar_red_and(1 + g, 128, !pred); }
-__device__ __forceinline__ bool vote_both(bool pred) { return !bar_red_and(3, 256, !pred); }
 
 // kH: query heads computed (G rounded up to 2, 4, 8 or 16).
 template <int D, int kH>
@@ -183,9 +184,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   uint8_t* s_q = sm + kST * C::kStage;
   uint8_t* s_p = s_q + kSlots * C::kQBytes;
   float2* s_meta = reinterpret_cast<float2*>(sm + C::kMetaOff);
-  float* s_join = reinterpret_cast<float*>(sm + C::kJoinOff);
   __shared__ __align__(8) uint64_t full[kST], empty[kST], s_full[2], s_empty[2], p_full[2], p_empty[2],
-      o_full[2], o_empty[2], d_full[kSlots], q_full[kSlots], q_empty[kSlots], drain;
+      j_full[2], j_empty[2], d_full[kSlots], q_full[kSlots], q_empty[kSlots], drain;
   __shared__ Segment seg[kSlots];
   __shared__ float s_qf[kSlots][16];
   __shared__ float s_red[2][4][16];
@@ -203,9 +203,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1), mbar_init(&s_empty[i], 4);
       mbar_init(&p_full[i], 128), mbar_init(&p_empty[i], 1);
-      mbar_init(&o_full[i], 1), mbar_init(&o_empty[i], 8);
+      mbar_init(&j_full[i], 128), mbar_init(&j_empty[i], 128);
     }
-    for (int i = 0; i < kSlots; ++i) mbar_init(&d_full[i], 1), mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 10);
+    for (int i = 0; i < kSlots; ++i) mbar_init(&d_full[i], 1), mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 11);
     mbar_init(&drain, 1);
     s_abort = 0;
     s_b0 = a.batch;
@@ -260,26 +260,28 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     const int P = 1 << a.shift, ppt = kTile >> a.shift;      // pages per tile
     Ring ring;
     int64_t issued = 0;
-    bool ok = true;
+    bool ok = true, ahead = false;
+    int id_ahead = -1;
     for (int s = 0, ph = 0; ok; s == kSlots - 1 ? (s = 0, ph ^= 1) : ++s) {
       if (!(ok = wait_warp(&d_full[s], ph, abort, status))) break;
       const Segment g = seg[s];
       if (g.b < 0) break;
-      const int pages = (g.len + P - 1) >> a.shift;          // of the whole sequence
-      const int end = min((g.tile0 + g.tiles) * ppt, pages);
-      const int32_t* row = a.table + (int64_t)g.b * a.max_blocks;
+      const int end = page_end(a, g);
       // lane i holds page p0 + i: 32 pages, a whole number of tiles
       int p0 = g.tile0 * ppt;
-      int id = p0 + lane < end ? __ldg(row + p0 + lane) : -1;
+      int id = ahead ? id_ahead : page_at(a, g, p0 + lane, end);
+      // the next segment's first pages, if it is known yet
+      const int sn = s == kSlots - 1 ? 0 : s + 1;
+      ahead = __all_sync(0xffffffffu, mbar_test(&d_full[sn], s == kSlots - 1 ? ph ^ 1 : ph));
+      if (ahead) {
+        const Segment gn = seg[sn];
+        id_ahead = gn.b >= 0 ? page_at(a, gn, gn.tile0 * ppt + lane, page_end(a, gn)) : -1;
+      }
       for (int t = 0; t < g.tiles && ok; p0 += 32) {
-        const bool stored = p0 + lane < end, good = stored && id >= 0 && id < a.num_blocks;
+        const bool stored = p0 + lane < end, good = id >= 0 && id < a.num_blocks;
         if (stored && !good) raise_flag(a.flags, RKV_FLAG_BAD_INDEX);
-        const int64_t head = (int64_t)id * a.N + g.h;
-        // a page that is not there has a negative scale
-        float2 sc = make_float2(0.f, -1.f);
-        if (good) sc = make_float2(__ldg(a.ks + head), __ldg(a.vs + head));
-        const int next = p0 + 32 + lane;
-        const int id_next = next < end ? __ldg(row + next) : -1;
+        const int row = (int)(((int64_t)id * a.N + g.h) << a.shift);
+        const int id_next = page_at(a, g, p0 + 32 + lane, end);
         for (int i = 0; i < 32 && t < g.tiles; i += ppt, ++t) {
           if (!(ok = wait_warp(&empty[ring.stage], ring.phase ^ 1u, abort, status))) break;
           uint8_t* st = sm + ring.stage * C::kStage;
@@ -289,13 +291,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           __syncwarp();
           if (here && good) {
             const uint32_t off = (uint32_t)(lane - i) * (uint32_t)(P * D);
-            tma_load_2d(st + off, &tm_v, &full[ring.stage], 0, (int32_t)(head << a.shift));
-            tma_load_2d(st + C::kHalf + off, &tm_k, &full[ring.stage], 0, (int32_t)(head << a.shift));
+            tma_load_2d(st + off, &tm_v, &full[ring.stage], 0, row);
+            tma_load_2d(st + C::kHalf + off, &tm_k, &full[ring.stage], 0, row);
           }
-          // the scales arrive while the copies are under way
-          if (here) s_meta[ring.stage * kMaxTilePages + lane - i] = sc;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full[ring.stage]);
           ring.next(kST);
           ++issued;
         }
@@ -314,53 +312,54 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     if (elect_one()) {
       constexpr uint32_t id_s = idesc_f8(128, kNQ, false), id_o = idesc_f8(128, kNP, true);
       Ring ring, done;                                       // stages of the next S and V products
-      uint32_t s_ph[2] = {1, 1}, p_ph[2] = {0, 0}, n_seg = 0;
+      uint32_t s_ph[2] = {1, 1}, p_ph[2] = {0, 0};
+      uint32_t k = 0, acc = 0;                               // tile; bit g: group g's last tile goes on with a sum
       bool ok = true;
-      for (int s = 0, ph = 0; ok; s == kSlots - 1 ? (s = 0, ph ^= 1) : ++s, ++n_seg) {
-        if (!(ok = mbar_wait(&q_full[s], ph, abort, status))) break;
+      // O_g (+)= V^T P of the tile two before tile k (group k & 1)
+      auto pv = [&]() {
+        const uint32_t g = k & 1u;
+        ok = ok && wait_one(&p_full[g], p_ph[g], abort, status);
+        if (!ok) return;
+        p_ph[g] ^= 1u;
+        tc_fence_after();
+        const uint32_t vt = smem_u32(sm + done.stage * C::kStage);
+        const uint32_t pt = smem_u32(s_p + g * C::kPBytes);
+        // M = 128 lanes; for D = 64 the upper 64 read the K tile behind V and are unused
+#pragma unroll
+        for (int i = 0; i < kTile / 32; ++i)
+          umma_f8(tmem + kOCol + g * kOStride, sdesc_rows<D>(vt + i * 32 * D, C::kHalf),
+                  sdesc_rows<128>(pt + i * 32, 16), id_o, (acc >> g & 1u) || i > 0);
+        umma_commit(&empty[done.stage]);
+        umma_commit(&p_empty[g]);
+        done.next(kST);
+      };
+      for (int s = 0, ph = 0; ok; s == kSlots - 1 ? (s = 0, ph ^= 1) : ++s) {
+        if (!(ok = wait_one(&q_full[s], ph, abort, status))) break;
         if (seg[s].b < 0) break;
         const int tiles = seg[s].tiles;
-        const uint32_t o_tm = tmem + kOCol + (n_seg & 1u) * 2 * kOStride;
-        // the accumulator of the segment before the last has been read
-        if (!(ok = mbar_wait(&o_empty[n_seg & 1u], ((n_seg >> 1) & 1u) ^ 1u, abort, status))) break;
         // a tile's scores are issued as soon as its group has read its last ones, two tiles
         // ahead of the second product
-        for (int t = 0; t < tiles + 2; ++t) {
-          if (t < tiles) {
-            const uint32_t sb = (uint32_t)t & 1u;
-            if (!(ok = mbar_wait(&full[ring.stage], ring.phase, abort, status))) break;
-            if (!(ok = mbar_wait(&s_empty[sb], s_ph[sb], abort, status))) break;
-            s_ph[sb] ^= 1u;
-            tc_fence_after();
-            const uint32_t kt = smem_u32(sm + ring.stage * C::kStage + C::kHalf);
-            const uint32_t qt = smem_u32(s_q + s * C::kQBytes);
+        for (int t = 0; t < tiles && ok; ++t, ++k) {
+          const uint32_t g = k & 1u;
+          if (!(ok = wait_one(&full[ring.stage], ring.phase, abort, status))) break;
+          if (!(ok = wait_one(&s_empty[g], s_ph[g], abort, status))) break;
+          s_ph[g] ^= 1u;
+          tc_fence_after();
+          const uint32_t kt = smem_u32(sm + ring.stage * C::kStage + C::kHalf);
+          const uint32_t qt = smem_u32(s_q + s * C::kQBytes);
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i)
-              umma_f8(tmem + kSCol + sb * kSStride, sdesc_rows<D>(kt + i * 32, 16), sdesc_rows<D>(qt + i * 32, 16),
-                      id_s, i > 0);
-            umma_commit(&s_full[sb]);
-            if (t == tiles - 1) umma_commit(&q_empty[s]);
-            ring.next(kST);
-          }
-          if (t >= 2) {                                      // O += V^T P of tile t - 2
-            const uint32_t pb = (uint32_t)t & 1u;
-            if (!(ok = mbar_wait(&p_full[pb], p_ph[pb], abort, status))) break;
-            p_ph[pb] ^= 1u;
-            tc_fence_after();
-            const uint32_t vt = smem_u32(sm + done.stage * C::kStage);
-            const uint32_t pt = smem_u32(s_p + pb * C::kPBytes);
-            // M = 128 lanes; for D = 64 the upper 64 read the K tile behind V and are unused
-#pragma unroll
-            for (int i = 0; i < kTile / 32; ++i)
-              umma_f8(o_tm + pb * kOStride, sdesc_rows<D>(vt + i * 32 * D, C::kHalf), sdesc_rows<128>(pt + i * 32, 16), id_o,
-                      t >= 4 || i > 0);
-            umma_commit(&empty[done.stage]);
-            umma_commit(&p_empty[pb]);
-            if (t == tiles + 1) umma_commit(&o_full[n_seg & 1u]);
-            done.next(kST);
-          }
+          for (int i = 0; i < D / 32; ++i)
+            umma_f8(tmem + kSCol + g * kSStride, sdesc_rows<D>(kt + i * 32, 16), sdesc_rows<D>(qt + i * 32, 16),
+                    id_s, i > 0);
+          umma_commit(&s_full[g]);
+          if (t == tiles - 1) umma_commit(&q_empty[s]);
+          ring.next(kST);
+          if (k >= 2) pv();
+          acc = t >= 2 ? acc | 1u << g : acc & ~(1u << g);   // the group's first tile of a segment begins
         }
       }
+      for (int i = 0; i < 2 && ok; ++i, ++k)                 // the last two tiles
+        if (k >= 2 && done.stage != ring.stage) pv();
       if (*abort) {
         umma_commit(&drain);
         drain_wait(&drain, 0);
@@ -368,31 +367,45 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     }
   } else if (warp == 2) {
     // ------------------------------------------------- segments and their query tiles
-    int64_t f = f0, pre = f0 < f1 ? s_pref : 0;
-    int b = s_b0, chunk = -1, len_l = 0;                     // lane i: length of sequence chunk + i
+    constexpr int kW = D / 64;                               // words (2 values) per lane and head
+    int64_t left = f1 - f0;                                  // tiles of the share still to come
+    int b = s_b0, h = 0, tile = 0, chunk = -1, len_l = 0;    // lane i: length of sequence chunk + i
     bool first = true, ok = true;
     for (int s = 0, ph = 1; ok; s == kSlots - 1 ? (s = 0, ph ^= 1) : ++s) {
       Segment g{-1, 0, 0, 0, 0, -1};
-      while (f < f1 && g.b < 0 && b < a.batch) {
+      while (left > 0 && b < a.batch) {
         if (chunk != (b & ~31)) {
           chunk = b & ~31;
           bool bad;
           len_l = chunk + lane < a.batch ? length_of(a, chunk + lane, bad) : 0;
         }
-        const int len = __shfl_sync(0xffffffffu, len_l, b & 31);
-        const int nb = tiles_of(len);
-        const int64_t rel = f - pre * a.N;
-        if (rel >= (int64_t)nb * a.N) {
-          pre += nb;
+        g.len = __shfl_sync(0xffffffffu, len_l, b & 31);
+        const int nb = tiles_of(g.len);
+        if (nb == 0) {
           ++b;
           continue;
         }
-        g.b = b, g.len = len;
-        g.h = (int)(rel / nb), g.tile0 = (int)(rel % nb);
-        g.tiles = (int)min((int64_t)(nb - g.tile0), f1 - f);
+        if (first) {                                         // where the share begins
+          const int64_t rel = f0 - s_pref * a.N;
+          h = (int)(rel / nb), tile = (int)(rel % nb);
+        }
+        g.b = b, g.h = h, g.tile0 = tile;
+        g.tiles = (int)min((int64_t)(nb - tile), left);
         g.slot = g.tiles == nb ? -1 : 2 * cta + (first ? 0 : 1);
-        f += g.tiles;
+        left -= g.tiles;
         first = false;
+        tile = 0;
+        if (++h == a.N) h = 0, ++b;
+        break;
+      }
+      uint32_t raw[kH][kW];                                  // loaded while the slot is awaited
+      if (g.b >= 0) {
+        const __nv_bfloat16* q = a.q + g.b * a.qst.row + (int64_t)g.h * a.G * a.qst.head + lane * (2 * kW);
+#pragma unroll
+        for (int i = 0; i < kH; ++i)
+#pragma unroll
+          for (int e = 0; e < kW; ++e)
+            raw[i][e] = i < a.G ? __ldg(reinterpret_cast<const uint32_t*>(q + i * a.qst.head) + e) : 0u;
       }
       if (!(ok = wait_warp(&q_empty[s], ph, abort, status))) break;
       if (lane == 0) {
@@ -400,49 +413,41 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         mbar_arrive(&d_full[s]);                             // the copies need no more
       }
       if (g.b >= 0) {
-        const __nv_bfloat16* q = a.q + g.b * a.qst.row + (int64_t)g.h * a.G * a.qst.head;
         uint8_t* qt = s_q + s * C::kQBytes;
-        constexpr int kE = D / 32;                           // values per lane
-#pragma unroll 4
-        for (int h = 0; h < kH; ++h) {
-          float v[kE];
-          float amax = 0.f;
+        const int col = lane * 2 * kW;
 #pragma unroll
-          for (int e = 0; e < kE; e += 2) {
-            uint32_t u = 0;
-            if (h < a.G) u = *reinterpret_cast<const uint32_t*>(q + h * a.qst.head + lane * kE + e);
-            v[e] = __uint_as_float(u << 16), v[e + 1] = __uint_as_float(u & 0xFFFF0000u);
+        for (int i = 0; i < kH; ++i) {
+          // the largest finite magnitude, on the bits; what is not finite becomes NaN
+          uint32_t m2 = 0;
+#pragma unroll
+          for (int e = 0; e < kW; ++e) {
+            const uint32_t mag = raw[i][e] & 0x7FFF7FFFu;
+            m2 = __vmaxu2(m2, mag & ~__vcmpgeu2(mag, 0x7F807F80u));
+            raw[i][e] |= __vcmpgeu2(mag, 0x7F807F80u) & 0x7FFF7FFFu;
           }
-#pragma unroll
-          for (int e = 0; e < kE; ++e) {
-            if (!(fabsf(v[e]) < INFINITY)) v[e] = NAN;       // an infinity has no product either
-            amax = fmaxf(amax, fabsf(v[e]));
-          }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          const uint32_t amax = __reduce_max_sync(0xffffffffu, max(m2 >> 16, m2 & 0xFFFFu));   // bf16 bits
           // 2^7 <= amax 2^-ex < 2^8
-          const int ex = max((int)(__float_as_uint(amax) >> 23) - 127, -100) - 7;
+          const int ex = max((int)(amax >> 7) - 127, -100) - 7;
           const float mul = __uint_as_float((uint32_t)(127 - ex) << 23);
           uint32_t hi = 0, lo = 0;
 #pragma unroll
-          for (int e = 0; e < kE; e += 2) {
-            const float x = v[e] * mul, y = v[e + 1] * mul;
+          for (int e = 0; e < kW; ++e) {
+            const float x = __uint_as_float(raw[i][e] << 16) * mul, y = __uint_as_float(raw[i][e] & 0xFFFF0000u) * mul;
             const uint32_t c = e4m3x2(x, y);
             const float2 r = from_e4m3x2(c);
-            hi |= c << (8 * e);
-            lo |= e4m3x2((x - r.x) * 16.f, (y - r.y) * 16.f) << (8 * e);
+            hi |= c << (16 * e);
+            lo |= e4m3x2((x - r.x) * 16.f, (y - r.y) * 16.f) << (16 * e);
           }
-          const int col = lane * kE;
-          const uint32_t oh = chunk_off<D>(h, col >> 4) + (col & 15);
-          const uint32_t ol = chunk_off<D>(kGP + h, col >> 4) + (col & 15);
-          if (kE == 4) {
-            *reinterpret_cast<uint32_t*>(qt + oh) = hi;
-            *reinterpret_cast<uint32_t*>(qt + ol) = lo;
+          uint8_t* oh = qt + chunk_off<D>(i, col >> 4) + (col & 15);
+          uint8_t* ol = qt + chunk_off<D>(kGP + i, col >> 4) + (col & 15);
+          if (kW == 2) {
+            *reinterpret_cast<uint32_t*>(oh) = hi;
+            *reinterpret_cast<uint32_t*>(ol) = lo;
           } else {
-            *reinterpret_cast<uint16_t*>(qt + oh) = (uint16_t)hi;
-            *reinterpret_cast<uint16_t*>(qt + ol) = (uint16_t)lo;
+            *reinterpret_cast<uint16_t*>(oh) = (uint16_t)hi;
+            *reinterpret_cast<uint16_t*>(ol) = (uint16_t)lo;
           }
-          if (lane == 0) s_qf[s][h] = __uint_as_float((uint32_t)(127 + ex) << 23) * a.scale_log2;
+          if (lane == 0) s_qf[s][i] = __uint_as_float((uint32_t)(127 + ex) << 23) * a.scale_log2;
         }
       }
       fence_proxy_async_smem();
@@ -450,29 +455,61 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       if (lane == 0) mbar_arrive(&q_full[s]);
       if (g.b < 0) break;
     }
+  } else if (warp == 3) {
+    // --------------------------------------------------- page scales, a tile at a time
+    const int ppt = kTile >> a.shift;
+    Ring ring;
+    bool ok = true;
+    for (int s = 0, ph = 0; ok; s == kSlots - 1 ? (s = 0, ph ^= 1) : ++s) {
+      if (!(ok = wait_warp(&d_full[s], ph, abort, status))) break;
+      const Segment g = seg[s];
+      if (g.b < 0) break;
+      const int end = page_end(a, g);
+      int p0 = g.tile0 * ppt, id = page_at(a, g, p0 + lane, end);
+      for (int t = 0; t < g.tiles && ok; p0 += 32) {
+        // a page that is not there has a negative scale
+        const int64_t head = (int64_t)id * a.N + g.h;
+        float2 sc = make_float2(0.f, -1.f);
+        if (id >= 0 && id < a.num_blocks) sc = make_float2(__ldg(a.ks + head), __ldg(a.vs + head));
+        id = page_at(a, g, p0 + 32 + lane, end);
+        for (int i = 0; i < 32 && t < g.tiles; i += ppt, ++t) {
+          if (!(ok = wait_warp(&empty[ring.stage], ring.phase ^ 1u, abort, status))) break;
+          if (lane >= i && lane < i + ppt) s_meta[ring.stage * kMaxTilePages + lane - i] = sc;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[ring.stage]);
+          ring.next(kST);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_empty[s]);
+    }
   } else if (warp >= kSoftWarp0) {
     // ---------------------------------------------------------------------- softmax
     const int wg = (warp - kSoftWarp0) >> 2, tok = tid & 127, w = warp & 3;
     const uint32_t tm = tmem + ((uint32_t)(w * 32) << 16);
     const uint32_t s_tm = tm + kSCol + wg * kSStride;
     uint8_t* pt = s_p + wg * C::kPBytes;
+    float* s_join = reinterpret_cast<float*>(sm + C::kJoinOff);
     Ring ring;                                               // stage of the segment's tile t
-    uint32_t n_seg = 0, s_ph = 0, p_ph = 1;                  // p_ph: of the group's last product
+    uint32_t k = 0, s_ph = 0, p_ph = 0, j_ph[2] = {0, 0};    // k: the CTA's tile
     bool ok = true;
-    for (int s = 0, ph = 0; ok; s == kSlots - 1 ? (s = 0, ph ^= 1) : ++s, ++n_seg) {
-      ok = wait_warp(&q_full[s], ph, abort, status);
-      if (vote_both(!ok)) break;
+    for (int s = 0, ph = 0; true; s == kSlots - 1 ? (s = 0, ph ^= 1) : ++s) {
+      ok = ok && wait_warp(&q_full[s], ph, abort, status);
+      if (vote_group(wg, !ok)) break;
       const Segment g = seg[s];
       if (g.b < 0) break;
       float m[kH], l[kH], qf[kH];
 #pragma unroll
       for (int h = 0; h < kH; ++h) m[h] = -FLT_MAX, l[h] = 0.f, qf[h] = s_qf[s][h];
-      const uint32_t o_tm = tm + kOCol + ((n_seg & 1u) * 2 + wg) * kOStride;
-      for (int t = 0; t < g.tiles; ++t) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_empty[s]);
+      const uint32_t o_tm = tm + kOCol + wg * kOStride;
+      bool first = true;                                     // the group's first tile of the segment
+      for (int t = 0; t < g.tiles; ++t, ++k) {
         const int stage = ring.stage;
         const uint32_t st_ph = ring.phase;
         ring.next(kST);
-        if ((t & 1) != wg) continue;
+        if ((k & 1u) != (uint32_t)wg) continue;
         ok = ok && wait_warp(&full[stage], st_ph, abort, status) && wait_warp(&s_full[wg], s_ph, abort, status);
         s_ph ^= 1u;
         float x[kH];
@@ -494,14 +531,16 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         }
         // log2 of the value scale: the weights times it are what has to stay in range
         const float ev = (float)((int)(__float_as_uint(sc.y) >> 23) - 127);
-        bool raise = !ok || t < 2;
+        bool raise = !ok || first;
         if (ok) {
 #pragma unroll
           for (int h = 0; h < kH; ++h) raise |= x[h] + ev > m[h] + kRaise;
         }
         // the products of the group's last tile have been added, its weights can go
-        ok = ok && wait_warp(&p_empty[wg], p_ph, abort, status);
-        p_ph ^= 1u;
+        if (!first) {
+          ok = ok && wait_warp(&p_empty[wg], p_ph, abort, status);
+          p_ph ^= 1u;
+        }
         if (vote_group(wg, raise || !ok)) {
           if (vote_group(wg, !ok)) {
             ok = false;
@@ -530,7 +569,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             l[h] *= f[h];
             m[h] = mn;
           }
-          if (t >= 2) {
+          if (!first) {
             tc_fence_after();
 #pragma unroll
             for (int part = 0; part < 3; ++part) {
@@ -576,67 +615,73 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(&p_full[wg]);
+        first = false;
       }
+      const int owner = (int)((k - 1) & 1u);                 // group of the last tile
+      if (first && ok) continue;                             // none of the tiles was the group's
       // the group's sums and accumulator
-      if (ok) ok = wait_warp(&o_full[n_seg & 1u], (n_seg >> 1) & 1u, abort, status);
-      if (vote_both(!ok)) {                                  // also: s_join and s_red are free
-        ok = false;
-        break;
+      if (ok && !first) {
+        ok = wait_warp(&p_empty[wg], p_ph, abort, status);
+        p_ph ^= 1u;
       }
+      if (vote_group(wg, !ok)) break;
       tc_fence_after();
       float o[kH];
 #pragma unroll
       for (int h = 0; h < kH; ++h) o[h] = 0.f;
-      if (wg < g.tiles) {
 #pragma unroll
-        for (int part = 2; part >= 0; --part) {
-          uint32_t r[kGP];
-          if (kGP == 8) tmem_ld8(o_tm + part * kGP, r);
-          else tmem_ld16(o_tm + part * kGP, r);
-          tmem_ld_wait();
+      for (int part = 2; part >= 0; --part) {
+        uint32_t r[kGP];
+        if (kGP == 8) tmem_ld8(o_tm + part * kGP, r);
+        else tmem_ld16(o_tm + part * kGP, r);
+        tmem_ld_wait();
 #pragma unroll
-          for (int h = 0; h < kH; ++h) o[h] = fmaf(o[h], 0.0625f, __uint_as_float(r[h]));
-        }
-        tc_fence_before();
+        for (int h = 0; h < kH; ++h) o[h] = fmaf(o[h], 0.0625f, __uint_as_float(r[h]));
+      }
+      tc_fence_before();
 #pragma unroll
-        for (int h = 0; h < kH; ++h) {
+      for (int h = 0; h < kH; ++h) {
 #pragma unroll
-          for (int i = 16; i > 0; i >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], i);
-        }
-        if (lane == 0) {
-#pragma unroll
-          for (int h = 0; h < kH; ++h) s_red[wg][w][h] = l[h];
-        }
-        bar_sync(1 + wg, 128);
-#pragma unroll
-        for (int h = 0; h < kH; ++h)
-          l[h] = s_red[wg][0][h] + s_red[wg][1][h] + s_red[wg][2][h] + s_red[wg][3][h];
+        for (int i = 16; i > 0; i >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], i);
       }
       if (lane == 0) {
-        mbar_arrive(&o_empty[n_seg & 1u]);
-        mbar_arrive(&q_empty[s]);
+#pragma unroll
+        for (int h = 0; h < kH; ++h) s_red[wg][w][h] = l[h];
       }
-      if (g.tiles > 1) {                                     // the second group's tiles
-        if (wg == 1) {
+      bar_sync(1 + wg, 128);
+#pragma unroll
+      for (int h = 0; h < kH; ++h)
+        l[h] = s_red[wg][0][h] + s_red[wg][1][h] + s_red[wg][2][h] + s_red[wg][3][h];
+      if (g.tiles > 1) {                                     // the other group's part
+        const int other = owner ^ 1;
+        float* part = s_join + other * (C::kJoin / 4);
+        if (wg == other) {
+          // its place is free once the last part has been taken
+          ok = wait_warp(&j_empty[other], j_ph[other] ^ 1u, abort, status);
+          j_ph[other] ^= 1u;
+          if (!ok) continue;
 #pragma unroll
           for (int h = 0; h < kH; ++h) {
-            s_join[h * kTile + tok] = o[h];
-            if (tok == 0) s_join[16 * kTile + h] = m[h], s_join[16 * kTile + 16 + h] = l[h];
+            part[h * kTile + tok] = o[h];
+            if (tok == 0) part[16 * kTile + h] = m[h], part[16 * kTile + 16 + h] = l[h];
           }
+          mbar_arrive(&j_full[other]);
+          continue;
         }
-        bar_sync(3, 256);
-        if (wg == 0) {
+        ok = wait_warp(&j_full[other], j_ph[other], abort, status);
+        j_ph[other] ^= 1u;
+        if (!ok) continue;
 #pragma unroll
-          for (int h = 0; h < kH; ++h) {
-            const float m1 = s_join[16 * kTile + h], mn = fmaxf(m[h], m1);
-            const float fa = ex2_approx(m[h] - mn), fb = ex2_approx(m1 - mn);
-            o[h] = o[h] * fa + s_join[h * kTile + tok] * fb;
-            l[h] = l[h] * fa + s_join[16 * kTile + 16 + h] * fb;
-            m[h] = mn;
-          }
+        for (int h = 0; h < kH; ++h) {
+          const float m1 = part[16 * kTile + h], mn = fmaxf(m[h], m1);
+          const float fa = ex2_approx(m[h] - mn), fb = ex2_approx(m1 - mn);
+          o[h] = o[h] * fa + part[h * kTile + tok] * fb;
+          l[h] = l[h] * fa + part[16 * kTile + 16 + h] * fb;
+          m[h] = mn;
         }
+        mbar_arrive(&j_empty[other]);
       }
-      if (wg == 0) {
+      {
         const int64_t row = g.slot < 0 ? ((int64_t)g.b * a.N + g.h) * a.G : (int64_t)g.slot * a.G;
 #pragma unroll
         for (int h = 0; h < kH; ++h) {

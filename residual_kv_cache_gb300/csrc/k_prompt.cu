@@ -38,8 +38,7 @@
 // Warps: 0-3 and 4-7 softmax of tiles 0 and 1, 8 TMA, 9 MMA, 10 work list, 11 TMEM.
 #include <cuda_bf16.h>
 
-#include "pages.h"
-#include "tc_common.cuh"
+#include "pages.cuh"
 
 namespace rkv {
 namespace {
@@ -295,12 +294,6 @@ __device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t lbo) {
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
-// Every lane waits (a lane's wait handed on by a shuffle costs some 200 cycles more); the
-// verdict is the warp's.
-__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
-}
-
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -393,19 +386,19 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         uint32_t q_ph = 1;
         bool ok = true;
         for (int s = 0, ph = 0; ok; s == kItems - 1 ? (s = 0, ph ^= 1) : ++s) {
-          if (!(ok = mbar_wait(&i_full[s], ph, abort, status))) break;
+          if (!(ok = wait_one(&i_full[s], ph, abort, status))) break;
           const Item it = items[s];
           mbar_arrive(&i_empty[s]);
           if (it.kvh < 0) break;
           if (it.n[1] == 0) continue;
           const bool both = it.n[0] > it.j0;
-          if (!(ok = mbar_wait(&q_empty, q_ph, abort, status))) break;
+          if (!(ok = wait_one(&q_empty, q_ph, abort, status))) break;
           q_ph ^= 1u;
           mbar_arrive_expect_tx(&q_full, (both ? 2 : 1) * C::kTileB);
           if (both) load_tile<D>(s_q, &tm_q, &q_full, it.head[0], it.row[0]);
           load_tile<D>(s_q + C::kTileB, &tm_q, &q_full, it.head[1], it.row[1]);
           for (int j = 2 * it.j0; j < 2 * it.n[1]; ++j) {            // K 0, V 0, K 1, V 1, ...
-            if (!(ok = mbar_wait(&kv_empty[kv.stage], kv.phase ^ 1u, abort, status))) break;
+            if (!(ok = wait_one(&kv_empty[kv.stage], kv.phase ^ 1u, abort, status))) break;
             mbar_arrive_expect_tx(&kv_full[kv.stage], C::kTileB);
             load_tile<D>(s_kv + kv.stage * C::kTileB, (j & 1) ? &tm_v : &tm_k, &kv_full[kv.stage], it.kvh,
                          it.k0 + (j >> 1) * kKeys);
@@ -435,7 +428,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         // S_t = Q_t K^T
         auto qk = [&](int t, int slot) {
           if (C::kApart) {                                   // the last S_t has been read
-            ok = ok && mbar_wait(&s_empty[t], s_ph[t], abort, status);
+            ok = ok && wait_one(&s_empty[t], s_ph[t], abort, status);
             s_ph[t] ^= 1u;
             if (!ok) return;
             tc_fence_after();
@@ -452,7 +445,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         auto pv = [&](int t, int slot, bool acc) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            ok = ok && mbar_wait(h ? &p_full[t] : &p_half[t], p_ph[t], abort, status);
+            ok = ok && wait_one(h ? &p_full[t] : &p_half[t], p_ph[t], abort, status);
             if (!ok) return;
             tc_fence_after();
 #pragma unroll
@@ -465,14 +458,14 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           if (C::kApart) umma_commit(&p_empty[t]);
         };
         for (int s = 0, ph = 0; ok; s == kItems - 1 ? (s = 0, ph ^= 1) : ++s) {
-          if (!(ok = mbar_wait(&i_full[s], ph, abort, status))) break;
+          if (!(ok = wait_one(&i_full[s], ph, abort, status))) break;
           const int kvh = items[s].kvh, n0 = items[s].n[0], n1 = items[s].n[1], j0 = items[s].j0;
           mbar_arrive(&i_empty[s]);
           if (kvh < 0) break;
           if (n1 == 0) continue;
-          if (!(ok = mbar_wait(&q_full, q_ph, abort, status))) break;
+          if (!(ok = wait_one(&q_full, q_ph, abort, status))) break;
           q_ph ^= 1u;
-          if (!(ok = mbar_wait(&kv_full[kv.stage], kv.phase, abort, status))) break;
+          if (!(ok = wait_one(&kv_full[kv.stage], kv.phase, abort, status))) break;
           tc_fence_after();
           if (n0 > j0) qk(0, kv.stage);
           qk(1, kv.stage);
@@ -491,11 +484,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
               }
             };
             if (C::kApart) {
-              if (j + 1 < n1 && !(ok = ok && mbar_wait(&kv_full[kv.stage], kv.phase, abort, status))) break;
+              if (j + 1 < n1 && !(ok = ok && wait_one(&kv_full[kv.stage], kv.phase, abort, status))) break;
 #pragma unroll
               for (int t = 0; t < 2; ++t) {
                 next_qk(t);
-                if (t == 0 && !(ok = ok && mbar_wait(&kv_full[v.stage], v.phase, abort, status))) break;
+                if (t == 0 && !(ok = ok && wait_one(&kv_full[v.stage], v.phase, abort, status))) break;
                 if (j < (t ? n1 : n0)) {
                   pv(t, v.stage, j > j0);
                   if (j + 1 == (t ? n1 : n0)) umma_commit(&o_full[t]);
@@ -503,15 +496,15 @@ __global__ void __launch_bounds__(kPrThreads, 1)
               }
               umma_commit(&kv_empty[v.stage]);
             } else {
-              if (!(ok = ok && mbar_wait(&kv_full[v.stage], v.phase, abort, status))) break;
+              if (!(ok = ok && wait_one(&kv_full[v.stage], v.phase, abort, status))) break;
 #pragma unroll
               for (int t = 0; t < 2; ++t) {
                 if (j < (t ? n1 : n0)) {
                   pv(t, v.stage, j > j0);
                   if (t == 1) umma_commit(&kv_empty[v.stage]);
-                  if (t == 0 && j + 1 < n1) ok = ok && mbar_wait(&kv_full[kv.stage], kv.phase, abort, status);
+                  if (t == 0 && j + 1 < n1) ok = ok && wait_one(&kv_full[kv.stage], kv.phase, abort, status);
                   if (t == 1 && j + 1 < n1 && j >= n0)       // tile 0 has not waited for it
-                    ok = ok && mbar_wait(&kv_full[kv.stage], kv.phase, abort, status);
+                    ok = ok && wait_one(&kv_full[kv.stage], kv.phase, abort, status);
                   if (!ok) break;
                   next_qk(t);
                   if (j + 1 == (t ? n1 : n0)) umma_commit(&o_full[t]);
@@ -532,7 +525,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       uint32_t ph = 1;
       load_seq(a, lane, q0, lq, k0, lk);
       auto emit = [&](const Item& it) {
-        if (!wait_all(&i_empty[s], ph, abort, status)) return false;
+        if (!wait_warp(&i_empty[s], ph, abort, status)) return false;
         if (lane == 0) {
           items[s] = it;
           mbar_arrive(&i_full[s]);
@@ -556,7 +549,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     const float c = a.scale_log2;
     bool ok = true;
     for (int si = 0, ph = 0; ok; si == kItems - 1 ? (si = 0, ph ^= 1) : ++si) {
-      if (!(ok = wait_all(&i_full[si], ph, abort, status))) break;
+      if (!(ok = wait_warp(&i_full[si], ph, abort, status))) break;
       const int kvh = items[si].kvh, n = items[si].n[t], n1 = items[si].n[1], lk = items[si].lk;
       const int j0 = items[si].j0;
       // keys that this row sees
@@ -568,7 +561,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       for (int j = j0; j < n1; ++j) {
         kv.next(kSlots);                                     // now V j
         if (j < n) {
-          if (!(ok = wait_all(&s_full[t], s_ph, abort, status))) break;
+          if (!(ok = wait_warp(&s_full[t], s_ph, abort, status))) break;
           s_ph ^= 1u;
           tc_fence_after();
           const bool masked = (j + 1) * kKeys > see0;        // some row does not see every key
@@ -631,7 +624,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           };
           float part;
           if (C::kApart) {                                   // P V of tile j - 1 is complete
-            if (!(ok = wait_all(&p_empty[t], p_ph, abort, status))) break;
+            if (!(ok = wait_warp(&p_empty[t], p_ph, abort, status))) break;
             p_ph ^= 1u;
             tc_fence_after();
           }
@@ -665,7 +658,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           }
           l += part;
           if ((j + 1) * kKeys > lk) {                        // values behind the sequence
-            if (!(ok = wait_all(&kv_full[kv.stage], kv.phase, abort, status))) break;
+            if (!(ok = wait_warp(&kv_full[kv.stage], kv.phase, abort, status))) break;
             if (j * kKeys + r >= lk) {
               uint8_t* v = s_kv + kv.stage * C::kTileB + r * 128;
 #pragma unroll
@@ -697,7 +690,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             part = total(sum);
             if (again || !__any_sync(0xffffffffu, part > kPrRaise)) break;
             // the first half's product has to be complete
-            if (!(ok = wait_all(&p_mid[t], mid_ph, abort, status))) break;
+            if (!(ok = wait_warp(&p_mid[t], mid_ph, abort, status))) break;
             tc_fence_after();
             raise_to(fmaxf(top_of(xa), top_of(xb)), true);
             again = true;
@@ -720,7 +713,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&i_empty[si]);
       if (n > j0) {
-        if (!(ok = wait_all(&o_full[t], o_ph, abort, status))) break;
+        if (!(ok = wait_warp(&o_full[t], o_ph, abort, status))) break;
         o_ph ^= 1u;
         tc_fence_after();
       }
