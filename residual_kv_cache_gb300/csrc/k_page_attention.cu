@@ -208,7 +208,6 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     for (int i = 0; i < kSlots; ++i) mbar_init(&d_full[i], 1), mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 11);
     mbar_init(&drain, 1);
     s_abort = 0;
-    s_b0 = a.batch;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -217,38 +216,57 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   }
 
   // the call's tiles, and the sequence in which this CTA's share begins
-  int64_t total = 0, incl = 0, mine = 0;
-  bool any_bad = false;
-  for (int b0 = 0; b0 < a.batch; b0 += kPaThreads) {
-    bool bad = false;
-    const int b = b0 + tid;
-    mine = b < a.batch ? tiles_of(length_of(a, b, bad)) : 0;
-    any_bad |= bad;
-    int64_t n = mine, t;
-    int x = 0, tx;
-    block_scan<kPaThreads>(n, x, t, tx);
-    incl = total + n;
-    total += t;
-  }
-  if (any_bad && blockIdx.x == 0) raise_flag(a.flags, RKV_FLAG_BAD_INDEX);
-  const Shares shares(total * a.N, gridDim.x);
   const int cta = blockIdx.x;
-  const int64_t f0 = cta < shares.C ? shares.start(cta) : 0, f1 = cta < shares.C ? shares.start(cta + 1) : 0;
-  if (a.batch <= kPaThreads) {
-    if (mine > 0 && (incl - mine) * a.N <= f0 && f0 < incl * a.N) s_b0 = tid, s_pref = incl - mine;
+  int64_t total = 0, incl = 0, mine = 0, f0 = 0, f1 = 0;
+  bool any_bad = false;
+  auto cut = [&]() {                                         // the share
+    const Shares shares(total * a.N, gridDim.x);
+    f0 = cta < shares.C ? shares.start(cta) : 0;
+    f1 = cta < shares.C ? shares.start(cta + 1) : 0;
+  };
+  if (a.batch <= 32) {
+    // up to a warp's width every warp scans by itself
+    mine = lane < a.batch ? tiles_of(length_of(a, lane, any_bad)) : 0;
+    incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    total = __shfl_sync(0xffffffffu, incl, 31);
+    cut();
+    if (warp == 2 && mine > 0 && (incl - mine) * a.N <= f0 && f0 < incl * a.N) s_b0 = lane, s_pref = incl - mine;
   } else {
-    int64_t pref = 0;
-    for (int b0 = 0; b0 < a.batch && pref * a.N <= f0; b0 += kPaThreads) {
-      bool bad;
+    for (int b0 = 0; b0 < a.batch; b0 += kPaThreads) {
+      bool bad = false;
       const int b = b0 + tid;
       mine = b < a.batch ? tiles_of(length_of(a, b, bad)) : 0;
+      any_bad |= bad;
       int64_t n = mine, t;
       int x = 0, tx;
       block_scan<kPaThreads>(n, x, t, tx);
-      if (mine > 0 && (pref + n - mine) * a.N <= f0 && f0 < (pref + n) * a.N) s_b0 = b, s_pref = pref + n - mine;
-      pref += t;
+      incl = total + n;
+      total += t;
+    }
+    cut();
+    int64_t pref = incl - mine;
+    if (a.batch <= kPaThreads) {
+      if (mine > 0 && pref * a.N <= f0 && f0 < incl * a.N) s_b0 = tid, s_pref = pref;
+    } else {
+      pref = 0;
+      for (int b0 = 0; b0 < a.batch && pref * a.N <= f0; b0 += kPaThreads) {
+        bool bad;
+        const int b = b0 + tid;
+        mine = b < a.batch ? tiles_of(length_of(a, b, bad)) : 0;
+        int64_t n = mine, t;
+        int x = 0, tx;
+        block_scan<kPaThreads>(n, x, t, tx);
+        if (mine > 0 && (pref + n - mine) * a.N <= f0 && f0 < (pref + n) * a.N) s_b0 = b, s_pref = pref + n - mine;
+        pref += t;
+      }
     }
   }
+  if (any_bad && blockIdx.x == 0) raise_flag(a.flags, RKV_FLAG_BAD_INDEX);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -369,7 +387,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     // ------------------------------------------------- segments and their query tiles
     constexpr int kW = D / 64;                               // words (2 values) per lane and head
     int64_t left = f1 - f0;                                  // tiles of the share still to come
-    int b = s_b0, h = 0, tile = 0, chunk = -1, len_l = 0;    // lane i: length of sequence chunk + i
+    int b = left > 0 ? s_b0 : a.batch, h = 0, tile = 0, chunk = -1, len_l = 0;    // lane i: length of sequence chunk + i
     bool first = true, ok = true;
     for (int s = 0, ph = 1; ok; s == kSlots - 1 ? (s = 0, ph ^= 1) : ++s) {
       Segment g{-1, 0, 0, 0, 0, -1};
@@ -386,8 +404,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           continue;
         }
         if (first) {                                         // where the share begins
-          const int64_t rel = f0 - s_pref * a.N;
-          h = (int)(rel / nb), tile = (int)(rel % nb);
+          const int64_t rel = f0 - s_pref * a.N;             // 32 bits spare a long division
+          if (rel <= INT32_MAX) h = (int)rel / nb, tile = (int)rel % nb;
+          else h = (int)(rel / nb), tile = (int)(rel % nb);
         }
         g.b = b, g.h = h, g.tile0 = tile;
         g.tiles = (int)min((int64_t)(nb - tile), left);
@@ -547,17 +566,13 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             break;
           }
           // the reference becomes the maximum so far
-          float y[kH];
+          // (one instruction a warp and head, on integers of the same order; NaN left out)
 #pragma unroll
-          for (int h = 0; h < kH; ++h) y[h] = x[h] + ev;
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) {
-#pragma unroll
-            for (int h = 0; h < kH; ++h) y[h] = fmaxf(y[h], __shfl_xor_sync(0xffffffffu, y[h], o));
-          }
-          if (lane == 0) {
-#pragma unroll
-            for (int h = 0; h < kH; ++h) s_red[wg][w][h] = y[h];
+          for (int h = 0; h < kH; ++h) {
+            const float y = fmaxf(x[h] + ev, -INFINITY);
+            const int i = __float_as_int(y), key = i ^ (i >> 31 & 0x7FFFFFFF);
+            const int top = __reduce_max_sync(0xffffffffu, key);
+            if (lane == 0) s_red[wg][w][h] = __int_as_float(top ^ (top >> 31 & 0x7FFFFFFF));
           }
           bar_sync(1 + wg, 128);
           float f[kH];
