@@ -863,9 +863,7 @@ extern "C" rkv_status rkv_page_attention(const rkv_pages* pages, const rkv_page_
       q_strides[1] < 0 || q_strides[0] % 8 || q_strides[1] % 8)
     return fail_with(RKV_EALIGN, "q, out, workspace and q's strides must be whole 16 bytes");
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
-    return fail_with(RKV_ECUDA, "no usable current device");
+  if (!current_device(dev, sms)) return fail_with(RKV_ECUDA, "no usable current device");
   const int D = pages->head_dim;
   const uint64_t rows = (uint64_t)pages->num_blocks * pages->n_kv_heads * pages->block_tokens;
   CUtensorMap mk, mv;

@@ -691,9 +691,7 @@ extern "C" rkv_status rkv_page_append(const rkv_pages* pages, const rkv_page_tab
   a.shift = log2_block(pages->block_tokens);
   a.n_rows = n_rows;
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return fail_with(RKV_ECUDA, "no usable current device");
+  if (!current_device(dev, sms)) return fail_with(RKV_ECUDA, "no usable current device");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int P = pages->block_tokens;
   if (dtype == RKV_F32)

@@ -908,9 +908,7 @@ extern "C" rkv_status rkv_prompt_attention(const rkv_prompt* pr, int32_t* flags,
     return fail_with(RKV_ECAPACITY, "workspace has %zu of %zu bytes", p.workspace ? p.workspace_bytes : (size_t)0, need);
   if (!is_aligned(p.workspace, 16)) return fail_with(RKV_EALIGN, "workspace must be 16-byte aligned");
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
-    return fail_with(RKV_ECUDA, "no usable current device");
+  if (!current_device(dev, sms)) return fail_with(RKV_ECUDA, "no usable current device");
   // without keys the maps are never read; they still need an extent
   const uint64_t D = p.head_dim;
   const bool keys = p.total_k > 0;

@@ -40,6 +40,16 @@ bool encode_map_bytes(CUtensorMap* m, const void* base, uint64_t inner, uint64_t
 bool encode_map_heads(CUtensorMap* m, const void* base, uint64_t D, uint64_t heads, uint64_t rows,
                       const int64_t strides[2], uint32_t box_rows);
 
+// The current device and its number of SMs (looked up once a device); false without one.
+inline bool current_device(int& dev, int& sms) {
+  static std::atomic<int> known[64];
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return true;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) return false;
+  if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
+  return true;
+}
+
 // Opts a kernel into `smem` bytes of dynamic shared memory on the current device, once per
 // device (the attribute belongs to the device's copy of the function).  One instance per
 // kernel; concurrent first calls set the same value twice.

@@ -547,3 +547,63 @@ def test_streams_and_calls_at_once():
     torch.cuda.synchronize()
     for (a, b), (c, d) in zip(alone, got):
         assert torch.equal(a, c) and torch.equal(b, d)
+
+
+# --------------------------------------------------------------------------- refusals
+@cuda
+def test_binding_refusals():
+    """Shapes, types, strides, devices and streams that a call cannot use are refused before
+    anything is launched; the library's own refusals arrive as RkvError."""
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    q, k = bf(6, 4, 64), bf(6, 2, 64)
+    cu = i32([0, 6])
+    ok = lambda **kw: rkv.prompt_attention(**{**dict(q=q, k=k, v=k, cu_q=cu), **kw})  # noqa: E731
+    ok()
+    odd = torch.zeros((6, 4, 67), dtype=torch.bfloat16, device="cuda")[:, :, :64]
+    for bad in (dict(q=q.float()), dict(q=q[0]), dict(k=bf(6, 2, 128)), dict(v=bf(5, 2, 64)), dict(q=odd),
+                dict(q=bf(6, 64, 4).transpose(1, 2)), dict(cu_q=cu.long()), dict(cu_q=cu[None]),
+                dict(cu_k=i32([0, 3, 6])), dict(cu_q=cu.cpu()), dict(k=k.cpu()), dict(out=bf(6, 4, 128)),
+                dict(lse=bf(6, 4)), dict(flags=i32([0, 0])), dict(scale=0.0), dict(scale=math.nan),
+                dict(scale=math.inf), dict(scale=-1.0)):
+        with pytest.raises(ValueError):
+            ok(**bad)
+    with pytest.raises(TypeError):
+        ok(scale="x")
+    with pytest.raises(AttributeError):
+        ok(stream=7)
+    with pytest.raises(rkv.RkvError) as e:
+        ok(q=bf(6, 3, 64))                                   # 3 query heads over 2
+    assert e.value.status == -1
+    ok(q=odd[:1, :1], k=k[:, :1], v=k[:, :1], cu_q=i32([0, 1]), cu_k=i32([0, 6]))   # strides of one row, one head
+
+    u8, f = torch.zeros((3, 2, 16, 64), dtype=torch.uint8, device="cuda"), torch.ones((3, 2), device="cuda")
+    t, ln = i32([[0, 1], [2, 0]]), i32([1, 1])
+    att = lambda **kw: rkv.page_attention(**{**dict(q=bf(2, 4, 64), k8=u8, v8=u8, k_scale=f, v_scale=f,  # noqa: E731
+                                                    block_table=t, seq_len=ln), **kw})
+    att()
+    for bad in (dict(q=bf(3, 4, 64)), dict(q=bf(2, 4, 128)), dict(k8=u8.view(torch.int8)), dict(v8=u8[:2]),
+                dict(k_scale=f.double()), dict(v_scale=f.t()), dict(block_table=t.long()), dict(seq_len=i32([1])),
+                dict(block_table=t[0]), dict(out=bf(2, 4, 64).transpose(0, 1)), dict(lse=torch.zeros(8, device="cuda"))):
+        with pytest.raises(ValueError):
+            att(**bad)
+    for bad in (dict(k8=u8[:, :, :8].contiguous(), v8=u8[:, :, :8].contiguous()), dict(q=bf(2, 34, 64))):
+        with pytest.raises(rkv.RkvError):
+            att(**bad)
+    app = lambda **kw: rkv.page_append(**{**dict(k=bf(2, 2, 64), v=bf(2, 2, 64), k8=u8.clone(), v8=u8.clone(),  # noqa: E731
+                                                 k_scale=f.clone(), v_scale=f.clone(), block_table=t, seq_len=ln,
+                                                 cu_rows=i32([0, 1, 2])), **kw})
+    app()
+    for bad in (dict(v=bf(2, 2, 64).float()), dict(k=bf(2, 3, 64)), dict(k=bf(2, 2, 64).half(), v=bf(2, 2, 64).half()),
+                dict(cu_rows=i32([0, 2])), dict(v=bf(3, 2, 64))):
+        with pytest.raises(ValueError):
+            app(**bad)
+    pl = lambda **kw: rkv.page_plan(**{**dict(new_tokens=i32([1, 1]), seq_len=ln.clone(), block_table=t.clone(),  # noqa: E731
+                                              free_blocks=i32([0, 1, 2]), n_free=i32([3]), block_tokens=16,
+                                              max_rows=4), **kw})
+    pl()
+    for bad in (dict(new_tokens=i32([1])), dict(n_free=i32([3, 3])), dict(free_blocks=i32([[0]])),
+                dict(seq_len_out=i32([1])), dict(n_free_out=i32([]))):
+        with pytest.raises(ValueError):
+            pl(**bad)
+    with pytest.raises(rkv.RkvError):
+        pl(block_tokens=20)

@@ -9,7 +9,27 @@ import torch
 
 import residual_kv_cache_gb300 as rkv
 from oracle import pages as OP
-from residual_kv_cache_gb300 import pages as RP
+
+
+class RP:
+    """The structures of include/rkv.h's page and prompt entry points."""
+    _Strides = ctypes.c_int64 * 2
+
+    class _Pages(ctypes.Structure):
+        _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                    ("v_scale", ctypes.c_void_p), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                    ("block_tokens", ctypes.c_int32), ("num_blocks", ctypes.c_int32)]
+
+    class _Table(ctypes.Structure):
+        _fields_ = [("block_table", ctypes.c_void_p), ("seq_len", ctypes.c_void_p), ("batch", ctypes.c_int32),
+                    ("max_blocks", ctypes.c_int32)]
+
+    class _Prompt(ctypes.Structure):
+        _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "out", "lse")] + \
+            [(n + "_strides", ctypes.c_int64 * 2) for n in ("q", "k", "v", "out")] + \
+            [("cu_q", ctypes.c_void_p), ("cu_k", ctypes.c_void_p)] + \
+            [(n, ctypes.c_int32) for n in ("batch", "total_q", "total_k", "n_q_heads", "n_kv_heads", "head_dim")] + \
+            [("scale", ctypes.c_double), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
 @pytest.fixture(scope="module")
@@ -148,50 +168,38 @@ def test_prompt_refusals(lib):
     assert call(total_k=5000, workspace=A + 4, workspace_bytes=n) == -2
 
 
-def test_binding_refuses_what_the_library_cannot_see():
-    """CPU tensors, wrong types and shapes are refused with ValueError before any call."""
+def test_binding_refuses_what_the_library_cannot_see(lib):
+    """CPU tensors, other objects and wrong types are refused with ValueError or TypeError
+    before any call."""
     i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
     bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
     u8, f32 = torch.zeros((3, 2, 16, 64), dtype=torch.uint8), torch.zeros((3, 2))
-    with pytest.raises(ValueError, match="block_table"):
+    with pytest.raises(ValueError, match="block_table must be a CUDA"):
         rkv.page_plan(i32(2), i32(2), i32(2, 4), i32(3), i32(1), 16, 8)
     with pytest.raises(ValueError, match="max_rows"):
         rkv.page_plan(i32(2), i32(2), i32(2, 4), i32(3), i32(1), 16, -1)
+    with pytest.raises(ValueError, match="out of range"):
+        rkv.page_plan(i32(2), i32(2), i32(2, 4), i32(3), i32(1), 16, 2 ** 31)
+    with pytest.raises(TypeError):
+        rkv.page_plan(i32(2), i32(2), i32(2, 4), i32(3), i32(1), None, 8)
     with pytest.raises(ValueError, match="block_table"):
-        rkv.page_release(i32(2), i32(2), i32(2, 4), i32(3), i32(1), 16)
+        rkv.page_release(i32(2), i32(2), [[1]], i32(3), i32(1), 16)
     with pytest.raises(ValueError, match="k8"):
         rkv.page_append(bf(4, 2, 64), bf(4, 2, 64), u8, u8, f32, f32, i32(2, 4), i32(2), i32(3))
     with pytest.raises(ValueError, match="k8"):
         rkv.page_attention(bf(2, 4, 64), u8, u8, f32, f32, i32(2, 4), i32(2))
     with pytest.raises(ValueError, match="q must be a CUDA"):
         rkv.prompt_attention(bf(4, 4, 64), bf(4, 2, 64), bf(4, 2, 64), i32(2))
-    for s in (0.0, -1.0, math.inf, math.nan):
-        with pytest.raises(ValueError, match="scale"):
-            RP._scale(s, 64)
-    assert RP._scale(None, 64) == 0.125
+    with pytest.raises(ValueError, match="q must be a tensor"):
+        rkv.prompt_attention(None, bf(4, 2, 64), bf(4, 2, 64), i32(2))
 
 
-def test_rows_strides():
-    """Rows may be strided views of a projection's output; strides of dimensions of one are
-    not looked at, others must be whole 16 bytes.  (Device -1 stands for the CPU here.)"""
-    bf = torch.bfloat16
-    x = torch.zeros((6, 10, 64), dtype=bf)
-    assert list(RP._rows(x[:, 2:5], "x", (6, 3, 64), -1, bf)) == [640, 64]
-    assert list(RP._rows(x.transpose(0, 1), "x", (10, 6, 64), -1, bf)) == [64, 640]
-    assert list(RP._rows(x[:0], "x", (0, 10, 64), -1, bf)) == [0, 64]
-    odd = torch.zeros((6, 10, 67), dtype=bf)[:, :, :64]
-    with pytest.raises(ValueError, match="16 bytes"):
-        RP._rows(odd, "x", (6, 10, 64), -1, bf)
-    assert list(RP._rows(odd[:1, :1], "x", (1, 1, 64), -1, bf)) == [0, 0]
-    assert list(RP._rows(odd[:0], "x", (0, 10, 64), -1, bf)) == [0, 0]
-    with pytest.raises(ValueError, match="x must be"):
-        RP._rows(x.transpose(1, 2), "x", (6, 10, 64), -1, bf)
-    with pytest.raises(ValueError, match="16 bytes"):
-        RP._rows(x.transpose(1, 2), "x", (6, 64, 10), -1, bf)
-    with pytest.raises(ValueError, match="x must be"):
-        RP._rows(x.float(), "x", (6, 10, 64), -1, bf)
-    with pytest.raises(ValueError, match="x must be"):
-        RP._rows(x, "x", (6, 10, 64), 0, bf)
+def test_missing_binding_fails_loudly(tmp_path, monkeypatch):
+    from residual_kv_cache_gb300 import pages
+    monkeypatch.setattr(pages, "__file__", str(tmp_path / "pages.py"))
+    monkeypatch.setattr(pages, "_module", None)
+    with pytest.raises(rkv.RkvLibraryMissing):
+        rkv.page_release(None, None, None, None, None, 16)
 
 
 # ------------------------------------------------------------- pins of the definitions
