@@ -114,14 +114,17 @@ struct Seq {
     it.kvh = h;
     it.k0 = k0, it.lk = lk;
     it.j0 = 0, it.slot = -1;
+    // query tile and head of r1, and of the row tile before it
+    int qt = (int)((uint32_t)r1 / (uint32_t)G), e = r1 - qt * G;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int r = t ? r1 : r0, qt = r >= 0 ? r / G : 0;
+    for (int t = 1; t >= 0; --t) {
+      const bool is = t == 1 || r0 >= 0;
       it.row[t] = q0 + qt * kRows;
-      it.rows[t] = r >= 0 ? min(kRows, lq - qt * kRows) : 0;
-      it.head[t] = h * G + (r >= 0 ? r % G : 0);
+      it.rows[t] = is ? min(kRows, lq - qt * kRows) : 0;
+      it.head[t] = h * G + e;
       it.lim[t] = lk - lq + qt * kRows + 1;
-      it.n[t] = r >= 0 ? n(qt) : 0;
+      it.n[t] = is ? n(qt) : 0;
+      if (is && --e < 0) e = G - 1, --qt;
     }
   }
 };
@@ -155,7 +158,7 @@ __device__ __forceinline__ void walk_pairs(const PrArgs& a, int q0, int lq, int 
         load_seq(a, chunk + lane, q0, lq, k0, lk);
       }
       const int my_pairs = Seq(q0, lq, k0, lk, a.G).pairs();
-      if (b == chunk) {                    // skip the chunk if it ends before i
+      if (b == chunk && a.batch > 32) {    // skip the chunk if it ends before i
         int64_t sum = (int64_t)my_pairs * a.N;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -173,8 +176,9 @@ __device__ __forceinline__ void walk_pairs(const PrArgs& a, int q0, int lq, int 
       }
       const Seq q(__shfl_sync(0xffffffffu, q0, b & 31), __shfl_sync(0xffffffffu, lq, b & 31),
                   __shfl_sync(0xffffffffu, k0, b & 31), __shfl_sync(0xffffffffu, lk, b & 31), a.G);
-      const int rel = (int)(i - base), r1 = q.tiles() - 1 - 2 * (rel / a.N);   // longest first
-      q.item(it, r1 - 1, r1, rel % a.N);
+      const uint32_t rel = (uint32_t)(i - base), p = rel / (uint32_t)a.N;
+      const int r1 = q.tiles() - 1 - 2 * (int)p;             // longest first
+      q.item(it, r1 - 1, r1, (int)(rel - p * a.N));
       break;
     }
     if (!emit(it) || it.kvh < 0) return;
@@ -570,8 +574,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           // scores of keys k .. k + 31 that the row does not see
           auto mask = [&](uint32_t* x, int k) {
             if (masked) {
+              const int n_vis = vis - k;
+              const uint32_t bits = n_vis >= 32 ? 0xFFFFFFFFu : n_vis <= 0 ? 0u : (1u << n_vis) - 1;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] = k + e < vis ? x[e] : 0xFF800000u;
+              for (int e = 0; e < 32; ++e) x[e] = bits >> e & 1u ? x[e] : 0xFF800000u;
             }
           };
           auto top_of = [&](const uint32_t* x) {
