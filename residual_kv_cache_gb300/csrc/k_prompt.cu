@@ -14,8 +14,8 @@
 // What bounds the loop is the chain from S_t over P_t to the next S_t (with D = 128: softmax,
 // P V, Q K^T and two hand-overs of some 350 cycles, where the two tiles' products take 2048
 // cycles a key tile).  So the softmax is short: no reduction crosses threads, and no maximum
-// is taken in the usual tile.  m is the maximum over the first tile's keys; a bf16 weight has
-// the range of an fp32, and nothing is lost while weights grow past 1.  Only when a row's
+// is taken in the usual tile.  m is the maximum over the first 64 keys; a bf16 weight has the
+// range of an fp32, and nothing is lost while weights grow past 1.  Only when a row's
 // weights of 64 keys sum to more than 2^24 is m raised to the scores' maximum, the sum and the
 // accumulator rescaled and the half tile done again.  P_t is handed over in halves of 64
 // keys, so that its product starts on the first.  Sums are fp32 over the unrounded weights.
@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             p_ph ^= 1u;
             tc_fence_after();
           }
-          bool again = j == j0;                              // the first tile's maximum
+          bool again = __any_sync(0xffffffffu, m == -INFINITY);   // to begin with
           while (true) {
             if (again) {
               float top = -INFINITY;
@@ -644,6 +644,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
                 tmem_ld_wait();
                 mask(xa, 32 * i);
                 top = fmaxf(top, top_of(xa));
+                // to begin with, the first 64 keys do
+                if (i == 1 && j == j0 && __all_sync(0xffffffffu, top > -INFINITY)) break;
               }
               raise_to(top, j > j0);
             }
