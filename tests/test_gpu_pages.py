@@ -439,6 +439,44 @@ def test_prompt_attention_cuts_bad_offsets():
     assert torch.equal(out[:30], rkv.prompt_attention(q, k, v, i32([0, 30]))[:30])
 
 
+@cuda
+def test_prompt_attention_broadcast_rows_and_heads_in_place_and_without_keys():
+    cu = i32([0, 100, 150])
+    q, k, v = randn(150, 8, 128, seed=831), randn(150, 4, 128, seed=832), randn(150, 4, 128, seed=833)
+    base = rkv.prompt_attention(q, k, v, cu)
+    one = rkv.prompt_attention(q, k[:, :1].expand(150, 4, 128), v[:, :1].expand(150, 4, 128), cu)
+    assert torch.equal(one, rkv.prompt_attention(q, k[:, :1], v[:, :1], cu))
+    row = rkv.prompt_attention(q[:1].expand(150, 8, 128), k, v, cu)
+    assert torch.equal(row, rkv.prompt_attention(q[:1].repeat(150, 1, 1), k, v, cu))
+    q2 = q.clone()
+    assert rkv.prompt_attention(q2, k, v, cu, out=q2) is q2 and torch.equal(q2, base)
+    assert not rkv.prompt_attention(q[:5], k[:0], v[:0], i32([0, 5]), i32([0, 0])).any()
+    assert rkv.prompt_attention(q[:0], k, v, i32([0, 0]), i32([0, 150])).shape == (0, 8, 128)
+
+
+@cuda
+@pytest.mark.parametrize("B", [33, 700, 8192])
+def test_many_short_sequences(B):
+    """Batches past a warp, past a block and at the limit, half the sequences empty: prompts of
+    up to two tokens, and decode steps over up to 39."""
+    g = np.random.default_rng(B)
+    lens = g.integers(0, 3, size=B).tolist()
+    cu = _cu(lens)
+    q, k, v = randn(cu[-1], 4, 64, seed=841), randn(cu[-1], 2, 64, seed=842), randn(cu[-1], 2, 64, seed=843)
+    flags = i32([0])
+    out = rkv.prompt_attention(q, k, v, i32(cu), flags=flags)
+    ref, _, a, big = OP.prompt_attention(np64(q), np64(k), np64(v), cu, cu, 0.125)
+    close(out, ref, a, big, 64, 2.0 ** -8)
+    lens = g.integers(0, 40, size=B)
+    lens[g.integers(0, B, size=B // 2)] = 0
+    cache, table, tb, (kv, vv) = _paged(lens.tolist(), 2, 16, 64, 850)
+    q = randn(B, 4, 64, seed=851)
+    out = rkv.page_attention(q, *cache, table, i32(lens), flags=flags)
+    ref, _, a, big = OP.page_attention(np64(q), kv, vv, tb, lens.tolist(), 16, 0.125)
+    close(out, ref, a, big, 64, 2.0 ** -11)
+    assert flags.item() == 0
+
+
 # --------------------------------------------------------------------- the run together
 @cuda
 def test_serving_loop_with_graph_replay():
