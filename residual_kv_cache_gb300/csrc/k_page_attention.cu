@@ -19,7 +19,9 @@
 //   Softmax: two groups of 128 threads take a CTA's tiles in turn, each with its own score
 //   buffer, weights, sums and accumulator, so that one group's chain of dependent steps runs
 //   beside the other's, across the ends of sequences too.  The group of a segment's last tile
-//   joins the other's part to its own.  Thread t of a group owns token t (TMEM lane t).  Scores s are kept in base 2, and a page's
+//   joins the other's part to its own.  Of many short segments a group takes each whole: two
+//   of them then run side by side, where both groups' turns at one would mostly wait for its
+//   ends (1024 sequences of 256 tokens, 8 heads: 228 us by turns, @@ us whole).  Thread t of a group owns token t (TMEM lane t).  Scores s are kept in base 2, and a page's
 //   value scale 2^e is folded into the weights: the second product takes 2^(s + e - m), the
 //   sum 2^(s - m).  The reference m of a head is the maximum of s + e over some earlier
 //   tiles, so the parts hold the terms that weigh most, whatever the pages' scales.  It is
@@ -55,10 +57,16 @@ constexpr uint32_t kPaTmemCols = 256;
 constexpr uint32_t kSCol = 0, kSStride = 32;      // a score buffer for each group
 constexpr uint32_t kOCol = 64, kOStride = 64;     // an accumulator for each group
 constexpr float kRaise = 8.f;              // weights stay below 2^8
+constexpr int kSoloTiles = 8, kSoloShare = 4;   // solo: at most so many tiles, 1 / so many of the share
 
 // A run of tiles of one (sequence, head) inside a CTA's share.
 struct Segment {
   int b, h, tile0, tiles, len, slot;       // slot: workspace partial, or -1 for the whole
+  int solo;                                // one softmax group takes all of it
+  // Softmax group of tile t, where the segment begins with group g; group of the next
+  // segment's first tile.
+  __device__ __forceinline__ int group(int g, int t) const { return solo ? g : (g + t) & 1; }
+  __device__ __forceinline__ int next_group(int g) const { return solo ? g ^ 1 : (g + tiles) & 1; }
 };
 
 struct PaArgs {
@@ -327,57 +335,90 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
+    // Whatever is ready is issued: the next tile's scores once its bytes are there and its
+    // group has read its last ones, a group's second product once its weights are there.
+    // (In a fixed order, a segment's last product waited for the other group's next scores.)
     if (elect_one()) {
       constexpr uint32_t id_s = idesc_f8(128, kNQ, false), id_o = idesc_f8(128, kNP, true);
-      Ring ring, done;                                       // stages of the next S and V products
+      Ring ring;                                             // stage of the next scores
       uint32_t s_ph[2] = {1, 1}, p_ph[2] = {0, 0};
-      uint32_t k = 0, acc = 0;                               // tile; bit g: group g's last tile goes on with a sum
-      bool ok = true;
-      // O_g (+)= V^T P of the tile two before tile k (group k & 1)
-      auto pv = [&]() {
-        const uint32_t g = k & 1u;
-        ok = ok && wait_one(&p_full[g], p_ph[g], abort, status);
-        if (!ok) return;
-        p_ph[g] ^= 1u;
-        tc_fence_after();
-        const uint32_t vt = smem_u32(sm + done.stage * C::kStage);
-        const uint32_t pt = smem_u32(s_p + g * C::kPBytes);
-        // M = 128 lanes; for D = 64 the upper 64 read the K tile behind V and are unused
+      // each group's tiles between their two products, oldest lowest: 8 bits of a stage + 1,
+      // the top one set where the tile goes on with a sum
+      uint64_t queue[2] = {0, 0};
+      int s = 0, t = 0, begin = 0;
+      uint32_t ph = 0;
+      bool have = false, ended = false;
+      Segment sg;
+      long long t0 = clock64();
+      while (!(ended && queue[0] == 0 && queue[1] == 0)) {
+        bool moved = false;
+        // the tests at once: their latencies overlap
+        const int gs = have ? sg.group(begin, t) : 0;
+        const bool p_ok[2] = {mbar_test(&p_full[0], p_ph[0]), mbar_test(&p_full[1], p_ph[1])};
+        const bool bytes_ok = mbar_test(&full[ring.stage], ring.phase), s_ok = mbar_test(&s_empty[gs], s_ph[gs]);
+        const bool seg_ok = mbar_test(&q_full[s], ph);
 #pragma unroll
-        for (int i = 0; i < kTile / 32; ++i)
-          umma_f8(tmem + kOCol + g * kOStride, sdesc_rows<D>(vt + i * 32 * D, C::kHalf),
-                  sdesc_rows<128>(pt + i * 32, 16), id_o, (acc >> g & 1u) || i > 0);
-        umma_commit(&empty[done.stage]);
-        umma_commit(&p_empty[g]);
-        done.next(kST);
-      };
-      for (int s = 0, ph = 0; ok; s == kSlots - 1 ? (s = 0, ph ^= 1) : ++s) {
-        if (!(ok = wait_one(&q_full[s], ph, abort, status))) break;
-        if (seg[s].b < 0) break;
-        const int tiles = seg[s].tiles;
-        // a tile's scores are issued as soon as its group has read its last ones, two tiles
-        // ahead of the second product
-        for (int t = 0; t < tiles && ok; ++t, ++k) {
-          const uint32_t g = k & 1u;
-          if (!(ok = wait_one(&full[ring.stage], ring.phase, abort, status))) break;
-          if (!(ok = wait_one(&s_empty[g], s_ph[g], abort, status))) break;
-          s_ph[g] ^= 1u;
-          tc_fence_after();
-          const uint32_t kt = smem_u32(sm + ring.stage * C::kStage + C::kHalf);
-          const uint32_t qt = smem_u32(s_q + s * C::kQBytes);
+        for (int g = 0; g < 2; ++g) {
+          if (queue[g] != 0 && p_ok[g]) {
+            // O_g (+)= V^T P; M = 128 lanes: for D = 64 the upper 64 read the K tile behind V
+            // and are unused
+            const uint32_t e = (uint32_t)queue[g] & 0xFFu, stage = (e & 0x7Fu) - 1u;
+            queue[g] >>= 8;
+            p_ph[g] ^= 1u;
+            tc_fence_after();
+            const uint32_t vt = smem_u32(sm + stage * C::kStage);
+            const uint32_t pt = smem_u32(s_p + g * C::kPBytes);
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i)
-            umma_f8(tmem + kSCol + g * kSStride, sdesc_rows<D>(kt + i * 32, 16), sdesc_rows<D>(qt + i * 32, 16),
-                    id_s, i > 0);
-          umma_commit(&s_full[g]);
-          if (t == tiles - 1) umma_commit(&q_empty[s]);
-          ring.next(kST);
-          if (k >= 2) pv();
-          acc = t >= 2 ? acc | 1u << g : acc & ~(1u << g);   // the group's first tile of a segment begins
+            for (int i = 0; i < kTile / 32; ++i)
+              umma_f8(tmem + kOCol + g * kOStride, sdesc_rows<D>(vt + i * 32 * D, C::kHalf),
+                      sdesc_rows<128>(pt + i * 32, 16), id_o, (e & 0x80u) != 0 || i > 0);
+            umma_commit(&empty[stage]);
+            umma_commit(&p_empty[g]);
+            moved = true;
+          }
+        }
+        if (!have && !ended && seg_ok) {
+          sg = seg[s];
+          have = sg.b >= 0;
+          ended = !have;
+          t = 0;
+          moved = true;
+        } else if (have) {
+          const int g = gs;
+          if (bytes_ok && s_ok) {
+            s_ph[g] ^= 1u;
+            tc_fence_after();
+            const uint32_t kt = smem_u32(sm + ring.stage * C::kStage + C::kHalf);
+            const uint32_t qt = smem_u32(s_q + s * C::kQBytes);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+              umma_f8(tmem + kSCol + g * kSStride, sdesc_rows<D>(kt + i * 32, 16), sdesc_rows<D>(qt + i * 32, 16),
+                      id_s, i > 0);
+            umma_commit(&s_full[g]);
+            const uint64_t e = (uint64_t)(ring.stage + 1) | (t >= (sg.solo ? 1 : 2) ? 0x80u : 0u);
+            // behind the group's older ones (never more than there are stages)
+            const int n = queue[g] == 0 ? 0 : (71 - __clzll((long long)queue[g])) / 8;
+            queue[g] |= e << (8 * n);
+            ring.next(kST);
+            if (++t == sg.tiles) {
+              umma_commit(&q_empty[s]);
+              begin = sg.next_group(begin);
+              have = false;
+              if (++s == kSlots) s = 0, ph ^= 1u;
+            }
+            moved = true;
+          }
+        }
+        if (moved) {
+          t0 = clock64();
+        } else if (*abort || clock64() - t0 > kWaitCycles) {
+          if (!*abort) {
+            *abort = 1;
+            atomicOr(status, RKV_FLAG_TIMEOUT);
+          }
+          break;
         }
       }
-      for (int i = 0; i < 2 && ok; ++i, ++k)                 // the last two tiles
-        if (k >= 2 && done.stage != ring.stage) pv();
       if (*abort) {
         umma_commit(&drain);
         drain_wait(&drain, 0);
@@ -390,7 +431,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     int b = left > 0 ? s_b0 : a.batch, h = 0, tile = 0, chunk = -1, len_l = 0;    // lane i: length of sequence chunk + i
     bool first = true, ok = true;
     for (int s = 0, ph = 1; ok; s == kSlots - 1 ? (s = 0, ph ^= 1) : ++s) {
-      Segment g{-1, 0, 0, 0, 0, -1};
+      Segment g{-1, 0, 0, 0, 0, -1, 0};
       while (left > 0 && b < a.batch) {
         if (chunk != (b & ~31)) {
           chunk = b & ~31;
@@ -411,6 +452,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         g.b = b, g.h = h, g.tile0 = tile;
         g.tiles = (int)min((int64_t)(nb - tile), left);
         g.slot = g.tiles == nb ? -1 : 2 * cta + (first ? 0 : 1);
+        g.solo = g.tiles <= kSoloTiles && (int64_t)g.tiles * kSoloShare <= f1 - f0;
         left -= g.tiles;
         first = false;
         tile = 0;
@@ -510,13 +552,21 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     uint8_t* pt = s_p + wg * C::kPBytes;
     float* s_join = reinterpret_cast<float*>(sm + C::kJoinOff);
     Ring ring;                                               // stage of the segment's tile t
-    uint32_t k = 0, s_ph = 0, p_ph = 0, j_ph[2] = {0, 0};    // k: the CTA's tile
+    uint32_t s_ph = 0, p_ph = 0, j_ph[2] = {0, 0};
+    int begin = 0;                                           // group of the segment's first tile
     bool ok = true;
     for (int s = 0, ph = 0; true; s == kSlots - 1 ? (s = 0, ph ^= 1) : ++s) {
       ok = ok && wait_warp(&q_full[s], ph, abort, status);
       if (vote_group(wg, !ok)) break;
       const Segment g = seg[s];
       if (g.b < 0) break;
+      if (g.solo && begin != wg) {                           // the other group's
+        begin ^= 1;
+        for (int t = 0; t < g.tiles; ++t) ring.next(kST);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_empty[s]);
+        continue;
+      }
       float m[kH], l[kH], qf[kH];
 #pragma unroll
       for (int h = 0; h < kH; ++h) m[h] = -FLT_MAX, l[h] = 0.f, qf[h] = s_qf[s][h];
@@ -524,11 +574,12 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       if (lane == 0) mbar_arrive(&q_empty[s]);
       const uint32_t o_tm = tm + kOCol + wg * kOStride;
       bool first = true;                                     // the group's first tile of the segment
-      for (int t = 0; t < g.tiles; ++t, ++k) {
+      const int owner = g.group(begin, g.tiles - 1);         // group of the last tile
+      for (int t = 0; t < g.tiles; ++t) {
         const int stage = ring.stage;
         const uint32_t st_ph = ring.phase;
         ring.next(kST);
-        if ((k & 1u) != (uint32_t)wg) continue;
+        if (g.group(begin, t) != wg) continue;
         ok = ok && wait_warp(&full[stage], st_ph, abort, status) && wait_warp(&s_full[wg], s_ph, abort, status);
         s_ph ^= 1u;
         float x[kH];
@@ -632,7 +683,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         mbar_arrive(&p_full[wg]);
         first = false;
       }
-      const int owner = (int)((k - 1) & 1u);                 // group of the last tile
+      begin = g.next_group(begin);
       if (first && ok) continue;                             // none of the tiles was the group's
       // the group's sums and accumulator
       if (ok && !first) {
@@ -667,7 +718,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
 #pragma unroll
       for (int h = 0; h < kH; ++h)
         l[h] = s_red[wg][0][h] + s_red[wg][1][h] + s_red[wg][2][h] + s_red[wg][3][h];
-      if (g.tiles > 1) {                                     // the other group's part
+      if (g.tiles > 1 && !g.solo) {                          // the other group's part
         const int other = owner ^ 1;
         float* part = s_join + other * (C::kJoin / 4);
         if (wg == other) {
@@ -702,7 +753,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         for (int h = 0; h < kH; ++h) {
           if (h < a.G) {
             if (g.slot < 0) {
-              if (tok < D) a.out[(row + h) * D + tok] = __float2bfloat16(l[h] != 0.f ? o[h] / l[h] : 0.f);
+              if (tok < D) a.out[(row + h) * D + tok] = __float2bfloat16(l[h] != 0.f ? __fdividef(o[h], l[h]) : 0.f);
               if (a.lse && tok == 0)
                 a.lse[row + h] = l[h] != 0.f ? (m[h] + log2f(l[h])) * 0.6931471805599453f : -INFINITY;
             } else {
