@@ -21,7 +21,7 @@
 //   beside the other's, across the ends of sequences too.  The group of a segment's last tile
 //   joins the other's part to its own.  Of many short segments a group takes each whole: two
 //   of them then run side by side, where both groups' turns at one would mostly wait for its
-//   ends (1024 sequences of 256 tokens, 8 heads: 228 us by turns, @@ us whole).  Thread t of a group owns token t (TMEM lane t).  Scores s are kept in base 2, and a page's
+//   ends (1024 sequences of 256 tokens, 8 heads: 228 us by turns, 190 us whole).  Thread t of a group owns token t (TMEM lane t).  Scores s are kept in base 2, and a page's
 //   value scale 2^e is folded into the weights: the second product takes 2^(s + e - m), the
 //   sum 2^(s - m).  The reference m of a head is the maximum of s + e over some earlier
 //   tiles, so the parts hold the terms that weigh most, whatever the pages' scales.  It is
@@ -204,6 +204,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   volatile int* abort = &s_abort;
   int* status = a.flags ? a.flags : &s_status;               // where a wait that gives up reports
 
+  // of a small batch every warp reads the lengths at once, ahead of the set-up
+  bool any_bad = false;
+  int64_t mine = a.batch <= 32 && lane < a.batch ? tiles_of(length_of(a, lane, any_bad)) : 0;
   if (tid == 0) {
     tma_prefetch(&tm_k);
     tma_prefetch(&tm_v);
@@ -225,8 +228,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
 
   // the call's tiles, and the sequence in which this CTA's share begins
   const int cta = blockIdx.x;
-  int64_t total = 0, incl = 0, mine = 0, f0 = 0, f1 = 0;
-  bool any_bad = false;
+  int64_t total = 0, incl = 0, f0 = 0, f1 = 0;
   auto cut = [&]() {                                         // the share
     const Shares shares(total * a.N, gridDim.x);
     f0 = cta < shares.C ? shares.start(cta) : 0;
@@ -234,7 +236,6 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   };
   if (a.batch <= 32) {
     // up to a warp's width every warp scans by itself
-    mine = lane < a.batch ? tiles_of(length_of(a, lane, any_bad)) : 0;
     incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -426,7 +427,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     }
   } else if (warp == 2) {
     // ------------------------------------------------- segments and their query tiles
-    constexpr int kW = D / 64;                               // words (2 values) per lane and head
+    // eight lanes a head: D / 8 values each, four heads at a time
+    constexpr int kW = D / 16, kRounds = (kH + 3) / 4;       // words (2 values) per lane; passes
+    const int sub = lane & 7;
     int64_t left = f1 - f0;                                  // tiles of the share still to come
     int b = left > 0 ? s_b0 : a.batch, h = 0, tile = 0, chunk = -1, len_l = 0;    // lane i: length of sequence chunk + i
     bool first = true, ok = true;
@@ -459,14 +462,19 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         if (++h == a.N) h = 0, ++b;
         break;
       }
-      uint32_t raw[kH][kW];                                  // loaded while the slot is awaited
+      uint32_t raw[kRounds][kW];                             // loaded while the slot is awaited
       if (g.b >= 0) {
-        const __nv_bfloat16* q = a.q + g.b * a.qst.row + (int64_t)g.h * a.G * a.qst.head + lane * (2 * kW);
+        const __nv_bfloat16* q = a.q + g.b * a.qst.row + (int64_t)g.h * a.G * a.qst.head + sub * (2 * kW);
 #pragma unroll
-        for (int i = 0; i < kH; ++i)
+        for (int i = 0; i < kRounds; ++i) {
+          const int head = 4 * i + (lane >> 3);
 #pragma unroll
-          for (int e = 0; e < kW; ++e)
-            raw[i][e] = i < a.G ? __ldg(reinterpret_cast<const uint32_t*>(q + i * a.qst.head) + e) : 0u;
+          for (int e = 0; e < kW; e += 4) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (head < a.G) v = __ldg(reinterpret_cast<const uint4*>(q + head * a.qst.head + 2 * e));
+            raw[i][e] = v.x, raw[i][e + 1] = v.y, raw[i][e + 2] = v.z, raw[i][e + 3] = v.w;
+          }
+        }
       }
       if (!(ok = wait_warp(&q_empty[s], ph, abort, status))) break;
       if (lane == 0) {
@@ -475,40 +483,47 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       }
       if (g.b >= 0) {
         uint8_t* qt = s_q + s * C::kQBytes;
-        const int col = lane * 2 * kW;
 #pragma unroll
-        for (int i = 0; i < kH; ++i) {
+        for (int i = 0; i < kRounds; ++i) {
+          const int head = 4 * i + (lane >> 3);
           // the largest finite magnitude, on the bits; what is not finite becomes NaN
           uint32_t m2 = 0;
 #pragma unroll
           for (int e = 0; e < kW; ++e) {
-            const uint32_t mag = raw[i][e] & 0x7FFF7FFFu;
-            m2 = __vmaxu2(m2, mag & ~__vcmpgeu2(mag, 0x7F807F80u));
-            raw[i][e] |= __vcmpgeu2(mag, 0x7F807F80u) & 0x7FFF7FFFu;
+            const uint32_t mag = raw[i][e] & 0x7FFF7FFFu, over = __vcmpgeu2(mag, 0x7F807F80u);
+            m2 = __vmaxu2(m2, mag & ~over);
+            raw[i][e] |= over & 0x7FFF7FFFu;
           }
-          const uint32_t amax = __reduce_max_sync(0xffffffffu, max(m2 >> 16, m2 & 0xFFFFu));   // bf16 bits
+          uint32_t amax = max(m2 >> 16, m2 & 0xFFFFu);       // bf16 bits
+#pragma unroll
+          for (int o = 4; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
           // 2^7 <= amax 2^-ex < 2^8
           const int ex = max((int)(amax >> 7) - 127, -100) - 7;
           const float mul = __uint_as_float((uint32_t)(127 - ex) << 23);
-          uint32_t hi = 0, lo = 0;
+          uint32_t hi[kW / 2], lo[kW / 2];
 #pragma unroll
           for (int e = 0; e < kW; ++e) {
             const float x = __uint_as_float(raw[i][e] << 16) * mul, y = __uint_as_float(raw[i][e] & 0xFFFF0000u) * mul;
             const uint32_t c = e4m3x2(x, y);
             const float2 r = from_e4m3x2(c);
-            hi |= c << (16 * e);
-            lo |= e4m3x2((x - r.x) * 16.f, (y - r.y) * 16.f) << (16 * e);
+            const uint32_t d = e4m3x2((x - r.x) * 16.f, (y - r.y) * 16.f);
+            hi[e / 2] = e & 1 ? hi[e / 2] | c << 16 : c;
+            lo[e / 2] = e & 1 ? lo[e / 2] | d << 16 : d;
           }
-          uint8_t* oh = qt + chunk_off<D>(i, col >> 4) + (col & 15);
-          uint8_t* ol = qt + chunk_off<D>(kGP + i, col >> 4) + (col & 15);
-          if (kW == 2) {
-            *reinterpret_cast<uint32_t*>(oh) = hi;
-            *reinterpret_cast<uint32_t*>(ol) = lo;
-          } else {
-            *reinterpret_cast<uint16_t*>(oh) = (uint16_t)hi;
-            *reinterpret_cast<uint16_t*>(ol) = (uint16_t)lo;
+          if (head < kH) {
+            // the lane's D / 8 bytes of the head's rows
+            const int col = sub * (D / 8);
+            uint8_t* oh = qt + chunk_off<D>(head, col >> 4) + (col & 15);
+            uint8_t* ol = qt + chunk_off<D>(kGP + head, col >> 4) + (col & 15);
+            if (kW == 8) {
+              *reinterpret_cast<uint4*>(oh) = make_uint4(hi[0], hi[1], hi[kW / 2 - 2], hi[kW / 2 - 1]);
+              *reinterpret_cast<uint4*>(ol) = make_uint4(lo[0], lo[1], lo[kW / 2 - 2], lo[kW / 2 - 1]);
+            } else {
+              *reinterpret_cast<uint2*>(oh) = make_uint2(hi[0], hi[1]);
+              *reinterpret_cast<uint2*>(ol) = make_uint2(lo[0], lo[1]);
+            }
+            if (sub == 0) s_qf[s][head] = __uint_as_float((uint32_t)(127 + ex) << 23) * a.scale_log2;
           }
-          if (lane == 0) s_qf[s][i] = __uint_as_float((uint32_t)(127 + ex) << 23) * a.scale_log2;
         }
       }
       fence_proxy_async_smem();
