@@ -455,6 +455,28 @@ def test_prompt_attention_broadcast_rows_and_heads_in_place_and_without_keys():
 
 
 @cuda
+@pytest.mark.parametrize("B", [6, 32, 33])
+def test_prompt_attention_of_more_pairs_than_ctas(B):
+    """Every CTA takes several pairs, of sequences of all lengths, with fewer and with more keys
+    than queries, among them empty ones."""
+    g = np.random.default_rng(900 + B)
+    top = 6000 // B
+    lq = np.where(g.random(B) < 0.15, 0, g.integers(1, top, size=B))
+    lq[0] = top
+    lk = np.where(g.random(B) < 0.5, lq, g.integers(0, 2 * top, size=B))
+    Hq, N, D = 30, 10, 64
+    assert ((-(-lq // 128) * 3 + 1) // 2).sum() * N > 2 * 160
+    cq, ck = _cu(lq.tolist()), _cu(lk.tolist())
+    q = randn(cq[-1], Hq, D, seed=861)
+    k, v = randn(ck[-1], N, D, seed=862), randn(ck[-1], N, D, seed=863)
+    flags = i32([0])
+    out = rkv.prompt_attention(q, k, v, i32(cq), i32(ck), flags=flags)
+    assert flags.item() == 0
+    ref, _, a, big = OP.prompt_attention(np64(q), np64(k), np64(v), cq, ck, 0.125)
+    close(out, ref, a, big, D, 2.0 ** -8)
+
+
+@cuda
 @pytest.mark.parametrize("B", [33, 700, 8192])
 def test_many_short_sequences(B):
     """Batches past a warp, past a block and at the limit, half the sequences empty: prompts of
