@@ -364,7 +364,9 @@ rkv_status rkv_retrieve_noalloc(const void* queries, const int32_t* q_pos, int32
  * device when the graph runs.
  *   flags (device, int32) or NULL: RKV_FLAG_* bits are ORed into it (the caller clears it).
  * What only the device can see never faults: lengths, offsets and block ids are checked
- * there, and what is out of range is treated as absent.
+ * there, and what is out of range is treated as absent.  A call in whose flags
+ * RKV_FLAG_TIMEOUT appears gave up a wait (about a second): its output is incomplete.
+ * An output must not overlap an input or another output but where a call says so.
  * ------------------------------------------------------------------------- */
 
 /*
@@ -393,7 +395,7 @@ typedef struct {
  *   block_table (device, int32) [batch, max_blocks]; entries past a sequence's pages are
  *     ignored.
  *   seq_len     (device, int32) [batch]  positions stored (after a step's appends).
- * batch in [1, 8192]; max_blocks * block_tokens < 2^31.
+ * batch in [1, 8192]; max_blocks * block_tokens at most 2^31 - 128.
  */
 typedef struct {
   int32_t* block_table;
@@ -452,7 +454,8 @@ rkv_status rkv_page_release(const rkv_page_table* table, const int32_t* finished
  * the rows that the page held before are rounded again at the new scale (exact but for
  * values below 2^-6 s).
  * Pages of different sequences must differ where they are written.
- * A row whose position or page is out of range is left out (RKV_FLAG_BAD_INDEX).
+ * A row whose position or page is out of range is left out (RKV_FLAG_BAD_INDEX), and so
+ * are offsets past n_rows.
  * Errors (nothing launched): RKV_EINVAL, RKV_EALIGN, RKV_ECUDA.
  */
 rkv_status rkv_page_append(const rkv_pages* pages, const rkv_page_table* table, const void* k,
@@ -506,7 +509,10 @@ rkv_status rkv_page_attention_workspace(const rkv_pages* pages, const rkv_page_t
  * the last one have no effect, whatever they hold.  Within a sequence a NaN or infinity of V
  * reaches rows that see it and may reach up to 255 rows before it (weights of 0 times NaN).
  * Scores are exact bf16 products summed in fp32; the weights enter the second product as
- * bf16; sums are fp32.  batch in [1, 8192]; total_q and total_k at most 2^30.
+ * bf16; sums are fp32.  batch in [1, 8192]; total_q and total_k at most 2^30, total_q *
+ * n_q_heads at most 2^33.
+ * Rows of out must not overlap each other, lse or k and v; out may be q itself.  q, k and v
+ * may overlap, and a stride may be 0 (one row or head for all).
  * Offsets that decrease or pass total_q / total_k are cut (RKV_FLAG_BAD_INDEX).
  * Errors (nothing launched): RKV_EINVAL, RKV_EALIGN, RKV_ECAPACITY (workspace), RKV_ECUDA.
  */

@@ -350,6 +350,7 @@ __device__ __forceinline__ bool find_run(const AppendArgs& p, int shift, Run& ou
         if (rows > 0 && r0 >= 0 && rows <= len && len <= (int64_t)p.max_blocks << p.shift) {
           lo = (int)(len - rows);
           hi = lo + (int)max((int64_t)0, min(rows, (int64_t)p.n_rows - r0));
+          if (checks && hi - lo < rows) raise_flag(p.flags, RKV_FLAG_BAD_INDEX);
         } else if (checks) {
           raise_flag(p.flags, RKV_FLAG_BAD_INDEX);
         }
@@ -580,8 +581,9 @@ rkv_status check_table(const rkv_page_table* t, int block_tokens) {
   if (!t) return fail_with(RKV_EINVAL, "table is NULL");
   if (!t->block_table || !t->seq_len) return fail_with(RKV_EINVAL, "NULL block_table or seq_len");
   if (t->batch < 1 || t->batch > kMaxBatch) return fail_with(RKV_EINVAL, "batch must be in 1..%d", kMaxBatch);
-  if (t->max_blocks < 1 || (int64_t)t->max_blocks * block_tokens > INT32_MAX)
-    return fail_with(RKV_EINVAL, "max_blocks must be >= 1 and max_blocks * block_tokens below 2^31");
+  // (the reads count positions up to the end of a tile of 128)
+  if (t->max_blocks < 1 || (int64_t)t->max_blocks * block_tokens > INT32_MAX - 127)
+    return fail_with(RKV_EINVAL, "max_blocks must be >= 1 and max_blocks * block_tokens at most 2^31 - 128");
   return RKV_OK;
 }
 

@@ -932,8 +932,8 @@ rkv_status check_prompt(const rkv_prompt* pr) {
     return fail_with(RKV_EINVAL, "n_q_heads must be a multiple of n_kv_heads, at most 65535");
   if (p.batch < 1 || p.batch > kMaxBatch) return fail_with(RKV_EINVAL, "batch must be in 1..%d", kMaxBatch);
   if (p.total_q < 0 || p.total_k < 0 || p.total_q > 1 << 30 || p.total_k > 1 << 30 ||
-      (int64_t)p.total_q * p.n_q_heads > (int64_t)1 << 38)
-    return fail_with(RKV_EINVAL, "total_q and total_k must be in 0..2^30, total_q * n_q_heads at most 2^38");
+      (int64_t)p.total_q * p.n_q_heads > (int64_t)1 << 33)
+    return fail_with(RKV_EINVAL, "total_q and total_k must be in 0..2^30, total_q * n_q_heads at most 2^33");
   if (!(p.scale > 0.0 && p.scale < 1e30)) return fail_with(RKV_EINVAL, "scale must be finite and > 0");
   return RKV_OK;
 }
@@ -965,6 +965,12 @@ extern "C" rkv_status rkv_prompt_attention(const rkv_prompt* pr, int32_t* flags,
       return fail_with(RKV_EALIGN, "strides must be >= 0 and multiples of 16 bytes");
   if (!is_aligned(p.q, 16) || !is_aligned(p.k, 16) || !is_aligned(p.v, 16) || !is_aligned(p.out, 16))
     return fail_with(RKV_EALIGN, "q, k, v and out must be 16-byte aligned");
+  // out's rows of D: apart, in one order of the strides or the other
+  const int64_t row = p.out_strides[0], head = p.out_strides[1], Dl = p.head_dim;
+  const bool rows1 = p.total_q == 1, heads1 = p.n_q_heads == 1;
+  const bool apart = (heads1 || head >= Dl) && (rows1 || row >= Dl) &&
+                     (rows1 || heads1 || row >= (p.n_q_heads - 1) * head + Dl || head >= (p.total_q - 1) * row + Dl);
+  if (!apart) return fail_with(RKV_EINVAL, "rows of out overlap");
   size_t need = 0;
   if (rkv_status st = rkv_prompt_attention_workspace(pr, &need)) return st;
   if (p.workspace_bytes < need || (need > 0 && !p.workspace))

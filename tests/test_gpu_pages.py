@@ -242,6 +242,23 @@ def test_append_leaves_out_what_is_out_of_range():
         assert flags.item() == rkv.FLAG_BAD_INDEX
 
 
+@cuda
+def test_append_flags_rows_that_are_not_there():
+    """Offsets past the rows: the rows that exist are stored."""
+    P, N, D = 16, 2, 64
+    x = randn(5, N, D, seed=18)
+    for narrow in (False, True):                            # both kernels (by rows a sequence)
+        B = 5 if narrow else 1
+        k8, v8, ks, vs = _cache(3, N, P, D, 19)
+        rc, rs = _f8(k8), np64(ks)
+        flags = i32([0])
+        rkv.page_append(x, x, k8, v8, ks, vs, i32([[1, 2]] * B), i32([9] + [0] * (B - 1)), i32([0] + [9] * B),
+                        flags=flags)
+        OP.append(np64(x), rc, rs, [[1, 2]] * B, [5] + [0] * (B - 1), [0] + [5] * B, P)
+        assert np.array_equal(np64(ks), rs) and np.array_equal(_f8(k8), rc)
+        assert flags.item() == rkv.FLAG_BAD_INDEX
+
+
 # --------------------------------------------------------------------- page attention
 def _paged(lens, N, P, D, seed, poison=True, spread=0):
     """Pages holding random K/V for sequences of these lengths; NaN codes and scales

@@ -58,7 +58,7 @@ BAD_PAGES = [(dict(k=None), -1), (dict(v_scale=None), -1), (dict(k=A + 8), -2), 
              (dict(head_dim=96), -1), (dict(block_tokens=8), -1), (dict(block_tokens=48), -1),
              (dict(num_blocks=0), -1), (dict(num_blocks=1 << 22, n_kv_heads=8), -1)]
 BAD_TABLE = [(dict(block_table=None), -1), (dict(seq_len=None), -1), (dict(batch=0), -1),
-             (dict(batch=8193), -1), (dict(max_blocks=0), -1), (dict(max_blocks=1 << 26), -1)]
+             (dict(batch=8193), -1), (dict(max_blocks=0), -1), (dict(max_blocks=1 << 26), -1), (dict(max_blocks=(1 << 25) - 1), -1)]
 
 
 def test_plan_and_release_refusals(lib):
@@ -153,6 +153,11 @@ def test_prompt_refusals(lib):
                 dict(v_strides=S(1024, -128)), dict(out_strides=S(4096, 4))):
         assert call(**bad) == -2, bad
     assert call(total_q=0) == 0
+    # rows of out that overlap, and sizes whose items would not fit their counters
+    for bad in (dict(out_strides=S(0, 128)), dict(out_strides=S(4096, 0)), dict(out_strides=S(4088, 128)),
+                dict(out_strides=S(4096, 120)), dict(out_strides=S(128, 1272)),
+                dict(total_q=2 ** 30, n_q_heads=16)):
+        assert call(**bad) == -1, bad
 
     def workspace(**kw):
         d = dict(total_q=500, total_k=500, n_q_heads=32, n_kv_heads=8, head_dim=128, batch=2, scale=0.1)
