@@ -34,8 +34,8 @@
 // o), at most two a CTA, which the second kernel joins in tile order: no atomics, the same
 // bits on every run.
 //
-// Warps: 0 TMA producer, 1 MMA issuer, 2 queries and segment list, 3 page scales, 4-7 and
-// 8-11 softmax.
+// Warps: 0 TMA producer, 1 MMA issuer, 2 queries and segment list, 3 page scales and the rows
+// of empty sequences, 4-7 and 8-11 softmax.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
@@ -69,6 +69,12 @@ struct Segment {
   __device__ __forceinline__ int next_group(int g) const { return solo ? g ^ 1 : (g + tiles) & 1; }
 };
 
+// What the joining kernel has to know of a share's partial.
+struct PartialOf {
+  int row;                                 // b N + h, -1: there is none
+  int ends;                                // 1: begins its (b, h), 2: ends it
+};
+
 struct PaArgs {
   const float *ks, *vs;
   const int32_t *table, *seq_len;
@@ -77,6 +83,7 @@ struct PaArgs {
   __nv_bfloat16* out;
   float* lse;
   int32_t* flags;
+  PartialOf* info;                         // of partial 2 c + i, the i-th that share c may leave
   float *pm, *pl, *po;                     // partials [2 kMaxCtas][G], [..][G], [..][G][D]
   int batch, N, G, shift, num_blocks, max_blocks;
   float scale_log2;
@@ -433,6 +440,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     int64_t left = f1 - f0;                                  // tiles of the share still to come
     int b = left > 0 ? s_b0 : a.batch, h = 0, tile = 0, chunk = -1, len_l = 0;    // lane i: length of sequence chunk + i
     bool first = true, ok = true;
+    if (lane < 2) a.info[2 * cta + lane] = {-1, 0};
+    __syncwarp();
     for (int s = 0, ph = 1; ok; s == kSlots - 1 ? (s = 0, ph ^= 1) : ++s) {
       Segment g{-1, 0, 0, 0, 0, -1, 0};
       while (left > 0 && b < a.batch) {
@@ -455,6 +464,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         g.b = b, g.h = h, g.tile0 = tile;
         g.tiles = (int)min((int64_t)(nb - tile), left);
         g.slot = g.tiles == nb ? -1 : 2 * cta + (first ? 0 : 1);
+        if (g.slot >= 0 && lane == 0) a.info[g.slot] = {b * a.N + h, (tile == 0 ? 1 : 0) | (tile + g.tiles == nb ? 2 : 0)};
         g.solo = g.tiles <= kSoloTiles && (int64_t)g.tiles * kSoloShare <= f1 - f0;
         left -= g.tiles;
         first = false;
@@ -558,6 +568,19 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_empty[s]);
+    }
+    // the rows of empty sequences, dealt out to the CTAs
+    const int chunks = a.N * a.G * (D / 8);
+    for (int b0 = cta; b0 < a.batch; b0 += 32 * gridDim.x) {
+      bool bad;
+      const int b = b0 + lane * gridDim.x;
+      uint32_t none = __ballot_sync(0xffffffffu, b < a.batch && length_of(a, b, bad) == 0);
+      for (; none != 0; none &= none - 1) {
+        const int64_t e = b0 + (__ffs(none) - 1) * gridDim.x;
+        uint4* out = reinterpret_cast<uint4*>(a.out) + e * chunks;
+        for (int i = lane; i < chunks; i += 32) out[i] = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = lane; a.lse && i < a.N * a.G; i += 32) a.lse[e * a.N * a.G + i] = -INFINITY;
+      }
     }
   } else if (warp >= kSoftWarp0) {
     // ---------------------------------------------------------------------- softmax
@@ -786,81 +809,100 @@ __global__ void __launch_bounds__(kPaThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, kPaTmemCols);
 }
 
-// Joins the partials of each (sequence, head) that several shares hold, in their order, and
-// zeroes the rows of empty sequences.  Grid (batch, N, G), D threads.
+// Joins the partials of the (sequence, key/value head) that share blockIdx.x begins and does
+// not end: its own, then those of the shares after it up to the one that ends it.  Grid
+// (shares, G / 4 rounded up).  A warp takes a query head, or, of fewer than four, a part of its
+// partials; a row of D floats is one load of D / 4 lanes, kJoinAhead of them in flight.  (A
+// block for each sequence and head, each of which found its shares from the lengths, took 40 us
+// longer for 1024 sequences; partials read one after the other 16 us longer for 38 of them.)
+constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32, kJoinAhead = 8;
+
 template <int D>
-__global__ void __launch_bounds__(D) page_attention_join_kernel(PaArgs a, int grid) {
-  const int b = blockIdx.x, h = blockIdx.y, g = blockIdx.z, tid = threadIdx.x;
-  __shared__ int64_t s_all[D / 32], s_before[D / 32];
-  __shared__ float s_m[kMaxCtas], s_l[kMaxCtas], s_red[2][D / 32];
-  bool bad;
-  const int nb = tiles_of(length_of(a, b, bad));
-  int64_t before = 0, all = 0;
-  for (int i = tid; i < a.batch; i += D) {
-    const int n = tiles_of(length_of(a, i, bad));
-    all += n;
-    if (i < b) before += n;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
-  if ((tid & 31) == 0) s_all[tid >> 5] = all, s_before[tid >> 5] = before;
-  __syncthreads();
-  all = before = 0;
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) all += s_all[i], before += s_before[i];
-  const int64_t row = (((int64_t)b * a.N + h) * a.G + g);
-  const int64_t total = all * a.N, f0 = before * a.N + (int64_t)h * nb, f1 = f0 + nb;
-  const Shares shares(total, grid);
-  // the share in which the head's tiles begin, and the last one that has any of them
-  int c0 = total > 0 ? min(shares.C - 1, (int)((float)f0 / (float)total * shares.C)) : 0, c1;
-  while (c0 > 0 && shares.start(c0) > f0) --c0;
-  while (c0 + 1 < shares.C && shares.start(c0 + 1) <= f0) ++c0;
-  c1 = c0;
-  while (c1 + 1 < shares.C && shares.start(c1 + 1) < f1) ++c1;
+__global__ void __launch_bounds__(kJoinThreads, 8) page_attention_join_kernel(PaArgs a, int grid) {
+  constexpr int kLanes = D / 4, kRows = 32 / kLanes, kChunks = kMaxCtas / 32;
+  const int c0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ float4 s_o[kJoinWarps][kLanes];
+  __shared__ float s_f[kJoinWarps][kMaxCtas];
   pdl_wait_previous_grid();
-  if (nb == 0) {
-    a.out[row * D + tid] = __float2bfloat16(0.f);
-    if (a.lse && tid == 0) a.lse[row] = -INFINITY;
-    return;
+  // the share's last partial, if it goes on in the next one
+  const int4 both = __ldcg(reinterpret_cast<const int4*>(a.info + 2 * c0));
+  const PartialOf p0{both.x, both.y}, p1{both.z, both.w};
+  const bool second = p1.row >= 0;
+  if (!second && (p0.row < 0 || p0.ends != 1)) return;
+  const int first = second ? 2 * c0 + 1 : 2 * c0;
+  int n = 0;                                 // partials
+  for (int i0 = 1; n == 0 && c0 + i0 < grid; i0 += 32) {
+    const int c = c0 + i0 + lane;
+    const uint32_t at_end = __ballot_sync(0xffffffffu, c < grid && (__ldcg(&a.info[2 * c].ends) & 2));
+    if (at_end) n = i0 + __ffs(at_end);
   }
-  if (c0 == c1) return;                      // written by its one share
-  // partial i: the first segment of share c0 + i, but for c0's unless it begins there
-  const int n = c1 - c0 + 1, first = shares.start(c0) == f0 ? 2 * c0 : 2 * c0 + 1;
-  float m = -FLT_MAX;
-  for (int i = tid; i < n; i += D) {
-    const int64_t at = (int64_t)(i == 0 ? first : 2 * (c0 + i)) * a.G + g;
-    s_m[i] = __ldcg(a.pm + at);
-    s_l[i] = __ldcg(a.pl + at);
-    m = fmaxf(m, s_m[i]);
+  if (n == 0) return;                        // of a call that gave up
+  const int heads = a.G > 2 ? 4 : a.G;       // of this CTA
+  const int parts = kJoinWarps / heads, part = warp / heads, g = blockIdx.y * heads + warp % heads;
+  const bool live = g < a.G;
+  const int64_t row = (int64_t)(second ? p1.row : p0.row) * a.G + g;
+  auto slot_of = [&](int i) { return (i == 0 ? first : 2 * (c0 + i)) * a.G + g; };
+  float m = -FLT_MAX, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (live) {
+    float f[kChunks], pl[kChunks];           // lane i: partials i, 32 + i, ..
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const int i = 32 * c + lane;
+      f[c] = -FLT_MAX, pl[c] = 0.f;
+      if (i < n) f[c] = __ldcg(a.pm + slot_of(i)), pl[c] = __ldcg(a.pl + slot_of(i));
+    }
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) m = fmaxf(m, f[c]);
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      if (32 * c >= n) break;
+      const float w = ex2_approx(f[c] - m);
+      l += pl[c] * w;
+      s_f[warp][32 * c + lane] = w;
+    }
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
+    __syncwarp();
+    const float4* po = reinterpret_cast<const float4*>(a.po) + lane % kLanes;
+    const int step = parts * kRows;
+    for (int i0 = part * kRows + lane / kLanes; i0 < n; i0 += kJoinAhead * step) {
+      float4 x[kJoinAhead];
+#pragma unroll
+      for (int u = 0; u < kJoinAhead; ++u) {
+        x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i0 + u * step < n) x[u] = __ldcg(po + (int64_t)slot_of(i0 + u * step) * kLanes);
+      }
+#pragma unroll
+      for (int u = 0; u < kJoinAhead; ++u) {
+        const float w = i0 + u * step < n ? s_f[warp][i0 + u * step] : 0.f;
+        o.x = fmaf(x[u].x, w, o.x), o.y = fmaf(x[u].y, w, o.y);
+        o.z = fmaf(x[u].z, w, o.z), o.w = fmaf(x[u].w, w, o.w);
+      }
+    }
+    __syncwarp();
+    if (kRows == 2) {
+      o.x += __shfl_xor_sync(0xffffffffu, o.x, 16), o.y += __shfl_xor_sync(0xffffffffu, o.y, 16);
+      o.z += __shfl_xor_sync(0xffffffffu, o.z, 16), o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
+    }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((tid & 31) == 0) s_red[0][tid >> 5] = m;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) m = fmaxf(m, s_red[0][i]);
-  float l = 0.f;
-  for (int i = tid; i < n; i += D) {
-    const float f = ex2_approx(s_m[i] - m);
-    l += s_l[i] * f;
-    s_m[i] = f;
+  if (parts > 1) {                           // the parts' sums, in their order
+    if (lane < kLanes) s_o[warp][lane] = o;
+    __syncthreads();
+    for (int k = 1; part == 0 && k < parts; ++k) {
+      const float4 x = s_o[warp + k * heads][lane % kLanes];
+      o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
+    }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  if ((tid & 31) == 0) s_red[1][tid >> 5] = l;
-  __syncthreads();
-  l = 0.f;
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) l += s_red[1][i];
-  float o = 0.f;
-#pragma unroll 8
-  for (int i = 0; i < n; ++i)
-    o = fmaf(__ldcg(a.po + ((int64_t)(i == 0 ? first : 2 * (c0 + i)) * a.G + g) * D + tid), s_m[i], o);
-  a.out[row * D + tid] = __float2bfloat16(l != 0.f ? o / l : 0.f);
-  if (a.lse && tid == 0) a.lse[row] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  if (!live || part > 0) return;
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+  if (lane < kLanes)
+    reinterpret_cast<uint2*>(a.out + row * D)[lane] =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  if (a.lse && lane == 0) a.lse[row] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 rkv_status check_heads(const rkv_pages* pages, int n_q_heads) {
@@ -888,8 +930,8 @@ cudaError_t launch_all(const CUtensorMap& mk, const CUtensorMap& mv, const PaArg
                              : launch_main<D, 16>(mk, mv, a, grid, dev, s);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(a.batch, a.N, a.G);
-  lc.blockDim = dim3(D);
+  lc.gridDim = dim3(grid, ceil_div(a.G, 4));
+  lc.blockDim = dim3(kJoinThreads);
   lc.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -912,7 +954,7 @@ extern "C" rkv_status rkv_page_attention_workspace(const rkv_pages* pages, const
   if (rkv_status st = check_table(table, pages->block_tokens)) return st;
   if (rkv_status st = check_heads(pages, n_q_heads)) return st;
   const size_t G = n_q_heads / pages->n_kv_heads;
-  *bytes = sizeof(float) * 2 * kMaxCtas * G * (2 + (size_t)pages->head_dim);
+  *bytes = 2 * kMaxCtas * (sizeof(PartialOf) + sizeof(float) * G * (2 + (size_t)pages->head_dim));
   return RKV_OK;
 }
 
@@ -945,7 +987,8 @@ extern "C" rkv_status rkv_page_attention(const rkv_pages* pages, const rkv_page_
   a.lse = lse, a.flags = flags;
   a.batch = table->batch;
   a.N = pages->n_kv_heads, a.G = n_q_heads / a.N;
-  a.pm = static_cast<float*>(workspace);
+  a.info = static_cast<PartialOf*>(workspace);
+  a.pm = reinterpret_cast<float*>(a.info + 2 * kMaxCtas);
   a.pl = a.pm + 2 * kMaxCtas * a.G;
   a.po = a.pl + 2 * kMaxCtas * a.G;
   a.shift = 4;
