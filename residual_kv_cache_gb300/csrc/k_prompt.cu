@@ -831,15 +831,18 @@ constexpr int kJoinThreads = 256;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PrArgs a, int grid) {
-  constexpr int kE = D / 32;
+  constexpr int kE = D / 32, kAhead = 8;                     // partials' rows in flight
   const int c = blockIdx.x, t = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait_previous_grid();
   const Partial own = a.info[2 * c + 1];
   if (!own.valid || own.last) return;
-  int end = c + 1;
-  while (end < grid && a.info[2 * end].valid && !a.info[2 * end].last) ++end;
-  end = min(end, grid - 1);
-  const int n = end - c + 1;
+  int n = 0;                                                 // partials
+  for (int e0 = c + 1; n == 0 && e0 < grid; e0 += 32) {
+    const int e = e0 + lane;
+    const uint32_t at_end = __ballot_sync(0xffffffffu, e < grid && a.info[2 * e].valid && a.info[2 * e].last);
+    if (at_end) n = e0 - c + __ffs(at_end);
+  }
+  if (n == 0) return;                                        // of a call that gave up
   auto slot_of = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
   for (int r = blockIdx.z * (kJoinThreads / 32) + warp; r < own.rows[t]; r += gridDim.z * (kJoinThreads / 32)) {
     float m = -INFINITY, l = 0.f, o[kE];
@@ -864,20 +867,28 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PrArgs a, int
       m = top;
 #pragma unroll
       for (int e = 0; e < kE; ++e) o[e] *= fm;
-#pragma unroll 4
-      for (int i = i0; i < min(n, i0 + 32); ++i) {
-        const float w = __shfl_sync(0xffffffffu, f, i - i0);
-        const float* src = a.po + (((int64_t)slot_of(i) * 2 + t) * kRows + r) * D + lane * kE;
-        float po[kE];
-        if (kE == 4) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-          po[0] = v.x, po[1] = v.y, po[kE - 2] = v.z, po[kE - 1] = v.w;
-        } else {
-          const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-          po[0] = v.x, po[1] = v.y;
+      for (int i1 = i0; i1 < min(n, i0 + 32); i1 += kAhead) {
+        float po[kAhead][kE];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+#pragma unroll
+          for (int e = 0; e < kE; ++e) po[u][e] = 0.f;
+          if (i1 + u >= n) continue;
+          const float* src = a.po + (((int64_t)slot_of(i1 + u) * 2 + t) * kRows + r) * D + lane * kE;
+          if (kE == 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+            po[u][0] = v.x, po[u][1] = v.y, po[u][kE - 2] = v.z, po[u][kE - 1] = v.w;
+          } else {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+            po[u][0] = v.x, po[u][1] = v.y;
+          }
         }
 #pragma unroll
-        for (int e = 0; e < kE; ++e) o[e] = fmaf(po[e], w, o[e]);
+        for (int u = 0; u < kAhead; ++u) {
+          const float w = __shfl_sync(0xffffffffu, f, i1 + u - i0);
+#pragma unroll
+          for (int e = 0; e < kE; ++e) o[e] = fmaf(po[u][e], w, o[e]);
+        }
       }
     }
     const int64_t at = own.row[t] + r;
