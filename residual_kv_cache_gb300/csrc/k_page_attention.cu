@@ -21,7 +21,10 @@
 //   beside the other's, across the ends of sequences too.  The group of a segment's last tile
 //   joins the other's part to its own.  Of many short segments a group takes each whole: two
 //   of them then run side by side, where both groups' turns at one would mostly wait for its
-//   ends (1024 sequences of 256 tokens, 8 heads: 228 us by turns, 190 us whole).  Thread t of a group owns token t (TMEM lane t).  Scores s are kept in base 2, and a page's
+//   ends (1024 sequences of 256 tokens, 8 heads: 166 us by turns, 126 us whole).  More groups
+//   do not help: a tile's bytes stay until its group is done with them, and what bounds short
+//   segments is how many tiles fit (three groups 139 us, four 158 us).  Thread t of a group
+//   owns token t (TMEM lane t).  Scores s are kept in base 2, and a page's
 //   value scale 2^e is folded into the weights: the second product takes 2^(s + e - m), the
 //   sum 2^(s - m).  The reference m of a head is the maximum of s + e over some earlier
 //   tiles, so the parts hold the terms that weigh most, whatever the pages' scales.  It is
@@ -48,14 +51,13 @@ namespace rkv {
 namespace {
 
 constexpr int kTile = 128;                 // positions per tile
-constexpr int kPaThreads = 384;
 constexpr int kSoftWarp0 = 4;
+constexpr int kNG = 2;                     // softmax groups
+constexpr int kPaThreads = 128 + 128 * kNG;
 constexpr int kSlots = 4;                  // segments whose queries are held ahead
 constexpr int kMaxCtas = 256;              // shares of a call (partials in the workspace)
 constexpr int kMaxTilePages = kTile / 16;
 constexpr uint32_t kPaTmemCols = 256;
-constexpr uint32_t kSCol = 0, kSStride = 32;      // a score buffer for each group
-constexpr uint32_t kOCol = 64, kOStride = 64;     // an accumulator for each group
 constexpr float kRaise = 8.f;              // weights stay below 2^8
 constexpr int kSoloTiles = 8, kSoloShare = 4;   // solo: at most so many tiles, 1 / so many of the share
 
@@ -65,8 +67,8 @@ struct Segment {
   int solo;                                // one softmax group takes all of it
   // Softmax group of tile t, where the segment begins with group g; group of the next
   // segment's first tile.
-  __device__ __forceinline__ int group(int g, int t) const { return solo ? g : (g + t) & 1; }
-  __device__ __forceinline__ int next_group(int g) const { return solo ? g ^ 1 : (g + tiles) & 1; }
+  __device__ __forceinline__ int group(int g, int t) const { return solo ? g : (int)((uint32_t)(g + t) % kNG); }
+  __device__ __forceinline__ int next_group(int g) const { return (int)((uint32_t)(g + (solo ? 1 : tiles)) % kNG); }
 };
 
 // What the joining kernel has to know of a share's partial.
@@ -89,18 +91,26 @@ struct PaArgs {
   float scale_log2;
 };
 
-template <int D>
+// kH: query heads computed (G rounded up to 2, 4, 8 or 16).
+template <int D, int kH>
 struct PaCfg {
+  static constexpr int kGP = kH <= 8 ? 8 : 16;               // rows of one part
+  static constexpr int kNQ = 2 * kGP;                        // score columns: hi, lo
+  static constexpr int kNP = kGP == 8 ? 32 : 48;             // weight columns: hi, mid, lo (+ padding)
+  // TMEM columns: a score buffer for each group, then an accumulator for each
+  static constexpr uint32_t kSStride = 32, kOCol = kNG * kSStride, kOStride = kGP == 8 ? 32 : 64;
+  static_assert(kOCol + kNG * kOStride <= kPaTmemCols);
   static constexpr uint32_t kHalf = kTile * D;               // bytes of a K or V tile
   static constexpr uint32_t kStage = 2 * kHalf;
   static constexpr int kStages = D == 128 ? 5 : 10;
-  static constexpr uint32_t kQBytes = 32 * D;                // one segment's query tile
-  static constexpr uint32_t kPBytes = 48 * kTile;            // one weight tile
-  static constexpr uint32_t kMetaOff = kStages * kStage + kSlots * kQBytes + 2 * kPBytes;
+  static constexpr uint32_t kQBytes = kNQ * D;               // one segment's query tile
+  static constexpr uint32_t kPBytes = kNP * kTile;           // one weight tile
+  static constexpr uint32_t kPOff = kStages * kStage + kSlots * kQBytes;
+  static constexpr uint32_t kMetaOff = kPOff + kNG * kPBytes;
   static constexpr uint32_t kMeta = kStages * kMaxTilePages * 8;   // (k scale, v scale)
   static constexpr uint32_t kJoinOff = kMetaOff + kMeta;           // a group's o, m, l
-  static constexpr uint32_t kJoin = (16 * kTile + 32) * 4;
-  static constexpr uint32_t kSmem = 1024 + kJoinOff + 2 * kJoin;
+  static constexpr uint32_t kJoin = kH * (kTile + 2);              // floats
+  static constexpr uint32_t kSmem = 1024 + kJoinOff + kNG * kJoin * 4;
 };
 
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
@@ -184,26 +194,22 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
 // Whether pred holds in any thread of softmax group g.
 __device__ __forceinline__ bool vote_group(int g, bool pred) { return !bar_red_and(1 + g, 128, !pred); }
 
-// kH: query heads computed (G rounded up to 2, 4, 8 or 16).
 template <int D, int kH>
 __global__ void __launch_bounds__(kPaThreads, 1)
     page_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                           PaArgs a) {
-  using C = PaCfg<D>;
-  constexpr int kST = C::kStages;
-  constexpr int kGP = kH <= 8 ? 8 : 16;              // rows of one part
-  constexpr int kNQ = 2 * kGP;                       // score columns: hi, lo
-  constexpr int kNP = kGP == 8 ? 32 : 48;            // weight columns: hi, mid, lo (+ padding)
+  using C = PaCfg<D, kH>;
+  constexpr int kST = C::kStages, kGP = C::kGP, kNQ = C::kNQ, kNP = C::kNP;
   extern __shared__ uint8_t raw[];
   uint8_t* sm = align1024(raw);
   uint8_t* s_q = sm + kST * C::kStage;
-  uint8_t* s_p = s_q + kSlots * C::kQBytes;
+  uint8_t* s_p = sm + C::kPOff;
   float2* s_meta = reinterpret_cast<float2*>(sm + C::kMetaOff);
-  __shared__ __align__(8) uint64_t full[kST], empty[kST], s_full[2], s_empty[2], p_full[2], p_empty[2],
-      j_full[2], j_empty[2], d_full[kSlots], q_full[kSlots], q_empty[kSlots], drain;
+  __shared__ __align__(8) uint64_t full[kST], empty[kST], s_full[kNG], s_empty[kNG], p_full[kNG], p_empty[kNG],
+      j_full[kNG], j_empty[kNG], d_full[kSlots], q_full[kSlots], q_empty[kSlots], drain;
   __shared__ Segment seg[kSlots];
   __shared__ float s_qf[kSlots][16];
-  __shared__ float s_red[2][4][16];
+  __shared__ float s_red[kNG][4][16];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_status, s_b0;
   __shared__ int64_t s_pref;
@@ -218,12 +224,12 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     tma_prefetch(&tm_k);
     tma_prefetch(&tm_v);
     for (int i = 0; i < kST; ++i) mbar_init(&full[i], 2), mbar_init(&empty[i], 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kNG; ++i) {
       mbar_init(&s_full[i], 1), mbar_init(&s_empty[i], 4);
       mbar_init(&p_full[i], 128), mbar_init(&p_empty[i], 1);
       mbar_init(&j_full[i], 128), mbar_init(&j_empty[i], 128);
     }
-    for (int i = 0; i < kSlots; ++i) mbar_init(&d_full[i], 1), mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 11);
+    for (int i = 0; i < kSlots; ++i) mbar_init(&d_full[i], 1), mbar_init(&q_full[i], 1), mbar_init(&q_empty[i], 3 + 4 * kNG);
     mbar_init(&drain, 1);
     s_abort = 0;
     fence_barrier_init();
@@ -349,36 +355,40 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     if (elect_one()) {
       constexpr uint32_t id_s = idesc_f8(128, kNQ, false), id_o = idesc_f8(128, kNP, true);
       Ring ring;                                             // stage of the next scores
-      uint32_t s_ph[2] = {1, 1}, p_ph[2] = {0, 0};
+      uint32_t s_ph = 0xFFFFFFFFu, p_ph = 0;                 // bit g: group g's
       // each group's tiles between their two products, oldest lowest: 8 bits of a stage + 1,
       // the top one set where the tile goes on with a sum
-      uint64_t queue[2] = {0, 0};
+      uint64_t queue[kNG] = {};
+      int open = 0;                                          // tiles in the queues
       int s = 0, t = 0, begin = 0;
       uint32_t ph = 0;
       bool have = false, ended = false;
       Segment sg;
       long long t0 = clock64();
-      while (!(ended && queue[0] == 0 && queue[1] == 0)) {
+      while (!(ended && open == 0)) {
         bool moved = false;
         // the tests at once: their latencies overlap
         const int gs = have ? sg.group(begin, t) : 0;
-        const bool p_ok[2] = {mbar_test(&p_full[0], p_ph[0]), mbar_test(&p_full[1], p_ph[1])};
-        const bool bytes_ok = mbar_test(&full[ring.stage], ring.phase), s_ok = mbar_test(&s_empty[gs], s_ph[gs]);
+        bool p_ok[kNG];
+#pragma unroll
+        for (int g = 0; g < kNG; ++g) p_ok[g] = mbar_test(&p_full[g], p_ph >> g & 1u);
+        const bool bytes_ok = mbar_test(&full[ring.stage], ring.phase), s_ok = mbar_test(&s_empty[gs], s_ph >> gs & 1u);
         const bool seg_ok = mbar_test(&q_full[s], ph);
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
+        for (int g = 0; g < kNG; ++g) {
           if (queue[g] != 0 && p_ok[g]) {
             // O_g (+)= V^T P; M = 128 lanes: for D = 64 the upper 64 read the K tile behind V
             // and are unused
             const uint32_t e = (uint32_t)queue[g] & 0xFFu, stage = (e & 0x7Fu) - 1u;
             queue[g] >>= 8;
-            p_ph[g] ^= 1u;
+            --open;
+            p_ph ^= 1u << g;
             tc_fence_after();
             const uint32_t vt = smem_u32(sm + stage * C::kStage);
             const uint32_t pt = smem_u32(s_p + g * C::kPBytes);
 #pragma unroll
             for (int i = 0; i < kTile / 32; ++i)
-              umma_f8(tmem + kOCol + g * kOStride, sdesc_rows<D>(vt + i * 32 * D, C::kHalf),
+              umma_f8(tmem + C::kOCol + g * C::kOStride, sdesc_rows<D>(vt + i * 32 * D, C::kHalf),
                       sdesc_rows<128>(pt + i * 32, 16), id_o, (e & 0x80u) != 0 || i > 0);
             umma_commit(&empty[stage]);
             umma_commit(&p_empty[g]);
@@ -394,19 +404,21 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         } else if (have) {
           const int g = gs;
           if (bytes_ok && s_ok) {
-            s_ph[g] ^= 1u;
+            s_ph ^= 1u << g;
             tc_fence_after();
             const uint32_t kt = smem_u32(sm + ring.stage * C::kStage + C::kHalf);
             const uint32_t qt = smem_u32(s_q + s * C::kQBytes);
 #pragma unroll
             for (int i = 0; i < D / 32; ++i)
-              umma_f8(tmem + kSCol + g * kSStride, sdesc_rows<D>(kt + i * 32, 16), sdesc_rows<D>(qt + i * 32, 16),
+              umma_f8(tmem + g * C::kSStride, sdesc_rows<D>(kt + i * 32, 16), sdesc_rows<D>(qt + i * 32, 16),
                       id_s, i > 0);
             umma_commit(&s_full[g]);
-            const uint64_t e = (uint64_t)(ring.stage + 1) | (t >= (sg.solo ? 1 : 2) ? 0x80u : 0u);
+            const uint64_t e = (uint64_t)(ring.stage + 1) | (t >= (sg.solo ? 1 : kNG) ? 0x80u : 0u);
             // behind the group's older ones (never more than there are stages)
-            const int n = queue[g] == 0 ? 0 : (71 - __clzll((long long)queue[g])) / 8;
-            queue[g] |= e << (8 * n);
+#pragma unroll
+            for (int i = 0; i < kNG; ++i)
+              if (i == g) queue[i] |= e << (queue[i] == 0 ? 0 : (71 - __clzll((long long)queue[i])) / 8 * 8);
+            ++open;
             ring.next(kST);
             if (++t == sg.tiles) {
               umma_commit(&q_empty[s]);
@@ -586,11 +598,11 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     // ---------------------------------------------------------------------- softmax
     const int wg = (warp - kSoftWarp0) >> 2, tok = tid & 127, w = warp & 3;
     const uint32_t tm = tmem + ((uint32_t)(w * 32) << 16);
-    const uint32_t s_tm = tm + kSCol + wg * kSStride;
+    const uint32_t s_tm = tm + wg * C::kSStride;
     uint8_t* pt = s_p + wg * C::kPBytes;
     float* s_join = reinterpret_cast<float*>(sm + C::kJoinOff);
     Ring ring;                                               // stage of the segment's tile t
-    uint32_t s_ph = 0, p_ph = 0, j_ph[2] = {0, 0};
+    uint32_t s_ph = 0, p_ph = 0, j_ph = 0;                   // j_ph: bit g, group g's parts
     int begin = 0;                                           // group of the segment's first tile
     bool ok = true;
     for (int s = 0, ph = 0; true; s == kSlots - 1 ? (s = 0, ph ^= 1) : ++s) {
@@ -599,7 +611,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       const Segment g = seg[s];
       if (g.b < 0) break;
       if (g.solo && begin != wg) {                           // the other group's
-        begin ^= 1;
+        begin = g.next_group(begin);
         for (int t = 0; t < g.tiles; ++t) ring.next(kST);
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_empty[s]);
@@ -610,9 +622,9 @@ __global__ void __launch_bounds__(kPaThreads, 1)
       for (int h = 0; h < kH; ++h) m[h] = -FLT_MAX, l[h] = 0.f, qf[h] = s_qf[s][h];
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_empty[s]);
-      const uint32_t o_tm = tm + kOCol + wg * kOStride;
+      const uint32_t o_tm = tm + C::kOCol + wg * C::kOStride;
       bool first = true;                                     // the group's first tile of the segment
-      const int owner = g.group(begin, g.tiles - 1);         // group of the last tile
+      const int owner = g.group(begin, g.tiles - 1);   // of the last tile
       for (int t = 0; t < g.tiles; ++t) {
         const int stage = ring.stage;
         const uint32_t st_ph = ring.phase;
@@ -722,6 +734,12 @@ __global__ void __launch_bounds__(kPaThreads, 1)
         first = false;
       }
       begin = g.next_group(begin);
+      // the groups that hand their part to the last tile's
+      const int others = g.solo ? 0 : min(g.tiles, kNG) - 1;
+      const uint32_t j_now = j_ph;
+#pragma unroll
+      for (int i = 1; i < kNG; ++i)
+        if (i <= others) j_ph ^= 1u << ((uint32_t)(owner + kNG - i) % kNG);
       if (first && ok) continue;                             // none of the tiles was the group's
       // the group's sums and accumulator
       if (ok && !first) {
@@ -756,35 +774,35 @@ __global__ void __launch_bounds__(kPaThreads, 1)
 #pragma unroll
       for (int h = 0; h < kH; ++h)
         l[h] = s_red[wg][0][h] + s_red[wg][1][h] + s_red[wg][2][h] + s_red[wg][3][h];
-      if (g.tiles > 1 && !g.solo) {                          // the other group's part
-        const int other = owner ^ 1;
-        float* part = s_join + other * (C::kJoin / 4);
-        if (wg == other) {
-          // its place is free once the last part has been taken
-          ok = wait_warp(&j_empty[other], j_ph[other] ^ 1u, abort, status);
-          j_ph[other] ^= 1u;
-          if (!ok) continue;
-#pragma unroll
-          for (int h = 0; h < kH; ++h) {
-            part[h * kTile + tok] = o[h];
-            if (tok == 0) part[16 * kTile + h] = m[h], part[16 * kTile + 16 + h] = l[h];
-          }
-          mbar_arrive(&j_full[other]);
-          continue;
-        }
-        ok = wait_warp(&j_full[other], j_ph[other], abort, status);
-        j_ph[other] ^= 1u;
+      if (others > 0 && wg != owner) {
+        // its place is free once the last part has been taken
+        ok = wait_warp(&j_empty[wg], (j_now >> wg & 1u) ^ 1u, abort, status);
         if (!ok) continue;
+        float* part = s_join + wg * C::kJoin;
 #pragma unroll
         for (int h = 0; h < kH; ++h) {
-          const float m1 = part[16 * kTile + h], mn = fmaxf(m[h], m1);
+          part[h * kTile + tok] = o[h];
+          if (tok == 0) part[kH * kTile + h] = m[h], part[kH * kTile + kH + h] = l[h];
+        }
+        mbar_arrive(&j_full[wg]);
+        continue;
+      }
+      for (int i = 1; i <= others && ok; ++i) {              // the others' parts
+        const int other = (int)((uint32_t)(owner + kNG - i) % kNG);
+        const float* part = s_join + other * C::kJoin;
+        ok = wait_warp(&j_full[other], j_now >> other & 1u, abort, status);
+        if (!ok) break;
+#pragma unroll
+        for (int h = 0; h < kH; ++h) {
+          const float m1 = part[kH * kTile + h], mn = fmaxf(m[h], m1);
           const float fa = ex2_approx(m[h] - mn), fb = ex2_approx(m1 - mn);
           o[h] = o[h] * fa + part[h * kTile + tok] * fb;
-          l[h] = l[h] * fa + part[16 * kTile + 16 + h] * fb;
+          l[h] = l[h] * fa + part[kH * kTile + kH + h] * fb;
           m[h] = mn;
         }
         mbar_arrive(&j_empty[other]);
       }
+      if (!ok) continue;
       {
         const int64_t row = g.slot < 0 ? ((int64_t)g.b * a.N + g.h) * a.G : (int64_t)g.slot * a.G;
 #pragma unroll
@@ -915,9 +933,10 @@ template <int D, int kH>
 cudaError_t launch_main(const CUtensorMap& mk, const CUtensorMap& mv, const PaArgs& a, int grid, int dev,
                         cudaStream_t s) {
   static SmemOptIn opt_in;
-  const cudaError_t e = opt_in(page_attention_kernel<D, kH>, PaCfg<D>::kSmem, dev);
+  using C = PaCfg<D, kH>;
+  const cudaError_t e = opt_in(page_attention_kernel<D, kH>, C::kSmem, dev);
   if (e != cudaSuccess) return e;
-  page_attention_kernel<D, kH><<<grid, kPaThreads, PaCfg<D>::kSmem, s>>>(mk, mv, a);
+  page_attention_kernel<D, kH><<<grid, kPaThreads, C::kSmem, s>>>(mk, mv, a);
   return cudaGetLastError();
 }
 
