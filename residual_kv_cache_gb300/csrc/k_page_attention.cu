@@ -21,21 +21,25 @@
 //   beside the other's, across the ends of sequences too.  The group of a segment's last tile
 //   joins the other's part to its own.  Of many short segments a group takes each whole: two
 //   of them then run side by side, where both groups' turns at one would mostly wait for its
-//   ends (1024 sequences of 256 tokens, 8 heads: 166 us by turns, 126 us whole).  More groups
-//   do not help: a tile's bytes stay until its group is done with them, and what bounds short
-//   segments is how many tiles fit (three groups 139 us, four 158 us).  Thread t of a group
-//   owns token t (TMEM lane t).  Scores s are kept in base 2, and a page's
-//   value scale 2^e is folded into the weights: the second product takes 2^(s + e - m), the
-//   sum 2^(s - m).  The reference m of a head is the maximum of s + e over some earlier
-//   tiles, so the parts hold the terms that weigh most, whatever the pages' scales.  It is
-//   raised (sums and accumulators rescaled) only when an s + e exceeds it by 8, which one
-//   vote a tile finds: the usual tile has no reduction across tokens.
+//   ends (1024 sequences of 256 tokens, 8 heads: 166 us by turns, 122 us whole; of three
+//   groups 139, of four 158: short segments run all of the code every 2 us, and a fifth of
+//   their stalls already wait for instructions).  Thread t of a group owns token t (TMEM lane
+//   t).  Scores s are kept in base 2, and a page's value scale 2^e is
+//   folded into the weights: the second product takes 2^(s + e - m), the sum 2^(s - m).  The
+//   reference m of a head is the maximum of s + e over some earlier tiles, so the parts hold
+//   the terms that weigh most, whatever the pages' scales.  It is raised (sums and
+//   accumulators rescaled) only when an s + e exceeds it by 8, which one vote a tile finds:
+//   the usual tile has no reduction across tokens.
 //
 // Work split: all tiles of the call in the order (sequence, head, tile) are cut into equal
 // contiguous shares, one a CTA (one CTA an SM), whatever the lengths.  A (sequence, head)
 // that lies inside one share is written to `out` directly; others leave fp32 partials (m, l,
 // o), at most two a CTA, which the second kernel joins in tile order: no atomics, the same
 // bits on every run.
+//
+// Measured, 32 query heads on 8 of 128, pages of 64: 16 sequences of up to 131072 tokens, 3.34
+// GB, 473-484 us (7.0 TB/s, where a copy reaches 6.8); one of 1000 tokens 10 us, the latency of
+// one tile's chain, the join's and two launches; between, about 11 us on top of the bytes.
 //
 // Warps: 0 TMA producer, 1 MMA issuer, 2 queries and segment list, 3 page scales and the rows
 // of empty sequences, 4-7 and 8-11 softmax.
