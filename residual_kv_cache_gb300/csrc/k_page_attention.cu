@@ -23,13 +23,13 @@
 //   of them then run side by side, where both groups' turns at one would mostly wait for its
 //   ends (1024 sequences of 256 tokens, 8 heads: 166 us by turns, 122 us whole; of three
 //   groups 139, of four 158: short segments run all of the code every 2 us, and a fifth of
-//   their stalls already wait for instructions).  Thread t of a group owns token t (TMEM lane
-//   t).  Scores s are kept in base 2, and a page's value scale 2^e is
-//   folded into the weights: the second product takes 2^(s + e - m), the sum 2^(s - m).  The
-//   reference m of a head is the maximum of s + e over some earlier tiles, so the parts hold
-//   the terms that weigh most, whatever the pages' scales.  It is raised (sums and
-//   accumulators rescaled) only when an s + e exceeds it by 8, which one vote a tile finds:
-//   the usual tile has no reduction across tokens.
+//   their stalls already wait for instructions).
+//   Thread t of a group owns token t (TMEM lane t).  Scores s are kept in base 2, and a page's
+//   value scale 2^e is folded into the weights: the second product takes 2^(s + e - m), the
+//   sum 2^(s - m).  The reference m of a head is the maximum of s + e over some earlier tiles,
+//   so the parts hold the terms that weigh most, whatever the pages' scales.  It is raised
+//   (sums and accumulators rescaled) only when an s + e exceeds it by 8, which one vote a tile
+//   finds: the usual tile has no reduction across tokens.
 //
 // Work split: all tiles of the call in the order (sequence, head, tile) are cut into equal
 // contiguous shares, one a CTA (one CTA an SM), whatever the lengths.  A (sequence, head)
