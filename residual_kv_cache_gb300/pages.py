@@ -16,7 +16,8 @@ CUDA tensors; ``PageTable`` and ``PagedCache`` hold the ones that a serving loop
 
 Every tensor of a call must lie on one device, which need not be the current one.  Work goes
 to ``stream`` (a ``torch.cuda.Stream`` of that device), or to the device's current stream;
-tensors made on another stream must be ready there, as for any torch operation.
+tensors made on another stream must be ready there, as for any torch operation.  Nothing is
+differentiable: results carry no gradient.
 """
 from __future__ import annotations
 
