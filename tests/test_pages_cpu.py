@@ -154,7 +154,7 @@ def test_prompt_refusals(lib):
         assert call(**bad) == -2, bad
     assert call(total_q=0) == 0
     # rows of out that overlap, and sizes whose items would not fit their counters
-    for bad in (dict(out_strides=S(0, 128)), dict(out_strides=S(4096, 0)), dict(out_strides=S(4088, 128)),
+    for bad in (dict(out_strides=S(1 << 60, 120)), dict(out_strides=S(120, 1 << 60)), dict(out_strides=S(0, 128)), dict(out_strides=S(4096, 0)), dict(out_strides=S(4088, 128)),
                 dict(out_strides=S(4096, 120)), dict(out_strides=S(128, 1272)),
                 dict(total_q=2 ** 30, n_q_heads=16)):
         assert call(**bad) == -1, bad
