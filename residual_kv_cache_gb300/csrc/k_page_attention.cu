@@ -95,7 +95,7 @@ struct PaArgs {
   float scale_log2;
 };
 
-// kH: query heads computed (G rounded up to 2, 4, 8 or 16).
+// kH: query heads computed (G rounded up to 2, 4, 6, 8, 12 or 16).
 template <int D, int kH>
 struct PaCfg {
   static constexpr int kGP = kH <= 8 ? 8 : 16;               // rows of one part
@@ -947,10 +947,15 @@ cudaError_t launch_main(const CUtensorMap& mk, const CUtensorMap& mv, const PaAr
 template <int D>
 cudaError_t launch_all(const CUtensorMap& mk, const CUtensorMap& mv, const PaArgs& a, int grid, int dev,
                         cudaStream_t s) {
-  cudaError_t e = a.G <= 2   ? launch_main<D, 2>(mk, mv, a, grid, dev, s)
-                  : a.G <= 4 ? launch_main<D, 4>(mk, mv, a, grid, dev, s)
-                  : a.G <= 8 ? launch_main<D, 8>(mk, mv, a, grid, dev, s)
-                             : launch_main<D, 16>(mk, mv, a, grid, dev, s);
+  // As many heads as there are, nearly: short calls pay for the code of every head (12 against
+  // 16: 18 sequences of up to 16927 tokens, one key head, 21.5 and 23.7 us, 256 of 1024, two
+  // key heads, 43 and 52; 6 against 8: 256 of 1024, four key heads, 52 and 55).
+  cudaError_t e = a.G <= 2    ? launch_main<D, 2>(mk, mv, a, grid, dev, s)
+                  : a.G <= 4  ? launch_main<D, 4>(mk, mv, a, grid, dev, s)
+                  : a.G <= 6  ? launch_main<D, 6>(mk, mv, a, grid, dev, s)
+                  : a.G <= 8  ? launch_main<D, 8>(mk, mv, a, grid, dev, s)
+                  : a.G <= 12 ? launch_main<D, 12>(mk, mv, a, grid, dev, s)
+                              : launch_main<D, 16>(mk, mv, a, grid, dev, s);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(grid, ceil_div(a.G, 4));

@@ -288,7 +288,8 @@ ATTEND = [  # lens, Hq, N, P, D
     ([1], 1, 1, 16, 128), ([0, 1, 2, 15, 16, 17], 8, 2, 16, 64), ([127, 128, 129, 0, 255], 28, 4, 64, 128),
     ([1000], 32, 8, 64, 128), ([300, 5, 77], 32, 2, 32, 128), ([513, 1, 64], 9, 1, 128, 128),
     ([700, 650], 12, 1, 16, 64), ([40] * 70, 5, 5, 32, 64), ([5000, 3, 2047], 14, 2, 64, 64),
-    ([130] * 3, 24, 2, 128, 128)]
+    ([130] * 3, 24, 2, 128, 128), ([300, 5, 900], 24, 4, 64, 128), ([257, 0, 1500], 10, 2, 16, 64),
+    ([129, 2000], 10, 1, 32, 128), ([640, 33, 1], 26, 2, 64, 64)]
 
 
 @cuda
