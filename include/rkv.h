@@ -478,8 +478,10 @@ rkv_status rkv_page_append(const rkv_pages* pages, const rkv_page_table* table, 
  * range are left out, and a length past the table is cut (RKV_FLAG_BAD_INDEX).  Bytes of a
  * page behind the sequence's last position are never used, whatever they hold.
  * The scores are exact products of bf16 q and the stored codes summed in fp32 (elements of
- * q below 2^-21 of their row's largest are rounded to it); the weights enter the second
- * product with 12 significant bits; sums are fp32.
+ * q below 2^-21 of their row's largest are rounded to it).  Of the weights times their page's
+ * value scale, the second product holds each to 2^-15 of itself where it is at least 2^-18 of
+ * the head's largest, to 2^-11 down to 2^-28 of that, and to 2^-40 of it below: what all of T
+ * positions can lose is T 2^-40 of the largest.  Sums are fp32.
  * Errors (nothing launched): RKV_EINVAL, RKV_EALIGN, RKV_ECAPACITY (workspace), RKV_ECUDA.
  */
 rkv_status rkv_page_attention(const rkv_pages* pages, const rkv_page_table* table, const void* q,

@@ -9,13 +9,20 @@
 //   Tile = 128 positions of one (sequence, key/value head); its pages are 1 to 8 boxes of
 //   [P rows x D bytes], stacked into a K tile and a V tile (rows swizzled by TMA).
 //   Scores:   S[token, n]  = K_tile Q^T       M = 128 tokens, N = 16 or 32, K = D
-//   Values:   O[d, n]     += V_tile^T P       M = D (128 lanes), N = 32 or 48, K = 128 tokens
+//   Values:   O[d, n]     += V_tile^T P       M = D (128 lanes), N = 32 or 64, K = 128 tokens
 //   both tcgen05.mma kind::f8f6f4 with fp32 accumulation in TMEM; V enters as an MN-major A.
-//   The operands that are not stored in 8 bits are split into E4M3 parts, one column each:
-//   a bf16 q (scaled to its row's largest) is exactly hi + lo / 16 where it is within 2^-14
-//   of that largest, and within 2^-21 of it everywhere; a weight is hi + mid / 16 + lo / 256,
-//   12 significant bits for weights down to 2^-6 and an absolute 2^-18 below.  The products
-//   are exact and the parts are joined in fp32.
+//   The operands that are not stored in 8 bits are split into parts, one column each.  A bf16
+//   q (scaled to its row's largest) is two E4M3 parts, hi + lo / 16: exact where it is within
+//   2^-14 of that largest, and within 2^-21 of it everywhere.  A weight is four E5M2 parts,
+//   a + (b + (c + d / 16) / 16) / 2048.  A part takes 4 bits off what is left (three and a
+//   sign), and with the largest weight of a tile at 2^4 or more the last one's step, 2^-16 /
+//   2^19, is 2^-39 of it: a weight is off by 2^-15 of itself down to 2^-18 of the largest, by
+//   2^-11 down to 2^-28, and by 2^-40 of the largest at any size.  The range is what long
+//   contexts need: beside one key that takes most of the weight, the others have 2^-17 and
+//   less each and still are most of the result where that key's value is small.  (Three E4M3
+//   parts, with their range of 2^-18, lost them; a fourth E4M3 part would have 2^-28 of the
+//   largest as its last step, for more bits than an output of bf16 shows.)  The products are
+//   exact and the parts are joined in fp32.
 //   Softmax: two groups of 128 threads take a CTA's tiles in turn, each with its own score
 //   buffer, weights, sums and accumulator, so that one group's chain of dependent steps runs
 //   beside the other's, across the ends of sequences too.  The group of a segment's last tile
@@ -26,10 +33,10 @@
 //   their stalls already wait for instructions).
 //   Thread t of a group owns token t (TMEM lane t).  Scores s are kept in base 2, and a page's
 //   value scale 2^e is folded into the weights: the second product takes 2^(s + e - m), the
-//   sum 2^(s - m).  The reference m of a head is the maximum of s + e over some earlier tiles,
-//   so the parts hold the terms that weigh most, whatever the pages' scales.  It is raised
-//   (sums and accumulators rescaled) only when an s + e exceeds it by 8, which one vote a tile
-//   finds: the usual tile has no reduction across tokens.
+//   sum 2^(s - m).  The reference m of a head is the maximum of s + e over some earlier tiles
+//   less 4, so the parts hold the terms that weigh most, whatever the pages' scales.  It is
+//   raised (sums and accumulators rescaled) only when an s + e exceeds it by 8, which one vote
+//   a tile finds: the usual tile has no reduction across tokens.
 //
 // Work split: all tiles of the call in the order (sequence, head, tile) are cut into equal
 // contiguous shares, one a CTA (one CTA an SM), whatever the lengths.  A (sequence, head)
@@ -62,7 +69,12 @@ constexpr int kSlots = 4;                  // segments whose queries are held ah
 constexpr int kMaxCtas = 256;              // shares of a call (partials in the workspace)
 constexpr int kMaxTilePages = kTile / 16;
 constexpr uint32_t kPaTmemCols = 256;
-constexpr float kRaise = 8.f;              // weights stay below 2^8
+constexpr float kRaise = 8.f;              // weights stay below 2^8: what is left of them after a
+                                           // part, 2^-4 of them, times its factor below 2^15
+constexpr float kBelow = 4.f;              // a new reference lies so far below the maximum
+constexpr int kParts = 4;                  // parts of a weight
+// Part i + 1 holds what part i has left, times this.
+__host__ __device__ constexpr float part_factor(int i) { return i == 0 ? 2048.f : 16.f; }
 constexpr int kSoloTiles = 8, kSoloShare = 4;   // solo: at most so many tiles, 1 / so many of the share
 
 // A run of tiles of one (sequence, head) inside a CTA's share.
@@ -100,9 +112,9 @@ template <int D, int kH>
 struct PaCfg {
   static constexpr int kGP = kH <= 8 ? 8 : 16;               // rows of one part
   static constexpr int kNQ = 2 * kGP;                        // score columns: hi, lo
-  static constexpr int kNP = kGP == 8 ? 32 : 48;             // weight columns: hi, mid, lo (+ padding)
+  static constexpr int kNP = kParts * kGP;                   // weight columns
   // TMEM columns: a score buffer for each group, then an accumulator for each
-  static constexpr uint32_t kSStride = 32, kOCol = kNG * kSStride, kOStride = kGP == 8 ? 32 : 64;
+  static constexpr uint32_t kSStride = 32, kOCol = kNG * kSStride, kOStride = kNP;
   static_assert(kOCol + kNG * kOStride <= kPaTmemCols);
   static constexpr uint32_t kHalf = kTile * D;               // bytes of a K or V tile
   static constexpr uint32_t kStage = 2 * kHalf;
@@ -156,7 +168,7 @@ __device__ __forceinline__ int page_at(const PaArgs& a, const Segment& g, int pa
   return page < end ? __ldg(a.table + (int64_t)g.b * a.max_blocks + page) : -1;
 }
 
-// tcgen05.mma kind::f8f6f4, E4M3 operands in shared memory, fp32 accumulation.
+// tcgen05.mma kind::f8f6f4, 8-bit operands in shared memory, fp32 accumulation.
 __device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n"
@@ -168,9 +180,9 @@ __device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint
       : "memory");
 }
 
-// Instruction descriptor: fp32 D, E4M3 A and B; kTransA: A is MN-major.
-__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, bool trans_a) {
-  return (1u << 4) | (trans_a ? 1u << 15 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// Instruction descriptor: fp32 D, E4M3 A, E4M3 or E5M2 B; trans_a: A is MN-major.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, bool b_e5m2, bool trans_a) {
+  return (1u << 4) | (b_e5m2 ? 1u << 10 : 0u) | (trans_a ? 1u << 15 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 // Descriptor of a tile with D-byte rows (128- or 64-byte swizzle, groups of 8 rows).
@@ -194,6 +206,16 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 __device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+__device__ __forceinline__ uint32_t e5m2x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %2, %1;" : "=h"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+// (an E5M2 code is the upper byte of an fp16)
+__device__ __forceinline__ float2 from_e5m2x2(uint32_t c) {
+  const uint32_t h = __byte_perm(c, 0u, 0x1404u);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
@@ -359,7 +381,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
     // group has read its last ones, a group's second product once its weights are there.
     // (In a fixed order, a segment's last product waited for the other group's next scores.)
     if (elect_one()) {
-      constexpr uint32_t id_s = idesc_f8(128, kNQ, false), id_o = idesc_f8(128, kNP, true);
+      constexpr uint32_t id_s = idesc_f8(128, kNQ, false, false), id_o = idesc_f8(128, kNP, true, true);
       Ring ring;                                             // stage of the next scores
       uint32_t s_ph = 0xFFFFFFFFu, p_ph = 0;                 // bit g: group g's
       // each group's tiles between their two products, oldest lowest: 8 bits of a stage + 1,
@@ -672,7 +694,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
             ok = false;
             break;
           }
-          // the reference becomes the maximum so far
+          // the reference becomes the maximum so far, less kBelow
           // (one instruction a warp and head, on integers of the same order; NaN left out)
 #pragma unroll
           for (int h = 0; h < kH; ++h) {
@@ -686,7 +708,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
 #pragma unroll
           for (int h = 0; h < kH; ++h) {
             const float mn = fmaxf(m[h], fmaxf(fmaxf(s_red[wg][0][h], s_red[wg][1][h]),
-                                               fmaxf(s_red[wg][2][h], s_red[wg][3][h])));
+                                               fmaxf(s_red[wg][2][h], s_red[wg][3][h])) - kBelow);
             f[h] = ex2_approx(m[h] - mn);
             l[h] *= f[h];
             m[h] = mn;
@@ -694,7 +716,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           if (!first) {
             tc_fence_after();
 #pragma unroll
-            for (int part = 0; part < 3; ++part) {
+            for (int part = 0; part < kParts; ++part) {
               uint32_t r[kGP];
               if (kGP == 8) tmem_ld8(o_tm + part * kGP, r);
               else tmem_ld16(o_tm + part * kGP, r);
@@ -717,15 +739,15 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           l[h + 1] += p1;
           float u0 = valid ? p0 * sc.y : 0.f, u1 = valid ? p1 * sc.y : 0.f;
 #pragma unroll
-          for (int part = 0; part < 3; ++part) {
-            const uint32_t c = e4m3x2(u0, u1);
+          for (int part = 0; part < kParts; ++part) {
+            const uint32_t c = e5m2x2(u0, u1);
             const int n0 = part * kGP + h, n1 = n0 + 1;
             pt[n0 * 128 + ((c16 ^ (n0 & 7)) << 4) + c0] = (uint8_t)c;
             pt[n1 * 128 + ((c16 ^ (n1 & 7)) << 4) + c0] = (uint8_t)(c >> 8);
-            if (part < 2) {
-              const float2 e = from_e4m3x2(c);
-              u0 = (u0 - e.x) * 16.f;
-              u1 = (u1 - e.y) * 16.f;
+            if (part + 1 < kParts) {
+              const float2 e = from_e5m2x2(c);
+              u0 = (u0 - e.x) * part_factor(part);
+              u1 = (u1 - e.y) * part_factor(part);
             }
           }
         }
@@ -758,13 +780,13 @@ __global__ void __launch_bounds__(kPaThreads, 1)
 #pragma unroll
       for (int h = 0; h < kH; ++h) o[h] = 0.f;
 #pragma unroll
-      for (int part = 2; part >= 0; --part) {
+      for (int part = kParts - 1; part >= 0; --part) {
         uint32_t r[kGP];
         if (kGP == 8) tmem_ld8(o_tm + part * kGP, r);
         else tmem_ld16(o_tm + part * kGP, r);
         tmem_ld_wait();
 #pragma unroll
-        for (int h = 0; h < kH; ++h) o[h] = fmaf(o[h], 0.0625f, __uint_as_float(r[h]));
+        for (int h = 0; h < kH; ++h) o[h] = fmaf(o[h], 1.f / part_factor(part), __uint_as_float(r[h]));
       }
       tc_fence_before();
 #pragma unroll

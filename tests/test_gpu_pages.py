@@ -366,6 +366,86 @@ def test_page_attention_nan_stays_with_its_head_and_sequence():
     assert torch.equal(bad, want) and torch.equal(out[~bad], clean[~bad])
 
 
+# ------------------------------------------------- page attention beside a dominant key
+def _softmax64(q, k, v, lens, scale):
+    """q [B, G, D] against one key/value head's rows k, v [T, D], all in binary64 on the GPU.
+    Returns what oracle.pages.page_attention does, as arrays."""
+    o, a, lse, big = [], [], [], 0.0
+    for b, n in enumerate(lens):
+        s = scale * (q[b] @ k[:n].T)
+        m = s.max(-1, keepdim=True).values
+        w = torch.exp(s - m)
+        l = w.sum(-1, keepdim=True)
+        o.append(w @ v[:n] / l)
+        a.append(w @ v[:n].abs() / l)
+        lse.append((m + torch.log(l))[:, 0])
+        big = max(big, scale * (q[b].abs() @ k[:n].abs().T).max().item())
+    return [torch.stack(x).cpu().numpy() for x in (o, lse, a)] + [big]
+
+
+def _sunk(T, B, G, P, D, at, mass, std, small, loud, seed):
+    """B sequences of T positions that share their pages, one key/value head: scores of
+    deviation `std`, of which the key at `at` takes `mass` of the weight; values of mean 0.5,
+    2^-6 of that at the key if `small`.  loud: one other page's values are 2^8 times as large."""
+    g = gen(seed)
+    M = -(-T // P)
+    page = torch.randperm(M, generator=g)
+    kc = torch.randn((T, D), generator=g) * 16 * std
+    kc[:, 0] = 0
+    kc[at] = 0
+    kc[at, 0] = 448
+    vc = (torch.randn((T, D), generator=g) * 0.5 + 1) * 16
+    if small:
+        vc[at] /= 64
+    codes = torch.full((2, M * P, D), 0x7F, dtype=torch.uint8)
+    for i, c in enumerate((kc, vc)):
+        codes[i, :T] = c.to(torch.float8_e4m3fn).view(torch.uint8)
+    k8, v8 = (torch.empty((M, 1, P, D), dtype=torch.uint8) for _ in range(2))
+    k8[page, 0], v8[page, 0] = codes[0].view(M, P, D), codes[1].view(M, P, D)
+    ks, vs = torch.full((M, 1), 2.0 ** -4), torch.full((M, 1), 2.0 ** -5)
+    if loud:
+        vs[page[(at // P + M // 2) % M], 0] *= 256
+    cache = [x.cuda() for x in (k8, v8, ks, vs)]
+    val = [c.cuda()[page.cuda(), 0].view(torch.float8_e4m3fn).double() * s.cuda()[page.cuda()].double()[:, :, None]
+           for c, s in ((k8, ks), (v8, vs))]
+    k, v = (x.reshape(-1, D)[:T] for x in val)
+    q = torch.randn((B, G, D), generator=g).to(torch.bfloat16).cuda()
+    q[:, :, 0] = 0
+    s = torch.einsum("bgd,td->bgt", q.double(), k) / math.sqrt(D)
+    s[:, :, at] = -math.inf
+    q[:, :, 0] = ((torch.logsumexp(s, -1) + math.log(mass / (1 - mass))) * math.sqrt(D) / 28).to(torch.bfloat16)
+    return q, cache, page.to(torch.int32).repeat(B, 1).cuda(), k, v
+
+
+SINK = [  # T, B, G, P, D, at, mass, std, small, loud
+    (1000, 3, 4, 64, 128, 0, 0.9, 1.0, True, False), (1000, 160, 12, 16, 64, 500, 0.99, 1.0, False, False),
+    (1000, 160, 8, 32, 128, 999, 0.5, 0.1, True, False), (16384, 1, 4, 64, 128, 0, 0.99, 1.0, True, False),
+    (16384, 156, 4, 64, 128, 0, 0.9, 1.0, True, False), (16384, 156, 2, 16, 64, 8000, 0.99, 0.1, True, False),
+    (16384, 156, 16, 128, 128, 0, 0.99, 1.0, True, False), (16384, 156, 9, 64, 64, 8191, 0.5, 0.0, True, False),
+    (16384, 156, 7, 32, 128, 0, 0.9, 1.0, False, True), (16384, 156, 12, 64, 128, 300, 0.9, 0.1, True, True),
+    (131072, 1, 4, 64, 128, 0, 0.9, 1.0, True, False), (131072, 156, 4, 64, 128, 0, 0.9, 1.0, True, False),
+    (131072, 156, 4, 64, 128, 0, 0.99, 0.0, True, False), (131072, 156, 8, 32, 64, 65536, 0.99, 1.0, True, False),
+    (131072, 156, 16, 64, 128, 0, 0.5, 0.1, True, False), (131072, 156, 10, 128, 64, 70001, 0.99, 0.1, False, False)]
+
+
+@cuda
+@pytest.mark.parametrize("case", range(len(SINK)))
+def test_page_attention_keeps_the_weights_beside_a_dominant_key(case):
+    """One key takes most of the weight, as in the long contexts of trained models; the many
+    others, 2^-8 to 2^-24 of it each, are most of the result where its value is small.  The
+    bound is that of any other input.  (156 sequences: a CTA weighs the whole of one against
+    the key; 1 and 3: a CTA has a share of one.)"""
+    T, B, G, P, D = SINK[case][:5]
+    q, cache, table, k, v = _sunk(*SINK[case], seed=1400 + case)
+    lse = torch.empty((B, G), device="cuda")
+    flags = i32([0])
+    out = rkv.page_attention(q, *cache, table, i32([T] * B), lse=lse, flags=flags)
+    assert flags.item() == 0
+    ref, rl, a, big = _softmax64(q.double(), k, v, [T] * B, 1 / math.sqrt(D))
+    close(out, ref, a, big, D, 2.0 ** -11)
+    close_lse(lse, rl, big, D)
+
+
 # ------------------------------------------------------------------- prompt attention
 PROMPT = [  # lq, lk, Hq, N, D
     ([1], [1], 1, 1, 128), ([1, 2, 3], [1, 2, 3], 4, 2, 64), ([77], [77], 32, 8, 128),
