@@ -432,9 +432,12 @@ rkv_status rkv_page_plan(const rkv_page_table* table, const int32_t* new_tokens,
 /*
  * Give finished sequences' pages back: for each b with finished[b] != 0 (device, int32
  * [batch]), in order of sequence and position, its pages are put on the end of the free
- * list, its table entries become -1 and its length 0.  If they do not fit the list (more
- * than num_blocks), or a length is out of range, nothing changes and RKV_FLAG_NO_SPACE or
- * RKV_FLAG_BAD_INDEX is raised.  Errors (nothing launched): RKV_EINVAL.
+ * list, its table entries become -1 and its length 0.  Entries that are no page (outside
+ * [0, num_blocks)) do not go to the list (RKV_FLAG_BAD_INDEX).  If the others do not fit it
+ * (more than num_blocks), or a length is out of range, nothing changes and RKV_FLAG_NO_SPACE
+ * or RKV_FLAG_BAD_INDEX is raised.  A page that several sequences read must be in one
+ * released sequence only, and its other readers done with it.
+ * Errors (nothing launched): RKV_EINVAL.
  */
 rkv_status rkv_page_release(const rkv_page_table* table, const int32_t* finished,
                             int32_t* free_blocks, int32_t* n_free, int32_t num_blocks,

@@ -150,6 +150,71 @@ def test_release_matches_the_definition_and_refuses_what_does_not_fit():
         assert all(torch.equal(x, y) for x, y in zip(before, (t, ln, f, n)))
 
 
+@cuda
+@pytest.mark.parametrize("room", ["much", "just", "too little"])
+def test_release_leaves_out_entries_that_are_no_page(room):
+    """Entries outside the pages are flagged and never reach the free list, nor a later plan;
+    the list needs room for the pages that are there alone."""
+    g = np.random.default_rng(7)
+    lens = [int(x) for x in g.integers(0, 3000, size=60)]
+    fin = [int(x) for x in g.integers(0, 2, size=60)]
+    table, free, nf = _plan_inputs([0] * 60, lens, 16, 190, 40, 8)
+    num = len(free)
+    for b in range(60):
+        if lens[b] > 600:
+            table[b, [0, 7, 36, 37]] = -1, num, 10 ** 9, -2 ** 31
+    t2, l2, good = table.copy(), list(lens), []
+    for b in range(60):
+        if fin[b]:
+            n = -(-lens[b] // 16)
+            good += [int(x) for x in table[b, :n] if 0 <= x < num]
+            t2[b, :n], l2[b] = -1, 0
+    assert len(good) < sum(-(-n // 16) for n, x in zip(lens, fin) if x)
+    nf = {"much": nf, "just": num - len(good), "too little": num - len(good) + 1}[room]
+    had = [int(x) for x in g.integers(0, num, size=nf)]
+    f = torch.full((num,), -9, dtype=torch.int32, device="cuda")
+    f[:nf] = i32(had)
+    t, ln, n, flags = i32(table), i32(lens), i32([nf]), i32([0])
+    before = [x.clone() for x in (t, ln, f, n)]
+    rkv.page_release(i32(fin), ln, t, f, n, 16, flags=flags)
+    if room == "too little":
+        assert flags.item() == rkv.FLAG_NO_SPACE
+        assert all(torch.equal(x, y) for x, y in zip(before, (t, ln, f, n)))
+        return
+    assert flags.item() == rkv.FLAG_BAD_INDEX
+    want = had + good
+    assert n.item() == len(want) and f[:len(want)].tolist() == want
+    assert ln.tolist() == l2 and np.array_equal(t.cpu().numpy(), t2)
+    flags.zero_()
+    p = rkv.page_plan(i32([16 * len(good)]), i32([0]), i32(np.full((1, num), -1)), f, n, 16, 16 * len(good), flags=flags)
+    assert flags.item() == 0 and (p.row_slot >= 0).all()
+
+
+@cuda
+def test_release_of_many_pages():
+    """More pages than a pass of the kernel takes, from sequences of all lengths."""
+    g = np.random.default_rng(9)
+    lens = [int(x) for x in g.integers(0, 40, size=8192)]
+    lens[100], lens[101], lens[8191] = 130000, 0, 64000
+    fin = [int(x) for x in g.integers(0, 3, size=8192)]
+    fin[100] = fin[8191] = 1
+    M, P = -(-130000 // 16), 16
+    have = [-(-x // P) for x in lens]
+    ids, at = g.permutation(sum(have) + 9), np.concatenate([[0], np.cumsum(have)])
+    t = torch.full((8192, M), -1, dtype=torch.int32, device="cuda")
+    for b in range(8192):
+        t[b, :have[b]] = i32(ids[at[b]:at[b + 1]])
+    f = torch.full((len(ids),), -9, dtype=torch.int32, device="cuda")
+    f[:9] = i32(ids[at[-1]:])
+    want = [int(x) for x in ids[at[-1]:]] + [int(x) for b in range(8192) if fin[b] for x in ids[at[b]:at[b + 1]]]
+    ln, n, flags = i32(lens), i32([9]), i32([0])
+    rkv.page_release(i32(fin), ln, t, f, n, P, flags=flags)
+    assert flags.item() == 0 and n.item() == len(want) and f[:len(want)].tolist() == want
+    assert ln.tolist() == [0 if fin[b] else lens[b] for b in range(8192)]
+    left = (t >= 0).sum(1).tolist()
+    assert left == [0 if fin[b] else have[b] for b in range(8192)]
+
+
 # ------------------------------------------------------------------------------ append
 def _f8(codes):
     return np64(codes.view(torch.float8_e4m3fn).float())
