@@ -32,6 +32,7 @@ namespace {
 
 constexpr int kPlanThreads = 512;
 constexpr int kPlanRows = 4;         // rows of one thread at a time
+constexpr int kPlanMaxCtas = 512;
 
 // Largest index i in [0, n) with v[i] <= x (v non-decreasing, v[0] <= x).
 __device__ __forceinline__ int last_not_above(const int* v, int n, int x) {
@@ -95,17 +96,20 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanArgs p) {
   const bool ok = !bad && !full;
   const int total = ok ? (int)rows : 0;
   const int step = gridDim.x * kPlanThreads, first = blockIdx.x * kPlanThreads + tid;
-  for (int r0 = first; r0 < p.max_rows; r0 += step * kPlanRows) {
+  // rows without a sign: up to 2^20 past a max_rows of up to 2^31 - 1
+  static_assert((int64_t)kPlanMaxCtas * kPlanThreads * kPlanRows <= 1 << 20);
+  const uint32_t max_rows = p.max_rows;
+  for (uint32_t r0 = first; r0 < max_rows; r0 += step * kPlanRows) {
     int seq[kPlanRows], pos[kPlanRows], id[kPlanRows];
 #pragma unroll
     for (int i = 0; i < kPlanRows; ++i) {
-      const int r = r0 + i * step;
+      const uint32_t r = r0 + i * step;
       seq[i] = pos[i] = id[i] = -1;
-      if (r < total) {
+      if (r < (uint32_t)total) {
         // empty sequences share their first row with the next: the last one is the owner
-        const int b = last_not_above(s_cu, p.batch, r);
+        const int b = last_not_above(s_cu, p.batch, (int)r);
         seq[i] = b;
-        pos[i] = s_len[b] + r - s_cu[b];
+        pos[i] = s_len[b] + ((int)r - s_cu[b]);
         const int page = pos[i] >> p.shift, have = (s_len[b] + P1) >> p.shift;
         const int32_t* at = page < have ? p.table + (int64_t)b * p.max_blocks + page
                                         : p.free_blocks + (n_free - 1 - (s_first[b] + page - have));
@@ -114,10 +118,10 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanArgs p) {
     }
 #pragma unroll
     for (int i = 0; i < kPlanRows; ++i) {
-      const int r = r0 + i * step;
-      if (r < p.max_rows) {
+      const uint32_t r = r0 + i * step;
+      if (r < max_rows) {
         const bool fine = id[i] >= 0 && id[i] < p.num_blocks;
-        if (r < total && !fine) raise_flag(p.flags, RKV_FLAG_BAD_INDEX);
+        if (r < (uint32_t)total && !fine) raise_flag(p.flags, RKV_FLAG_BAD_INDEX);
         p.row_seq[r] = seq[i];
         p.row_pos[r] = pos[i];
         p.row_slot[r] = fine ? (id[i] << p.shift) + (pos[i] & P1) : -1;
@@ -687,8 +691,8 @@ extern "C" rkv_status rkv_page_plan(const rkv_page_table* table, const int32_t* 
   a.max_rows = max_rows;
   // one CTA for up to four rows a thread twice over; then as many as that takes
   int ctas = 1;
-  if (max_rows > 2 * kPlanRows * kPlanThreads) ctas = ceil_div(max_rows, kPlanRows * kPlanThreads);
-  ctas = ctas < 512 ? ctas : 512;
+  if (max_rows > 2 * kPlanRows * kPlanThreads) ctas = (max_rows - 1) / (kPlanRows * kPlanThreads) + 1;
+  ctas = ctas < kPlanMaxCtas ? ctas : kPlanMaxCtas;
   const bool in_place = seq_len_out == a.seq_len || n_free_out == n_free;
   a.state = ctas == 1 || !in_place;
   const size_t smem = sizeof(int) * 3 * (size_t)a.batch;

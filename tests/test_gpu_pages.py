@@ -128,6 +128,24 @@ def test_plan_that_does_not_fit_changes_nothing(why):
 
 
 @cuda
+def test_plan_of_the_largest_row_maps():
+    """max_rows up to 2^31 - 1 (26 GB of maps): rows are counted without a sign, so that none
+    lands before the maps and every one past the total is -1."""
+    lens, new, P = [5, 0, 40], [30, 7, 100000], 16
+    table, free, nf = _plan_inputs(new, lens, P, 7000, 2, 3)
+    cu, ref_rows, lens2, left, table2 = OP.plan(new, lens, table, free, nf, P, 2 ** 31 - 1)
+    t, ln, n, flags = i32(table), i32(lens), i32([nf]), i32([0])
+    p = rkv.page_plan(i32(new), ln, t, i32(free), n, P, 2 ** 31 - 1, flags=flags)
+    assert flags.item() == 0 and p.cu_rows.tolist() == cu and ln.tolist() == lens2 and n.item() == left
+    assert np.array_equal(t.cpu().numpy(), table2)
+    for x, want in zip((p.row_seq, p.row_pos, p.row_slot), np.array(ref_rows).T):
+        assert x.shape == (2 ** 31 - 1,) and np.array_equal(x[:cu[-1]].cpu().numpy(), want)
+        assert all((c == -1).all().item() for c in x[cu[-1]:].split(1 << 28))
+    del p, x
+    torch.cuda.empty_cache()
+
+
+@cuda
 def test_release_matches_the_definition_and_refuses_what_does_not_fit():
     g = np.random.default_rng(5)
     lens = [int(x) for x in g.integers(0, 300, size=700)]
