@@ -410,6 +410,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   __shared__ Item items[kItems];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_status;
+  __shared__ volatile int s_moved;         // key and value tiles asked for
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* abort = &s_abort;
   int* status = a.flags ? a.flags : &s_status;               // where a wait that gives up reports
@@ -427,7 +428,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     }
     for (int i = 0; i < kItems; ++i) mbar_init(&i_full[i], 1), mbar_init(&i_empty[i], 10);
     mbar_init(&drain, 1);
-    s_abort = 0;
+    s_abort = s_moved = 0;
     fence_barrier_init();
   }
   if (warp == 11) {
@@ -466,7 +467,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             load_tile<D>(s_kv + kv.stage * C::kTileB, (j & 1) ? &tm_v : &tm_k, &kv_full[kv.stage], it.kvh,
                          it.k0 + (j >> 1) * kKeys);
             kv.next(kSlots);
-            ++issued;
+            s_moved = (int)++issued;
           }
         }
         if (*abort) {                                        // no copy may outlive the CTA
@@ -588,7 +589,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       uint32_t ph = 1;
       load_seq(a, lane, q0, lq, k0, lk);
       auto emit = [&](const Item& it) {
-        if (!wait_warp(&i_empty[s], ph, abort, status)) return false;
+        // (a place is free when a whole item is done: a second, for some 10^8 keys)
+        if (!wait_warp_while_moving(&i_empty[s], ph, &s_moved, abort, status)) return false;
         if (lane == 0) {
           items[s] = it;
           mbar_arrive(&i_full[s]);

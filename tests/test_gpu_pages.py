@@ -658,6 +658,22 @@ def test_prompt_attention_of_more_pairs_than_ctas(B):
 
 
 @cuda
+def test_prompt_attention_of_more_than_a_second_an_item():
+    """Pairs that take a CTA longer than its bounded waits last: 3 for each CTA, one query row
+    over 1.2 10^8 keys (the keys of one head, read by all)."""
+    T, N = 120_000_000, 456
+    q = randn(1, 2 * N, 64, seed=871)
+    kv = torch.zeros((T, 1, 64), dtype=torch.bfloat16, device="cuda")
+    lse, flags = torch.empty((1, 2 * N), device="cuda"), i32([0])
+    out = rkv.prompt_attention(q, kv.expand(T, N, 64), kv.expand(T, N, 64), i32([0, 1]), i32([0, T]), lse=lse,
+                               flags=flags)
+    assert flags.item() == 0 and not out.any()
+    assert torch.all((lse.double() - math.log(T)).abs() <= 2.0 ** -20 * math.log(T))
+    del kv
+    torch.cuda.empty_cache()
+
+
+@cuda
 @pytest.mark.parametrize("B", [33, 700, 8192])
 def test_many_short_sequences(B):
     """Batches past a warp, past a block and at the limit, half the sequences empty: prompts of
