@@ -472,7 +472,7 @@ rkv_status rkv_page_append(const rkv_pages* pages, const rkv_page_table* table, 
  *   q (device, bf16) [batch, n_q_heads, D], row b, head h at q + b * q_strides[0] +
  *     h * q_strides[1] elements (16-byte aligned); query head h reads key/value head
  *     h / (n_q_heads / N).  n_q_heads: a multiple of N, at most 16 N.
- *   scale: finite, > 0 (usually 1 / sqrt(D)).
+ *   scale: at least 1e-30 and below 1e30 (usually 1 / sqrt(D)).
  *   out (device, bf16) [batch, n_q_heads, D], contiguous.
  *   lse (device, fp32) [batch, n_q_heads] or NULL: log of the sum of exp(scale q.k).
  *   workspace (device, 16-byte aligned): rkv_page_attention_workspace bytes, this call's
@@ -506,7 +506,7 @@ rkv_status rkv_page_attention_workspace(const rkv_pages* pages, const rkv_page_t
  *     non-decreasing from 0.  The queries are the last positions of their sequence: query i of
  *     Lq sees keys 0 .. Lk - Lq + i (an earlier chunk's keys come first).  A query that sees
  *     none (Lk < Lq) gives a zero row (lse -inf).
- *   scale: finite, > 0 (usually 1 / sqrt(D)).
+ *   scale: at least 1e-30 and below 1e30 (usually 1 / sqrt(D)).
  *   lse (device, fp32) [total_q, n_q_heads] or NULL: log of the sum of exp(scale q.k).
  *   workspace (device, 16-byte aligned): rkv_prompt_attention_workspace bytes, this call's
  *     alone while it runs (NULL where that is 0); needs no initialisation.

@@ -1015,7 +1015,7 @@ extern "C" rkv_status rkv_page_attention(const rkv_pages* pages, const rkv_page_
   size_t need = 0;
   if (rkv_status st = rkv_page_attention_workspace(pages, table, n_q_heads, &need)) return st;
   if (!q || !q_strides || !out || !workspace) return fail_with(RKV_EINVAL, "NULL pointer");
-  if (!(scale > 0.0 && scale < 1e30)) return fail_with(RKV_EINVAL, "scale must be finite and > 0");
+  if (!scale_ok(scale)) return fail_with(RKV_EINVAL, "scale must be at least 1e-30 and below 1e30");
   if (workspace_bytes < need) return fail_with(RKV_ECAPACITY, "workspace has %zu of %zu bytes", workspace_bytes, need);
   if (!is_aligned(q, 16) || !is_aligned(out, 16) || !is_aligned(workspace, 16) || q_strides[0] < 0 ||
       q_strides[1] < 0 || q_strides[0] % 8 || q_strides[1] % 8)

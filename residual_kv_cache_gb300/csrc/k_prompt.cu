@@ -951,7 +951,7 @@ rkv_status check_prompt(const rkv_prompt* pr) {
   if (p.total_q < 0 || p.total_k < 0 || p.total_q > 1 << 30 || p.total_k > 1 << 30 ||
       (int64_t)p.total_q * p.n_q_heads > (int64_t)1 << 33)
     return fail_with(RKV_EINVAL, "total_q and total_k must be in 0..2^30, total_q * n_q_heads at most 2^33");
-  if (!(p.scale > 0.0 && p.scale < 1e30)) return fail_with(RKV_EINVAL, "scale must be finite and > 0");
+  if (!scale_ok(p.scale)) return fail_with(RKV_EINVAL, "scale must be at least 1e-30 and below 1e30");
   return RKV_OK;
 }
 

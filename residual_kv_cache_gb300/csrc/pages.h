@@ -23,6 +23,10 @@ inline bool is_aligned(const void* p, uintptr_t n) {
   return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
 }
 
+// Whether scores times the scale stay numbers: one that fp32 cannot hold makes NaN of a masked
+// score (0 times infinity).
+inline bool scale_ok(double scale) { return scale >= 1e-30 && scale < 1e30; }
+
 // Row r, head h of a strided [rows, heads, D] tensor.
 struct Strides {
   int64_t row, head;

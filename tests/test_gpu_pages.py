@@ -610,6 +610,21 @@ def test_prompt_attention_keeps_sequences_apart():
 
 
 @cuda
+@pytest.mark.parametrize("scale", [1e-30, 1e-20, 2e-3])
+def test_small_scales_weigh_alike(scale):
+    """Scores that are next to nothing: the mean of what a row sees, masked keys left out."""
+    T, Hq, N, D = 150, 4, 2, 64
+    q, k, v = randn(T, Hq, D, seed=816), randn(T, N, D, seed=817), randn(T, N, D, seed=818)
+    out = rkv.prompt_attention(q, k, v, i32([0, 70, T]), scale=scale)
+    ref, _, a, big = OP.prompt_attention(np64(q), np64(k), np64(v), [0, 70, T], [0, 70, T], scale)
+    close(out, ref, a, big, D, 2.0 ** -8)
+    cache, table, tb, (kv, vv) = _paged([130, 7], 2, 32, D, 819)
+    out = rkv.page_attention(q[:2], *cache, table, i32([130, 7]), scale=scale)
+    ref, _, a, big = OP.page_attention(np64(q[:2]), kv, vv, tb, [130, 7], 32, scale)
+    close(out, ref, a, big, D, 2.0 ** -11)
+
+
+@cuda
 def test_prompt_attention_cuts_bad_offsets():
     T, Hq, N, D = 40, 2, 1, 64
     q, k, v = randn(T, Hq, D, seed=821), randn(T, N, D, seed=822), randn(T, N, D, seed=823)

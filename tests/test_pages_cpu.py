@@ -173,6 +173,21 @@ def test_prompt_refusals(lib):
     assert call(total_k=5000, workspace=A + 4, workspace_bytes=n) == -2
 
 
+@pytest.mark.parametrize("scale", [1e-46, 1e-31, math.nextafter(1e-30, 0), 1e30, 1e39, -1e-30])
+def test_scales_outside_their_range_are_refused(lib, scale):
+    """A scale that underflows in fp32 would make NaN of masked scores, one that overflows of all."""
+    S = RP._Strides
+    p = RP._Prompt(q=A, k=A, v=A, out=A, q_strides=S(4096, 128), k_strides=S(1024, 128), v_strides=S(1024, 128),
+                   out_strides=S(4096, 128), cu_q=A, cu_k=A, batch=2, total_q=10, total_k=10, n_q_heads=32,
+                   n_kv_heads=8, head_dim=128, scale=scale)
+    n = ctypes.c_size_t()
+    assert lib.rkv_prompt_attention(ctypes.byref(p), None, None) == -1 and b"scale" in lib.rkv_last_error()
+    assert lib.rkv_prompt_attention_workspace(ctypes.byref(p), ctypes.byref(n)) == -1
+    assert lib.rkv_page_attention_workspace(_pages(), _table(), 32, ctypes.byref(n)) == 0
+    assert lib.rkv_page_attention(_pages(), _table(), A, S(4096, 128), 32, scale, A, None, A, n.value, None, None) == -1
+    assert b"scale" in lib.rkv_last_error()
+
+
 def test_binding_refuses_what_the_library_cannot_see(lib):
     """CPU tensors, other objects and wrong types are refused with ValueError or TypeError
     before any call."""
