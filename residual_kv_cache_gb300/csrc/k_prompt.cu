@@ -35,7 +35,7 @@
 //     fp32 partials (m, l, O) by a second kernel, in their order.
 //
 // Packed rows: a tile's rows behind its sequence are other sequences' rows.  Their queries
-// fill lanes whose results are not stored; their keys are masked by position; their values
+// fill lanes whose results are not stored and who have no vote; their keys are masked by position; their values
 // are zeroed in shared memory, for 0 times what they hold must be 0.
 //
 // Measured, one prompt of 16384 tokens, 32 heads on 8: heads of 128 1.37 ms (1.61 PFLOP/s; a
@@ -621,8 +621,13 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       // keys that this row sees
       const int see = min(items[si].lim[t] + r, lk);
       const int see0 = items[si].lim[t];
+      const int rows = items[si].rows[t];
       if (kvh < 0) break;
-      float m = -INFINITY, l = 0.f;                          // m in base 2
+      // m in base 2.  A lane behind the sequence holds another's query: with an infinite m its
+      // weights are 0 or NaN and it never votes for a maximum to be taken.  (Nobody shares the
+      // votes of a warp that lies wholly behind; one that ran ahead of the others through its
+      // first tile cost a prompt of 77 tokens 0.3 us.)
+      float m = r < rows || (r & ~31) >= rows ? -INFINITY : INFINITY, l = 0.f;
       const uint64_t cc = f32x2_pack(c, c);
       for (int j = j0; j < n1; ++j) {
         kv.next(kSlots);                                     // now V j
@@ -707,7 +712,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
                 mask(xa, 32 * i);
                 top = fmaxf(top, top_of(xa));
                 // to begin with, the first 64 keys do
-                if (i == 1 && j == j0 && __all_sync(0xffffffffu, top > -INFINITY)) break;
+                if (i == 1 && j == j0 && __all_sync(0xffffffffu, top > -INFINITY || m == INFINITY)) break;
               }
               raise_to(top, j > j0);
             }

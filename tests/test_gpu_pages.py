@@ -610,6 +610,26 @@ def test_prompt_attention_keeps_sequences_apart():
 
 
 @cuda
+@pytest.mark.parametrize("lk", [300, 6000])                 # whole pairs, and in shares
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompt_attention_bits_are_the_sequences_own(lk, D):
+    """The next sequence's queries lie in the same tile of rows: whatever they are, and also
+    where they are overwritten meanwhile, the first one's bits are the same."""
+    lq, T, Hq, N = 70, 190, 6, 2
+    cq, ck = i32([0, lq, T]), i32([0, lk, lk + 200])
+    q, k, v = randn(T, Hq, D, seed=841), randn(lk + 200, N, D, seed=842) * 2, randn(lk + 200, N, D, seed=843)
+    base = rkv.prompt_attention(q, k, v, cq, ck)
+    for rows in (math.nan, math.inf, -1e30, 1e4, 0.0):
+        other = q.clone()
+        other[lq:] = rows
+        assert torch.equal(rkv.prompt_attention(other, k, v, cq, ck)[:lq], base[:lq]), rows
+    loud = q.clone()
+    loud[lq:] *= 300
+    assert torch.equal(rkv.prompt_attention(loud, k, v, cq, ck)[:lq], base[:lq])
+    assert torch.equal(rkv.prompt_attention(q, k, v, cq, ck, out=q), base)
+
+
+@cuda
 @pytest.mark.parametrize("scale", [1e-30, 1e-20, 2e-3])
 def test_small_scales_weigh_alike(scale):
     """Scores that are next to nothing: the mean of what a row sees, masked keys left out."""
