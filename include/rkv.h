@@ -365,7 +365,7 @@ rkv_status rkv_retrieve_noalloc(const void* queries, const int32_t* q_pos, int32
  *   flags (device, int32) or NULL: RKV_FLAG_* bits are ORed into it (the caller clears it).
  * What only the device can see never faults: lengths, offsets and block ids are checked
  * there, and what is out of range is treated as absent.  A call in whose flags
- * RKV_FLAG_TIMEOUT appears gave up a wait (about a second): its output is incomplete.
+ * RKV_FLAG_TIMEOUT appears gave up a wait (a second or more): its output is incomplete.
  * An output must not overlap an input or another output but where a call says so.
  * ------------------------------------------------------------------------- */
 
@@ -511,8 +511,10 @@ rkv_status rkv_page_attention_workspace(const rkv_pages* pages, const rkv_page_t
  *   workspace (device, 16-byte aligned): rkv_prompt_attention_workspace bytes, this call's
  *     alone while it runs (NULL where that is 0); needs no initialisation.
  * Rows of out past cu_q[batch] are left as they are.  Rows of other sequences and rows past
- * the last one have no effect, whatever they hold.  Within a sequence a NaN or infinity of V
- * reaches rows that see it and may reach up to 255 rows before it (weights of 0 times NaN).
+ * the last one have no effect, whatever they hold, and neither have keys and values that a row
+ * does not see.  (Rows with a NaN or infinity of V close behind the last key that they see are
+ * computed a second time without the tensor core, 255 rows at most for each, in about 0.15 us
+ * a row and key.)
  * Scores are exact bf16 products summed in fp32; the weights enter the second product as
  * bf16; sums are fp32.  batch in [1, 8192]; total_q and total_k at most 2^30, total_q *
  * n_q_heads at most 2^33.

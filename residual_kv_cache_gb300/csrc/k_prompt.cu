@@ -35,8 +35,10 @@
 //     fp32 partials (m, l, O) by a second kernel, in their order.
 //
 // Packed rows: a tile's rows behind its sequence are other sequences' rows.  Their queries
-// fill lanes whose results are not stored and who have no vote; their keys are masked by position; their values
-// are zeroed in shared memory, for 0 times what they hold must be 0.
+// fill lanes whose results are not stored and who have no vote; their keys are masked by
+// position; their values are zeroed in shared memory, for 0 times what they hold must be 0.
+// Within the sequence that is left to the end: only a NaN or infinity of V that a row does not
+// see can reach it so, and the result shows it (hidden_stray).
 //
 // Measured, one prompt of 16384 tokens, 32 heads on 8: heads of 128 1.37 ms (1.61 PFLOP/s; a
 // library product of two matrices reaches 1.92), heads of 64 1.22 ms (0.90: the chain of waits
@@ -54,6 +56,9 @@ namespace {
 constexpr int kRows = 128;                 // query rows of a tile
 constexpr int kKeys = 128;                 // keys of a tile
 constexpr int kPrThreads = 384;
+// Limit of a wait, some 8 s: a warp that weighs rows again keeps the other roles waiting, 32 rows
+// over 10^6 keys for some 4 s.
+constexpr long long kPrWait = 8 * kWaitCycles;
 constexpr int kItems = 3;                  // work items held ahead
 constexpr float kPrRaise = 16777216.f;     // 2^24: a row's weights of 64 keys may sum to it
 
@@ -75,13 +80,15 @@ constexpr int kMinShare = 8;               // key tiles (of one row tile) that a
 // What the joining kernel has to know of a partial.
 struct Partial {
   int valid, last;                         // last: it ends its pair
-  int row[2], rows[2], head[2];
+  int row[2], rows[2], head[2], lim[2];
+  int k0, lk;
 };
 
 struct PrArgs {
+  const __nv_bfloat16 *q, *k, *v;          // (where the tensor maps do not serve)
   __nv_bfloat16* out;
   float* lse;
-  Strides ost;
+  Strides qst, kst, vst, ost;
   const int32_t *cu_q, *cu_k;
   int32_t* flags;
   int batch, total_q, total_k, Hq, N, G;
@@ -306,9 +313,11 @@ __device__ __forceinline__ void walk_shares(const PrArgs& a, int q0, int lq, int
           const int w = j0 > 0 ? 0 : 1;
           it.slot = 2 * cta + w;
           part[w].valid = 1, part[w].last = j1 == n1;
+          part[w].k0 = it.k0, part[w].lk = it.lk;
 #pragma unroll
           for (int t = 0; t < 2; ++t)
-            part[w].row[t] = it.row[t], part[w].rows[t] = it.rows[t], part[w].head[t] = it.head[t];
+            part[w].row[t] = it.row[t], part[w].rows[t] = it.rows[t], part[w].head[t] = it.head[t],
+            part[w].lim[t] = it.lim[t];
         }
         go = emit(it);
       }
@@ -357,6 +366,15 @@ __device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t lbo) {
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
+// tmem_ld32, and the largest magnitude of the 32 (NaN if there is one).
+__device__ __forceinline__ void tmem_ld32_top(uint32_t taddr, uint32_t* r, uint32_t& top) {
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.abs.NaN.f32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(top)
+      : "r"(taddr));
+}
+
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -396,6 +414,86 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t* w, in
   }
 }
 
+// A NaN or infinity of V makes NaN also of the rows that do not see it, where it shares a tile
+// with keys that they see: their weight of 0 times it.  So a row whose result is not finite is
+// looked at again, by a warp: do the values from the row's last key on to the end of its tiles
+// hold one, in an element that is not NaN among the last values that the row sees?
+template <int D>
+__device__ __forceinline__ bool hidden_stray(const PrArgs& a, int kvh, int k0, int see, int end) {
+  constexpr int kW = D / 64;                                 // words of a lane
+  const __nv_bfloat16* v0 = a.v + (int64_t)k0 * a.vst.row + kvh * a.vst.head + (threadIdx.x & 31) * (2 * kW);
+  uint32_t nan[kW] = {}, stray = 0;
+#pragma unroll 2
+  for (int j = max(see - 32, 0); j < see; ++j) {
+#pragma unroll
+    for (int i = 0; i < kW; ++i)
+      nan[i] |= __vcmpgtu2(reinterpret_cast<const uint32_t*>(v0 + j * a.vst.row)[i] & 0x7FFF7FFFu, 0x7F807F80u);
+  }
+#pragma unroll 2
+  for (int j = see; j < end; ++j) {
+#pragma unroll
+    for (int i = 0; i < kW; ++i)
+      stray |= __vcmpgeu2(reinterpret_cast<const uint32_t*>(v0 + j * a.vst.row)[i] & 0x7FFF7FFFu, 0x7F807F80u) & ~nan[i];
+  }
+  return __any_sync(0xffffffffu, stray != 0);
+}
+
+// Then the row (of q, of query head `head`) is weighed again without the tensor core, over the
+// keys that it sees and no others: some 20 instructions of a warp a key.  A lane scores a key;
+// of the result, relative to m, it holds D / 32 elements.  (`moved`: for the patient wait.)
+template <int D>
+__device__ __forceinline__ void weigh_visible(const PrArgs& a, int64_t row, int head, int k0, int see, float m,
+                                              float* o, volatile int* moved) {
+  constexpr int kW = D / 64, kFlight = 4;                   // values' rows in flight
+  const int lane = threadIdx.x & 31, kvh = head / a.G;
+  const uint4* q = reinterpret_cast<const uint4*>(a.q + row * a.qst.row + head * a.qst.head);
+#pragma unroll
+  for (int e = 0; e < 2 * kW; ++e) o[e] = 0.f;
+#pragma unroll 1
+  for (int j0 = 0; j0 < see; j0 += 32) {
+    const int n = min(32, see - j0);
+    const uint4* k = reinterpret_cast<const uint4*>(a.k + (int64_t)(k0 + j0 + min(lane, n - 1)) * a.kst.row +
+                                                    kvh * a.kst.head);
+    float s = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < D / 8; ++c) {
+      const uint4 x = q[c], y = k[c];
+      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s = fmaf(__uint_as_float(xs[i] << 16), __uint_as_float(ys[i] << 16), s);
+        s = fmaf(__uint_as_float(xs[i] & 0xFFFF0000u), __uint_as_float(ys[i] & 0xFFFF0000u), s);
+      }
+    }
+    const float p = ex2_approx(fmaf(s, a.scale_log2, -m));
+    const __nv_bfloat16* v = a.v + (int64_t)(k0 + j0) * a.vst.row + kvh * a.vst.head + lane * (2 * kW);
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += kFlight) {
+      uint32_t x[kFlight][kW];
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i) {
+#pragma unroll
+        for (int e = 0; e < kW; ++e)                         // (none: 0 times 0)
+          x[i][e] = i0 + i < n ? reinterpret_cast<const uint32_t*>(v + (i0 + i) * a.vst.row)[e] : 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i) {
+        const float w = __shfl_sync(0xffffffffu, p, i0 + i);
+#pragma unroll
+        for (int e = 0; e < kW; ++e) {
+          o[2 * e] = fmaf(w, __uint_as_float(x[i][e] << 16), o[2 * e]);
+          o[2 * e + 1] = fmaf(w, __uint_as_float(x[i][e] & 0xFFFF0000u), o[2 * e + 1]);
+        }
+      }
+    }
+    bool lost = true;                                        // nothing changes any more
+#pragma unroll
+    for (int e = 0; e < 2 * kW; ++e) lost &= o[e] != o[e];
+    if (__all_sync(0xffffffffu, lost)) break;
+    if (moved && lane == 0) *moved = *moved + 0x10000;
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kPrThreads, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -410,7 +508,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   __shared__ Item items[kItems];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_status;
-  __shared__ volatile int s_moved;         // key and value tiles asked for
+  __shared__ volatile int s_moved;         // changes as work is done
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* abort = &s_abort;
   int* status = a.flags ? a.flags : &s_status;               // where a wait that gives up reports
@@ -450,19 +548,19 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         uint32_t q_ph = 1;
         bool ok = true;
         for (int s = 0, ph = 0; ok; s == kItems - 1 ? (s = 0, ph ^= 1) : ++s) {
-          if (!(ok = wait_one(&i_full[s], ph, abort, status))) break;
+          if (!(ok = wait_one<kPrWait>(&i_full[s], ph, abort, status))) break;
           const Item it = items[s];
           mbar_arrive(&i_empty[s]);
           if (it.kvh < 0) break;
           if (it.n[1] == 0) continue;
           const bool both = it.n[0] > it.j0;
-          if (!(ok = wait_one(&q_empty, q_ph, abort, status))) break;
+          if (!(ok = wait_one<kPrWait>(&q_empty, q_ph, abort, status))) break;
           q_ph ^= 1u;
           mbar_arrive_expect_tx(&q_full, (both ? 2 : 1) * C::kTileB);
           if (both) load_tile<D>(s_q, &tm_q, &q_full, it.head[0], it.row[0]);
           load_tile<D>(s_q + C::kTileB, &tm_q, &q_full, it.head[1], it.row[1]);
           for (int j = 2 * it.j0; j < 2 * it.n[1]; ++j) {            // K 0, V 0, K 1, V 1, ...
-            if (!(ok = wait_one(&kv_empty[kv.stage], kv.phase ^ 1u, abort, status))) break;
+            if (!(ok = wait_one<kPrWait>(&kv_empty[kv.stage], kv.phase ^ 1u, abort, status))) break;
             mbar_arrive_expect_tx(&kv_full[kv.stage], C::kTileB);
             load_tile<D>(s_kv + kv.stage * C::kTileB, (j & 1) ? &tm_v : &tm_k, &kv_full[kv.stage], it.kvh,
                          it.k0 + (j >> 1) * kKeys);
@@ -492,7 +590,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         // S_t = Q_t K^T
         auto qk = [&](int t, int slot) {
           if (C::kApart) {                                   // the last S_t has been read
-            ok = ok && wait_one(&s_empty[t], s_ph[t], abort, status);
+            ok = ok && wait_one<kPrWait>(&s_empty[t], s_ph[t], abort, status);
             s_ph[t] ^= 1u;
             if (!ok) return;
             tc_fence_after();
@@ -509,7 +607,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         auto pv = [&](int t, int slot, bool acc) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            ok = ok && wait_one(h ? &p_full[t] : &p_half[t], p_ph[t], abort, status);
+            ok = ok && wait_one<kPrWait>(h ? &p_full[t] : &p_half[t], p_ph[t], abort, status);
             if (!ok) return;
             tc_fence_after();
 #pragma unroll
@@ -522,14 +620,14 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           if (C::kApart) umma_commit(&p_empty[t]);
         };
         for (int s = 0, ph = 0; ok; s == kItems - 1 ? (s = 0, ph ^= 1) : ++s) {
-          if (!(ok = wait_one(&i_full[s], ph, abort, status))) break;
+          if (!(ok = wait_one<kPrWait>(&i_full[s], ph, abort, status))) break;
           const int kvh = items[s].kvh, n0 = items[s].n[0], n1 = items[s].n[1], j0 = items[s].j0;
           mbar_arrive(&i_empty[s]);
           if (kvh < 0) break;
           if (n1 == 0) continue;
-          if (!(ok = wait_one(&q_full, q_ph, abort, status))) break;
+          if (!(ok = wait_one<kPrWait>(&q_full, q_ph, abort, status))) break;
           q_ph ^= 1u;
-          if (!(ok = wait_one(&kv_full[kv.stage], kv.phase, abort, status))) break;
+          if (!(ok = wait_one<kPrWait>(&kv_full[kv.stage], kv.phase, abort, status))) break;
           tc_fence_after();
           if (n0 > j0) qk(0, kv.stage);
           qk(1, kv.stage);
@@ -548,11 +646,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
               }
             };
             if (C::kApart) {
-              if (j + 1 < n1 && !(ok = ok && wait_one(&kv_full[kv.stage], kv.phase, abort, status))) break;
+              if (j + 1 < n1 && !(ok = ok && wait_one<kPrWait>(&kv_full[kv.stage], kv.phase, abort, status))) break;
 #pragma unroll
               for (int t = 0; t < 2; ++t) {
                 next_qk(t);
-                if (t == 0 && !(ok = ok && wait_one(&kv_full[v.stage], v.phase, abort, status))) break;
+                if (t == 0 && !(ok = ok && wait_one<kPrWait>(&kv_full[v.stage], v.phase, abort, status))) break;
                 if (j < (t ? n1 : n0)) {
                   pv(t, v.stage, j > j0);
                   if (j + 1 == (t ? n1 : n0)) umma_commit(&o_full[t]);
@@ -560,15 +658,15 @@ __global__ void __launch_bounds__(kPrThreads, 1)
               }
               umma_commit(&kv_empty[v.stage]);
             } else {
-              if (!(ok = ok && wait_one(&kv_full[v.stage], v.phase, abort, status))) break;
+              if (!(ok = ok && wait_one<kPrWait>(&kv_full[v.stage], v.phase, abort, status))) break;
 #pragma unroll
               for (int t = 0; t < 2; ++t) {
                 if (j < (t ? n1 : n0)) {
                   pv(t, v.stage, j > j0);
                   if (t == 1) umma_commit(&kv_empty[v.stage]);
-                  if (t == 0 && j + 1 < n1) ok = ok && wait_one(&kv_full[kv.stage], kv.phase, abort, status);
+                  if (t == 0 && j + 1 < n1) ok = ok && wait_one<kPrWait>(&kv_full[kv.stage], kv.phase, abort, status);
                   if (t == 1 && j + 1 < n1 && j >= n0)       // tile 0 has not waited for it
-                    ok = ok && wait_one(&kv_full[kv.stage], kv.phase, abort, status);
+                    ok = ok && wait_one<kPrWait>(&kv_full[kv.stage], kv.phase, abort, status);
                   if (!ok) break;
                   next_qk(t);
                   if (j + 1 == (t ? n1 : n0)) umma_commit(&o_full[t]);
@@ -590,7 +688,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       load_seq(a, lane, q0, lq, k0, lk);
       auto emit = [&](const Item& it) {
         // (a place is free when a whole item is done: a second, for some 10^8 keys)
-        if (!wait_warp_while_moving(&i_empty[s], ph, &s_moved, abort, status)) return false;
+        if (!wait_warp_while_moving<kPrWait>(&i_empty[s], ph, &s_moved, abort, status)) return false;
         if (lane == 0) {
           items[s] = it;
           mbar_arrive(&i_full[s]);
@@ -615,7 +713,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     const float c = a.scale_log2;
     bool ok = true;
     for (int si = 0, ph = 0; ok; si == kItems - 1 ? (si = 0, ph ^= 1) : ++si) {
-      if (!(ok = wait_warp(&i_full[si], ph, abort, status))) break;
+      if (!(ok = wait_warp<kPrWait>(&i_full[si], ph, abort, status))) break;
       const int kvh = items[si].kvh, n = items[si].n[t], n1 = items[si].n[1], lk = items[si].lk;
       const int j0 = items[si].j0;
       // keys that this row sees
@@ -632,7 +730,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       for (int j = j0; j < n1; ++j) {
         kv.next(kSlots);                                     // now V j
         if (j < n) {
-          if (!(ok = wait_warp(&s_full[t], s_ph, abort, status))) break;
+          if (!(ok = wait_warp<kPrWait>(&s_full[t], s_ph, abort, status))) break;
           s_ph ^= 1u;
           tc_fence_after();
           const bool masked = (j + 1) * kKeys > see0;        // some row does not see every key
@@ -697,7 +795,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           };
           float part;
           if (C::kApart) {                                   // P V of tile j - 1 is complete
-            if (!(ok = wait_warp(&p_empty[t], p_ph, abort, status))) break;
+            if (!(ok = wait_warp<kPrWait>(&p_empty[t], p_ph, abort, status))) break;
             p_ph ^= 1u;
             tc_fence_after();
           }
@@ -733,7 +831,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           }
           l += part;
           if ((j + 1) * kKeys > lk) {                        // values behind the sequence
-            if (!(ok = wait_warp(&kv_full[kv.stage], kv.phase, abort, status))) break;
+            if (!(ok = wait_warp<kPrWait>(&kv_full[kv.stage], kv.phase, abort, status))) break;
             if (j * kKeys + r >= lk) {
               uint8_t* v = s_kv + kv.stage * C::kTileB + r * 128;
 #pragma unroll
@@ -765,7 +863,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             part = total(sum);
             if (again || !__any_sync(0xffffffffu, part > kPrRaise)) break;
             // the first half's product has to be complete
-            if (!(ok = wait_warp(&p_mid[t], mid_ph, abort, status))) break;
+            if (!(ok = wait_warp<kPrWait>(&p_mid[t], mid_ph, abort, status))) break;
             tc_fence_after();
             raise_to(fmaxf(top_of(xa), top_of(xb)), true);
             again = true;
@@ -784,11 +882,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       // the rows' results
       const int w0 = (warp & 3) * 32, live = items[si].rows[t] - w0;       // of the warp's rows
       const int64_t at = items[si].row[t] + w0;
-      const int head = items[si].head[t], slot = items[si].slot;
+      const int head = items[si].head[t], slot = items[si].slot, k0 = items[si].k0;
       __syncwarp();
       if (lane == 0) mbar_arrive(&i_empty[si]);
       if (n > j0) {
-        if (!(ok = wait_warp(&o_full[t], o_ph, abort, status))) break;
+        if (!(ok = wait_warp<kPrWait>(&o_full[t], o_ph, abort, status))) break;
         o_ph ^= 1u;
         tc_fence_after();
       }
@@ -811,19 +909,48 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       } else {
         const float inv = l != 0.f ? 1.f / l : 0.f;
         uint8_t* dst = reinterpret_cast<uint8_t*>(a.out + at * a.ost.row + head * a.ost.head);
+        uint32_t w[D / 2];
+        float top = 0.f;                                     // largest magnitude, or NaN
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
-          uint32_t x[64], w[32];
+          uint32_t x[64];
           if (n > j0) {
-            tmem_ld32(o_tm + 64 * i, x);
-            tmem_ld32(o_tm + 64 * i + 32, x + 32);
+            uint32_t m0, m1;
+            tmem_ld32_top(o_tm + 64 * i, x, m0);
+            tmem_ld32_top(o_tm + 64 * i + 32, x + 32, m1);
             tmem_ld_wait();
+            top += __uint_as_float(m0) + __uint_as_float(m1);
           }
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            w[e] = l != 0.f ? bf16x2(__uint_as_float(x[2 * e]) * inv, __uint_as_float(x[2 * e + 1]) * inv) : 0u;
-          store_rows(stage, w, live, dst + 128 * i, a.ost.row * 2);
+          for (int e = 0; e < 32; ++e) {
+            w[32 * i + e] =
+                l != 0.f ? bf16x2(__uint_as_float(x[2 * e]) * inv, __uint_as_float(x[2 * e + 1]) * inv) : 0u;
+          }
         }
+        // a row whose result is not finite though its sum is: what it does not see may be why
+        // (looked at before the row is stored: out may be q)
+        const bool finite = top - top == 0.f || l == 0.f || !(l - l == 0.f) || lane >= live;
+        for (uint32_t rest = __ballot_sync(0xffffffffu, !finite); rest != 0; rest &= rest - 1) {
+          const int b = __ffs(rest) - 1, see_b = __shfl_sync(0xffffffffu, see, b);
+          if (!hidden_stray<D>(a, kvh, k0, see_b, min(lk, n * kKeys))) continue;
+          float o[D / 32];
+          weigh_visible<D>(a, at + b, head, k0, see_b, __shfl_sync(0xffffffffu, m, b), o, &s_moved);
+          const float inv_b = __shfl_sync(0xffffffffu, inv, b);
+#pragma unroll
+          for (int e = 0; e < D / 64; ++e)
+            reinterpret_cast<uint32_t*>(stage)[lane * (D / 64) + e] = bf16x2(o[2 * e] * inv_b, o[2 * e + 1] * inv_b);
+          __syncwarp();
+          if (lane == b) {
+#pragma unroll
+            for (int e = 0; e < D / 8; ++e) {
+              const uint4 x = reinterpret_cast<const uint4*>(stage)[e];
+              w[4 * e] = x.x, w[4 * e + 1] = x.y, w[4 * e + 2] = x.z, w[4 * e + 3] = x.w;
+            }
+          }
+          __syncwarp();
+        }
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) store_rows(stage, w + 32 * i, live, dst + 128 * i, a.ost.row * 2);
         if (lane < live && a.lse)
           a.lse[(at + lane) * a.Hq + head] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
       }
@@ -846,8 +973,9 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PrArgs a, int
   constexpr int kE = D / 32, kAhead = 8;                     // partials' rows in flight
   const int c = blockIdx.x, t = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait_previous_grid();
-  const Partial own = a.info[2 * c + 1];
-  if (!own.valid || own.last) return;
+  const Partial& part = a.info[2 * c + 1];
+  if (!part.valid || part.last) return;
+  const int row0 = part.row[t], rows = part.rows[t], head = part.head[t];
   int n = 0;                                                 // partials
   for (int e0 = c + 1; n == 0 && e0 < grid; e0 += 32) {
     const int e = e0 + lane;
@@ -856,7 +984,7 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PrArgs a, int
   }
   if (n == 0) return;                                        // of a call that gave up
   auto slot_of = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
-  for (int r = blockIdx.z * (kJoinThreads / 32) + warp; r < own.rows[t]; r += gridDim.z * (kJoinThreads / 32)) {
+  for (int r = blockIdx.z * (kJoinThreads / 32) + warp; r < rows; r += gridDim.z * (kJoinThreads / 32)) {
     float m = -INFINITY, l = 0.f, o[kE];
 #pragma unroll
     for (int e = 0; e < kE; ++e) o[e] = 0.f;
@@ -903,14 +1031,22 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PrArgs a, int
         }
       }
     }
-    const int64_t at = own.row[t] + r;
+    const int64_t at = row0 + r;
+    float none = 0.f;                                        // NaN where the result is not finite
+#pragma unroll
+    for (int e = 0; e < kE; ++e) none = fmaf(o[e], 0.f, none);
+    if (__any_sync(0xffffffffu, none != 0.f) && l != 0.f && l - l == 0.f) {
+      const int see = min(part.lim[t] + r, part.lk);         // (a row's tiles end 255 keys behind it at most)
+      if (hidden_stray<D>(a, head / a.G, part.k0, see, (int)min((int64_t)part.lk, (int64_t)see + 255)))
+        weigh_visible<D>(a, at, head, part.k0, see, m, o, nullptr);
+    }
     const float inv = l != 0.f ? 1.f / l : 0.f;
-    __nv_bfloat16* dst = a.out + at * a.ost.row + own.head[t] * a.ost.head + lane * kE;
+    __nv_bfloat16* dst = a.out + at * a.ost.row + head * a.ost.head + lane * kE;
 #pragma unroll
     for (int e = 0; e < kE; e += 2)
       *reinterpret_cast<uint32_t*>(dst + e) = l != 0.f ? bf16x2(o[e] * inv, o[e + 1] * inv) : 0u;
     if (a.lse && lane == 0)
-      a.lse[at * a.Hq + own.head[t]] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      a.lse[at * a.Hq + head] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
   }
 }
 
@@ -1015,6 +1151,9 @@ extern "C" rkv_status rkv_prompt_attention(const rkv_prompt* pr, int32_t* flags,
   a.out = static_cast<__nv_bfloat16*>(p.out);
   a.lse = p.lse;
   a.ost = {p.out_strides[0], p.out_strides[1]};
+  a.q = static_cast<const __nv_bfloat16*>(p.q), a.qst = {p.q_strides[0], p.q_strides[1]};
+  a.k = static_cast<const __nv_bfloat16*>(p.k), a.kst = {p.k_strides[0], p.k_strides[1]};
+  a.v = static_cast<const __nv_bfloat16*>(p.v), a.vst = {p.v_strides[0], p.v_strides[1]};
   a.cu_q = p.cu_q, a.cu_k = p.cu_k;
   a.flags = flags;
   a.batch = p.batch, a.total_q = p.total_q, a.total_k = p.total_k;

@@ -90,6 +90,7 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
 
 // Bounded wait for the phase with the given parity.  `abort` is a shared-memory flag
 // that any role raises when it gives up; every waiter then gives up too.
+template <long long kCycles = kWaitCycles>
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
                                           int* status) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -97,7 +98,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   while (true) {
     if (mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
-    if (clock64() - t0 > kWaitCycles) {
+    if (clock64() - t0 > kCycles) {
       *abort = 1;
       atomicOr(status, RKV_FLAG_TIMEOUT);
       return false;

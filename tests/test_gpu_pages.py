@@ -609,6 +609,51 @@ def test_prompt_attention_keeps_sequences_apart():
     close(big, ref, a, s, D, 2.0 ** -8)
 
 
+STRAY = [  # lq, lk, Hq, N, D: whole pairs, shares, more pairs than CTAs; a second sequence of clean rows
+    (300, 300, 4, 2, 128), (300, 300, 3, 3, 64), (200, 6000, 4, 2, 128), (130, 7001, 7, 1, 64),
+    (500, 640, 80, 40, 64), (400, 400, 100, 50, 128), (90, 50, 4, 2, 128), (257, 129, 2, 1, 64)]
+
+
+@cuda
+@pytest.mark.parametrize("case", range(len(STRAY)))
+@pytest.mark.parametrize("inplace", [False, True])
+def test_prompt_attention_hidden_values_have_no_effect(case, inplace):
+    """NaN and infinities of V reach the rows that see them and no row before: one element, a
+    whole row, all rows from one on (a padded prompt), both infinities of one channel."""
+    lq, lk, Hq, N, D = STRAY[case]
+    cq, ck = [0, lq, lq + 40], [0, lk, lk + 40]
+    q = randn(cq[-1], Hq, D, seed=1500 + case)
+    k, v0 = randn(ck[-1], N, D, seed=1520 + case), randn(ck[-1], N, D, seed=1540 + case)
+    clean = rkv.prompt_attention(q, k, v0, i32(cq), i32(ck))
+    few = min(Hq, 6)                                        # heads that are checked one by one
+    heads = sorted({*range(few), Hq - 1})
+    first = max(0, lk - lq)                                 # (the first keys that some query does not see)
+    for what in ("element", "row", "rest", "infinities"):
+        v = v0.clone()
+        if what == "element":
+            v[first + (lk - first) // 2, 0, 5], v[lk - 1, N - 1, D - 1] = math.nan, math.inf
+        elif what == "row":
+            v[first + (lk - first) // 3], v[lk - 2] = math.nan, -math.inf
+        elif what == "rest":
+            v[first + (lk - first) // 2:lk] = math.nan
+        else:
+            v[first + (lk - first) // 4, :, 3], v[lk - 3, :, 3] = math.inf, -math.inf
+            v[lk - 20, :, 7] = -math.inf
+        args, flags = q.clone(), i32([0])
+        out = rkv.prompt_attention(args, k, v, i32(cq), i32(ck), out=args if inplace else None, flags=flags)
+        assert flags.item() == 0 and torch.equal(out[lq:], clean[lq:])
+        for h in heads:
+            n = slice(h // (Hq // N), h // (Hq // N) + 1)
+            ref, _, a, big = OP.prompt_attention(np64(q[:lq, h:h + 1]), np64(k[:lk, n]), np64(v[:lk, n]), [0, lq],
+                                                 [0, lk], 1 / math.sqrt(D))
+            got, fin = np64(out[:lq, h:h + 1]), np.isfinite(ref)
+            assert np.array_equal(got[~fin], ref[~fin], equal_nan=True), what
+            close(torch.from_numpy(got[fin]), ref[fin], a[fin], big, D, 2.0 ** -8)
+        bad = ~torch.isfinite(out)
+        same = torch.isfinite(clean) & ~bad                  # of all heads: what is finite is what it was, nearly
+        assert torch.allclose(out[same].float(), clean[same].float(), rtol=2 ** -6, atol=2 ** -6)
+
+
 @cuda
 @pytest.mark.parametrize("lk", [300, 6000])                 # whole pairs, and in shares
 @pytest.mark.parametrize("D", [64, 128])
