@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(kPaThreads, 1)
           }
         }
       }
-      if (!(ok = wait_warp(&q_empty[s], ph, abort, status))) break;
+      if (!(ok = wait_warp<kWaitForWork>(&q_empty[s], ph, abort, status))) break;
       if (lane == 0) {
         seg[s] = g;
         mbar_arrive(&d_full[s]);                             // the copies need no more

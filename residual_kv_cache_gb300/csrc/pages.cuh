@@ -20,6 +20,10 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, wait_one<kCycles>(bar, parity, abort, status));
 }
 
+// Limit of a wait for a place that whole pieces of work leave, whatever their length: the roles at
+// work wait for each other with the usual limit, and give up for this one too.
+constexpr long long kWaitForWork = 64 * kWaitCycles;
+
 // A warp's wait for something that takes as long as the work in between: it gives up only when
 // `moved`, which that work changes, has stood still for as long as any other wait lasts.
 template <long long kCycles = kWaitCycles>

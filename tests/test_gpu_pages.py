@@ -529,6 +529,22 @@ def test_page_attention_keeps_the_weights_beside_a_dominant_key(case):
     close_lse(lse, rl, big, D)
 
 
+@cuda
+def test_page_attention_of_more_than_a_second_a_sequence():
+    """Sequences (of the same few pages) that take a CTA longer than its bounded waits last: four
+    of 4 10^8 positions for each CTA.  Equal scores: the sums are exact."""
+    T, B, N, P, D = 400_000_000, 152, 4, 128, 64
+    k8 = torch.zeros((64, N, P, D), dtype=torch.uint8, device="cuda")
+    one = torch.ones((64, N), device="cuda")
+    table = (torch.arange(-(-T // P), dtype=torch.int32, device="cuda") % 64).repeat(B, 1)
+    lse, flags = torch.empty((B, N), device="cuda"), i32([0])
+    out = rkv.page_attention(randn(B, N, D, seed=1450), k8, k8, one, one, table, i32([T] * B), lse=lse, flags=flags)
+    assert flags.item() == 0 and not out.any()
+    assert torch.all((lse.double() - math.log(T)).abs() <= 2.0 ** -20 * math.log(T))
+    del table
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------------------------- prompt attention
 PROMPT = [  # lq, lk, Hq, N, D
     ([1], [1], 1, 1, 128), ([1, 2, 3], [1, 2, 3], 4, 2, 64), ([77], [77], 32, 8, 128),
