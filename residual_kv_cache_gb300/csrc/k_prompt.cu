@@ -440,10 +440,10 @@ __device__ __forceinline__ bool hidden_stray(const PrArgs& a, int kvh, int k0, i
 
 // Then the row (of q, of query head `head`) is weighed again without the tensor core, over the
 // keys that it sees and no others: some 20 instructions of a warp a key.  A lane scores a key;
-// of the result, relative to m, it holds D / 32 elements.  (`moved`: for the patient wait.)
+// of the result, relative to m, it holds D / 32 elements.
 template <int D>
 __device__ __forceinline__ void weigh_visible(const PrArgs& a, int64_t row, int head, int k0, int see, float m,
-                                              float* o, volatile int* moved) {
+                                              float* o) {
   constexpr int kW = D / 64, kFlight = 4;                   // values' rows in flight
   const int lane = threadIdx.x & 31, kvh = head / a.G;
   const uint4* q = reinterpret_cast<const uint4*>(a.q + row * a.qst.row + head * a.qst.head);
@@ -490,7 +490,6 @@ __device__ __forceinline__ void weigh_visible(const PrArgs& a, int64_t row, int 
 #pragma unroll
     for (int e = 0; e < 2 * kW; ++e) lost &= o[e] != o[e];
     if (__all_sync(0xffffffffu, lost)) break;
-    if (moved && lane == 0) *moved = *moved + 0x10000;
   }
 }
 
@@ -508,7 +507,6 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   __shared__ Item items[kItems];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_status;
-  __shared__ volatile int s_moved;         // changes as work is done
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* abort = &s_abort;
   int* status = a.flags ? a.flags : &s_status;               // where a wait that gives up reports
@@ -526,7 +524,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     }
     for (int i = 0; i < kItems; ++i) mbar_init(&i_full[i], 1), mbar_init(&i_empty[i], 10);
     mbar_init(&drain, 1);
-    s_abort = s_moved = 0;
+    s_abort = 0;
     fence_barrier_init();
   }
   if (warp == 11) {
@@ -565,7 +563,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             load_tile<D>(s_kv + kv.stage * C::kTileB, (j & 1) ? &tm_v : &tm_k, &kv_full[kv.stage], it.kvh,
                          it.k0 + (j >> 1) * kKeys);
             kv.next(kSlots);
-            s_moved = (int)++issued;
+            ++issued;
           }
         }
         if (*abort) {                                        // no copy may outlive the CTA
@@ -687,8 +685,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       uint32_t ph = 1;
       load_seq(a, lane, q0, lq, k0, lk);
       auto emit = [&](const Item& it) {
-        // (a place is free when a whole item is done: a second, for some 10^8 keys)
-        if (!wait_warp_while_moving<kPrWait>(&i_empty[s], ph, &s_moved, abort, status)) return false;
+        if (!wait_warp<kWaitForWork>(&i_empty[s], ph, abort, status)) return false;
         if (lane == 0) {
           items[s] = it;
           mbar_arrive(&i_full[s]);
@@ -934,7 +931,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           const int b = __ffs(rest) - 1, see_b = __shfl_sync(0xffffffffu, see, b);
           if (!hidden_stray<D>(a, kvh, k0, see_b, min(lk, n * kKeys))) continue;
           float o[D / 32];
-          weigh_visible<D>(a, at + b, head, k0, see_b, __shfl_sync(0xffffffffu, m, b), o, &s_moved);
+          weigh_visible<D>(a, at + b, head, k0, see_b, __shfl_sync(0xffffffffu, m, b), o);
           const float inv_b = __shfl_sync(0xffffffffu, inv, b);
 #pragma unroll
           for (int e = 0; e < D / 64; ++e)
@@ -1038,7 +1035,7 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PrArgs a, int
     if (__any_sync(0xffffffffu, none != 0.f) && l != 0.f && l - l == 0.f) {
       const int see = min(part.lim[t] + r, part.lk);         // (a row's tiles end 255 keys behind it at most)
       if (hidden_stray<D>(a, head / a.G, part.k0, see, (int)min((int64_t)part.lk, (int64_t)see + 255)))
-        weigh_visible<D>(a, at, head, part.k0, see, m, o, nullptr);
+        weigh_visible<D>(a, at, head, part.k0, see, m, o);
     }
     const float inv = l != 0.f ? 1.f / l : 0.f;
     __nv_bfloat16* dst = a.out + at * a.ost.row + head * a.ost.head + lane * kE;

@@ -24,27 +24,4 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
 // work wait for each other with the usual limit, and give up for this one too.
 constexpr long long kWaitForWork = 64 * kWaitCycles;
 
-// A warp's wait for something that takes as long as the work in between: it gives up only when
-// `moved`, which that work changes, has stood still for as long as any other wait lasts.
-template <long long kCycles = kWaitCycles>
-__device__ __forceinline__ bool wait_warp_while_moving(uint64_t* bar, uint32_t parity, volatile int* moved,
-                                                       volatile int* abort, int* status) {
-  bool ok = mbar_test(bar, parity);
-  if (!ok) {
-    long long t0 = clock64();
-    int last = *moved;
-    while (!(ok = mbar_try_wait(bar, parity)) && !*abort) {
-      const int now = *moved;
-      if (now != last) {
-        last = now, t0 = clock64();
-      } else if (clock64() - t0 > kCycles) {
-        *abort = 1;
-        atomicOr(status, RKV_FLAG_TIMEOUT);
-        break;
-      }
-    }
-  }
-  return __all_sync(0xffffffffu, ok);
-}
-
 }  // namespace rkv
