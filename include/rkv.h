@@ -484,7 +484,7 @@ rkv_status rkv_page_append(const rkv_pages* pages, const rkv_page_table* table, 
  * q below 2^-21 of their row's largest are rounded to it).  Of the weights times their page's
  * value scale, the second product holds each to 2^-15 of itself where it is at least 2^-18 of
  * the head's largest, to 2^-11 down to 2^-28 of that, and to 2^-40 of it below: what all of T
- * positions can lose is T 2^-40 of the largest.  Sums are fp32.
+ * positions can lose is T 2^-40 of the largest (value scales up to 2^80).  Sums are fp32.
  * Errors (nothing launched): RKV_EINVAL, RKV_EALIGN, RKV_ECAPACITY (workspace), RKV_ECUDA.
  */
 rkv_status rkv_page_attention(const rkv_pages* pages, const rkv_page_table* table, const void* q,
@@ -516,7 +516,9 @@ rkv_status rkv_page_attention_workspace(const rkv_pages* pages, const rkv_page_t
  * computed a second time without the tensor core, 255 rows at most for each, in about 0.15 us
  * a row and key.)
  * Scores are exact bf16 products summed in fp32; the weights enter the second product as
- * bf16; sums are fp32.  batch in [1, 8192]; total_q and total_k at most 2^30, total_q *
+ * bf16; sums are fp32, that of the second product in the tensor core, which cuts off what an
+ * addend has below some 2^-25 of the sum: of n like weights and values of one sign up to n
+ * 2^-27 of it is lost (0.1 % at 131072 keys, 0.8 % at 2^20).  batch in [1, 8192]; total_q and total_k at most 2^30, total_q *
  * n_q_heads at most 2^33.
  * Rows of out must not overlap each other, lse or k and v; out may be q itself.  q, k and v
  * may overlap, and a stride may be 0 (one row or head for all).

@@ -15,20 +15,21 @@
 //   q (scaled to its row's largest) is two E4M3 parts, hi + lo / 16: exact where it is within
 //   2^-14 of that largest, and within 2^-21 of it everywhere.  A weight is four E5M2 parts,
 //   a + (b + (c + d / 16) / 16) / 2048.  A part takes 4 bits off what is left (three and a
-//   sign), and with the largest weight of a tile at 2^4 or more the last one's step, 2^-16 /
-//   2^19, is 2^-39 of it: a weight is off by 2^-15 of itself down to 2^-18 of the largest, by
+//   sign), and with a head's largest weight at 2^4 or more the last one's step, 2^-16 / 2^19,
+//   is 2^-39 of it: a weight is off by 2^-15 of itself down to 2^-18 of the largest, by
 //   2^-11 down to 2^-28, and by 2^-40 of the largest at any size.  The range is what long
 //   contexts need: beside one key that takes most of the weight, the others have 2^-17 and
 //   less each and still are most of the result where that key's value is small.  (Three E4M3
 //   parts, with their range of 2^-18, lost them; a fourth E4M3 part would have 2^-28 of the
-//   largest as its last step, for more bits than an output of bf16 shows.)  The products are
-//   exact and the parts are joined in fp32.
+//   largest as its last step, for more bits than an output of bf16 shows.  The fourth part
+//   costs long reads nothing, 256 sequences of 1024 tokens 2 us of 55, and 4 of 49 with 16
+//   heads of 64 a key head.)  The products are exact and the parts are joined in fp32.
 //   Softmax: two groups of 128 threads take a CTA's tiles in turn, each with its own score
 //   buffer, weights, sums and accumulator, so that one group's chain of dependent steps runs
 //   beside the other's, across the ends of sequences too.  The group of a segment's last tile
 //   joins the other's part to its own.  Of many short segments a group takes each whole: two
 //   of them then run side by side, where both groups' turns at one would mostly wait for its
-//   ends (1024 sequences of 256 tokens, 8 heads: 166 us by turns, 122 us whole; of three
+//   ends (1024 sequences of 256 tokens, 8 heads: 162 us by turns, 122 us whole; of three
 //   groups 139, of four 158: short segments run all of the code every 2 us, and a fifth of
 //   their stalls already wait for instructions).
 //   Thread t of a group owns token t (TMEM lane t).  Scores s are kept in base 2, and a page's
@@ -45,8 +46,10 @@
 // bits on every run.
 //
 // Measured, 32 query heads on 8 of 128, pages of 64: 16 sequences of up to 131072 tokens, 3.34
-// GB, 473-484 us (7.0 TB/s, where a copy reaches 6.8); one of 1000 tokens 10 us, the latency of
-// one tile's chain, the join's and two launches; between, about 11 us on top of the bytes.
+// GB, 480-484 us (6.9 TB/s, where a copy reaches 6.8); one of 1000 tokens 9.4 us, the latency
+// of one tile's chain, the join's and two launches; between, about 11 us on top of the bytes.
+// Heads of 64 are half the bytes and the same chain: the same lengths 305 us (5.5 TB/s), up to
+// 16384 tokens 49 us, where heads of 128 take 70.
 //
 // Warps: 0 TMA producer, 1 MMA issuer, 2 queries and segment list, 3 page scales and the rows
 // of empty sequences, 4-7 and 8-11 softmax.
@@ -119,7 +122,7 @@ struct PaCfg {
   static constexpr uint32_t kHalf = kTile * D;               // bytes of a K or V tile
   static constexpr uint32_t kStage = 2 * kHalf;
   // as many as fit (of up to 8 heads; with 5 against 6, 61 sequences of up to 5000 tokens take
-  // 52.3 against 51.2 us)
+  // 53.4 against 52.3 us)
   static constexpr int kStages = (kH <= 8 ? 6 : 5) * (128 / D);
   static constexpr uint32_t kQBytes = kNQ * D;               // one segment's query tile
   static constexpr uint32_t kPBytes = kNP * kTile;           // one weight tile
@@ -970,8 +973,8 @@ template <int D>
 cudaError_t launch_all(const CUtensorMap& mk, const CUtensorMap& mv, const PaArgs& a, int grid, int dev,
                         cudaStream_t s) {
   // As many heads as there are, nearly: short calls pay for the code of every head (12 against
-  // 16: 18 sequences of up to 16927 tokens, one key head, 21.5 and 23.7 us, 256 of 1024, two
-  // key heads, 43 and 52; 6 against 8: 256 of 1024, four key heads, 52 and 55).
+  // 16: 18 sequences of up to 16927 tokens, one key head, 21.4 and 23.8 us, 256 of 1024, two
+  // key heads, 48 and 59; 6 against 8: 256 of 1024, four key heads, 57 and 63).
   cudaError_t e = a.G <= 2    ? launch_main<D, 2>(mk, mv, a, grid, dev, s)
                   : a.G <= 4  ? launch_main<D, 4>(mk, mv, a, grid, dev, s)
                   : a.G <= 6  ? launch_main<D, 6>(mk, mv, a, grid, dev, s)

@@ -12,7 +12,7 @@
 // place, a second kernel does that from the offsets.  The call is a handful of dependent
 // loads and latency bounds it: a thread takes kPlanRows rows whose loads overlap (up to
 // 512 new tokens for each of 256 sequences: 14.6 us on one cluster of 8 CTAs, one row at a
-// time, 6.0 us so; one token for each of 16 3.9 us).
+// time, 5.2 us so; one token for each of 16 3.2 us).
 //
 // Append.  A CTA takes the rows that a step brings to a run of 64 positions (whole pages; one
 // page of 128), of K or of V, and one or more heads in turn: it holds a head's rows in
@@ -20,8 +20,8 @@
 // row is read once, and no other CTA touches the pages' scales.  Bandwidth bounds long
 // appends, latency single tokens: finding the run takes about as long as a head's rows, so a
 // CTA takes several heads where there are CTAs enough (32768 rows of 8 heads of 128: 64 us
-// with a head a CTA, 36 us so, 5.6 TB/s; on pages of 16 62 us with a page a CTA, 43 us so; one
-// row for each of 16 sequences 3.4 us).
+// with a head a CTA, 36 us so, 5.6 TB/s, as fp32 55 us, 6.1 TB/s; on pages of 16 62 us with a
+// page a CTA, 43 us so; one row for each of 16 sequences 2.9 us).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -614,7 +614,9 @@ void launch_page(const AppendArgs& a, int sms, cudaStream_t s) {
 
 template <typename T, int D>
 void launch_append(const AppendArgs& a, int block_tokens, int sms, cudaStream_t s) {
-  // up to two rows a sequence on average: a warp a head
+  // Up to two rows a sequence on average: a warp a head (8 heads of 128, pages of 64: one row
+  // for each of 256 sequences 3.9 us, 11.8 with the other kernel, two for each of 64 3.0 and
+  // 6.8.  512 rows of one sequence of 256: 8.8 and 8.2, on pages of 16 4.5 and 10.7).
   if (a.n_rows <= 2 * a.batch) {
     const dim3 grid((unsigned)touched_runs(a, block_tokens), (unsigned)ceil_div(a.N, kAppendThreads / 32), 2);
     page_append_narrow_kernel<T, D><<<grid, kAppendThreads, 0, s>>>(a);

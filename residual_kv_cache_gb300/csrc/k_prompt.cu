@@ -40,10 +40,10 @@
 // Within the sequence that is left to the end: only a NaN or infinity of V that a row does not
 // see can reach it so, and the result shows it (hidden_stray).
 //
-// Measured, one prompt of 16384 tokens, 32 heads on 8: heads of 128 1.37 ms (1.61 PFLOP/s; a
-// library product of two matrices reaches 1.92), heads of 64 1.22 ms (0.90: the chain of waits
-// is the same, for half the flops; without any arithmetic between them it takes 0.99 ms); one
-// of 77 tokens 9.2 us, the latency of one tile.
+// Measured back to back, one prompt of 16384 tokens, 32 heads on 8: heads of 128 1.38 ms (1.59
+// PFLOP/s; a library product of two matrices reaches 1.92), heads of 64 1.24 ms (0.89: the
+// chain of waits is the same, for half the flops; without any arithmetic between them it takes
+// 0.99 ms); one of 77 tokens 9.1 us, the latency of one tile.
 //
 // Warps: 0-3 and 4-7 softmax of tiles 0 and 1, 8 TMA, 9 MMA, 10 work list, 11 TMEM.
 #include <cuda_bf16.h>
