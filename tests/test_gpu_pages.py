@@ -8,6 +8,8 @@ Tolerances, per element, from the roundings (u = half a step, relative):
   again for the scale, the subtraction and exp2, whose arguments are below 2^8;
 * page attention: the same with weights of 12 significant bits (2^-12) of the largest
   weight's scale: 2^-11 of sum w |v| covers it and the range kept below the maximum;
+  (each weight is within 2^-15 of itself down to 2^-18 of the head's largest and within 2^-11
+  down to 2^-28, which the cases with a dominant key reach: 2^-24 and less, 2^-11 of the sum);
 * lse: the fp32 score error and 2^-20 of its magnitude.
 """
 import math
