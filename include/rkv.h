@@ -356,7 +356,8 @@ rkv_status rkv_retrieve_noalloc(const void* queries, const int32_t* q_pos, int32
  * and stores their K/V quantised.  These entry points serve such layers: a step's pages
  * are planned on the GPU from the requests' lengths, the packed prompts are attended with
  * their raw K/V, every new K/V row is stored in 8 bits, and a decode step attends the
- * stored rows.  K arrives rotated (or with whatever position encoding the model uses).
+ * stored rows.  K arrives rotated (rkv_head_norm_rotate, or whatever position encoding the
+ * model uses).
  *
  * They need no context: every buffer is the caller's, nothing is allocated, kept from one
  * call for the next or looked up by address, and calls whose buffers differ may run
@@ -436,7 +437,7 @@ rkv_status rkv_page_plan(const rkv_page_table* table, const int32_t* new_tokens,
  * [0, num_blocks)) do not go to the list (RKV_FLAG_BAD_INDEX).  If the others do not fit it
  * (more than num_blocks), or a length is out of range, nothing changes and RKV_FLAG_NO_SPACE
  * or RKV_FLAG_BAD_INDEX is raised.  A page that several sequences read must be in one
- * released sequence only, and its other readers done with it.
+ * released sequence only, and its other readers done with it (rkv_page_fork frees shared pages).
  * Errors (nothing launched): RKV_EINVAL.
  */
 rkv_status rkv_page_release(const rkv_page_table* table, const int32_t* finished,
@@ -547,6 +548,149 @@ rkv_status rkv_prompt_attention(const rkv_prompt* prompt, int32_t* flags, void* 
  * (host); 0 for calls that need none.  No device work.
  */
 rkv_status rkv_prompt_attention_workspace(const rkv_prompt* prompt, size_t* bytes);
+
+/*
+ * Norm and rotation of query and key rows, before they are attended and stored.  Of each head
+ * x of D values of a row r with positions[r] >= 0:
+ *   norm != 0:  y = x / sqrt(mean(x^2) + eps) * weight; else y = x;
+ *   pair j of the first rotary_dim values, j < rotary_dim / 2, turns by the angle
+ *   a = positions[r] * freq[j]:  (y_a, y_b) -> (y_a cos a - y_b sin a, y_b cos a + y_a sin a).
+ *   A pair is y[j], y[j + rotary_dim / 2], or with adjacent != 0 y[2 j], y[2 j + 1].
+ * (freq[j] = base^(-2 j / rotary_dim) is the rotation that rkv_reconstruct gives K.)
+ *   q, k, q_out, k_out (device) [n_rows, heads, D]: row r, head h at r * strides[0] + h *
+ *     strides[1] elements; 16-byte aligned rows.  Inputs of dtype, outputs of out_dtype: the
+ *     same, or RKV_BF16.  An output may be its input itself (same address, strides and type);
+ *     rows of an output must not overlap.  Either head count may be 0 (its pointers are not
+ *     looked at).
+ *   q_weight, k_weight (device, dtype) [D] or NULL (all 1).
+ *   positions (device, int32) [n_rows]; rows at negative ones are left as they are in the
+ *     outputs (row_pos of rkv_page_plan is -1 past a step's rows).
+ *   freq (device, binary64) [rotary_dim / 2]: radians a position.
+ *   head_dim 64 or 128; rotary_dim a multiple of 16 from 0 (no rotation) to head_dim; n_rows at
+ *   most 2^30; eps in [1e-30, 1e30].
+ * Sums and products are fp32 with one rounding to out_dtype at the end; the angle is kept to
+ * 2^-32 of a turn, beside the 2^-54 of freq[j] in it for each position.
+ * Errors (nothing launched): RKV_EINVAL, RKV_EALIGN, RKV_ECUDA.
+ */
+typedef struct {
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  int64_t q_strides[2], k_strides[2], q_out_strides[2], k_out_strides[2];
+  const void* q_weight;
+  const void* k_weight;
+  const int32_t* positions;
+  const double* freq;
+  int32_t n_rows, n_q_heads, n_k_heads, head_dim, rotary_dim, adjacent, norm, dtype, out_dtype;
+  double eps;
+} rkv_head_rows;
+
+rkv_status rkv_head_norm_rotate(const rkv_head_rows* rows, void* stream);
+
+/*
+ * Pages that several sequences hold.  A page is free when no row of the table holds it: there
+ * are no counts to keep, and rows may share pages as long as none that another row holds is
+ * written.  These calls keep that so: a row's last page, where it is begun and not full, is
+ * held by that row alone after them.  (rkv_page_release frees a row's pages whoever else holds
+ * them: a table that rkv_page_fork has shared pages in frees rows by rkv_page_fork.)
+ *
+ * Fork: row b of the table becomes the first length[b] positions of row source[b] as it was
+ * before the call, for all rows at once.
+ *   source (device, int32) [batch] or NULL (every row its own); negative: an empty row.
+ *   length (device, int32) [batch] or NULL; negative (or NULL): all positions of the source.
+ *   finished (device, int32) [batch] or NULL: rows with finished[b] != 0 become empty.
+ * So source[b] = p forks row p, a length below its own cuts a row, and a finished row's pages
+ * are freed, but for those that other rows hold.
+ *   A begun last page that another row holds whole, or a lower row has begun too, is replaced by
+ * a page of the row's own, into which the first copy_rows[b] rows of page copy_src[b] have to be
+ * copied in every layer (rkv_page_copy takes the lists as they are) before anything is appended.
+ *   table: block_table and seq_len before the call.
+ *   block_table_out (device, int32) [batch, max_blocks], seq_len_out (device) [batch], n_free_out
+ *     (device) [1]: after it.  They may be the table's own and n_free (update in place).  Entries
+ *     past a row's pages are -1 in another table; in place, where the row had pages before.
+ *   free_blocks, n_free: the free list.  Pages that no row holds any more are put on its end, in
+ *     order of their first row and position; then the copies' pages are taken from its end, in
+ *     order of the rows.  The first n_free entries stay as they are.
+ *   copy_src, copy_dst, copy_rows (device, int32) [batch]: of each row its copy, -1, -1 and 0
+ *     where it needs none.
+ *   workspace (device, 16-byte aligned): rkv_page_fork_workspace bytes, this call's alone while
+ *     it runs; needs no initialisation.
+ * All or nothing: where a source is past the table, a length is out of range or above its
+ * source's (RKV_FLAG_BAD_INDEX), or the list would overflow or the copies' pages run out
+ * (RKV_FLAG_NO_SPACE), everything stays (other outputs than in place receive it as it was) and
+ * there are no copies.  Entries that are no page are kept as they are and never reach the list
+ * (RKV_FLAG_BAD_INDEX).
+ * batch * max_blocks below 2^31.
+ * Errors (nothing launched): RKV_EINVAL, RKV_EALIGN, RKV_ECAPACITY (workspace), RKV_ECUDA.
+ */
+rkv_status rkv_page_fork(const rkv_page_table* table, const int32_t* source, const int32_t* length,
+                         const int32_t* finished, int32_t* free_blocks, const int32_t* n_free,
+                         int32_t num_blocks, int32_t block_tokens, int32_t* block_table_out,
+                         int32_t* seq_len_out, int32_t* n_free_out, int32_t* copy_src,
+                         int32_t* copy_dst, int32_t* copy_rows, void* workspace,
+                         size_t workspace_bytes, int32_t* flags, void* stream);
+
+/* Workspace of rkv_page_fork for these sizes, in *bytes (host).  No device work. */
+rkv_status rkv_page_fork_workspace(const rkv_page_table* table, int32_t num_blocks,
+                                   int32_t block_tokens, size_t* bytes);
+
+/*
+ * Compact: the pages that rows hold, n_live of them, move to the numbers below n_live, so that
+ * the pool's end is free.  The i-th held page from n_live on (ascending) goes to the i-th number
+ * below n_live that no row holds.
+ *   table: read; block_table_out (device, int32) [batch, max_blocks] receives the new ids and may
+ *     be the table's own; entries past a row's pages are -1 in another table.
+ *   free_blocks, n_free: receive num_blocks - n_live pages, the last one first (a plan takes
+ *     n_live first).  What the list held before is not read: pages that were lost are free again.
+ *   src, dst (device, int32) [num_blocks / 2], count (device, int32) [1]: the moves, -1 past them;
+ *     rkv_page_copy has to follow in every layer before anything reads the pages.
+ *   workspace (device, 16-byte aligned): rkv_page_compact_workspace bytes, this call's alone
+ *     while it runs; needs no initialisation.
+ * Where a length is out of range, nothing moves, list and count stay (RKV_FLAG_BAD_INDEX).
+ * Entries that are no page are left as they are (RKV_FLAG_BAD_INDEX).
+ * Errors (nothing launched): RKV_EINVAL, RKV_EALIGN, RKV_ECAPACITY (workspace), RKV_ECUDA.
+ */
+rkv_status rkv_page_compact(const rkv_page_table* table, int32_t* free_blocks, int32_t* n_free,
+                            int32_t num_blocks, int32_t block_tokens, int32_t* block_table_out,
+                            int32_t* src, int32_t* dst, int32_t* count, void* workspace,
+                            size_t workspace_bytes, int32_t* flags, void* stream);
+
+/* Workspace of rkv_page_compact, in *bytes (host).  No device work. */
+rkv_status rkv_page_compact_workspace(int32_t num_blocks, size_t* bytes);
+
+/*
+ * Copy listed pages in the caches of n_layers layers (1 to 128, host array, all of one shape):
+ * the first rows[i] rows of every head of page src[i], and its scales, to page dst[i], K and V.
+ *   src, dst (device, int32) [n]; a pair with both negative is none.
+ *   rows (device, int32) [n] or NULL (whole pages).
+ *   count (device, int32) [1] or NULL: pairs from *count on are none.
+ * A pair with an id or a row count out of range is left out (RKV_FLAG_BAD_INDEX).  No page may be
+ * written twice, or written and read, by one call.
+ * Errors (nothing launched): RKV_EINVAL, RKV_EALIGN, RKV_ECUDA.
+ */
+rkv_status rkv_page_copy(const rkv_pages* layers, int32_t n_layers, const int32_t* src,
+                         const int32_t* dst, const int32_t* rows, const int32_t* count, int32_t n,
+                         int32_t* flags, void* stream);
+
+/*
+ * Gather: the first length[b] stored positions of each sequence as packed bf16 rows, for the
+ * attention of prompts behind a stored prefix (k, v and cu_rows are what rkv_prompt_attention
+ * takes as k, v and cu_k).
+ *   length (device, int32) [batch] or NULL (all): 0 leaves a sequence out.
+ *   k, v (device, bf16) [max_rows, N, D], row r, head h at r * strides[0] + h * strides[1]
+ *     elements, 16-byte aligned; rows must not overlap.  Rows past the total stay as they are.
+ *   cu_rows (device, int32) [batch + 1]: first row of each sequence, and the total.
+ * A value is its code times its page's scale, which bf16 holds exactly (from 2^128 on it is
+ * infinite).  Positions whose page is out of range give zero rows (RKV_FLAG_BAD_INDEX).  Where a
+ * length is negative, above seq_len or past the table (RKV_FLAG_BAD_INDEX), or the rows pass
+ * max_rows (RKV_FLAG_NO_SPACE), cu_rows is all 0 and nothing is written.
+ * Errors (nothing launched): RKV_EINVAL, RKV_EALIGN, RKV_ECUDA.
+ */
+rkv_status rkv_page_gather(const rkv_pages* pages, const rkv_page_table* table,
+                           const int32_t* length, void* k, const int64_t k_strides[2], void* v,
+                           const int64_t v_strides[2], int32_t max_rows, int32_t* cu_rows,
+                           int32_t* flags, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Instrumentation (not part of the method).

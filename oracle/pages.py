@@ -1,5 +1,6 @@
 """Full-attention layers written out in float64: the plan of a step's pages, K/V rows in
-8-bit pages, the decode attention over them and the causal attention of packed prompts.
+8-bit pages, the decode attention over them and the causal attention of packed prompts; norm
+and rotation of query and key rows; pages that several sequences hold.
 
 Test infrastructure, like the rest of ``oracle/``; it shares no code with the CUDA library.
 Everything is the operators' definitions, one element, page or row at a time.
@@ -10,7 +11,8 @@ import math
 
 import numpy as np
 
-__all__ = ["plan", "release", "scale_of", "e4m3_round", "append", "page_attention", "prompt_attention"]
+__all__ = ["plan", "release", "scale_of", "e4m3_round", "append", "page_attention", "prompt_attention",
+           "norm_rotate", "fork", "compact", "copy_pages", "gather"]
 
 
 def plan(new, lens, table, free, n_free, P, max_rows):
@@ -135,3 +137,112 @@ def prompt_attention(q, k, v, cu_q, cu_k, scale):
                 if n:
                     big = max(big, scale * (np.abs(kk[:n]) @ np.abs(q[r, h])).max())
     return o, lse, a, big
+
+
+def norm_rotate(x, positions, freq, weight=None, eps=None, adjacent=False):
+    """Rows x [n, H, D] divided by their root mean square (eps None: as they are) times weight
+    [D], then pair j of the first 2 len(freq) values of each head turned by positions freq[j]:
+    values j and j + len(freq), or 2 j and 2 j + 1 (adjacent).  Rows at negative positions
+    come back as NaN: nothing is written there."""
+    x, out = np.asarray(x, np.float64), np.full(np.shape(x), np.nan)
+    h = len(freq)
+    for r, p in enumerate(positions):
+        if p < 0:
+            continue
+        for i in range(x.shape[1]):
+            y = x[r, i].copy()
+            if eps is not None:
+                y /= math.sqrt(float(y @ y) / y.size + eps)
+                if weight is not None:
+                    y *= weight
+            out[r, i] = y
+            for j, f in enumerate(freq):
+                a, b = (2 * j, 2 * j + 1) if adjacent else (j, j + h)
+                c, s = math.cos(p * f), math.sin(p * f)
+                out[r, i, a], out[r, i, b] = y[a] * c - y[b] * s, y[b] * c + y[a] * s
+    return out
+
+
+def fork(source, length, lens, table, free, n_free, P):
+    """Row b of the table becomes the first length[b] positions (length None or length[b] < 0:
+    all) of row source[b] as it was (source None: b; negative: nothing).  Returns (table',
+    lens', free', n_free', copies {b: (src, dst, rows)}), or None where it does not fit."""
+    lens, table, free = [int(x) for x in lens], np.array(table), list(free)
+    B, M = table.shape
+    num = len(free)
+    new, rows = [], []
+    for b in range(B):
+        s = b if source is None else int(source[b])
+        n = 0
+        if s >= B or not 0 <= lens[b] <= M * P:
+            return None
+        if s >= 0:
+            n = lens[s] if length is None or length[b] < 0 else int(length[b])
+            if n > lens[s]:
+                return None
+        new.append(n)
+        rows.append([int(p) for p in table[s, :-(-n // P)]] if n else [])
+    whole, begun = set(), {}                   # pages held whole, and the first row that has begun one
+    for b in range(B):
+        for j, p in enumerate(rows[b]):
+            if (j + 1) * P <= new[b]:
+                whole.add(p)
+            else:
+                begun.setdefault(p, b)
+    there = lambda p: 0 <= p < num  # noqa: E731
+    end, seen = n_free, set()
+    for b in range(B):
+        for p in table[b, :-(-lens[b] // P)]:
+            p = int(p)
+            if there(p) and p not in whole and p not in begun and p not in seen:
+                if end >= num:
+                    return None
+                seen.add(p)
+                free[end] = p
+                end += 1
+    copies = {}
+    for b in range(B):
+        if new[b] % P and there(rows[b][-1]) and (rows[b][-1] in whole or begun[rows[b][-1]] != b):
+            if end == 0:
+                return None
+            end -= 1
+            copies[b] = (rows[b][-1], int(free[end]), new[b] % P)
+    for b in range(B):
+        if b in copies:
+            rows[b][-1] = copies[b][1]
+        table[b] = rows[b] + [-1] * (M - len(rows[b]))
+    return table, new, free, end, copies
+
+
+def compact(lens, table, num, P):
+    """Pages that a row holds, moved to the lowest numbers: the i-th (ascending) held page of at
+    least n_live goes to the i-th page below n_live that none holds.  Returns (table', n_live,
+    moves [(src, dst)]); everything from n_live on is free, the last page first in the list."""
+    table = np.array(table)
+    used = [[int(p) for p in table[b, :-(-int(n) // P)]] for b, n in enumerate(lens)]
+    live = sorted({p for row in used for p in row if 0 <= p < num})
+    holes = [p for p in range(len(live)) if p not in set(live)]
+    to = dict(zip([p for p in live if p >= len(live)], holes))
+    for b, row in enumerate(used):
+        table[b] = [to.get(p, p) for p in row] + [-1] * (table.shape[1] - len(row))
+    return table, len(live), list(to.items())
+
+
+def copy_pages(codes, scale, src, dst, rows=None):
+    """The first rows[i] rows (None: all) of every head of page src[i], and its scale, put in
+    page dst[i]: codes [blocks, N, P, D] and scale [blocks, N] change in place."""
+    for i, (a, b) in enumerate(zip(src, dst)):
+        if a >= 0 and b >= 0:
+            r = codes.shape[2] if rows is None else rows[i]
+            codes[b, :, :r] = codes[a, :, :r]
+            scale[b] = scale[a]
+
+
+def gather(codes, scale, table, lens, P):
+    """The stored rows of all sequences, packed: [sum lens, N, D] (codes as float64 values)."""
+    out = [np.zeros((0, codes.shape[1], codes.shape[3]))]
+    for b, n in enumerate(lens):
+        for p in range(n):
+            i = int(table[b][p // P])
+            out.append((codes[i, :, p % P] * scale[i][:, None])[None])
+    return np.concatenate(out)

@@ -17,7 +17,9 @@ import torch
 __all__ = ["RkvError", "RkvLibraryMissing", "Config", "Codec", "lib", "LIB_PATH", "retrieve_noalloc",
            "FLAG_TIMEOUT", "FLAG_BAD_INDEX", "FLAG_UNWRITTEN", "FLAG_FP16_SAT", "FLAG_BAD_SLOT",
            "ABI_FUNCTIONS", "reconstruct_multi", "FLAG_NO_SPACE", "PagedCache", "PagePlan", "PageTable",
-           "page_plan", "page_release", "page_append", "page_attention", "prompt_attention"]
+           "page_plan", "page_release", "page_append", "page_attention", "prompt_attention",
+           "PageCopies", "head_norm_rotate", "page_compact", "page_copy", "page_fork", "page_gather",
+           "rotation_freq"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "librkv.so")
 
@@ -94,6 +96,14 @@ ABI_FUNCTIONS = {
     "rkv_page_attention_workspace": (_I32, [_P, _P, _I32, ctypes.POINTER(ctypes.c_size_t)]),
     "rkv_prompt_attention": (_I32, [_P, _P, _P]),
     "rkv_prompt_attention_workspace": (_I32, [_P, ctypes.POINTER(ctypes.c_size_t)]),
+    "rkv_head_norm_rotate": (_I32, [_P, _P]),
+    "rkv_page_fork": (_I32, [_P, _P, _P, _P, _P, _P, _I32, _I32, _P, _P, _P, _P, _P, _P, _P,
+                             ctypes.c_size_t, _P, _P]),
+    "rkv_page_fork_workspace": (_I32, [_P, _I32, _I32, ctypes.POINTER(ctypes.c_size_t)]),
+    "rkv_page_compact": (_I32, [_P, _P, _P, _I32, _I32, _P, _P, _P, _P, _P, ctypes.c_size_t, _P, _P]),
+    "rkv_page_compact_workspace": (_I32, [_I32, ctypes.POINTER(ctypes.c_size_t)]),
+    "rkv_page_copy": (_I32, [_P, _I32, _P, _P, _P, _P, _I32, _P, _P]),
+    "rkv_page_gather": (_I32, [_P, _P, _P, _P, _P, _P, _P, _I32, _P, _P, _P]),
 }
 
 _lib = None
@@ -489,5 +499,6 @@ class Codec:
             pass
 
 
-from .pages import (PagedCache, PagePlan, PageTable, page_append, page_attention,  # noqa: E402
-                    page_plan, page_release, prompt_attention)
+from .pages import (PageCopies, PagedCache, PagePlan, PageTable, head_norm_rotate, page_append,  # noqa: E402
+                    page_attention, page_compact, page_copy, page_fork, page_gather, page_plan, page_release,
+                    prompt_attention, rotation_freq)

@@ -34,16 +34,6 @@ constexpr int kPlanThreads = 512;
 constexpr int kPlanRows = 4;         // rows of one thread at a time
 constexpr int kPlanMaxCtas = 512;
 
-// Largest index i in [0, n) with v[i] <= x (v non-decreasing, v[0] <= x).
-__device__ __forceinline__ int last_not_above(const int* v, int n, int x) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (v[mid] <= x) lo = mid; else hi = mid;
-  }
-  return lo;
-}
-
 struct PlanArgs {
   const int32_t* new_tokens;
   const int32_t* seq_len;
@@ -585,14 +575,6 @@ __global__ void __launch_bounds__(kAppendThreads) page_append_narrow_kernel(Appe
   if (held > 0.f && held < s)
     for (int r = r_in; r < u.lo; r += kRows) rescale8(codes + (int64_t)r * D, held / s);
 }
-
-int log2_block(int block_tokens) {
-  int s = 0;
-  while ((1 << s) < block_tokens) ++s;
-  return s;
-}
-
-bool block_ok(int b) { return b == 16 || b == 32 || b == 64 || b == 128; }
 
 // Runs that a step can touch: a sequence's rows touch at most (rows - 2) / length + 2, and no
 // more than its rows.

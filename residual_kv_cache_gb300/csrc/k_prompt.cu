@@ -1120,13 +1120,7 @@ extern "C" rkv_status rkv_prompt_attention(const rkv_prompt* pr, int32_t* flags,
       return fail_with(RKV_EALIGN, "strides must be >= 0 and multiples of 16 bytes");
   if (!is_aligned(p.q, 16) || !is_aligned(p.k, 16) || !is_aligned(p.v, 16) || !is_aligned(p.out, 16))
     return fail_with(RKV_EALIGN, "q, k, v and out must be 16-byte aligned");
-  // out's rows of D: apart, in one order of the strides or the other
-  // (in binary64: exact where it matters, and no product overflows)
-  const double row = (double)p.out_strides[0], head = (double)p.out_strides[1], Dl = p.head_dim;
-  const bool rows1 = p.total_q == 1, heads1 = p.n_q_heads == 1;
-  const bool apart = (heads1 || head >= Dl) && (rows1 || row >= Dl) &&
-                     (rows1 || heads1 || row >= (p.n_q_heads - 1) * head + Dl || head >= (p.total_q - 1) * row + Dl);
-  if (!apart) return fail_with(RKV_EINVAL, "rows of out overlap");
+  if (!rows_apart(p.total_q, p.n_q_heads, p.head_dim, p.out_strides)) return fail_with(RKV_EINVAL, "rows of out overlap");
   size_t need = 0;
   if (rkv_status st = rkv_prompt_attention_workspace(pr, &need)) return st;
   if (p.workspace_bytes < need || (need > 0 && !p.workspace))

@@ -27,6 +27,23 @@ inline bool is_aligned(const void* p, uintptr_t n) {
 // score (0 times infinity).
 inline bool scale_ok(double scale) { return scale >= 1e-30 && scale < 1e30; }
 
+inline bool block_ok(int b) { return b == 16 || b == 32 || b == 64 || b == 128; }
+
+inline int log2_block(int block_tokens) {
+  int s = 0;
+  while ((1 << s) < block_tokens) ++s;
+  return s;
+}
+
+// Whether the rows of D of a strided [rows, heads, D] tensor are apart, in one order of the
+// strides or the other (in binary64: exact where it matters, and no product overflows).
+inline bool rows_apart(int rows, int heads, int D, const int64_t strides[2]) {
+  const double row = (double)strides[0], head = (double)strides[1], Dl = D;
+  const bool rows1 = rows == 1, heads1 = heads == 1;
+  return (heads1 || head >= Dl) && (rows1 || row >= Dl) &&
+         (rows1 || heads1 || row >= (heads - 1) * head + Dl || head >= (rows - 1) * row + Dl);
+}
+
 // Row r, head h of a strided [rows, heads, D] tensor.
 struct Strides {
   int64_t row, head;
@@ -75,6 +92,16 @@ class SmemOptIn {
 
 __device__ __forceinline__ void raise_flag(int32_t* flags, int32_t bit) {
   if (flags) atomicOr(flags, bit);
+}
+
+// Largest index i in [0, n) with v[i] <= x (v non-decreasing, v[0] <= x).
+__device__ __forceinline__ int last_not_above(const int* v, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (v[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
 }
 
 // Inclusive prefix sums of (a, b) over the block, and the block's totals.

@@ -15,6 +15,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <cstring>
 #include <sstream>
 #include <stdexcept>
 
@@ -330,6 +331,213 @@ PyObject* prompt_attention(PyObject* const* a) {
   return a[6];
 }
 
+// (q, k, positions, freq, q_weight, k_weight, eps, adjacent, q_out, k_out, stream) -> (q_out, k_out)
+PyObject* head_norm_rotate(PyObject* const* a) {
+  PyObject *const x[2] = {a[0], a[1]}, *const w[2] = {a[4], a[5]}, *const given[2] = {a[8], a[9]};
+  static const char* const names[2][3] = {{"q", "q_weight", "q_out"}, {"k", "k_weight", "k_out"}};
+  const int any = x[0] == Py_None;
+  if (x[any] == Py_None) throw Refused("q and k are both None");
+  const at::Tensor& t = tensor(x[any], names[any][0]);
+  const int dev = device_of(t, names[any][0]);
+  check_dims(t, names[any][0], 3);
+  const at::ScalarType type = t.scalar_type() == at::kFloat ? at::kFloat : at::kBFloat16;
+  const int64_t rows = t.size(0), D = t.size(2);
+  if (rows > INT32_MAX || D > INT32_MAX) throw Refused(std::string(names[any][0]) + " is too large");
+  // outputs' type: that of one that is given, else the inputs'
+  at::ScalarType out_type = type;
+  for (int i = 0; i < 2; ++i)
+    if (given[i] != Py_None) out_type = tensor(given[i], names[i][2]).scalar_type();
+  if (out_type != type) out_type = at::kBFloat16;
+  const at::Tensor& f = tensor(a[3], "freq");
+  check_dims(f, "freq", 1);
+  rkv_head_rows r;
+  memset(&r, 0, sizeof r);
+  const void** in[2] = {&r.q, &r.k};
+  void** out[2] = {&r.q_out, &r.k_out};
+  const void** weight[2] = {&r.q_weight, &r.k_weight};
+  int64_t *strides[2] = {r.q_strides, r.k_strides}, *out_strides[2] = {r.q_out_strides, r.k_out_strides};
+  int32_t* heads[2] = {&r.n_q_heads, &r.n_k_heads};
+  int64_t shape[2][3] = {{rows, 0, D}, {rows, 0, D}};
+  for (int i = 0; i < 2; ++i) {
+    if (x[i] == Py_None) {
+      if (given[i] != Py_None || w[i] != Py_None) throw Refused(std::string(names[i][0]) + " is None, its output or weight is not");
+      continue;
+    }
+    const at::Tensor& xi = tensor(x[i], names[i][0]);
+    check_dims(xi, names[i][0], 3);
+    shape[i][1] = xi.size(1);
+    if (shape[i][1] > INT32_MAX) throw Refused(std::string(names[i][0]) + " has too many heads");
+    *in[i] = rows_of(xi, names[i][0], shape[i], dev, type, strides[i]);
+    *heads[i] = (int32_t)shape[i][1];
+    *weight[i] = array_or_none(w[i], names[i][1], {D}, dev, type);
+    if (given[i] != Py_None) *out[i] = rows_of(tensor(given[i], names[i][2]), names[i][2], shape[i], dev, out_type, out_strides[i]);
+  }
+  r.positions = static_cast<int32_t*>(array(a[2], "positions", {rows}, dev));
+  r.freq = static_cast<double*>(array(a[3], "freq", {f.size(0)}, dev, at::kDouble));
+  if (f.size(0) > 1 << 20) throw Refused("freq is too long");
+  r.n_rows = (int32_t)rows, r.head_dim = (int32_t)D, r.rotary_dim = 2 * (int32_t)f.size(0);
+  r.norm = a[6] != Py_None;
+  if (r.norm) {
+    r.eps = PyFloat_AsDouble(a[6]);
+    if (r.eps == -1.0 && PyErr_Occurred()) throw PythonError();
+  }
+  r.adjacent = PyObject_IsTrue(a[7]);
+  if (r.adjacent < 0) throw PythonError();
+  r.dtype = type == at::kFloat ? RKV_F32 : RKV_BF16;
+  r.out_dtype = out_type == at::kFloat ? RKV_F32 : RKV_BF16;
+  const On on(dev, a[10]);
+  at::Tensor made[2];
+  for (int i = 0; i < 2; ++i) {
+    if (x[i] == Py_None || given[i] != Py_None) continue;
+    made[i] = make(shape[i], out_type, dev);
+    *out[i] = made[i].data_ptr();
+    out_strides[i][0] = shape[i][1] * D, out_strides[i][1] = D;
+  }
+  check(rkv_head_norm_rotate(&r, on.raw));
+  PyObject* both = PyTuple_New(2);
+  if (!both) throw PythonError();
+  for (int i = 0; i < 2; ++i) {
+    PyObject* o = given[i];
+    if (made[i].defined()) o = THPVariable_Wrap(made[i]);
+    else Py_INCREF(o);
+    PyTuple_SET_ITEM(both, i, o);
+  }
+  return both;
+}
+
+// Three int32 tensors of n, n and m elements on one allocation, as a tuple.
+PyObject* three(const at::Tensor& buf, int64_t n, int64_t m) {
+  PyObject* out = PyTuple_New(3);
+  if (!out) throw PythonError();
+  for (int i = 0; i < 3; ++i) PyTuple_SET_ITEM(out, i, THPVariable_Wrap(part(buf, i * n, i < 2 ? n : m)));
+  return out;
+}
+
+// (source, seq_len, block_table, free_blocks, n_free, block_tokens, length, finished, block_table_out,
+//  seq_len_out, n_free_out, flags, stream) -> (src, dst, rows)
+PyObject* page_fork(PyObject* const* a) {
+  const int32_t P = int_of(a[5], "block_tokens");
+  const int dev = device_of(tensor(a[2], "block_table"), "block_table");
+  const rkv_page_table t = table_of(a[2], a[1], dev);
+  const int64_t B = t.batch, num = length_of(a[3], "free_blocks");
+  const int32_t* source = static_cast<int32_t*>(array_or_none(a[0], "source", {B}, dev));
+  int32_t* fb = static_cast<int32_t*>(array(a[3], "free_blocks", {num}, dev));
+  int32_t* nf = static_cast<int32_t*>(array(a[4], "n_free", {1}, dev));
+  const int32_t* length = static_cast<int32_t*>(array_or_none(a[6], "length", {B}, dev));
+  const int32_t* finished = static_cast<int32_t*>(array_or_none(a[7], "finished", {B}, dev));
+  int32_t* to = a[8] == Py_None ? t.block_table : static_cast<int32_t*>(array(a[8], "block_table_out", {B, t.max_blocks}, dev));
+  int32_t* lo = a[9] == Py_None ? t.seq_len : static_cast<int32_t*>(array(a[9], "seq_len_out", {B}, dev));
+  int32_t* no = a[10] == Py_None ? nf : static_cast<int32_t*>(array(a[10], "n_free_out", {1}, dev));
+  int32_t* fl = flags_of(a[11], dev);
+  size_t bytes = 0;
+  check(rkv_page_fork_workspace(&t, (int32_t)num, P, &bytes));
+  const On on(dev, a[12]);
+  const at::Tensor buf = make({3 * B}, at::kInt, dev), ws = make({(int64_t)bytes}, at::kByte, dev);
+  int32_t* p = static_cast<int32_t*>(buf.data_ptr());
+  check(rkv_page_fork(&t, source, length, finished, fb, nf, (int32_t)num, P, to, lo, no, p, p + B, p + 2 * B,
+                      ws.data_ptr(), bytes, fl, on.raw));
+  return three(buf, B, B);
+}
+
+// (seq_len, block_table, free_blocks, n_free, block_tokens, block_table_out, flags, stream) -> (src, dst, count)
+PyObject* page_compact(PyObject* const* a) {
+  const int32_t P = int_of(a[4], "block_tokens");
+  const int dev = device_of(tensor(a[1], "block_table"), "block_table");
+  const rkv_page_table t = table_of(a[1], a[0], dev);
+  const int64_t num = length_of(a[2], "free_blocks");
+  int32_t* fb = static_cast<int32_t*>(array(a[2], "free_blocks", {num}, dev));
+  int32_t* nf = static_cast<int32_t*>(array(a[3], "n_free", {1}, dev));
+  int32_t* to = a[5] == Py_None ? t.block_table
+                                : static_cast<int32_t*>(array(a[5], "block_table_out", {t.batch, t.max_blocks}, dev));
+  int32_t* fl = flags_of(a[6], dev);
+  size_t bytes = 0;
+  check(rkv_page_compact_workspace((int32_t)num, &bytes));
+  const On on(dev, a[7]);
+  const int64_t n = num / 2;
+  const at::Tensor buf = make({2 * n + 1}, at::kInt, dev), ws = make({(int64_t)bytes}, at::kByte, dev);
+  int32_t* p = static_cast<int32_t*>(buf.data_ptr());
+  check(rkv_page_compact(&t, fb, nf, (int32_t)num, P, to, p, p + n, p + 2 * n, ws.data_ptr(), bytes, fl, on.raw));
+  return three(buf, n, 1);
+}
+
+// (layers: a list or tuple of (k8, v8, k_scale, v_scale), src, dst, rows, count, flags, stream)
+PyObject* page_copy(PyObject* const* a) {
+  if (!PyList_Check(a[0]) && !PyTuple_Check(a[0])) throw Refused("caches must be a list or tuple");
+  const Py_ssize_t layers = PySequence_Fast_GET_SIZE(a[0]);
+  if (layers < 1 || layers > 128) throw Refused("caches must be 1 to 128");
+  rkv_pages pg[128];
+  int dev = 0;
+  for (Py_ssize_t i = 0; i < layers; ++i) {
+    PyObject* l = PySequence_Fast_GET_ITEM(a[0], i);
+    if (!PyTuple_Check(l) || PyTuple_GET_SIZE(l) != 4) throw Refused("a cache must be (k8, v8, k_scale, v_scale)");
+    int at = 0;
+    pg[i] = pages_of(PyTuple_GET_ITEM(l, 0), PyTuple_GET_ITEM(l, 1), PyTuple_GET_ITEM(l, 2), PyTuple_GET_ITEM(l, 3), at);
+    if (i == 0) dev = at;
+    if (at != dev) throw Refused("caches are on several devices");
+  }
+  const int64_t n = length_of(a[1], "src");
+  const int32_t* src = static_cast<int32_t*>(array(a[1], "src", {n}, dev));
+  const int32_t* dst = static_cast<int32_t*>(array(a[2], "dst", {n}, dev));
+  const int32_t* rows = static_cast<int32_t*>(array_or_none(a[3], "rows", {n}, dev));
+  const int32_t* count = static_cast<int32_t*>(array_or_none(a[4], "count", {1}, dev));
+  int32_t* fl = flags_of(a[5], dev);
+  const On on(dev, a[6]);
+  check(rkv_page_copy(pg, (int32_t)layers, src, dst, rows, count, (int32_t)n, fl, on.raw));
+  Py_RETURN_NONE;
+}
+
+// (k8, v8, k_scale, v_scale, block_table, seq_len, max_rows, length, k_out, v_out, flags, stream) -> (k, v, cu_rows)
+PyObject* page_gather(PyObject* const* a) {
+  int dev;
+  const rkv_pages pg = pages_of(a[0], a[1], a[2], a[3], dev);
+  const rkv_page_table t = table_of(a[4], a[5], dev);
+  PyObject* given[2] = {a[8], a[9]};
+  if ((given[0] == Py_None) != (given[1] == Py_None)) throw Refused("k_out and v_out go together");
+  const bool fresh = given[0] == Py_None;
+  int64_t rows = 0;
+  if (a[6] != Py_None) rows = int_of(a[6], "max_rows");
+  else if (fresh) throw Refused("max_rows or k_out and v_out must be given");
+  if (!fresh) {
+    const at::Tensor& k = tensor(given[0], "k_out");
+    check_dims(k, "k_out", 3);
+    if (k.size(0) > INT32_MAX) throw Refused("k_out has too many rows");
+    if (a[6] != Py_None && rows > k.size(0)) throw Refused("k_out has fewer than max_rows rows");
+    if (a[6] == Py_None) rows = k.size(0);
+  }
+  if (rows < 0) throw Refused("max_rows must be >= 0");
+  const int32_t* length = static_cast<int32_t*>(array_or_none(a[7], "length", {t.batch}, dev));
+  int32_t* fl = flags_of(a[10], dev);
+  int64_t strides[2][2];
+  void* out[2];
+  if (!fresh) {
+    static const char* const names[2] = {"k_out", "v_out"};
+    const int64_t n = tensor(given[0], names[0]).size(0), shape[3] = {n, pg.n_kv_heads, pg.head_dim};
+    for (int i = 0; i < 2; ++i) out[i] = rows_of(tensor(given[i], names[i]), names[i], shape, dev, at::kBFloat16, strides[i]);
+  }
+  const On on(dev, a[11]);
+  at::Tensor made[2];
+  if (fresh) {
+    for (int i = 0; i < 2; ++i) {
+      made[i] = make({rows, pg.n_kv_heads, pg.head_dim}, at::kBFloat16, dev);
+      out[i] = made[i].data_ptr();
+      strides[i][0] = (int64_t)pg.n_kv_heads * pg.head_dim, strides[i][1] = pg.head_dim;
+    }
+  }
+  const at::Tensor cu = make({(int64_t)t.batch + 1}, at::kInt, dev);
+  check(rkv_page_gather(&pg, &t, length, out[0], strides[0], out[1], strides[1], (int32_t)rows,
+                        static_cast<int32_t*>(cu.data_ptr()), fl, on.raw));
+  PyObject* all = PyTuple_New(3);
+  if (!all) throw PythonError();
+  for (int i = 0; i < 2; ++i) {
+    PyObject* o = given[i];
+    if (fresh) o = THPVariable_Wrap(made[i]);
+    else Py_INCREF(o);
+    PyTuple_SET_ITEM(all, i, o);
+  }
+  PyTuple_SET_ITEM(all, 2, THPVariable_Wrap(cu));
+  return all;
+}
+
 // No C++ exception leaves the module.
 template <PyObject* (*kFn)(PyObject* const*), int kArgs>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -364,6 +572,11 @@ PyMethodDef g_methods[] = {
     {"page_append", (PyCFunction)(void (*)(void)) & entry<page_append, 11>, METH_FASTCALL, nullptr},
     {"page_attention", (PyCFunction)(void (*)(void)) & entry<page_attention, 12>, METH_FASTCALL, nullptr},
     {"prompt_attention", (PyCFunction)(void (*)(void)) & entry<prompt_attention, 10>, METH_FASTCALL, nullptr},
+    {"head_norm_rotate", (PyCFunction)(void (*)(void)) & entry<head_norm_rotate, 11>, METH_FASTCALL, nullptr},
+    {"page_fork", (PyCFunction)(void (*)(void)) & entry<page_fork, 13>, METH_FASTCALL, nullptr},
+    {"page_compact", (PyCFunction)(void (*)(void)) & entry<page_compact, 8>, METH_FASTCALL, nullptr},
+    {"page_copy", (PyCFunction)(void (*)(void)) & entry<page_copy, 7>, METH_FASTCALL, nullptr},
+    {"page_gather", (PyCFunction)(void (*)(void)) & entry<page_gather, 12>, METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

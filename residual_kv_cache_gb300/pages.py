@@ -1,18 +1,28 @@
-"""Full-attention layers: a step's pages planned on the GPU, the attention of packed
-prompts, K/V stored in 8-bit pages and the decode attention that reads them.
+"""Full-attention layers: a step's pages planned on the GPU, queries' and keys' norm and
+rotation, the attention of packed prompts, K/V stored in 8-bit pages, the decode attention
+that reads them, and pages that several sequences hold.
 
-Argument marshalling for the ``rkv_page_*`` and ``rkv_prompt_attention`` entry points of
-``include/rkv.h``, which give each operator's formulas and limits.  The functions take plain
+Argument marshalling for the ``rkv_page_*``, ``rkv_head_norm_rotate`` and
+``rkv_prompt_attention`` entry points of ``include/rkv.h``, which give each operator's formulas and limits.  The functions take plain
 CUDA tensors; ``PageTable`` and ``PagedCache`` hold the ones that a serving loop keeps:
 
     table = PageTable(batch, max_blocks, num_blocks, block_tokens)
     caches = [PagedCache(n_kv_heads, head_dim, num_blocks, block_tokens) for _ in layers]
     plan = table.plan(new_tokens, max_rows)          # once a step
     for cache in caches:                             # in each layer
+        q, k = head_norm_rotate(q, k, plan.row_pos, freq)
         o = prompt_attention(q, k, v, plan.cu_rows)  # prompts, from their raw K/V
         cache.append(k, v, table, plan)
         o = cache.attend(q, table)                   # decode: one query a sequence
     table.release(finished)
+
+Requests that begin alike share the pages of what they have in common:
+
+    table = PageTable(batch, max_blocks, num_blocks, block_tokens, sharing=True)
+    copies = table.fork(source, length)              # rows become (prefixes of) other rows
+    page_copy(caches, *copies)                       # the pages that two of them have begun
+    k, v, cu_k = cache.gather(table, max_rows, length)     # the prefix, for a prompt behind it
+    page_copy(caches, *table.compact())              # all pages to the pool's low end
 
 Every tensor of a call must lie on one device, which need not be the current one.  Work goes
 to ``stream`` (a ``torch.cuda.Stream`` of that device), or to the device's current stream;
@@ -29,8 +39,9 @@ import torch
 
 import residual_kv_cache_gb300 as _rkv
 
-__all__ = ["PagedCache", "PagePlan", "PageTable", "page_append", "page_attention", "page_plan",
-           "page_release", "prompt_attention"]
+__all__ = ["PageCopies", "PagedCache", "PagePlan", "PageTable", "head_norm_rotate", "page_append",
+           "page_attention", "page_compact", "page_copy", "page_fork", "page_gather", "page_plan",
+           "page_release", "prompt_attention", "rotation_freq"]
 
 _module = None
 
@@ -104,13 +115,86 @@ def prompt_attention(q, k, v, cu_q, cu_k=None, scale=None, out=None, lse=None, f
     return _ext().prompt_attention(q, k, v, cu_q, cu_k, scale, out, lse, flags, stream)
 
 
+def rotation_freq(rotary_dim: int, base: float = 10000.0, device=None):
+    """base^(-2 j / rotary_dim) radians a position, j < rotary_dim / 2, as head_norm_rotate takes
+    them (float64; the codec's restore rotates K by the same angles)."""
+    j = torch.arange(0, rotary_dim, 2, dtype=torch.float64)
+    return torch.pow(torch.tensor(base, dtype=torch.float64), -j / max(1, rotary_dim)).to(device or "cuda")
+
+
+def head_norm_rotate(q, k, positions, freq, q_weight=None, k_weight=None, eps=None, adjacent: bool = False,
+                     q_out=None, k_out=None, stream=None):
+    """Root-mean-square norm of each head of q [rows, n_q_heads, D] and k [rows, N, D] (both bf16
+    or both fp32, strided rows allowed; either may be None), times q_weight and k_weight [D] of
+    the same type, then its rotation: pair j of the first 2 len(freq) values turns by
+    positions[r] * freq[j] (int32 [rows]; float64 radians, see rotation_freq).  Pairs are values
+    j and j + len(freq), or 2 j and 2 j + 1 where `adjacent`.  eps None leaves the norm out.
+    Returns (q, k) of the same type; q_out and k_out may be given (q and k themselves among
+    them, and bf16 for fp32 rows), and rows at negative positions are not written."""
+    return _ext().head_norm_rotate(q, k, positions, freq, q_weight, k_weight, eps, adjacent, q_out, k_out, stream)
+
+
+class PageCopies(NamedTuple):
+    """Pages to copy in every layer, int32: the first rows[i] rows (None: all) of page src[i] to
+    page dst[i]; -1 is none, and so is everything from count[0] on (None: the whole list)."""
+    src: torch.Tensor
+    dst: torch.Tensor
+    rows: torch.Tensor | None
+    count: torch.Tensor | None
+
+
+def page_fork(source, seq_len, block_table, free_blocks, n_free, block_tokens: int, length=None, finished=None,
+              block_table_out=None, seq_len_out=None, n_free_out=None, flags=None, stream=None) -> PageCopies:
+    """Row b of the table becomes the first length[b] positions (None or negative: all) of row
+    source[b] as it was (None: its own; negative: nothing); rows marked in `finished` become
+    empty.  Pages that no row holds any more go to the free list.  Rows of one call may share
+    pages; a last page that two rows have begun is replaced by one of its own for all but one of
+    them: the copies that are returned (page_copy) must be made before rows are appended.
+
+    All int32, as in page_plan; source, length, finished [batch].  The table, lengths and free
+    count after the call go to the _out tensors, by default to the inputs themselves.  A call
+    that does not fit changes nothing (FLAG_NO_SPACE or FLAG_BAD_INDEX in `flags`)."""
+    return PageCopies(*_ext().page_fork(source, seq_len, block_table, free_blocks, n_free, block_tokens, length,
+                                        finished, block_table_out, seq_len_out, n_free_out, flags, stream), None)
+
+
+def page_compact(seq_len, block_table, free_blocks, n_free, block_tokens: int, block_table_out=None, flags=None,
+                 stream=None) -> PageCopies:
+    """Move the pages that rows hold to the lowest numbers, so that the pool's end is free; the
+    free list becomes all others.  The returned copies must be made (page_copy) before the pages
+    are read."""
+    src, dst, count = _ext().page_compact(seq_len, block_table, free_blocks, n_free, block_tokens,
+                                          block_table_out, flags, stream)
+    return PageCopies(src, dst, None, count)
+
+
+def page_copy(caches, src, dst, rows=None, count=None, flags=None, stream=None):
+    """Make the copies of a PageCopies in `caches`, up to 128 layers of one shape: PagedCache
+    objects or (k8, v8, k_scale, v_scale) tuples."""
+    _ext().page_copy([c.arrays() if isinstance(c, PagedCache) else c for c in caches], src, dst, rows, count,
+                     flags, stream)
+
+
+def page_gather(k8, v8, k_scale, v_scale, block_table, seq_len, max_rows=None, length=None, k_out=None, v_out=None,
+                flags=None, stream=None):
+    """The first length[b] (int32 [batch]; None: all) stored positions of each sequence as packed
+    rows: (k, v, cu_rows) with k, v [max_rows, N, D] bf16 (k_out and v_out, if given, whose
+    rows max_rows is by default) and int32 cu_rows [batch + 1].  Rows past cu_rows[-1] are not
+    written.  More than max_rows rows: none, cu_rows all 0 and FLAG_NO_SPACE in `flags`."""
+    return _ext().page_gather(k8, v8, k_scale, v_scale, block_table, seq_len, max_rows, length, k_out, v_out, flags,
+                              stream)
+
+
 class PageTable:
     """The pages of `batch` sequence slots, shared by all layers: block table, lengths, free
-    list and a flags word (FLAG_*, ORed by the calls made through this table)."""
+    list and a flags word (FLAG_*, ORed by the calls made through this table).  With `sharing`,
+    rows may be forked: a release then frees pages that no other row holds."""
 
-    def __init__(self, batch: int, max_blocks: int, num_blocks: int, block_tokens: int = 64, device=None):
+    def __init__(self, batch: int, max_blocks: int, num_blocks: int, block_tokens: int = 64, device=None,
+                 sharing: bool = False):
         dev = torch.device(device or "cuda")
         self.block_tokens = block_tokens
+        self.sharing = sharing
         self.block_table = torch.full((batch, max_blocks), -1, dtype=torch.int32, device=dev)
         self.seq_len = torch.zeros(batch, dtype=torch.int32, device=dev)
         self.free_blocks = torch.arange(num_blocks - 1, -1, -1, dtype=torch.int32, device=dev)
@@ -124,8 +208,26 @@ class PageTable:
 
     def release(self, finished, stream=None):
         """Give back the pages of the sequences marked in `finished` (int32 [batch])."""
+        if self.sharing:                             # (a release shortens no row: there are no copies)
+            page_fork(None, self.seq_len, self.block_table, self.free_blocks, self.n_free, self.block_tokens,
+                      finished=finished, flags=self.flags, stream=stream)
+            return
         page_release(finished, self.seq_len, self.block_table, self.free_blocks, self.n_free,
                      self.block_tokens, flags=self.flags, stream=stream)
+
+    def fork(self, source, length=None, finished=None, stream=None) -> PageCopies:
+        """Rows become (the first length[b] positions of) rows source[b]; see page_fork.  The
+        copies must be made in every layer's cache before the next append."""
+        if not self.sharing:
+            raise ValueError("the table was made without sharing")
+        return page_fork(source, self.seq_len, self.block_table, self.free_blocks, self.n_free, self.block_tokens,
+                         length=length, finished=finished, flags=self.flags, stream=stream)
+
+    def compact(self, stream=None) -> PageCopies:
+        """Move all pages to the pool's low end (see page_compact); the copies must be made in
+        every layer's cache before the pages are read."""
+        return page_compact(self.seq_len, self.block_table, self.free_blocks, self.n_free, self.block_tokens,
+                            flags=self.flags, stream=stream)
 
 
 class PagedCache:
@@ -139,6 +241,9 @@ class PagedCache:
         self.k_scale = torch.empty(shape[:2], dtype=torch.float32, device=dev)
         self.v_scale = torch.empty(shape[:2], dtype=torch.float32, device=dev)
 
+    def arrays(self):
+        return self.k8, self.v8, self.k_scale, self.v_scale
+
     def append(self, k, v, table: PageTable, plan: PagePlan, stream=None):
         """Store the planned step's rows (see page_append)."""
         page_append(k, v, self.k8, self.v8, self.k_scale, self.v_scale, table.block_table,
@@ -149,3 +254,8 @@ class PagedCache:
         return page_attention(q, self.k8, self.v8, self.k_scale, self.v_scale, table.block_table,
                               table.seq_len, scale=scale, out=out, lse=lse, flags=table.flags,
                               stream=stream)
+
+    def gather(self, table: PageTable, max_rows=None, length=None, k_out=None, v_out=None, stream=None):
+        """Stored rows as packed bf16 rows: (k, v, cu_rows), see page_gather."""
+        return page_gather(self.k8, self.v8, self.k_scale, self.v_scale, table.block_table, table.seq_len, max_rows,
+                           length=length, k_out=k_out, v_out=v_out, flags=table.flags, stream=stream)
