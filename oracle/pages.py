@@ -220,8 +220,9 @@ def compact(lens, table, num, P):
     moves [(src, dst)]); everything from n_live on is free, the last page first in the list."""
     table = np.array(table)
     used = [[int(p) for p in table[b, :-(-int(n) // P)]] for b, n in enumerate(lens)]
-    live = sorted({p for row in used for p in row if 0 <= p < num})
-    holes = [p for p in range(len(live)) if p not in set(live)]
+    held = {p for row in used for p in row if 0 <= p < num}
+    live = sorted(held)
+    holes = [p for p in range(len(live)) if p not in held]
     to = dict(zip([p for p in live if p >= len(live)], holes))
     for b, row in enumerate(used):
         table[b] = [to.get(p, p) for p in row] + [-1] * (table.shape[1] - len(row))

@@ -9,12 +9,16 @@ namespace rkv {
 namespace {
 
 // ------------------------------------------------------------------- table operations
-// One cluster does a call, so that its phases can wait for one another; a warp takes a run of
-// tasks (128 neighbouring entries of a row of the table), the same ones in every phase.
+// A call is a few phases that wait for one another, each a load or two long, and latency bounds
+// it: one CTA does it, or a cluster of up to 16.  A warp takes a run of tasks (128 neighbouring
+// entries of a row of the table), the same ones in every phase, and holds the entries of the
+// first of them in registers from the first phase to the last.
 constexpr int kTableThreads = 1024;
 constexpr int kTableWarps = kTableThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr int kTaskEntries = 128;
+constexpr int kLaneEntries = kTaskEntries / 32;
+constexpr size_t kTableSmem = 220 * 1024;      // dynamic shared memory of a CTA at most
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -27,18 +31,44 @@ __device__ __forceinline__ uint32_t cluster_size() {
   return r;
 }
 // Every thread's earlier writes are seen by every thread of the cluster afterwards.
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+__device__ __forceinline__ void cluster_sync(uint32_t ctas) {
+  if (ctas == 1) __syncthreads();
+  else asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-
+// The same variable of another CTA of the cluster.
+template <typename T>
+__device__ __forceinline__ T* in_cta(T* p, uint32_t rank) {
+  uint64_t r;
+  asm("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
+  return reinterpret_cast<T*>(r);
+}
 struct Tasks {
   int first, last, per_row;          // this warp's [first, last)
-  __device__ __forceinline__ Tasks(int batch, int width) {
+  __device__ __forceinline__ Tasks(int batch, int width, uint32_t rank, uint32_t ctas) {
     per_row = (width + kTaskEntries - 1) / kTaskEntries;
-    const int64_t n = (int64_t)batch * per_row;
-    const int64_t warps = (int64_t)cluster_size() * kTableWarps;
-    const int64_t w = (int64_t)cluster_rank() * kTableWarps + threadIdx.x / 32;
+    const int64_t n = (int64_t)batch * per_row, warps = (int64_t)ctas * kTableWarps;
+    const int64_t w = (int64_t)rank * kTableWarps + threadIdx.x / 32;
     first = (int)(n * w / warps), last = (int)(n * (w + 1) / warps);
+  }
+  // f(i, row, entry of the row) for the entries of this lane: i counts those of the first kHold
+  // tasks and is -1 in the others.  Every lane of the warp makes the same calls.
+  template <int kHold, typename F>
+  __device__ __forceinline__ void each(F f) const {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 0; h < kHold; ++h) {
+      const int t = first + h;
+      if (t < last) {
+        const int b = t / per_row, j0 = (t - b * per_row) * kTaskEntries + lane;
+#pragma unroll
+        for (int k = 0; k < kLaneEntries; ++k) f(h * kLaneEntries + k, b, j0 + 32 * k);
+      }
+    }
+    for (int t = first + kHold; t < last; ++t) {
+      const int b = t / per_row, j0 = (t - b * per_row) * kTaskEntries + lane;
+#pragma unroll
+      for (int k = 0; k < kLaneEntries; ++k) f(-1, b, j0 + 32 * k);
+    }
   }
 };
 
@@ -56,15 +86,16 @@ struct ForkArgs {
   int32_t* copy_src;
   int32_t* copy_dst;
   int32_t* copy_rows;
-  int32_t* held;                     // [num_blocks] -1: held whole; the first row that has begun it; kNone
-  int32_t* first;                    // [num_blocks] first entry of the old table that may give it up
-  int32_t* counts;                   // [warps] pages that a warp's tasks free
+  int2* state;                       // [num_blocks], of calls whose CTA does not hold it
   int32_t* stage;                    // [batch, max_blocks] new rows, for a table changed in place
   int32_t* flags;
   int batch, max_blocks, num_blocks, shift;
 };
 
+// What is known of a page: x: -1 where a row holds it whole, else the first row that has begun
+// it, kNone without one; y: the first entry of the old table that lets go of it.
 constexpr int kNone = INT32_MAX;
+constexpr int kForkHold = 3;
 
 // The table, lengths and count as they were, and no copies.
 __device__ __forceinline__ void fork_refused(const ForkArgs& p, int32_t flag, int n_free) {
@@ -82,162 +113,187 @@ __device__ __forceinline__ void fork_refused(const ForkArgs& p, int32_t flag, in
   }
 }
 
+// kLocal: one CTA, with the pages' state in its shared memory.
+template <bool kLocal>
 __global__ void __launch_bounds__(kTableThreads) page_fork_kernel(const __grid_constant__ ForkArgs p) {
   extern __shared__ int fsm[];
   int* s_src = fsm;                  // [batch] source row, -1: none
   int* s_new = s_src + p.batch;      // [batch] positions after the call
   int* s_have = s_new + p.batch;     // [batch] pages before it
   int* s_copy = s_have + p.batch;    // [batch] place among the copies, -1: none
-  int* s_from = s_copy + p.batch;    // [batch] page that is copied
-  __shared__ int s_width, s_base[kTableWarps];
+  int* s_from = s_copy + p.batch;    // [batch] page that is copied, -1: none
+  int2* s_state = reinterpret_cast<int2*>(fsm + (5 * p.batch + 1) / 2 * 2);
+  __shared__ int s_width, s_count[kTableWarps], s_total[kMaxCluster], s_copies[kMaxBatch / kTableThreads][kTableWarps];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const uint32_t rank = cluster_rank(), ctas = cluster_size();
-  const int P1 = (1 << p.shift) - 1, M = p.max_blocks;
+  const uint32_t rank = kLocal ? 0 : cluster_rank(), ctas = kLocal ? 1 : cluster_size();
+  const int step = ctas * kTableThreads, me = rank * kTableThreads + tid;
+  const int P1 = (1 << p.shift) - 1, M = p.max_blocks, num = p.num_blocks;
   const int64_t cap = (int64_t)M << p.shift;
   const bool in_place = p.table_out == p.table;
-  const int n_free = *p.n_free;
-  auto is_page = [&](int id) { return id >= 0 && id < p.num_blocks; };
+  auto is_page = [&](int id) { return id >= 0 && id < num; };
   auto pages = [&](int n) { return (int)(((int64_t)n + P1) >> p.shift); };
+  auto state = [&](int id) {
+    if constexpr (kLocal) return s_state + id;
+    else return p.state + id;
+  };
+  auto read_state = [&](int id) {
+    if constexpr (kLocal) return s_state[id];
+    else return __ldcg(p.state + id);
+  };
 
-  for (int i = rank * kTableThreads + tid; i < p.num_blocks; i += ctas * kTableThreads) p.held[i] = p.first[i] = kNone;
+  const int n_free = *p.n_free;
+  for (int b = tid; b < p.batch; b += kTableThreads) s_have[b] = p.seq_len[b];
   if (tid == 0) s_width = 0;
-  bool bad = n_free < 0 || n_free > p.num_blocks;
+  for (int i = kLocal ? tid : me; i < num; i += step) *state(i) = make_int2(kNone, kNone);
+  __syncthreads();                   // s_have: positions before the call, at first
+  bool bad = n_free < 0 || n_free > num;
   int width = 0;
   for (int b = tid; b < p.batch; b += kTableThreads) {
-    int len = p.seq_len[b], s = p.source ? p.source[b] : b, n = 0;
+    int s = p.source ? p.source[b] : b, n = 0;
+    const int want = p.length ? p.length[b] : -1, len = s_have[b];
     if (p.finished && p.finished[b] != 0) s = -1;
-    if (len < 0 || len > cap) bad = true, len = 0;
+    if (len < 0 || len > cap) bad = true;
     if (s >= p.batch) bad = true, s = -1;
     if (s >= 0) {
-      const int all = p.seq_len[s];
-      n = p.length && p.length[b] >= 0 ? p.length[b] : all;
+      const int all = s_have[s];
+      n = want >= 0 ? want : all;
       if (n < 0 || n > all || all > cap) bad = true, n = 0;
     }
     s_src[b] = max(s, -1);
     s_new[b] = n;
-    s_have[b] = pages(len);
-    width = max(width, max(s_have[b], pages(n)));
+    width = max(width, max(pages(len), pages(n)));
   }
   bad = __syncthreads_or(bad);
   if (bad) {
     fork_refused(p, RKV_FLAG_BAD_INDEX, n_free);
     return;
   }
-  atomicMax(&s_width, width);
-  cluster_sync();
-  const Tasks tasks(p.batch, in_place ? s_width : M);
+  for (int b = tid; b < p.batch; b += kTableThreads) s_have[b] = pages(s_have[b]);
+  width = __reduce_max_sync(0xffffffffu, width);
+  if (lane == 0) atomicMax(&s_width, width);
+  cluster_sync(ctas);
+  const Tasks tasks(p.batch, in_place ? s_width : M, rank, ctas);
 
   // who holds what: rows after the call, and the entries that go
-  bool stray = false;
-  for (int t = tasks.first; t < tasks.last; ++t) {
-    const int b = t / tasks.per_row, j0 = (t - b * tasks.per_row) * kTaskEntries;
-    const int s = s_src[b], n = s_new[b], m = pages(n), have = s_have[b];
-#pragma unroll
-    for (int k = 0; k < kTaskEntries / 32; ++k) {
-      const int j = j0 + k * 32 + lane;
-      if (j < m) {
-        const int id = p.table[(int64_t)s * M + j];
-        if (in_place && s != b) p.stage[(int64_t)b * M + j] = id;
-        if (is_page(id)) atomicMin(p.held + id, j == m - 1 && (n & P1) ? b : -1);
-        else stray = true;
-      }
-      if (j < have && (s != b || j >= m)) {
-        const int id = p.table[(int64_t)b * M + j];
-        if (is_page(id)) atomicMin(p.first + id, b * M + j);
-        else stray = true;
-      }
-    }
+  int to[kForkHold * kLaneEntries], gone[kForkHold * kLaneEntries];      // -1: none
+  auto load = [&](int b, int j, int& t, int& g) {
+    const int s = s_src[b], m = pages(s_new[b]);
+    t = j < m ? p.table[(int64_t)s * M + j] : -1;
+    g = j < s_have[b] && (s != b || j >= m) ? p.table[(int64_t)b * M + j] : -1;
+  };
+  tasks.each<kForkHold>([&](int i, int b, int j) {
+    if (i >= 0) load(b, j, to[i], gone[i]);
+  });
+  for (int b = tid; b < p.batch; b += kTableThreads) {         // last pages that are begun
+    const int n = s_new[b];
+    s_from[b] = n & P1 ? p.table[(int64_t)s_src[b] * M + pages(n) - 1] : -1;
   }
+  bool stray = false;
+  tasks.each<kForkHold>([&](int i, int b, int j) {
+    int t, g;
+    if (i >= 0) t = to[i], g = gone[i];
+    else load(b, j, t, g);
+    const int s = s_src[b], n = s_new[b], m = pages(n);
+    if (j < m) {
+      // (-1 is the least: a plain store of it and another row's minimum end the same)
+      if (!is_page(t)) stray = true;
+      else if (j == m - 1 && (n & P1)) atomicMin(&state(t)->x, b);
+      else state(t)->x = -1;
+      if (i < 0 && in_place && s != b) p.stage[(int64_t)b * M + j] = t;
+    }
+    if (j < s_have[b] && (s != b || j >= m)) {
+      if (is_page(g)) atomicMin(&state(g)->y, b * M + j);
+      else stray = true;
+    }
+  });
   if (stray) raise_flag(p.flags, RKV_FLAG_BAD_INDEX);
-  cluster_sync();
+  cluster_sync(ctas);
 
   // pages that go, in the order of the entries; copies, in that of the rows
-  auto freed = [&](int b, int j, int& id) {
-    const int s = s_src[b];
-    if (j >= s_have[b] || (s == b && j < pages(s_new[b]))) return false;
-    id = p.table[(int64_t)b * M + j];
-    return is_page(id) && __ldcg(p.held + id) == kNone && __ldcg(p.first + id) == b * M + j;
+  auto goes = [&](int b, int j, int g) {
+    if (!is_page(g)) return false;
+    const int2 s = read_state(g);
+    return s.x == kNone && s.y == b * M + j;
   };
-  int gone = 0;
-  for (int t = tasks.first; t < tasks.last; ++t) {
-    const int b = t / tasks.per_row, j0 = (t - b * tasks.per_row) * kTaskEntries;
-#pragma unroll
-    for (int k = 0; k < kTaskEntries / 32; ++k) {
-      int id;
-      gone += __popc(__ballot_sync(0xffffffffu, freed(b, j0 + k * 32 + lane, id)));
-    }
-  }
-  if (lane == 0) p.counts[rank * kTableWarps + wid] = gone;
-  int copies = 0;
-  for (int b0 = 0; b0 < p.batch; b0 += kTableThreads) {
-    const int b = b0 + tid;
-    int id = -1;
-    if (b < p.batch && (s_new[b] & P1)) {
-      id = p.table[(int64_t)s_src[b] * M + pages(s_new[b]) - 1];
-      if (!is_page(id) || __ldcg(p.held + id) == b) id = -1;
-    }
-    int64_t none = 0, total_none;
-    int c = id >= 0, total;
-    block_scan<kTableThreads>(none, c, total_none, total);
+  int count = 0;
+  tasks.each<kForkHold>([&](int i, int b, int j) {
+    int t, g;
+    if (i >= 0) g = gone[i];
+    else load(b, j, t, g);
+    const bool go = goes(b, j, g);
+    if (i >= 0) gone[i] = go ? g : -1;
+    count += __popc(__ballot_sync(0xffffffffu, go));
+  });
+  if (lane == 0) s_count[wid] = count;
+  for (int r = 0, b = tid; r * kTableThreads < p.batch; ++r, b += kTableThreads) {
+    int id = b < p.batch ? s_from[b] : -1;
+    if (!is_page(id) || read_state(id).x == b) id = -1;
+    const uint32_t these = __ballot_sync(0xffffffffu, id >= 0);
+    if (lane == 0) s_copies[r][wid] = __popc(these);
     if (b < p.batch) {
-      s_copy[b] = id >= 0 ? copies + c - 1 : -1;
+      s_copy[b] = id >= 0 ? __popc(these & ((1u << lane) - 1)) : -1;     // of the warp's, at first
       s_from[b] = id;
     }
-    copies += total;
   }
-  cluster_sync();
-
-  int64_t none = 0, total_none;
-  const int warps = ctas * kTableWarps;
-  const int mine = tid < warps ? __ldcg(p.counts + tid) : 0;
-  int before = mine, total;
-  static_assert(kMaxCluster * kTableWarps <= kTableThreads);
-  block_scan<kTableThreads>(none, before, total_none, total);
-  if (tid / kTableWarps == rank) s_base[tid % kTableWarps] = before - mine;
   __syncthreads();
+  int copies = 0;
+  for (int r = 0, b = tid; r * kTableThreads < p.batch; ++r, b += kTableThreads) {
+    const int n = s_copies[r][lane];
+    const int earlier = copies + __reduce_add_sync(0xffffffffu, lane < wid ? n : 0);
+    if (b < p.batch && s_copy[b] >= 0) s_copy[b] += earlier;
+    copies += __reduce_add_sync(0xffffffffu, n);
+  }
+  int before = lane < wid ? s_count[lane] : 0, all = s_count[lane];
+  before = __reduce_add_sync(0xffffffffu, before);
+  all = __reduce_add_sync(0xffffffffu, all);
+  if (tid < ctas) *in_cta(&s_total[rank], tid) = all;
+  cluster_sync(ctas);
+
+  int total = 0;
+  for (uint32_t c = 0; c < ctas; ++c) {
+    if (c < rank) before += s_total[c];
+    total += s_total[c];
+  }
   const int64_t end = (int64_t)n_free + total;
-  if (end > p.num_blocks || end < copies) {
+  if (end > num || end < copies) {
     fork_refused(p, RKV_FLAG_NO_SPACE, n_free);
     return;
   }
-  int at = n_free + s_base[wid];
-  for (int t = tasks.first; t < tasks.last; ++t) {
-    const int b = t / tasks.per_row, j0 = (t - b * tasks.per_row) * kTaskEntries;
-#pragma unroll
-    for (int k = 0; k < kTaskEntries / 32; ++k) {
-      int id;
-      const bool goes = freed(b, j0 + k * 32 + lane, id);
-      const uint32_t all = __ballot_sync(0xffffffffu, goes);
-      if (goes) p.free_blocks[at + __popc(all & ((1u << lane) - 1))] = id;
-      at += __popc(all);
+  int at = n_free + before;
+  tasks.each<kForkHold>([&](int i, int b, int j) {
+    int t, g;
+    bool go;
+    if (i >= 0) {
+      g = gone[i], go = g >= 0;
+    } else {
+      load(b, j, t, g);
+      go = goes(b, j, g);
     }
-  }
-  cluster_sync();
+    const uint32_t these = __ballot_sync(0xffffffffu, go);
+    if (go) p.free_blocks[at + __popc(these & ((1u << lane) - 1))] = g;
+    at += __popc(these);
+  });
+  cluster_sync(ctas);
 
-  for (int t = tasks.first; t < tasks.last; ++t) {
-    const int b = t / tasks.per_row, j0 = (t - b * tasks.per_row) * kTaskEntries;
+  tasks.each<kForkHold>([&](int i, int b, int j) {
     const int s = s_src[b], m = pages(s_new[b]);
-#pragma unroll
-    for (int k = 0; k < kTaskEntries / 32; ++k) {
-      const int j = j0 + k * 32 + lane;
-      int32_t* out = p.table_out + (int64_t)b * M + j;
-      if (j < m) {
-        if (j == m - 1 && s_copy[b] >= 0) *out = __ldcg(p.free_blocks + (end - 1 - s_copy[b]));
-        else if (!in_place) *out = p.table[(int64_t)s * M + j];
-        else if (s != b) *out = p.stage[(int64_t)b * M + j];
-      } else if (j < (in_place ? s_have[b] : M)) {
-        *out = -1;
-      }
+    int32_t* out = p.table_out + (int64_t)b * M + j;
+    if (j < m) {
+      if (j == m - 1 && s_copy[b] >= 0) *out = __ldcg(p.free_blocks + (end - 1 - s_copy[b]));
+      else if (!in_place) *out = i >= 0 ? to[i] : p.table[(int64_t)s * M + j];
+      else if (s != b) *out = i >= 0 ? to[i] : p.stage[(int64_t)b * M + j];
+    } else if (j < (in_place ? s_have[b] : M)) {
+      *out = -1;
     }
-  }
-  for (int b = rank * kTableThreads + tid; b < p.batch; b += ctas * kTableThreads) {
+  });
+  for (int b = me; b < p.batch; b += step) {
     const int c = s_copy[b];
     p.seq_len_out[b] = s_new[b];
     p.copy_src[b] = s_from[b];
     p.copy_dst[b] = c >= 0 ? __ldcg(p.free_blocks + (end - 1 - c)) : -1;
     p.copy_rows[b] = c >= 0 ? s_new[b] & P1 : 0;
   }
-  if (rank == 0 && tid == 0) *p.n_free_out = (int)(end - copies);
+  if (me == 0) *p.n_free_out = (int)(end - copies);
 }
 
 struct CompactArgs {
@@ -249,27 +305,49 @@ struct CompactArgs {
   int32_t* src;
   int32_t* dst;
   int32_t* count;
-  uint32_t* bits;                    // [words] held pages
-  int32_t* before;                   // [words] held pages before a word's
-  int32_t* totals;                   // [CTAs] held pages of a CTA's words
+  int2* state;                       // [CTAs, words], of pools that shared memory does not take
   int32_t* flags;
-  int batch, max_blocks, num_blocks, shift;
+  int batch, max_blocks, num_blocks, shift, words;   // words of a CTA: a power of two
 };
 
+constexpr int kCompactHold = 4;
+
+// Of each 32 pages, x: which of them rows hold (a bit each); y: how many of the CTA's pages are
+// held before them.  kLocal: each CTA marks the pages of its own entries in its shared memory,
+// joins its words of all CTAs' marks, and takes the others' joined words over, so that every
+// look-up is its own; else all is in the workspace.
+template <bool kLocal>
 __global__ void __launch_bounds__(kTableThreads) page_compact_kernel(const __grid_constant__ CompactArgs p) {
   extern __shared__ int fsm[];
   int* s_have = fsm;                 // [batch] pages
-  __shared__ int s_width, s_low;
-  const int tid = threadIdx.x, lane = tid & 31;
+  int2* s_state = reinterpret_cast<int2*>(fsm + (p.batch + 1) / 2 * 2);
+  __shared__ int s_width, s_total[kMaxCluster], s_base[kMaxCluster + 1];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const uint32_t rank = cluster_rank(), ctas = cluster_size();
   const int step = ctas * kTableThreads, me = rank * kTableThreads + tid;
-  const int P1 = (1 << p.shift) - 1, M = p.max_blocks, num = p.num_blocks;
-  const int words = (int)(((int64_t)num + 31) / 32), places = num / 2;
+  const int P1 = (1 << p.shift) - 1, M = p.max_blocks, num = p.num_blocks, places = num / 2;
+  const int lg = __popc(p.words - 1), words = ctas << lg, first = rank << lg;
   const bool in_place = p.table_out == p.table;
+  int* s_mark = reinterpret_cast<int*>(s_state + words);       // [words], where there are several CTAs
   auto is_page = [&](int id) { return id >= 0 && id < num; };
+  auto state = [&](int w) {
+    if constexpr (kLocal) return s_state + w;
+    else return p.state + w;
+  };
+  auto read_state = [&](int w) {
+    if constexpr (kLocal) return s_state[w];
+    else return __ldcg(p.state + w);
+  };
 
-  for (int i = me; i < words; i += step) p.bits[i] = 0;
-  if (tid == 0) s_width = s_low = 0;
+  if constexpr (kLocal) {
+    for (int i = tid; i < words; i += kTableThreads) {
+      s_state[i].x = 0;
+      if (ctas > 1) s_mark[i] = 0;
+    }
+  } else {
+    for (int i = me; i < words; i += step) p.state[i].x = 0;
+  }
+  if (tid == 0) s_width = 0;
   bool bad = false;
   int width = 0;
   for (int b = tid; b < p.batch; b += kTableThreads) {
@@ -286,106 +364,120 @@ __global__ void __launch_bounds__(kTableThreads) page_compact_kernel(const __gri
     if (me == 0) *p.count = 0, raise_flag(p.flags, RKV_FLAG_BAD_INDEX);
     return;
   }
-  atomicMax(&s_width, width);
-  cluster_sync();
-  const Tasks tasks(p.batch, in_place ? s_width : M);
+  width = __reduce_max_sync(0xffffffffu, width);
+  if (lane == 0) atomicMax(&s_width, width);
+  if constexpr (kLocal) __syncthreads();
+  else cluster_sync(ctas);
+  const Tasks tasks(p.batch, in_place ? s_width : M, rank, ctas);
 
+  int held[kCompactHold * kLaneEntries];
+  tasks.each<kCompactHold>([&](int i, int b, int j) {
+    if (i >= 0) held[i] = j < s_have[b] ? p.table[(int64_t)b * M + j] : -1;
+  });
   bool stray = false;
-  for (int t = tasks.first; t < tasks.last; ++t) {
-    const int b = t / tasks.per_row, j0 = (t - b * tasks.per_row) * kTaskEntries;
-#pragma unroll
-    for (int k = 0; k < kTaskEntries / 32; ++k) {
-      const int j = j0 + k * 32 + lane;
-      if (j < s_have[b]) {
-        const int id = p.table[(int64_t)b * M + j];
-        if (is_page(id)) atomicOr(p.bits + (id >> 5), 1u << (id & 31));
-        else stray = true;
-      }
-    }
-  }
+  tasks.each<kCompactHold>([&](int i, int b, int j) {
+    if (j >= s_have[b]) return;
+    const int id = i >= 0 ? held[i] : p.table[(int64_t)b * M + j];
+    if (!is_page(id)) stray = true;
+    else if (kLocal && ctas > 1) atomicOr(s_mark + (id >> 5), 1 << (id & 31));
+    else atomicOr(&state(id >> 5)->x, 1 << (id & 31));
+  });
   if (stray) raise_flag(p.flags, RKV_FLAG_BAD_INDEX);
-  cluster_sync();
+  cluster_sync(ctas);
 
-  // this CTA's words, neighbouring ones to a thread
-  const int w0 = (int)((int64_t)words * rank / ctas), w1 = (int)((int64_t)words * (rank + 1) / ctas);
-  const int each = (w1 - w0 + kTableThreads - 1) / kTableThreads;
-  const int from = min(w1, w0 + tid * each), to = min(w1, from + each);
-  int mine = 0;
-  for (int w = from; w < to; ++w) mine += __popc(__ldcg(p.bits + w));
-  int64_t none = 0, total_none;
-  int sum = mine, total;
-  block_scan<kTableThreads>(none, sum, total_none, total);
-  if (tid == 0) p.totals[rank] = total;
-  cluster_sync();
-  int n_live = 0, base = 0, low = 0;
-  uint32_t owner = 0;                // of the word of page n_live
-  for (uint32_t c = 0; c < ctas; ++c) {
-    if (c == rank) base = n_live;
-    n_live += __ldcg(p.totals + c);
-  }
-  // held pages below n_live: those of the CTAs before that word's, and of its own words
-  for (uint32_t c = 0, sofar = 0; c < ctas; ++c) {
-    if ((int)((int64_t)words * c / ctas) <= n_live >> 5) owner = c, low = sofar;
-    sofar += __ldcg(p.totals + c);
-  }
-  int part = 0;
-  for (int w = (int)((int64_t)words * owner / ctas) + tid; w <= n_live >> 5 && w < words; w += kTableThreads) {
-    const uint32_t x = __ldcg(p.bits + w);
-    part += __popc(w == n_live >> 5 ? x & ((1u << (n_live & 31)) - 1) : x);
-  }
-  part = __reduce_add_sync(0xffffffffu, part);
-  if (lane == 0 && part) atomicAdd(&s_low, part);
-  __syncthreads();
-  low += s_low;
-  const int moves = n_live - low;
-  int at = base + sum - mine;
-  for (int w = from; w < to; ++w) {
-    const uint32_t x = __ldcg(p.bits + w);
-    p.before[w] = at;
-    int live = at;
-    for (int i = 0; i < 32 && w * 32 + i < num; ++i) {
-      const int id = w * 32 + i;
-      if (x >> i & 1) {
-        if (id >= n_live) p.src[live - low] = id;
-        ++live;
-      } else if (id < n_live) {
-        p.dst[id - live] = id;
-      }
-    }
-    at += __popc(x);
-  }
-  cluster_sync();
-
-  for (int t = tasks.first; t < tasks.last; ++t) {
-    const int b = t / tasks.per_row, j0 = (t - b * tasks.per_row) * kTaskEntries;
+  // held pages before each of this CTA's words
+  int total = 0;
+  for (int w0 = 0; w0 < p.words; w0 += kTableThreads) {
+    const int w = w0 + tid;
+    int x = 0;
+    if (w < p.words) {
+      x = read_state(first + w).x;
+      if (kLocal && ctas > 1) {
+        int part[kMaxCluster];
 #pragma unroll
-    for (int k = 0; k < kTaskEntries / 32; ++k) {
-      const int j = j0 + k * 32 + lane;
-      const int64_t e = (int64_t)b * M + j;
-      if (j < s_have[b]) {
-        const int id = p.table[e];
-        if (is_page(id) && id >= n_live) {
-          const int r = __ldcg(p.before + (id >> 5)) + __popc(__ldcg(p.bits + (id >> 5)) & ((1u << (id & 31)) - 1));
-          p.table_out[e] = __ldcg(p.dst + (r - low));
-        } else if (!in_place) {
-          p.table_out[e] = id;
-        }
-      } else if (!in_place && j < M) {
-        p.table_out[e] = -1;
+        for (uint32_t c = 0; c < kMaxCluster; ++c) part[c] = c < ctas ? *in_cta(s_mark + first + w, c) : 0;
+#pragma unroll
+        for (uint32_t c = 0; c < kMaxCluster; ++c) x |= part[c];
+      }
+    }
+    int64_t none = 0, total_none;
+    int sum = __popc(x), these;
+    const int n = sum;
+    block_scan<kTableThreads>(none, sum, total_none, these);
+    if (w < p.words) *state(first + w) = make_int2(x, total + sum - n);
+    total += these;
+  }
+  if (tid < ctas) *in_cta(&s_total[rank], tid) = total;
+  cluster_sync(ctas);
+  if (tid <= ctas) {
+    int n = 0;
+    for (uint32_t c = 0; c < tid; ++c) n += s_total[c];
+    s_base[tid] = n;
+  }
+  if (kLocal && ctas > 1) {
+    constexpr int kAhead = 4;
+    const int used = (num >> 5) + 1;
+    for (int w0 = tid; w0 < used; w0 += kAhead * kTableThreads) {
+      int2 v[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int w = w0 + k * kTableThreads;
+        if (w < used && w < words) v[k] = *in_cta(s_state + w, w >> lg);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int w = w0 + k * kTableThreads;
+        if (w < used && w < words && w >> lg != rank) s_state[w] = v[k];
       }
     }
   }
+  __syncthreads();
+  const int n_live = s_base[ctas];
+  auto below = [&](int id) {         // held pages before page id
+    const int2 s = read_state(id >> 5);
+    return s_base[id >> 5 >> lg] + s.y + __popc(s.x & ((1u << (id & 31)) - 1));
+  };
+  // those below n_live stay; each of the others goes to the next hole
+  const int stay = n_live < num ? below(n_live) : n_live, moves = n_live - stay;
+  for (int w = wid; w < p.words; w += kTableWarps) {
+    const int word = first + w;
+    if ((int64_t)word * 32 >= num) break;
+    const int2 s = read_state(word);
+    const int id = word * 32 + lane, live = s_base[rank] + s.y + __popc(s.x & ((1u << lane) - 1));
+    if (s.x >> lane & 1) {
+      if (id >= n_live) p.src[live - stay] = id;
+    } else if (id < n_live) {
+      p.dst[id - live] = id;
+    }
+  }
+  cluster_sync(ctas);                // (none reads another's shared memory from here on)
+
+  tasks.each<kCompactHold>([&](int i, int b, int j) {
+    const int64_t e = (int64_t)b * M + j;
+    if (j < s_have[b]) {
+      const int id = i >= 0 ? held[i] : p.table[e];
+      if (is_page(id) && id >= n_live) p.table_out[e] = __ldcg(p.dst + (below(id) - stay));
+      else if (!in_place) p.table_out[e] = id;
+    } else if (!in_place && j < M) {
+      p.table_out[e] = -1;
+    }
+  });
   for (int i = me; i < num - n_live; i += step) p.free_blocks[i] = num - 1 - i;
   for (int i = moves + me; i < places; i += step) p.src[i] = p.dst[i] = -1;
   if (me == 0) *p.n_free = num - n_live, *p.count = moves;
 }
 
-// Launches a table kernel as one cluster of as many CTAs as its entries fill.
-template <typename Args>
-cudaError_t launch_table(void (*kernel)(Args), const Args& a, int batch, int max_blocks, size_t smem, cudaStream_t s) {
-  const int64_t warps = (int64_t)batch * ceil_div(max_blocks, kTaskEntries);
+// CTAs for a table: as many as leave a warp up to kWarpTasks tasks.
+constexpr int kWarpTasks = 2;
+unsigned table_ctas(int batch, int max_blocks) {
+  const int64_t tasks = (int64_t)batch * ceil_div(max_blocks, kTaskEntries);
   unsigned ctas = 1;
-  while (ctas < kMaxCluster && (int64_t)ctas * kTableWarps < warps) ctas *= 2;
+  while (ctas < kMaxCluster && (int64_t)ctas * kTableWarps * kWarpTasks < tasks) ctas *= 2;
+  return ctas;
+}
+
+template <typename Args>
+cudaError_t launch_table(void (*kernel)(Args), const Args& a, unsigned ctas, size_t smem, cudaStream_t s) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim = {ctas, 1, 1};
@@ -579,10 +671,18 @@ rkv_status check_fork_table(const rkv_page_table* table, int32_t num_blocks, int
 
 size_t round16(size_t n) { return (n + 15) & ~(size_t)15; }
 
+// Workspaces: the pages' state, for tables of more pages than shared memory takes, and a fork's
+// new rows.
 size_t fork_bytes(const rkv_page_table* t, int num_blocks) {
-  return 4 * (2 * round16(num_blocks) + kMaxCluster * kTableWarps + (size_t)t->batch * t->max_blocks);
+  return round16(sizeof(int2) * (size_t)num_blocks) + sizeof(int32_t) * (size_t)t->batch * t->max_blocks;
 }
-size_t compact_bytes(int num_blocks) { return 4 * (2 * round16(((size_t)num_blocks + 31) / 32) + kMaxCluster); }
+// Words of a CTA: a power of two that `ctas` times covers the pages.
+int compact_words(int num_blocks, unsigned ctas) {
+  int w = 1;
+  while ((int64_t)w * ctas * 32 < num_blocks) w *= 2;
+  return w;
+}
+size_t compact_bytes(int num_blocks) { return sizeof(int2) * kMaxCluster * (size_t)compact_words(num_blocks, kMaxCluster); }
 
 rkv_status check_workspace(const void* workspace, size_t bytes, size_t need) {
   if (!workspace || bytes < need)
@@ -620,19 +720,20 @@ extern "C" rkv_status rkv_page_fork(const rkv_page_table* table, const int32_t* 
   a.table_out = block_table_out, a.seq_len_out = seq_len_out;
   a.free_blocks = free_blocks, a.n_free = n_free, a.n_free_out = n_free_out;
   a.copy_src = copy_src, a.copy_dst = copy_dst, a.copy_rows = copy_rows;
-  a.held = static_cast<int32_t*>(workspace);
-  a.first = a.held + round16(num_blocks);
-  a.counts = a.first + round16(num_blocks);
-  a.stage = a.counts + kMaxCluster * kTableWarps;
+  a.state = static_cast<int2*>(workspace);
+  a.stage = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + round16(sizeof(int2) * (size_t)num_blocks));
   a.flags = flags;
   a.batch = table->batch, a.max_blocks = table->max_blocks, a.num_blocks = num_blocks;
   a.shift = log2_block(block_tokens);
-  static SmemOptIn opt_in;
+  const unsigned ctas = table_ctas(a.batch, a.max_blocks);
+  const size_t fixed = sizeof(int) * 5 * (size_t)a.batch + 8, state = sizeof(int2) * (size_t)num_blocks;
+  const bool local = ctas == 1 && fixed + state <= kTableSmem;
+  void (*kernel)(ForkArgs) = local ? page_fork_kernel<true> : page_fork_kernel<false>;
+  static SmemOptIn opt_in[2];
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || opt_in(page_fork_kernel, sizeof(int) * 5 * (size_t)kMaxBatch, dev) != cudaSuccess)
+  if (cudaGetDevice(&dev) != cudaSuccess || opt_in[local](kernel, kTableSmem, dev, true) != cudaSuccess)
     return fail_with(RKV_ECUDA, "no usable current device");
-  const cudaError_t e = launch_table(page_fork_kernel, a, a.batch, a.max_blocks, sizeof(int) * 5 * (size_t)a.batch,
-                                     static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_table(kernel, a, ctas, fixed + (local ? state : 0), static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? RKV_OK : fail_with(RKV_ECUDA, "page fork launch failed: %s", cudaGetErrorString(e));
 }
 
@@ -651,19 +752,25 @@ extern "C" rkv_status rkv_page_compact(const rkv_page_table* table, int32_t* fre
   if (!free_blocks || !n_free || !block_table_out || !count || (num_blocks > 1 && (!src || !dst)))
     return fail_with(RKV_EINVAL, "NULL pointer");
   if (rkv_status st = check_workspace(workspace, workspace_bytes, compact_bytes(num_blocks))) return st;
-  const size_t words = round16(((size_t)num_blocks + 31) / 32);
   CompactArgs a;
   a.table = table->block_table, a.seq_len = table->seq_len, a.table_out = block_table_out;
   a.free_blocks = free_blocks, a.n_free = n_free;
   a.src = src, a.dst = dst, a.count = count;
-  a.bits = static_cast<uint32_t*>(workspace);
-  a.before = static_cast<int32_t*>(workspace) + words;
-  a.totals = a.before + words;
+  a.state = static_cast<int2*>(workspace);
   a.flags = flags;
   a.batch = table->batch, a.max_blocks = table->max_blocks, a.num_blocks = num_blocks;
   a.shift = log2_block(block_tokens);
-  const cudaError_t e = launch_table(page_compact_kernel, a, a.batch, a.max_blocks, sizeof(int) * (size_t)a.batch,
-                                     static_cast<cudaStream_t>(stream));
+  const unsigned ctas = table_ctas(a.batch, a.max_blocks);
+  a.words = compact_words(num_blocks, ctas);
+  const size_t fixed = sizeof(int) * (size_t)a.batch + 8;
+  const size_t state = (sizeof(int2) + (ctas > 1 ? sizeof(int) : 0)) * (size_t)a.words * ctas;
+  const bool local = fixed + state <= kTableSmem;
+  void (*kernel)(CompactArgs) = local ? page_compact_kernel<true> : page_compact_kernel<false>;
+  static SmemOptIn opt_in[2];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || opt_in[local](kernel, kTableSmem, dev, true) != cudaSuccess)
+    return fail_with(RKV_ECUDA, "no usable current device");
+  const cudaError_t e = launch_table(kernel, a, ctas, fixed + (local ? state : 0), static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? RKV_OK : fail_with(RKV_ECUDA, "page compact launch failed: %s", cudaGetErrorString(e));
 }
 

@@ -72,16 +72,16 @@ inline bool current_device(int& dev, int& sms) {
 }
 
 // Opts a kernel into `smem` bytes of dynamic shared memory on the current device, once per
-// device (the attribute belongs to the device's copy of the function).  One instance per
-// kernel; concurrent first calls set the same value twice.
+// device (the attribute belongs to the device's copy of the function), and where asked into
+// clusters of 16 CTAs.  One instance per kernel; concurrent first calls set the same value twice.
 class SmemOptIn {
  public:
   template <typename F>
-  cudaError_t operator()(F* fn, size_t smem, int dev) {
+  cudaError_t operator()(F* fn, size_t smem, int dev, bool wide_clusters = false) {
     const uint64_t bit = 1ull << (dev & 63);
     if (dev < 64 && (done_.load(std::memory_order_acquire) & bit)) return cudaSuccess;
-    const cudaError_t e =
-        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess && wide_clusters) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess && dev < 64) done_.fetch_or(bit, std::memory_order_release);
     return e;
   }
