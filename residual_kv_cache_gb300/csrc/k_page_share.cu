@@ -549,7 +549,8 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const __grid_co
 // ------------------------------------------------------------------------------ gather
 constexpr int kGatherThreads = 256;
 constexpr int kGatherRows = 16;      // positions of a chunk: never in two pages
-constexpr int kGatherCtas = 4;       // CTAs an SM
+constexpr int kGatherCtas = 3;       // CTAs an SM
+constexpr int kGatherHeads = 4;      // heads that a warp takes at most
 
 struct GatherArgs {
   const uint8_t* codes[2];
@@ -564,9 +565,42 @@ struct GatherArgs {
   int batch, max_blocks, num_blocks, N, shift, max_rows, shares;
 };
 
-// A warp takes a share of the heads of one chunk.
-template <int D>
-__global__ void __launch_bounds__(kGatherThreads) page_gather_kernel(const __grid_constant__ GatherArgs p) {
+// Sixteen codes, used once.
+__device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
+  uint4 u;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+               : "l"(p));
+  return u;
+}
+
+// Sixteen codes times a scale as bf16.
+__device__ __forceinline__ void decode16(const uint4& u, float scale, uint32_t* w) {
+  const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((uint16_t)(in[e / 2] >> (16 * (e & 1))), __NV_E4M3);
+    const float2 v = __half22float2(__half2(hr));
+    const __nv_bfloat162 t = __floats2bfloat162_rn(v.x * scale, v.y * scale);
+    w[e] = *reinterpret_cast<const uint32_t*>(&t);
+  }
+}
+// 32 bytes: one store where they are a sector.
+template <bool kWide>
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const uint32_t* w) {
+  if constexpr (kWide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// A warp takes a share of the heads of one chunk.  kWide: the rows of k and v start on 32 bytes.
+template <int D, bool kWide>
+__global__ void __launch_bounds__(kGatherThreads, kGatherCtas) page_gather_kernel(const __grid_constant__ GatherArgs p) {
   constexpr int kLanes = D / 16;                 // lanes of one row
   constexpr int kRows = 32 / kLanes;             // rows of one load
   constexpr int kLoads = kGatherRows / kRows;
@@ -627,32 +661,24 @@ __global__ void __launch_bounds__(kGatherThreads) page_gather_kernel(const __gri
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         const uint8_t* src = p.codes[kv] + ((head << p.shift) + (j0 & ((1 << p.shift) - 1))) * D + x;
-        s[kv] = there ? p.scale[kv][head] : 0.0f;
+        s[kv] = there ? __ldg(p.scale[kv] + head) : 0.0f;
 #pragma unroll
         for (int k = 0; k < kLoads; ++k) {
           const int r = k * kRows + r_in;
           u[kv][k] = make_uint4(0, 0, 0, 0);
-          if (there && r < left) u[kv][k] = *reinterpret_cast<const uint4*>(src + r * D);
+          if (there && r < left) u[kv][k] = load_codes(src + r * D);
         }
       }
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
+        __nv_bfloat16* dst = p.out[kv] + (int64_t)row0 * p.st[kv].row + (int64_t)h * p.st[kv].head + x;
 #pragma unroll
         for (int k = 0; k < kLoads; ++k) {
           const int r = k * kRows + r_in;
           if (r >= left) continue;
-          const uint32_t in[4] = {u[kv][k].x, u[kv][k].y, u[kv][k].z, u[kv][k].w};
           uint32_t w[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((uint16_t)(in[e / 2] >> (16 * (e & 1))), __NV_E4M3);
-            const float2 v = __half22float2(__half2(hr));
-            const __nv_bfloat162 t = __floats2bfloat162_rn(v.x * s[kv], v.y * s[kv]);
-            w[e] = *reinterpret_cast<const uint32_t*>(&t);
-          }
-          uint4* dst = reinterpret_cast<uint4*>(p.out[kv] + (int64_t)(row0 + r) * p.st[kv].row + (int64_t)h * p.st[kv].head + x);
-          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          decode16(u[kv][k], s[kv], w);
+          store16<kWide>(dst + r * p.st[kv].row, w);
         }
       }
     }
@@ -827,17 +853,22 @@ extern "C" rkv_status rkv_page_gather(const rkv_pages* pages, const rkv_page_tab
   a.cu = cu_rows, a.flags = flags;
   a.batch = table->batch, a.max_blocks = table->max_blocks, a.num_blocks = pages->num_blocks;
   a.N = pages->n_kv_heads, a.shift = log2_block(pages->block_tokens), a.max_rows = max_rows;
-  static SmemOptIn opt_in[2];
+  // 32-byte stores need rows that start on them
+  bool wide = is_aligned(k, 32) && is_aligned(v, 32);
+  for (int i = 0; i < 2; ++i) wide = wide && k_strides[i] % 16 == 0 && v_strides[i] % 16 == 0;
+  static SmemOptIn opt_in[2][2];
   int dev = 0, sms = 0;
-  const bool wide = pages->head_dim == 128;
-  void (*kernel)(GatherArgs) = wide ? page_gather_kernel<128> : page_gather_kernel<64>;
-  if (!current_device(dev, sms) || opt_in[wide](kernel, sizeof(int) * 2 * (size_t)kMaxBatch, dev) != cudaSuccess)
+  const bool d128 = pages->head_dim == 128;
+  void (*kernel)(GatherArgs) = d128 ? (wide ? page_gather_kernel<128, true> : page_gather_kernel<128, false>)
+                                    : (wide ? page_gather_kernel<64, true> : page_gather_kernel<64, false>);
+  if (!current_device(dev, sms) || opt_in[d128][wide](kernel, sizeof(int) * 2 * (size_t)kMaxBatch, dev) != cudaSuccess)
     return fail_with(RKV_ECUDA, "no usable current device");
-  // as many warps as the GPU holds; few rows are shared by warps, some heads each
+  // few heads a warp, so that a row's heads are written at about the same time; fewer where the
+  // GPU holds more warps than that makes
   const int64_t warps = (int64_t)sms * kGatherCtas * (kGatherThreads / 32);
   const int64_t chunks = (int64_t)max_rows / kGatherRows + a.batch;            // at most
-  const int64_t shares = warps / chunks;
-  a.shares = (int)(shares < 1 ? 1 : shares < a.N ? shares : a.N);
+  const int64_t shares = warps / chunks, least = ceil_div(a.N, kGatherHeads);
+  a.shares = (int)(shares < least ? least : shares < a.N ? shares : a.N);
   const int64_t ctas = (chunks * a.shares + kGatherThreads / 32 - 1) / (kGatherThreads / 32);
   const int64_t most = (int64_t)sms * kGatherCtas;
   kernel<<<(unsigned)(ctas < most ? ctas : most), kGatherThreads, sizeof(int) * 2 * (size_t)a.batch,

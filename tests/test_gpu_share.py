@@ -341,7 +341,7 @@ GATHERS = [([1], 1, 64, 16), ([0, 17, 0, 0, 64, 5, 0], 3, 64, 16), ([1000], 8, 1
 
 @cuda
 @pytest.mark.parametrize("case", range(len(GATHERS)))
-@pytest.mark.parametrize("given", ["made", "out", "strided", "length"])
+@pytest.mark.parametrize("given", ["made", "out", "strided", "odd", "length"])
 def test_gather_matches_the_definition(case, given):
     lens, N, D, P = GATHERS[case]
     table, free, _ = _table(lens, P, max(1, max(-(-n // P) for n in lens)) + 1, 3, case, 0.5)
@@ -356,6 +356,9 @@ def test_gather_matches_the_definition(case, given):
     if given == "strided":
         buf = torch.full((rows, 2 * N + 1, D), 7, dtype=torch.bfloat16, device="cuda")
         more = dict(k_out=buf[:, :N], v_out=buf[:, N:2 * N])
+    elif given == "odd":                                   # rows that start on 16 bytes, not on 32
+        buf = torch.full((rows, (2 * N + 1) * D + 8), 7, dtype=torch.bfloat16, device="cuda")
+        more = dict(k_out=buf[:, 8:8 + N * D].view(rows, N, D), v_out=buf[:, 8 + N * D:8 + 2 * N * D].view(rows, N, D))
     elif given != "made":
         more = dict(k_out=torch.full((N, rows, D), 7, dtype=torch.bfloat16, device="cuda").transpose(0, 1),
                     v_out=torch.full((rows, N, D), 7, dtype=torch.bfloat16, device="cuda"))
@@ -368,6 +371,8 @@ def test_gather_matches_the_definition(case, given):
         assert (x[total:] == 7).all() if more else True
     if given == "strided":
         assert (buf[:, 2 * N] == 7).all()
+    if given == "odd":
+        assert (buf[:, :8] == 7).all() and (buf[:, 8 + 2 * N * D:] == 7).all()
 
 
 @cuda
