@@ -493,6 +493,7 @@ cudaError_t launch_table(void (*kernel)(Args), const Args& a, unsigned ctas, siz
 
 // ------------------------------------------------------------------------- page copies
 constexpr int kCopyThreads = 256;
+constexpr int kCopyCtas = 24;        // CTAs an SM at most
 constexpr int kCopyLayers = 128;
 constexpr int kCopyLoads = 8;        // 16-byte loads of a lane in flight
 
@@ -550,6 +551,7 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const __grid_co
 constexpr int kGatherThreads = 256;
 constexpr int kGatherRows = 16;      // positions of a chunk: never in two pages
 constexpr int kGatherCtas = 3;       // CTAs an SM
+constexpr int kGatherWaves = 4;      // times that many in the grid
 constexpr int kGatherHeads = 4;      // heads that a warp takes at most
 
 struct GatherArgs {
@@ -824,7 +826,7 @@ extern "C" rkv_status rkv_page_copy(const rkv_pages* layers, int32_t n_layers, c
   int dev = 0, sms = 0;
   if (!current_device(dev, sms)) return fail_with(RKV_ECUDA, "no usable current device");
   const int64_t items = (int64_t)n * n_layers * 2 * a.N, ctas = (items + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
-  const int64_t most = 4 * (int64_t)sms;
+  const int64_t most = kCopyCtas * (int64_t)sms;
   page_copy_kernel<<<(unsigned)(ctas < most ? ctas : most), kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? RKV_OK : fail_with(RKV_ECUDA, "page copy launch failed: %s", cudaGetErrorString(e));
@@ -870,7 +872,7 @@ extern "C" rkv_status rkv_page_gather(const rkv_pages* pages, const rkv_page_tab
   const int64_t shares = warps / chunks, least = ceil_div(a.N, kGatherHeads);
   a.shares = (int)(shares < least ? least : shares < a.N ? shares : a.N);
   const int64_t ctas = (chunks * a.shares + kGatherThreads / 32 - 1) / (kGatherThreads / 32);
-  const int64_t most = (int64_t)sms * kGatherCtas;
+  const int64_t most = (int64_t)sms * kGatherCtas * kGatherWaves;
   kernel<<<(unsigned)(ctas < most ? ctas : most), kGatherThreads, sizeof(int) * 2 * (size_t)a.batch,
            static_cast<cudaStream_t>(stream)>>>(a);
   const cudaError_t e = cudaGetLastError();
