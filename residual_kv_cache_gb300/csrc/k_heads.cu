@@ -7,16 +7,25 @@
 // matters: freq_j / 2 pi is kept as a 64-bit binary fraction of a turn, an integer product with
 // the position drops the whole turns by overflow, and the upper 32 bits, taken as a signed
 // number, are the angle in (-pi, pi] to 2^-32 of a turn.
+//
+// Bandwidth bounds many rows, one chain of loads few (16 rows of 40 heads of 128 3.1 us).  A warp
+// takes a row: the sines are found once for its heads, a part of them in each lane.  The next
+// heads' values, or the next row's, are on their way while some are turned.  32768 rows of 32 + 8
+// heads of 128, normed and turned: 108 us, 6.2 TB/s (125 us with the sines found by every lane,
+// nothing loaded ahead and products one by one; 111 with the next row's values not loaded ahead).
+// Seven CTAs of 128 threads an SM: six are 112 us, eight spill (110); rows cut into two shares
+// 118, several waves of CTAs 112 to 120 (each sets the turns up again).
 #include <cuda_bf16.h>
 
 #include "pages.h"
+#include "ptx.cuh"
 
 namespace rkv {
 namespace {
 
-constexpr int kHeadThreads = 256;
+constexpr int kHeadThreads = 128;
 constexpr int kHeadWarps = kHeadThreads / 32;
-constexpr int kHeadCtas = 4;         // resident CTAs an SM that the registers allow
+constexpr int kHeadCtas = 7;         // resident CTAs an SM that the registers allow
 
 struct HeadRows {
   const void* x[2];                  // q, k
@@ -34,51 +43,88 @@ struct HeadArgs {
   float eps;                         // below 0: no norm
 };
 
+__device__ __forceinline__ uint64_t f32x2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+__device__ __forceinline__ uint4 load16(const void* p) { return *static_cast<const uint4*>(p); }
+
+// Eight consecutive values, as loaded; widen() gives four pairs of floats.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* f);
+struct Chunk;
 template <>
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* f) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Chunk<__nv_bfloat16> {
+  uint4 u = make_uint4(0, 0, 0, 0);
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = load16(p); }
+  __device__ __forceinline__ void widen(uint64_t* f) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    for (int i = 0; i < 4; ++i) f[i] = f32x2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
   }
-}
+};
 template <>
-__device__ __forceinline__ void load8(const float* p, float* f) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* f) {
+struct Chunk<float> {
+  uint4 u[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  __device__ __forceinline__ void load(const float* p) { u[0] = load16(p), u[1] = load16(p + 4); }
+  __device__ __forceinline__ void widen(uint64_t* f) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f[2 * i] = f32x2_pack(__uint_as_float(u[i].x), __uint_as_float(u[i].y));
+      f[2 * i + 1] = f32x2_pack(__uint_as_float(u[i].z), __uint_as_float(u[i].w));
+    }
+  }
+};
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const uint64_t* f) {
   uint4 u;
   uint32_t* w = &u.x;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 t = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    float lo, hi;
+    f32x2_unpack(f[i], lo, hi);
+    const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
     w[i] = *reinterpret_cast<const uint32_t*>(&t);
   }
   *reinterpret_cast<uint4*>(p) = u;
 }
-__device__ __forceinline__ void store8(float* p, const float* f) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+__device__ __forceinline__ void store8(float* p, const uint64_t* f) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f32x2_unpack(f[i], v[2 * i], v[2 * i + 1]);
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// Sum over the lanes of a head of the squares of 16 values.
+template <int kLanes>
+__device__ __forceinline__ float sum_squares(const uint64_t* x) {
+  uint64_t sum = f32x2_mul(x[0], x[0]);
+#pragma unroll
+  for (int e = 1; e < 8; ++e) sum = f32x2_fma(x[e], x[e], sum);
+  float lo, hi;
+  f32x2_unpack(sum, lo, hi);
+  lo += hi;
+#pragma unroll
+  for (int o = 1; o < kLanes; o <<= 1) lo += __shfl_xor_sync(0xffffffffu, lo, o);
+  return lo;
 }
 
 // D / 16 lanes share a head's row: each has two chunks of eight values, a pair's two values
-// both.  A warp takes a share of one row's heads.
+// both.  A warp takes a share of one row's heads, kPar at a time; the lanes that have a chunk of
+// different heads turn the same pairs, and each finds the sines of some of them for all.
 template <typename In, typename Out, int D>
-__global__ void __launch_bounds__(kHeadThreads) head_norm_rotate_kernel(const __grid_constant__ HeadArgs p) {
+__global__ void __launch_bounds__(kHeadThreads, kHeadCtas) head_norm_rotate_kernel(const __grid_constant__ HeadArgs p) {
   constexpr int kLanes = D / 16;
   constexpr int kPar = 32 / kLanes;  // heads that a warp takes at a time
+  constexpr int kMine = 8 / kPar;    // pairs of which a lane finds the sines
   __shared__ uint64_t s_turn[D / 2];
-  __shared__ float s_weight[2][D];
-  const int tid = threadIdx.x, lane = tid & 31, l = lane % kLanes;
-  if (tid < p.rotary / 2) {
-    double t = p.freq[tid] * 0.15915494309189533576888;          // 1 / (2 pi)
+  __shared__ __align__(16) float s_weight[2][D];
+  const int tid = threadIdx.x, lane = tid & 31, l = lane % kLanes, sub = lane / kLanes;
+  for (int i = tid; i < D / 2; i += kHeadThreads) {
+    double t = i < p.rotary / 2 ? p.freq[i] * 0.15915494309189533576888 : 0.0;      // 1 / (2 pi)
     t -= rint(t);
-    s_turn[tid] = (uint64_t)__double2ll_rn(t * 18446744073709551616.0);
+    s_turn[i] = (uint64_t)__double2ll_rn(t * 18446744073709551616.0);
   }
   for (int i = tid; i < 2 * D; i += kHeadThreads) {
     const In* w = static_cast<const In*>(p.h.weight[i / D]);
@@ -88,81 +134,123 @@ __global__ void __launch_bounds__(kHeadThreads) head_norm_rotate_kernel(const __
   const int half = p.rotary / 2;
   // the lane's chunks, and whether they turn (rotary is a multiple of 16)
   const bool turns = l * 16 < p.rotary;
-  int at[2];
-  if (p.adjacent || !turns) at[0] = l * 16, at[1] = at[0] + 8;
-  else at[0] = l * 8, at[1] = half + l * 8;
+  int at0 = l * 16, at1 = at0 + 8;
+  if (!p.adjacent && turns) at0 = l * 8, at1 = half + l * 8;
   const int parts_q = ceil_div(p.h.heads[0], kPar), parts = parts_q + ceil_div(p.h.heads[1], kPar);
   const int64_t tasks = (int64_t)p.n_rows * p.shares;
   const bool norm = p.eps >= 0.0f;
-  for (int64_t task = (int64_t)blockIdx.x * kHeadWarps + tid / 32; task < tasks; task += (int64_t)gridDim.x * kHeadWarps) {
-    const int row = (int)(task / p.shares), share = (int)(task - (int64_t)row * p.shares);
-    const int pos = p.positions[row];
-    if (pos < 0) continue;
-    float c[8], s[8];
-    if (turns) {
+  const int64_t stride = (int64_t)gridDim.x * kHeadWarps;
+  int64_t task = (int64_t)blockIdx.x * kHeadWarps + tid / 32;
+  if (task >= tasks) return;
+  Chunk<In> next[2];
+  auto fetch = [&](int row, int g) {
+    const int which = g >= parts_q, head = (which ? g - parts_q : g) * kPar + sub;
+    if (head < p.h.heads[which]) {
+      const In* src = static_cast<const In*>(p.h.x[which]) + row * p.h.st[which].row + head * p.h.st[which].head;
+      next[0].load(src + at0);
+      next[1].load(src + at1);
+    }
+  };
+  // a task's row and share of the parts; rows fit 32 bits
+  int row, lo, hi;
+  auto place = [&](int64_t t) {
+    row = (int)(t / p.shares);
+    const int share = (int)(t - (int64_t)row * p.shares);
+    lo = (int)((int64_t)parts * share / p.shares), hi = (int)((int64_t)parts * (share + 1) / p.shares);
+  };
+  place(task);
+  int pos = p.positions[row];
+  fetch(row, lo);
+  while (true) {
+    // the next task's first values are on their way before this one's last are done
+    const int row_now = row, lo_now = lo, hi_now = hi, pos_now = pos;
+    task += stride;
+    const bool more = task < tasks;
+    if (more) {
+      place(task);
+      pos = p.positions[row];
+    }
+    if (pos_now < 0) {
+      if (!more) break;
+      fetch(row, lo);
+      continue;
+    }
+    // cosines and sines of the lane's pairs, two by two
+    uint64_t c[4], s[4];
+    {
+      float cm[kMine], sm[kMine], cv[8], sv[8];
+#pragma unroll
+      for (int e = 0; e < kMine; ++e) {
+        const int32_t t = (int32_t)((s_turn[l * 8 + sub * kMine + e] * (uint64_t)pos_now) >> 32);
+        sincospif((float)t * 4.656612873077393e-10f, &sm[e], &cm[e]);            // 2^-31
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int32_t t = (int32_t)((s_turn[l * 8 + e] * (uint64_t)pos) >> 32);
-        sincospif((float)t * 4.656612873077393e-10f, &s[e], &c[e]);              // 2^-31
+        cv[e] = __shfl_sync(0xffffffffu, cm[e % kMine], e / kMine * kLanes + l);
+        sv[e] = __shfl_sync(0xffffffffu, sm[e % kMine], e / kMine * kLanes + l);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c[i] = f32x2_pack(cv[2 * i], cv[2 * i + 1]);
+        s[i] = f32x2_pack(sv[2 * i], sv[2 * i + 1]);
       }
     }
-    const int lo = (int)((int64_t)parts * share / p.shares), hi = (int)((int64_t)parts * (share + 1) / p.shares);
-    for (int g = lo; g < hi; ++g) {
-      const int which = g >= parts_q;
-      const int head = (which ? g - parts_q : g) * kPar + lane / kLanes;
-      const bool live = head < p.h.heads[which];
-      float x[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = 0.0f;
-      if (live) {
-        const In* src = static_cast<const In*>(p.h.x[which]) + row * p.h.st[which].row + head * p.h.st[which].head;
-        load8(src + at[0], x);
-        load8(src + at[1], x + 8);
-      }
+    for (int g = lo_now; g < hi_now; ++g) {
+      const int which = g >= parts_q, head = (which ? g - parts_q : g) * kPar + sub;
+      uint64_t x[8];
+      next[0].widen(x);
+      next[1].widen(x + 4);
+      if (g + 1 < hi_now) fetch(row_now, g + 1);
+      else if (more) fetch(row, lo);
       if (norm) {
-        float sum = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) sum = fmaf(x[e], x[e], sum);
-#pragma unroll
-        for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float sum = sum_squares<kLanes>(x);
         float r = rsqrtf(fmaf(sum, 1.0f / D, p.eps));
         if (__any_sync(0xffffffffu, !(sum < INFINITY))) {
           // squares past fp32: those of x 2^-70 are not, and eps is nothing beside them
           const float down = sum < INFINITY ? 1.0f : 8.470329472543003e-22f;
-          float small = 0.0f;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] *= down, small = fmaf(x[e], x[e], small);
-#pragma unroll
-          for (int o = 1; o < kLanes; o <<= 1) small += __shfl_xor_sync(0xffffffffu, small, o);
+          for (int e = 0; e < 8; ++e) x[e] = f32x2_mul(x[e], f32x2_pack(down, down));
+          const float small = sum_squares<kLanes>(x);
           if (!(sum < INFINITY)) r = rsqrtf(small * (1.0f / D));
         }
         const float* w = s_weight[which];
+        const uint64_t r2 = f32x2_pack(r, r);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = x[e] * r * w[at[e / 8] + e % 8];
+        for (int h = 0; h < 2; ++h) {
+          const float4* wf = reinterpret_cast<const float4*>(w + (h ? at1 : at0));
+          const float4 wa = wf[0], wb = wf[1];
+          const uint64_t w2[4] = {f32x2_pack(wa.x, wa.y), f32x2_pack(wa.z, wa.w), f32x2_pack(wb.x, wb.y), f32x2_pack(wb.z, wb.w)};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[4 * h + e] = f32x2_mul(f32x2_mul(x[4 * h + e], r2), w2[e]);
+        }
       }
       if (turns) {
         if (p.adjacent) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float a = x[2 * e], b = x[2 * e + 1];
-            x[2 * e] = a * c[e] - b * s[e];
-            x[2 * e + 1] = b * c[e] + a * s[e];
+            float a, b, c0, c1, s0, s1;
+            f32x2_unpack(x[e], a, b);
+            f32x2_unpack(c[e / 2], c0, c1);
+            f32x2_unpack(s[e / 2], s0, s1);
+            const float ce = e % 2 ? c1 : c0, se = e % 2 ? s1 : s0;
+            x[e] = f32x2_pack(a * ce - b * se, b * ce + a * se);
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float a = x[e], b = x[8 + e];
-            x[e] = a * c[e] - b * s[e];
-            x[8 + e] = b * c[e] + a * s[e];
+          for (int e = 0; e < 4; ++e) {
+            const uint64_t a = x[e], b = x[4 + e];
+            x[e] = f32x2_sub(f32x2_mul(a, c[e]), f32x2_mul(b, s[e]));
+            x[4 + e] = f32x2_fma(b, c[e], f32x2_mul(a, s[e]));
           }
         }
       }
-      if (live) {
-        Out* dst = static_cast<Out*>(p.h.out[which]) + row * p.h.ost[which].row + head * p.h.ost[which].head;
-        store8(dst + at[0], x);
-        store8(dst + at[1], x + 8);
+      if (head < p.h.heads[which]) {
+        Out* dst = static_cast<Out*>(p.h.out[which]) + row_now * p.h.ost[which].row + head * p.h.ost[which].head;
+        store8(dst + at0, x);
+        store8(dst + at1, x + 4);
       }
     }
+    if (!more) break;
   }
 }
 
