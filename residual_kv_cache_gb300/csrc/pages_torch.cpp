@@ -460,7 +460,19 @@ PyObject* page_compact(PyObject* const* a) {
   return three(buf, n, 1);
 }
 
-// (layers: a list or tuple of (k8, v8, k_scale, v_scale), src, dst, rows, count, flags, stream)
+// Address of a tensor as array() takes it; of the many tensors of a call that mostly are as asked.
+inline void* one_of(PyObject* o, const char* what, at::IntArrayRef shape, int dev, at::ScalarType type) {
+  if (THPVariable_Check(o)) {
+    const c10::TensorImpl* t = THPVariable_Unpack(o).unsafeGetTensorImpl();
+    if (t->dtype() == c10::scalarTypeToTypeMeta(type) && t->sizes() == shape && t->is_cuda() &&
+        t->device().index() == dev && t->is_contiguous())
+      return THPVariable_Unpack(o).data_ptr();
+  }
+  return array(o, what, shape, dev, type);
+}
+
+// (caches: a list or tuple of (k8, v8, k_scale, v_scale) or of objects whose arrays() are that, src,
+//  dst, rows, count, flags, stream)
 PyObject* page_copy(PyObject* const* a) {
   if (!PyList_Check(a[0]) && !PyTuple_Check(a[0])) throw Refused("caches must be a list or tuple");
   const Py_ssize_t layers = PySequence_Fast_GET_SIZE(a[0]);
@@ -469,11 +481,31 @@ PyObject* page_copy(PyObject* const* a) {
   int dev = 0;
   for (Py_ssize_t i = 0; i < layers; ++i) {
     PyObject* l = PySequence_Fast_GET_ITEM(a[0], i);
+    // a tuple that arrays() makes; its tensors are the object's, which outlives the call
+    PyObject* made = PyTuple_Check(l) ? nullptr : PyObject_CallMethod(l, "arrays", nullptr);
+    if (made) {
+      l = made;
+    } else if (PyErr_Occurred()) {
+      if (!PyErr_ExceptionMatches(PyExc_AttributeError)) throw PythonError();
+      PyErr_Clear();
+    }
+    struct Drop {
+      PyObject* o;
+      ~Drop() { Py_XDECREF(o); }
+    } drop{made};
     if (!PyTuple_Check(l) || PyTuple_GET_SIZE(l) != 4) throw Refused("a cache must be (k8, v8, k_scale, v_scale)");
-    int at = 0;
-    pg[i] = pages_of(PyTuple_GET_ITEM(l, 0), PyTuple_GET_ITEM(l, 1), PyTuple_GET_ITEM(l, 2), PyTuple_GET_ITEM(l, 3), at);
-    if (i == 0) dev = at;
-    if (at != dev) throw Refused("caches are on several devices");
+    PyObject* const* t = &PyTuple_GET_ITEM(l, 0);
+    if (i == 0) {
+      pg[0] = pages_of(t[0], t[1], t[2], t[3], dev);
+      continue;
+    }
+    const int64_t nb = pg[0].num_blocks, N = pg[0].n_kv_heads;
+    const int64_t shape[4] = {nb, N, pg[0].block_tokens, pg[0].head_dim};
+    pg[i] = pg[0];
+    pg[i].k = one_of(t[0], "k8", shape, dev, at::kByte);
+    pg[i].v = one_of(t[1], "v8", shape, dev, at::kByte);
+    pg[i].k_scale = static_cast<float*>(one_of(t[2], "k_scale", {shape, 2}, dev, at::kFloat));
+    pg[i].v_scale = static_cast<float*>(one_of(t[3], "v_scale", {shape, 2}, dev, at::kFloat));
   }
   const int64_t n = length_of(a[1], "src");
   const int32_t* src = static_cast<int32_t*>(array(a[1], "src", {n}, dev));

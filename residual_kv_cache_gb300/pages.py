@@ -169,10 +169,9 @@ def page_compact(seq_len, block_table, free_blocks, n_free, block_tokens: int, b
 
 
 def page_copy(caches, src, dst, rows=None, count=None, flags=None, stream=None):
-    """Make the copies of a PageCopies in `caches`, up to 128 layers of one shape: PagedCache
-    objects or (k8, v8, k_scale, v_scale) tuples."""
-    _ext().page_copy([c.arrays() if isinstance(c, PagedCache) else c for c in caches], src, dst, rows, count,
-                     flags, stream)
+    """Make the copies of a PageCopies in `caches`, a list of up to 128 layers of one shape:
+    PagedCache objects or (k8, v8, k_scale, v_scale) tuples."""
+    _ext().page_copy(caches, src, dst, rows, count, flags, stream)
 
 
 def page_gather(k8, v8, k_scale, v_scale, block_table, seq_len, max_rows=None, length=None, k_out=None, v_out=None,
