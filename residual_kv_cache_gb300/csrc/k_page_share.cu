@@ -142,16 +142,22 @@ __global__ void __launch_bounds__(kTableThreads) page_fork_kernel(const __grid_c
   };
 
   const int n_free = *p.n_free;
-  for (int b = tid; b < p.batch; b += kTableThreads) s_have[b] = p.seq_len[b];
+  // as given, at first: positions before the call in s_have, those asked for in s_new
+  for (int b = tid; b < p.batch; b += kTableThreads) {
+    s_have[b] = p.seq_len[b];
+    const int s = p.source ? p.source[b] : b, n = p.length ? p.length[b] : -1;
+    const bool ends = p.finished && p.finished[b] != 0;
+    s_src[b] = ends ? -1 : s;
+    s_new[b] = n;
+  }
   if (tid == 0) s_width = 0;
   for (int i = kLocal ? tid : me; i < num; i += step) *state(i) = make_int2(kNone, kNone);
-  __syncthreads();                   // s_have: positions before the call, at first
+  __syncthreads();
   bool bad = n_free < 0 || n_free > num;
   int width = 0;
   for (int b = tid; b < p.batch; b += kTableThreads) {
-    int s = p.source ? p.source[b] : b, n = 0;
-    const int want = p.length ? p.length[b] : -1, len = s_have[b];
-    if (p.finished && p.finished[b] != 0) s = -1;
+    int s = s_src[b], n = 0;
+    const int want = s_new[b], len = s_have[b];
     if (len < 0 || len > cap) bad = true;
     if (s >= p.batch) bad = true, s = -1;
     if (s >= 0) {
@@ -161,6 +167,7 @@ __global__ void __launch_bounds__(kTableThreads) page_fork_kernel(const __grid_c
     }
     s_src[b] = max(s, -1);
     s_new[b] = n;
+    if (kLocal) s_from[b] = -1;
     width = max(width, max(pages(len), pages(n)));
   }
   bad = __syncthreads_or(bad);
@@ -184,7 +191,7 @@ __global__ void __launch_bounds__(kTableThreads) page_fork_kernel(const __grid_c
   tasks.each<kForkHold>([&](int i, int b, int j) {
     if (i >= 0) load(b, j, to[i], gone[i]);
   });
-  for (int b = tid; b < p.batch; b += kTableThreads) {         // last pages that are begun
+  for (int b = tid; b < p.batch && !kLocal; b += kTableThreads) {        // last pages that are begun
     const int n = s_new[b];
     s_from[b] = n & P1 ? p.table[(int64_t)s_src[b] * M + pages(n) - 1] : -1;
   }
@@ -199,6 +206,7 @@ __global__ void __launch_bounds__(kTableThreads) page_fork_kernel(const __grid_c
       if (!is_page(t)) stray = true;
       else if (j == m - 1 && (n & P1)) atomicMin(&state(t)->x, b);
       else state(t)->x = -1;
+      if (kLocal && j == m - 1 && (n & P1)) s_from[b] = t;
       if (i < 0 && in_place && s != b) p.stage[(int64_t)b * M + j] = t;
     }
     if (j < s_have[b] && (s != b || j >= m)) {
