@@ -153,6 +153,14 @@ def test_fork_of_the_largest_batch_and_of_long_rows(inplace):
 
 
 @cuda
+def test_fork_in_a_pool_of_more_pages_than_shared_memory_takes():
+    lens, source, length, finished = _random_fork(20, 400, 16, 4)
+    table, free, nf = _table(lens, 16, 30, 60000, 5, 0.5)
+    for inplace in (False, True):
+        _check_fork(source, length, finished, lens, table, free, nf, 16, inplace)
+
+
+@cuda
 @pytest.mark.parametrize("why", ["source", "length", "above", "len", "table", "n_free", "space", "list"])
 @pytest.mark.parametrize("inplace", [False, True])
 def test_fork_that_does_not_fit_changes_nothing(why, inplace):
@@ -214,7 +222,8 @@ def test_release_of_a_sharing_table_is_the_plain_one_where_nothing_is_shared():
 
 # ----------------------------------------------------------------------------- compact
 COMPACTS = [([0], 16, 3), ([1], 16, 0), ([16 * 3], 16, 40), ([5, 0, 129, 64], 64, 7), (list(range(0, 900, 3)), 16, 500),
-            ([16 * 20000], 16, 20011), ([i % 50 for i in range(8192)], 16, 3000), ([100] * 33, 32, 100000)]
+            ([16 * 20000], 16, 20011), ([i % 50 for i in range(8192)], 16, 3000), ([100] * 33, 32, 100000),
+            ([100] * 300, 16, 700000), ([5, 300], 16, 1000000)]          # more pages than shared memory takes
 
 
 @cuda
