@@ -121,16 +121,6 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadCtas) head_norm_rotate_kern
   __shared__ uint64_t s_turn[D / 2];
   __shared__ __align__(16) float s_weight[2][D];
   const int tid = threadIdx.x, lane = tid & 31, l = lane % kLanes, sub = lane / kLanes;
-  for (int i = tid; i < D / 2; i += kHeadThreads) {
-    double t = i < p.rotary / 2 ? p.freq[i] * 0.15915494309189533576888 : 0.0;      // 1 / (2 pi)
-    t -= rint(t);
-    s_turn[i] = (uint64_t)__double2ll_rn(t * 18446744073709551616.0);
-  }
-  for (int i = tid; i < 2 * D; i += kHeadThreads) {
-    const In* w = static_cast<const In*>(p.h.weight[i / D]);
-    s_weight[i / D][i % D] = w ? (float)w[i % D] : 1.0f;
-  }
-  __syncthreads();
   const int half = p.rotary / 2;
   // the lane's chunks, and whether they turn (rotary is a multiple of 16)
   const bool turns = l * 16 < p.rotary;
@@ -141,7 +131,6 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadCtas) head_norm_rotate_kern
   const bool norm = p.eps >= 0.0f;
   const int64_t stride = (int64_t)gridDim.x * kHeadWarps;
   int64_t task = (int64_t)blockIdx.x * kHeadWarps + tid / 32;
-  if (task >= tasks) return;
   Chunk<In> next[2];
   auto fetch = [&](int row, int g) {
     const int which = g >= parts_q, head = (which ? g - parts_q : g) * kPar + sub;
@@ -158,9 +147,25 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadCtas) head_norm_rotate_kern
     const int share = (int)(t - (int64_t)row * p.shares);
     lo = (int)((int64_t)parts * share / p.shares), hi = (int)((int64_t)parts * (share + 1) / p.shares);
   };
-  place(task);
-  int pos = p.positions[row];
-  fetch(row, lo);
+  const bool any = task < tasks;
+  int pos = -1;
+  if (any) {
+    place(task);
+    pos = p.positions[row];
+    fetch(row, lo);
+  }
+  // while the first values are on their way: the turns, and the weights as floats
+  for (int i = tid; i < D / 2; i += kHeadThreads) {
+    double t = i < p.rotary / 2 ? p.freq[i] * 0.15915494309189533576888 : 0.0;      // 1 / (2 pi)
+    t -= rint(t);
+    s_turn[i] = (uint64_t)__double2ll_rn(t * 18446744073709551616.0);
+  }
+  for (int i = tid; i < 2 * D; i += kHeadThreads) {
+    const In* w = static_cast<const In*>(p.h.weight[i / D]);
+    s_weight[i / D][i % D] = w ? (float)w[i % D] : 1.0f;
+  }
+  __syncthreads();
+  if (!any) return;
   while (true) {
     // the next task's first values are on their way before this one's last are done
     const int row_now = row, lo_now = lo, hi_now = hi, pos_now = pos;
