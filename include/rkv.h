@@ -619,7 +619,8 @@ rkv_status rkv_head_norm_rotate(const rkv_head_rows* rows, void* stream);
  * All or nothing: where a source is past the table, a length is out of range or above its
  * source's (RKV_FLAG_BAD_INDEX), or the list would overflow or the copies' pages run out
  * (RKV_FLAG_NO_SPACE), everything stays (other outputs than in place receive it as it was) and
- * there are no copies.  Entries that are no page are kept as they are and never reach the list
+ * there are no copies.  Entries of the table that are no page are kept as they are and never reach
+ * the list, and one of the list that is taken for a copy is handed out as it is
  * (RKV_FLAG_BAD_INDEX).
  * batch * max_blocks below 2^31.
  * Errors (nothing launched): RKV_EINVAL, RKV_EALIGN, RKV_ECAPACITY (workspace), RKV_ECUDA.

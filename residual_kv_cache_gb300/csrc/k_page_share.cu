@@ -12,7 +12,24 @@ namespace {
 // A call is a few phases that wait for one another, each a load or two long, and latency bounds
 // it: one CTA does it, or a cluster of up to 16.  A warp takes a run of tasks (128 neighbouring
 // entries of a row of the table), the same ones in every phase, and holds the entries of the
-// first of them in registers from the first phase to the last.
+// first of them in registers from the first phase to the last.  More launches would cost the
+// host 2 us each, blocks of a whole grid a barrier of more than a microsecond.
+//
+// Fork.  With R the rows after the call, a page is held whole where some R has it as one of its
+// full pages, else begun by the rows that have it last.  One word a page says which (-1, or the
+// lowest row that has begun it), another the first entry of the old table that lets go of it;
+// both are minima, so the order of the threads does not matter.  A page goes where nobody holds
+// it, and its first entry gives it its place in the list.  16 beams of up to 16384 tokens (one
+// CTA, the words in its shared memory) 9.0 us, 256 slots of 4100 tokens on pages of 16 (16 CTAs,
+// the words in L2) 13.0.  Words in the cluster's shared memory instead: 20.8 on eight CTAs (an
+// SM passes on fewer atomics to another's memory than to L2).  Of the 13 some 2.5 are the launch, five
+// barriers and what they wait for 4, the rest nine dependent loads.
+//
+// Compact.  A bit a page says whether a row holds it.  Each CTA marks its own entries' pages in
+// a map of its own; the maps are joined a part a CTA, counted, and taken over by all, so that a
+// page's rank is one look-up.  16 requests of up to 2000 tokens 6.0 us, 256 of up to 8000 on
+// pages of 16 (78 000 entries, 104 000 pages) 14.5; with one map in L2 marked and read by all 24,
+// with one spread over the cluster's shared memory 30 (of eight CTAs 52).
 constexpr int kTableThreads = 1024;
 constexpr int kTableWarps = kTableThreads / 32;
 constexpr int kMaxCluster = 16;
@@ -33,7 +50,7 @@ __device__ __forceinline__ uint32_t cluster_size() {
 // Every thread's earlier writes are seen by every thread of the cluster afterwards.
 __device__ __forceinline__ void cluster_sync(uint32_t ctas) {
   if (ctas == 1) __syncthreads();
-  else asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  else asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
 }
 // The same variable of another CTA of the cluster.
 template <typename T>
@@ -298,7 +315,9 @@ __global__ void __launch_bounds__(kTableThreads) page_fork_kernel(const __grid_c
     const int c = s_copy[b];
     p.seq_len_out[b] = s_new[b];
     p.copy_src[b] = s_from[b];
-    p.copy_dst[b] = c >= 0 ? __ldcg(p.free_blocks + (end - 1 - c)) : -1;
+    const int page = c >= 0 ? __ldcg(p.free_blocks + (end - 1 - c)) : -1;
+    if (c >= 0 && !is_page(page)) raise_flag(p.flags, RKV_FLAG_BAD_INDEX);
+    p.copy_dst[b] = page;
     p.copy_rows[b] = c >= 0 ? s_new[b] & P1 : 0;
   }
   if (me == 0) *p.n_free_out = (int)(end - copies);
@@ -522,7 +541,11 @@ struct CopyArgs {
   int layers, n, N, num_blocks, block_tokens, head_dim;
 };
 
-// A warp copies the rows of one (pair, layer, K or V, head), which lie side by side.
+// A warp copies the rows of one (pair, layer, K or V, head), which lie side by side, eight loads in
+// flight a lane.  Bandwidth bounds it: 701 pages of 128 KB in 8 layers 217 us, the rate of a plain
+// copy.  One wave of CTAs with the same work to each is 234 us: those that finish early leave
+// their SM idle.  (24 CTAs an SM at most, since a list may be mostly empty.)  The 16 begun pages
+// of a forked step in 28 layers take 5.4 us, three dependent loads.
 __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const __grid_constant__ CopyArgs p) {
   const int lane = threadIdx.x & 31;
   const int n = p.count ? max(0, min(p.n, *p.count)) : p.n;
@@ -611,7 +634,11 @@ __device__ __forceinline__ void store16(__nv_bfloat16* p, const uint32_t* w) {
   }
 }
 
-// A warp takes a share of the heads of one chunk.  kWide: the rows of k and v start on 32 bytes.
+// A warp takes a share of the heads of one chunk, at most four, so that a row's heads are written
+// at about the same time.  Bandwidth bounds long ones (a third reads, two thirds writes): 109 500
+// rows of 8 heads of 128 107 us, 6.3 TB/s; 197 000 of 4 heads on pages of 16 97 us.  With a sector
+// written by two 16-byte stores 144 us, one wave of CTAs 113, the next head's codes loaded ahead no
+// gain, codes widened by integer instructions no gain.  1000 rows take 4 us.  kWide: the rows of k and v start on 32 bytes.
 template <int D, bool kWide>
 __global__ void __launch_bounds__(kGatherThreads, kGatherCtas) page_gather_kernel(const __grid_constant__ GatherArgs p) {
   constexpr int kLanes = D / 16;                 // lanes of one row

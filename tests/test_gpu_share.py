@@ -203,6 +203,19 @@ def test_fork_keeps_entries_that_are_no_page():
 
 
 @cuda
+def test_fork_flags_a_free_entry_that_is_no_page():
+    table, lens, free = np.array([[0, 1], [-1, -1]]), [20, 0], [2, 99, 3, 4]
+    for inplace in (False, True):
+        t, ln, f, n, c, flags = _run_fork([0, 0], None, None, lens, table, free, 2, 16, inplace)
+        assert flags == rkv.FLAG_BAD_INDEX and t.tolist() == [[0, 1], [0, 99]] and c.dst.tolist() == [-1, 99]
+        flag = i32([0])                                    # and such a copy is left out
+        cache = _cache(4, 2, 16, 64, 1)
+        before = [x.clone() for x in cache]
+        rkv.page_copy([cache], *c, flags=flag)
+        assert flag.item() == rkv.FLAG_BAD_INDEX and all(torch.equal(x, y) for x, y in zip(cache, before))
+
+
+@cuda
 def test_release_of_a_sharing_table_is_the_plain_one_where_nothing_is_shared():
     g = np.random.default_rng(5)
     lens = [int(x) for x in g.integers(0, 300, size=700)]
