@@ -20,15 +20,16 @@ namespace {
 // lowest row that has begun it), another the first entry of the old table that lets go of it;
 // both are minima, so the order of the threads does not matter.  A page goes where nobody holds
 // it, and its first entry gives it its place in the list.  16 beams of up to 16384 tokens (one
-// CTA, the words in its shared memory) 9.0 us, 256 slots of 4100 tokens on pages of 16 (16 CTAs,
-// the words in L2) 13.0.  Words in the cluster's shared memory instead: 20.8 on eight CTAs (an
-// SM passes on fewer atomics to another's memory than to L2).  Of the 13 some 2.5 are the launch, five
-// barriers and what they wait for 4, the rest nine dependent loads.
+// CTA, the words in its shared memory) 7.8 us, 256 slots of 4100 tokens on pages of 16 (16 CTAs,
+// the words in L2) 12.0.  Words in the cluster's shared memory instead: 20.8 on eight CTAs, where
+// words in L2 took 24 and on 16 CTAs 15 (random atomics on another CTA's memory pass no faster).
+// Of the 12 some 2.5 are the launch, the barriers and the writes that they wait for 4, the rest
+// nine dependent loads and the code itself.
 //
 // Compact.  A bit a page says whether a row holds it.  Each CTA marks its own entries' pages in
 // a map of its own; the maps are joined a part a CTA, counted, and taken over by all, so that a
-// page's rank is one look-up.  16 requests of up to 2000 tokens 6.0 us, 256 of up to 8000 on
-// pages of 16 (78 000 entries, 104 000 pages) 14.5; with one map in L2 marked and read by all 24,
+// page's rank is one look-up.  16 requests of up to 2000 tokens 4.8 us, 256 of up to 8000 on
+// pages of 16 (78 000 entries, 104 000 pages) 12.9; with one map in L2 marked and read by all 24,
 // with one spread over the cluster's shared memory 30 (of eight CTAs 52).
 constexpr int kTableThreads = 1024;
 constexpr int kTableWarps = kTableThreads / 32;
@@ -59,32 +60,39 @@ __device__ __forceinline__ T* in_cta(T* p, uint32_t rank) {
   asm("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
   return reinterpret_cast<T*>(r);
 }
+// Tasks of a warp.  These kernels run their code once, and much of what a phase costs beside its
+// loads is the fetching of its instructions: with two tasks held and not three or four, the others'
+// loop not unrolled, and no divisions, 16 beams went from 9.1 to 7.8 us, the compaction of 16
+// requests from 6.0 to 4.8.
 struct Tasks {
   int first, last, per_row;          // this warp's [first, last)
+  int row, part;                     // row of the first, and its place in it
   __device__ __forceinline__ Tasks(int batch, int width, uint32_t rank, uint32_t ctas) {
     per_row = (width + kTaskEntries - 1) / kTaskEntries;
-    const int64_t n = (int64_t)batch * per_row, warps = (int64_t)ctas * kTableWarps;
-    const int64_t w = (int64_t)rank * kTableWarps + threadIdx.x / 32;
-    first = (int)(n * w / warps), last = (int)(n * (w + 1) / warps);
+    const int64_t n = (int64_t)batch * per_row;
+    const int lg = __popc(ctas * kTableWarps - 1), w = (int)rank * kTableWarps + threadIdx.x / 32;     // a power of two of warps
+    first = (int)(n * w >> lg), last = (int)(n * (w + 1) >> lg);
+    row = per_row ? first / per_row : 0;
+    part = first - row * per_row;
   }
   // f(i, row, entry of the row) for the entries of this lane: i counts those of the first kHold
   // tasks and is -1 in the others.  Every lane of the warp makes the same calls.
   template <int kHold, typename F>
   __device__ __forceinline__ void each(F f) const {
     const int lane = threadIdx.x & 31;
+    int b = row, c = part;
 #pragma unroll
     for (int h = 0; h < kHold; ++h) {
-      const int t = first + h;
-      if (t < last) {
-        const int b = t / per_row, j0 = (t - b * per_row) * kTaskEntries + lane;
+      if (first + h < last) {
 #pragma unroll
-        for (int k = 0; k < kLaneEntries; ++k) f(h * kLaneEntries + k, b, j0 + 32 * k);
+        for (int k = 0; k < kLaneEntries; ++k) f(h * kLaneEntries + k, b, c * kTaskEntries + lane + 32 * k);
+        if (++c == per_row) c = 0, ++b;
       }
     }
     for (int t = first + kHold; t < last; ++t) {
-      const int b = t / per_row, j0 = (t - b * per_row) * kTaskEntries + lane;
-#pragma unroll
-      for (int k = 0; k < kLaneEntries; ++k) f(-1, b, j0 + 32 * k);
+#pragma unroll 1
+      for (int k = 0; k < kLaneEntries; ++k) f(-1, b, c * kTaskEntries + lane + 32 * k);
+      if (++c == per_row) c = 0, ++b;
     }
   }
 };
@@ -112,7 +120,7 @@ struct ForkArgs {
 // What is known of a page: x: -1 where a row holds it whole, else the first row that has begun
 // it, kNone without one; y: the first entry of the old table that lets go of it.
 constexpr int kNone = INT32_MAX;
-constexpr int kForkHold = 3;
+constexpr int kForkHold = 2;
 
 // The table, lengths and count as they were, and no copies.
 __device__ __forceinline__ void fork_refused(const ForkArgs& p, int32_t flag, int n_free) {
@@ -148,7 +156,7 @@ __global__ void __launch_bounds__(kTableThreads) page_fork_kernel(const __grid_c
   const int64_t cap = (int64_t)M << p.shift;
   const bool in_place = p.table_out == p.table;
   auto is_page = [&](int id) { return id >= 0 && id < num; };
-  auto pages = [&](int n) { return (int)(((int64_t)n + P1) >> p.shift); };
+  auto pages = [&](int n) { return (int)(((uint32_t)n + P1) >> p.shift); };      // (n + 127 < 2^31: check_table)
   auto state = [&](int id) {
     if constexpr (kLocal) return s_state + id;
     else return p.state + id;
@@ -337,7 +345,7 @@ struct CompactArgs {
   int batch, max_blocks, num_blocks, shift, words;   // words of a CTA: a power of two
 };
 
-constexpr int kCompactHold = 4;
+constexpr int kCompactHold = 2;
 
 // Of each 32 pages, x: which of them rows hold (a bit each); y: how many of the CTA's pages are
 // held before them.  kLocal: each CTA marks the pages of its own entries in its shared memory,
@@ -348,7 +356,7 @@ __global__ void __launch_bounds__(kTableThreads) page_compact_kernel(const __gri
   extern __shared__ int fsm[];
   int* s_have = fsm;                 // [batch] pages
   int2* s_state = reinterpret_cast<int2*>(fsm + (p.batch + 1) / 2 * 2);
-  __shared__ int s_width, s_total[kMaxCluster], s_base[kMaxCluster + 1];
+  __shared__ int s_width, s_count[kTableWarps], s_total[kMaxCluster], s_base[kMaxCluster + 1];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const uint32_t rank = cluster_rank(), ctas = cluster_size();
   const int step = ctas * kTableThreads, me = rank * kTableThreads + tid;
@@ -380,7 +388,7 @@ __global__ void __launch_bounds__(kTableThreads) page_compact_kernel(const __gri
   for (int b = tid; b < p.batch; b += kTableThreads) {
     int len = p.seq_len[b];
     if (len < 0 || len > (int64_t)M << p.shift) bad = true, len = 0;
-    s_have[b] = (int)(((int64_t)len + P1) >> p.shift);
+    s_have[b] = (int)(((uint32_t)len + P1) >> p.shift);
     width = max(width, s_have[b]);
   }
   bad = __syncthreads_or(bad);
@@ -427,12 +435,20 @@ __global__ void __launch_bounds__(kTableThreads) page_compact_kernel(const __gri
         for (uint32_t c = 0; c < kMaxCluster; ++c) x |= part[c];
       }
     }
-    int64_t none = 0, total_none;
-    int sum = __popc(x), these;
-    const int n = sum;
-    block_scan<kTableThreads>(none, sum, total_none, these);
-    if (w < p.words) *state(first + w) = make_int2(x, total + sum - n);
-    total += these;
+    const int n = __popc(x);
+    int sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    if (w0) __syncthreads();         // the last round's counts have been read
+    if (lane == 31) s_count[wid] = sum;
+    __syncthreads();
+    const int counted = s_count[lane];
+    sum += total + __reduce_add_sync(0xffffffffu, lane < wid ? counted : 0);
+    if (w < p.words) *state(first + w) = make_int2(x, sum - n);
+    total += __reduce_add_sync(0xffffffffu, counted);
   }
   if (tid < ctas) *in_cta(&s_total[rank], tid) = total;
   cluster_sync(ctas);
@@ -497,7 +513,8 @@ __global__ void __launch_bounds__(kTableThreads) page_compact_kernel(const __gri
 // CTAs for a table: one for up to `alone` tasks a warp (a cluster's barriers and its state in L2
 // cost more), else as many as leave a warp one task.  64 requests of up to 1000 tokens on pages of
 // 16, two tasks a warp: a fork on one CTA 9.2 us, on two 9.5, a compaction 9.1 and 8.7 (of up to
-// 2000 10.9 and 9.6); 128 of up to 2000, four tasks: a fork 16.4 and on four CTAs 11.0.
+// 2000 10.9 and 9.6); 128 of up to 2000, four tasks: a fork 16.4 and on four CTAs 11.0 (before
+// the code was shortened).
 unsigned table_ctas(int batch, int max_blocks, int alone) {
   const int64_t tasks = (int64_t)batch * ceil_div(max_blocks, kTaskEntries);
   unsigned ctas = 1;
