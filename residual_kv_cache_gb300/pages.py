@@ -21,7 +21,7 @@ Requests that begin alike share the pages of what they have in common:
     table = PageTable(batch, max_blocks, num_blocks, block_tokens, sharing=True)
     copies = table.fork(source, length)              # rows become (prefixes of) other rows
     page_copy(caches, *copies)                       # the pages that two of them have begun
-    k, v, cu_k = cache.gather(table, max_rows, length)     # the prefix, for a prompt behind it
+    k, v, cu_k = cache.gather(table, max_rows, length)     # a prompt's keys with its prefix's
     page_copy(caches, *table.compact())              # all pages to the pool's low end
 
 Every tensor of a call must lie on one device, which need not be the current one.  Work goes
