@@ -8,7 +8,7 @@
 // the position drops the whole turns by overflow, and the upper 32 bits, taken as a signed
 // number, are the angle in (-pi, pi] to 2^-32 of a turn.
 //
-// Bandwidth bounds many rows, one chain of loads few (16 rows of 40 heads of 128 3.1 us).  A warp
+// Bandwidth bounds many rows, one chain of loads few (16 rows of 40 heads of 128 2.9 us).  A warp
 // takes a row: the sines are found once for its heads, a part of them in each lane.  The next
 // heads' values, or the next row's, are on their way while some are turned.  32768 rows of 32 + 8
 // heads of 128, normed and turned: 108 us, 6.2 TB/s (125 us with the sines found by every lane,
@@ -148,6 +148,7 @@ __global__ void __launch_bounds__(kHeadThreads, kHeadCtas) head_norm_rotate_kern
     lo = (int)((int64_t)parts * share / p.shares), hi = (int)((int64_t)parts * (share + 1) / p.shares);
   };
   const bool any = task < tasks;
+  pdl_wait_previous_grid();
   int pos = -1;
   if (any) {
     place(task);
@@ -269,8 +270,7 @@ cudaError_t launch_heads(HeadArgs a, int sms, cudaStream_t s) {
   a.shares = (int)(shares < 1 ? 1 : shares < parts ? shares : parts);
   const int64_t ctas = ((int64_t)a.n_rows * a.shares + kHeadWarps - 1) / kHeadWarps;
   const int64_t grid = ctas < (int64_t)sms * kHeadCtas ? ctas : (int64_t)sms * kHeadCtas;
-  head_norm_rotate_kernel<In, Out, D><<<(unsigned)grid, kHeadThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_behind(head_norm_rotate_kernel<In, Out, D>, a, (unsigned)grid, kHeadThreads, 0, s);
 }
 
 template <int D>

@@ -4,6 +4,7 @@
 #include <cuda_fp8.h>
 
 #include "pages.h"
+#include "ptx.cuh"
 
 namespace rkv {
 namespace {
@@ -20,8 +21,8 @@ namespace {
 // lowest row that has begun it), another the first entry of the old table that lets go of it;
 // both are minima, so the order of the threads does not matter.  A page goes where nobody holds
 // it, and its first entry gives it its place in the list.  16 beams of up to 16384 tokens (one
-// CTA, the words in its shared memory) 7.8 us, 256 slots of 4100 tokens on pages of 16 (16 CTAs,
-// the words in L2) 12.0.  Words in the cluster's shared memory instead: 20.8 on eight CTAs, where
+// CTA, the words in its shared memory) 7.5 us, 256 slots of 4100 tokens on pages of 16 (16 CTAs,
+// the words in L2) 11.7.  Words in the cluster's shared memory instead: 20.8 on eight CTAs, where
 // words in L2 took 24 and on 16 CTAs 15 (random atomics on another CTA's memory pass no faster).
 // Of the 12 some 2.5 are the launch, the barriers and the writes that they wait for 4, the rest
 // nine dependent loads and the code itself.
@@ -29,7 +30,7 @@ namespace {
 // Compact.  A bit a page says whether a row holds it.  Each CTA marks its own entries' pages in
 // a map of its own; the maps are joined a part a CTA, counted, and taken over by all, so that a
 // page's rank is one look-up.  16 requests of up to 2000 tokens 4.8 us, 256 of up to 8000 on
-// pages of 16 (78 000 entries, 104 000 pages) 12.9; with one map in L2 marked and read by all 24,
+// pages of 16 (78 000 entries, 104 000 pages) 12.3; with one map in L2 marked and read by all 24,
 // with one spread over the cluster's shared memory 30 (of eight CTAs 52).
 constexpr int kTableThreads = 1024;
 constexpr int kTableWarps = kTableThreads / 32;
@@ -166,6 +167,7 @@ __global__ void __launch_bounds__(kTableThreads) page_fork_kernel(const __grid_c
     else return __ldcg(p.state + id);
   };
 
+  pdl_wait_previous_grid();
   const int n_free = *p.n_free;
   // as given, at first: positions before the call in s_have, those asked for in s_new
   for (int b = tid; b < p.batch; b += kTableThreads) {
@@ -374,6 +376,7 @@ __global__ void __launch_bounds__(kTableThreads) page_compact_kernel(const __gri
     else return __ldcg(p.state + w);
   };
 
+  pdl_wait_previous_grid();
   if constexpr (kLocal) {
     for (int i = tid; i < words; i += kTableThreads) {
       s_state[i].x = 0;
@@ -523,21 +526,6 @@ unsigned table_ctas(int batch, int max_blocks, int alone) {
   return ctas;
 }
 
-template <typename Args>
-cudaError_t launch_table(void (*kernel)(Args), const Args& a, unsigned ctas, size_t smem, cudaStream_t s) {
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim = {ctas, 1, 1};
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kTableThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
-}
-
 // ------------------------------------------------------------------------- page copies
 constexpr int kCopyThreads = 256;
 constexpr int kCopyCtas = 24;        // CTAs an SM at most
@@ -562,9 +550,10 @@ struct CopyArgs {
 // flight a lane.  Bandwidth bounds it: 701 pages of 128 KB in 8 layers 217 us, the rate of a plain
 // copy.  One wave of CTAs with the same work to each is 234 us: those that finish early leave
 // their SM idle.  (24 CTAs an SM at most, since a list may be mostly empty.)  The 16 begun pages
-// of a forked step in 28 layers take 5.4 us, three dependent loads.
+// of a forked step in 28 layers take 5.0 us, three dependent loads.
 __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const __grid_constant__ CopyArgs p) {
   const int lane = threadIdx.x & 31;
+  pdl_wait_previous_grid();
   const int n = p.count ? max(0, min(p.n, *p.count)) : p.n;
   const int64_t items = (int64_t)n * p.layers * 2 * p.N;
   const int64_t head_bytes = (int64_t)p.block_tokens * p.head_dim;
@@ -653,9 +642,9 @@ __device__ __forceinline__ void store16(__nv_bfloat16* p, const uint32_t* w) {
 
 // A warp takes a share of the heads of one chunk, at most four, so that a row's heads are written
 // at about the same time.  Bandwidth bounds long ones (a third reads, two thirds writes): 109 500
-// rows of 8 heads of 128 107 us, 6.3 TB/s; 197 000 of 4 heads on pages of 16 97 us.  With a sector
+// rows of 8 heads of 128 107 us, 6.3 TB/s; 197 000 of 4 heads on pages of 16 96.5 us.  With a sector
 // written by two 16-byte stores 144 us, one wave of CTAs 113, the next head's codes loaded ahead no
-// gain, codes widened by integer instructions no gain.  1000 rows take 4 us.  kWide: the rows of k and v start on 32 bytes.
+// gain, codes widened by integer instructions no gain.  1000 rows take 3.6 us.  kWide: the rows of k and v start on 32 bytes.
 template <int D, bool kWide>
 __global__ void __launch_bounds__(kGatherThreads, kGatherCtas) page_gather_kernel(const __grid_constant__ GatherArgs p) {
   constexpr int kLanes = D / 16;                 // lanes of one row
@@ -665,6 +654,7 @@ __global__ void __launch_bounds__(kGatherThreads, kGatherCtas) page_gather_kerne
   int* s_cu = fsm;                   // [batch] first row of each sequence
   int* s_chunk = s_cu + p.batch;     // [batch] first chunk of each
   const int tid = threadIdx.x, lane = tid & 31;
+  pdl_wait_previous_grid();
   int64_t rows = 0;
   int chunks = 0;                    // exact wherever the rows fit
   bool bad = false;
@@ -816,7 +806,8 @@ extern "C" rkv_status rkv_page_fork(const rkv_page_table* table, const int32_t* 
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || opt_in[local](kernel, kTableSmem, dev, true) != cudaSuccess)
     return fail_with(RKV_ECUDA, "no usable current device");
-  const cudaError_t e = launch_table(kernel, a, ctas, fixed + (local ? state : 0), static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_behind(kernel, a, ctas, kTableThreads, fixed + (local ? state : 0),
+                                      static_cast<cudaStream_t>(stream), ctas);
   return e == cudaSuccess ? RKV_OK : fail_with(RKV_ECUDA, "page fork launch failed: %s", cudaGetErrorString(e));
 }
 
@@ -853,7 +844,8 @@ extern "C" rkv_status rkv_page_compact(const rkv_page_table* table, int32_t* fre
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || opt_in[local](kernel, kTableSmem, dev, true) != cudaSuccess)
     return fail_with(RKV_ECUDA, "no usable current device");
-  const cudaError_t e = launch_table(kernel, a, ctas, fixed + (local ? state : 0), static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_behind(kernel, a, ctas, kTableThreads, fixed + (local ? state : 0),
+                                      static_cast<cudaStream_t>(stream), ctas);
   return e == cudaSuccess ? RKV_OK : fail_with(RKV_ECUDA, "page compact launch failed: %s", cudaGetErrorString(e));
 }
 
@@ -882,8 +874,8 @@ extern "C" rkv_status rkv_page_copy(const rkv_pages* layers, int32_t n_layers, c
   if (!current_device(dev, sms)) return fail_with(RKV_ECUDA, "no usable current device");
   const int64_t items = (int64_t)n * n_layers * 2 * a.N, ctas = (items + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
   const int64_t most = kCopyCtas * (int64_t)sms;
-  page_copy_kernel<<<(unsigned)(ctas < most ? ctas : most), kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_behind(page_copy_kernel, a, (unsigned)(ctas < most ? ctas : most), kCopyThreads, 0,
+                                      static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? RKV_OK : fail_with(RKV_ECUDA, "page copy launch failed: %s", cudaGetErrorString(e));
 }
 
@@ -928,8 +920,7 @@ extern "C" rkv_status rkv_page_gather(const rkv_pages* pages, const rkv_page_tab
   a.shares = (int)(shares < least ? least : shares < a.N ? shares : a.N);
   const int64_t ctas = (chunks * a.shares + kGatherThreads / 32 - 1) / (kGatherThreads / 32);
   const int64_t most = (int64_t)sms * kGatherCtas * kGatherWaves;
-  kernel<<<(unsigned)(ctas < most ? ctas : most), kGatherThreads, sizeof(int) * 2 * (size_t)a.batch,
-           static_cast<cudaStream_t>(stream)>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_behind(kernel, a, (unsigned)(ctas < most ? ctas : most), kGatherThreads,
+                                      sizeof(int) * 2 * (size_t)a.batch, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? RKV_OK : fail_with(RKV_ECUDA, "page gather launch failed: %s", cudaGetErrorString(e));
 }

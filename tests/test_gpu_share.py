@@ -614,6 +614,72 @@ def test_beam_search_step_captured_and_replayed():
 
 
 @cuda
+def test_calls_wait_for_what_precedes_them():
+    """Each call reads what the operation right before it writes, a kernel, a fill, a copy or another
+    stream's, made one by one and captured, and again and again: the results follow."""
+    N, D, P, n = 2, 64, 16, 4000
+    k8, v8, ks, vs = _cache(600, N, P, D, 9)
+    big = torch.zeros(1 << 26, device="cuda")
+    table, lens = i32(np.arange(500)[None]), i32([0])
+    q, pos, freq = randn(n, 3, D, seed=1), i32([0] * n), rkv.rotation_freq(D)
+    host_len, host_pos = torch.tensor([16 * 400], dtype=torch.int32).pin_memory(), torch.arange(n, dtype=torch.int32).pin_memory()
+    src, dst, free, nf = i32([-1]), i32([-1]), i32([0] * 600), i32([0])
+    side = torch.cuda.Stream()
+
+    def chain():
+        big.add_(1)                                        # some time during which the rest may run ahead
+        lens.copy_(host_len, non_blocking=True)
+        k, v, cu = rkv.page_gather(k8, v8, ks, vs, table, lens, 6400)
+        pos.copy_(host_pos, non_blocking=True)
+        pos.add_(big[0].int() * 0 + 3)
+        a, _ = rkv.head_norm_rotate(q, None, pos, freq, eps=1e-6)
+        b, _ = rkv.head_norm_rotate(a, None, pos, freq, eps=1e-6)          # reads what the last call wrote
+        src.fill_(5)
+        dst.fill_(599)
+        rkv.page_copy([(k8, v8, ks, vs)], src, dst)
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            big.add_(1)
+            lens.fill_(16 * 300)
+        main.wait_stream(side)
+        out, cut, left = torch.empty_like(table), torch.empty_like(lens), torch.empty_like(nf)
+        free2 = free.clone()
+        rkv.page_fork(None, lens, table, free2, nf, P, length=lens // 2, block_table_out=out, seq_len_out=cut, n_free_out=left)
+        c = rkv.page_compact(cut, out, free2, left, P, block_table_out=out)
+        k2, v2, cu2 = rkv.page_gather(k8, v8, ks, vs, out, cut, 2400)
+        return k, v, cu, a, b, k8.clone(), ks.clone(), out, cut, left, free2, c.count, k2, v2, cu2
+
+    def reset():
+        lens.zero_()
+        pos.zero_()
+        src.fill_(-1)
+        dst.fill_(-1)
+        k8[599], ks[599] = 0, 1
+    same = lambda x, y: all(torch.equal(a.view(torch.uint8) if a.element_size() < 4 else a,  # noqa: E731
+                                        b.view(torch.uint8) if b.element_size() < 4 else b) for a, b in zip(x, y))
+    reset()
+    want = [x.clone() for x in chain()]
+    torch.cuda.synchronize()
+    assert want[2].tolist() == [0, 6400] and want[8].item() == 2400 and want[9].item() == 450 and want[14].tolist() == [0, 2400]
+    check_a = OP.norm_rotate(np64(q[:5]), [3, 4, 5, 6, 7], np64(freq).tolist(), None, 1e-6)
+    assert np.all(np.abs(np64(want[3][:5]) - check_a) <= 2.0 ** -8 * np.abs(check_a) + 2.0 ** -18 * np.sqrt(D))
+    assert torch.equal(want[5][599], k8[5]) and np.array_equal(
+        np64(want[0]), OP.gather(*_stored(k8, ks), np.arange(500)[None], [6400], P), equal_nan=True)
+    for _ in range(20):
+        reset()
+        assert same(chain(), want)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = chain()
+    for _ in range(20):
+        reset()
+        graph.replay()
+        assert same(got, want)
+
+
+@cuda
 def test_two_streams_at_once():
     """Calls on different buffers in two streams give what they give alone."""
     def make(seed):
