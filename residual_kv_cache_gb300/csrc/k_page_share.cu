@@ -167,6 +167,9 @@ __global__ void __launch_bounds__(kTableThreads) page_fork_kernel(const __grid_c
     else return __ldcg(p.state + id);
   };
 
+  if (kLocal)
+    for (int i = tid; i < num; i += kTableThreads) s_state[i] = make_int2(kNone, kNone);
+  if (tid == 0) s_width = 0;
   pdl_wait_previous_grid();
   const int n_free = *p.n_free;
   // as given, at first: positions before the call in s_have, those asked for in s_new
@@ -177,8 +180,8 @@ __global__ void __launch_bounds__(kTableThreads) page_fork_kernel(const __grid_c
     s_src[b] = ends ? -1 : s;
     s_new[b] = n;
   }
-  if (tid == 0) s_width = 0;
-  for (int i = kLocal ? tid : me; i < num; i += step) *state(i) = make_int2(kNone, kNone);
+  if (!kLocal)
+    for (int i = me; i < num; i += step) p.state[i] = make_int2(kNone, kNone);
   __syncthreads();
   bool bad = n_free < 0 || n_free > num;
   int width = 0;
@@ -376,16 +379,16 @@ __global__ void __launch_bounds__(kTableThreads) page_compact_kernel(const __gri
     else return __ldcg(p.state + w);
   };
 
-  pdl_wait_previous_grid();
   if constexpr (kLocal) {
     for (int i = tid; i < words; i += kTableThreads) {
       s_state[i].x = 0;
       if (ctas > 1) s_mark[i] = 0;
     }
-  } else {
-    for (int i = me; i < words; i += step) p.state[i].x = 0;
   }
   if (tid == 0) s_width = 0;
+  pdl_wait_previous_grid();
+  if constexpr (!kLocal)
+    for (int i = me; i < words; i += step) p.state[i].x = 0;
   bool bad = false;
   int width = 0;
   for (int b = tid; b < p.batch; b += kTableThreads) {
@@ -555,13 +558,14 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const __grid_co
   const int lane = threadIdx.x & 31;
   pdl_wait_previous_grid();
   const int n = p.count ? max(0, min(p.n, *p.count)) : p.n;
-  const int64_t items = (int64_t)n * p.layers * 2 * p.N;
+  const int per_pair = p.layers * 2 * p.N;       // below 2^24
+  const int64_t items = (int64_t)n * per_pair;
   const int64_t head_bytes = (int64_t)p.block_tokens * p.head_dim;
   for (int64_t it = (int64_t)blockIdx.x * (kCopyThreads / 32) + threadIdx.x / 32; it < items;
        it += (int64_t)gridDim.x * (kCopyThreads / 32)) {
-    const int h = (int)(it % p.N);
-    const int64_t rest = it / p.N;
-    const int kv = (int)(rest & 1), layer = (int)((rest >> 1) % p.layers), i = (int)((rest >> 1) / p.layers);
+    const int i = (int)(it / per_pair);
+    const uint32_t in = (uint32_t)(it - (int64_t)i * per_pair), rest = in / (uint32_t)p.N;
+    const int h = (int)(in - rest * (uint32_t)p.N), kv = (int)(rest & 1), layer = (int)(rest >> 1);
     const int from = p.src[i], to = p.dst[i];
     int rows = p.rows ? p.rows[i] : p.block_tokens;
     if (from < 0 && to < 0) continue;
