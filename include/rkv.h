@@ -60,7 +60,7 @@ enum {
   RKV_FLAG_UNWRITTEN = 4,    /* a selected token was never written            */
   RKV_FLAG_FP16_SAT = 8,     /* a group extreme saturated at +-65504          */
   RKV_FLAG_BAD_SLOT = 16,    /* a pool slot outside [0, max_refs)             */
-  RKV_FLAG_NO_SPACE = 32     /* rkv_page_plan / rkv_page_release: refused     */
+  RKV_FLAG_NO_SPACE = 32     /* a page call did not fit and was refused       */
 };
 
 /*

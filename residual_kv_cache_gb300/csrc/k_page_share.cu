@@ -232,10 +232,10 @@ __global__ void __launch_bounds__(kTableThreads) page_fork_kernel(const __grid_c
     else load(b, j, t, g);
     const int s = s_src[b], n = s_new[b], m = pages(n);
     if (j < m) {
-      // (-1 is the least: a plain store of it and another row's minimum end the same)
+      // (-1 is the least: a store of it and another row's minimum end the same)
       if (!is_page(t)) stray = true;
       else if (j == m - 1 && (n & P1)) atomicMin(&state(t)->x, b);
-      else state(t)->x = -1;
+      else *const_cast<volatile int*>(&state(t)->x) = -1;
       if (kLocal && j == m - 1 && (n & P1)) s_from[b] = t;
       if (i < 0 && in_place && s != b) p.stage[(int64_t)b * M + j] = t;
     }
@@ -611,12 +611,14 @@ struct GatherArgs {
   int batch, max_blocks, num_blocks, N, shift, max_rows, shares;
 };
 
-// Sixteen codes, used once.
+// Sixteen codes, used once.  (Not the read-only path: the blocks may be on their SM while the
+// kernel that wrote the codes still runs.)
 __device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
   uint4 u;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-               : "l"(p));
+               : "l"(p)
+               : "memory");
   return u;
 }
 
@@ -648,7 +650,8 @@ __device__ __forceinline__ void store16(__nv_bfloat16* p, const uint32_t* w) {
 // at about the same time.  Bandwidth bounds long ones (a third reads, two thirds writes): 109 500
 // rows of 8 heads of 128 107 us, 6.3 TB/s; 197 000 of 4 heads on pages of 16 96.5 us.  With a sector
 // written by two 16-byte stores 144 us, one wave of CTAs 113, the next head's codes loaded ahead no
-// gain, codes widened by integer instructions no gain.  1000 rows take 3.6 us.  kWide: the rows of k and v start on 32 bytes.
+// gain, codes widened by integer instructions no gain.  1000 rows take 3.6 us.  kWide: the rows of
+// k and v start on 32 bytes.
 template <int D, bool kWide>
 __global__ void __launch_bounds__(kGatherThreads, kGatherCtas) page_gather_kernel(const __grid_constant__ GatherArgs p) {
   constexpr int kLanes = D / 16;                 // lanes of one row
@@ -712,7 +715,7 @@ __global__ void __launch_bounds__(kGatherThreads, kGatherCtas) page_gather_kerne
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         const uint8_t* src = p.codes[kv] + ((head << p.shift) + (j0 & ((1 << p.shift) - 1))) * D + x;
-        s[kv] = there ? __ldg(p.scale[kv] + head) : 0.0f;
+        s[kv] = there ? p.scale[kv][head] : 0.0f;
 #pragma unroll
         for (int k = 0; k < kLoads; ++k) {
           const int r = k * kRows + r_in;
