@@ -116,6 +116,13 @@ def test_outputs_are_made_and_one_of_the_two_may_be_left_out():
     c, d = rkv.head_norm_rotate(q, k, i32(pos), freq, k_weight=w, eps=1e-6)       # a weight for one of them
     check(c, q, pos, freq, None, 1e-6)
     check(d, k, pos, freq, w, 1e-6)
+    # fp32 rows: a bf16 output for one makes the other bf16; rows and heads that are one in memory
+    qf, kf = q.float()[:, :1].expand(6, 4, 64), k.float()[:1].expand(6, 3, 64)
+    qo = torch.empty(6, 4, 64, dtype=BF, device="cuda")
+    c, d = rkv.head_norm_rotate(qf, kf, i32(pos), freq, eps=1e-6, q_out=qo)
+    assert c is qo and d.dtype == BF
+    check(c, qf, pos, freq, None, 1e-6)
+    check(d, kf, pos, freq, None, 1e-6)
     e = torch.empty_like(q[:0])
     a, b = rkv.head_norm_rotate(e, e, i32([]), freq)
     assert a.shape == e.shape
