@@ -13,8 +13,9 @@ namespace {
 // A call is a few phases that wait for one another, each a load or two long, and latency bounds
 // it: one CTA does it, or a cluster of up to 16.  A warp takes a run of tasks (128 neighbouring
 // entries of a row of the table), the same ones in every phase, and holds the entries of the
-// first of them in registers from the first phase to the last.  More launches would cost the
-// host 2 us each, blocks of a whole grid a barrier of more than a microsecond.
+// first of them in registers from the first phase to the last.  (Not
+// built: several launches, or a whole grid with barriers of its own, put at a microsecond or two
+// for each boundary.)
 //
 // Fork.  With R the rows after the call, a page is held whole where some R has it as one of its
 // full pages, else begun by the rows that have it last.  One word a page says which (-1, or the
