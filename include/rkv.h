@@ -607,8 +607,9 @@ rkv_status rkv_head_norm_rotate(const rkv_head_rows* rows, void* stream);
  * copied in every layer (rkv_page_copy takes the lists as they are) before anything is appended.
  *   table: block_table and seq_len before the call.
  *   block_table_out (device, int32) [batch, max_blocks], seq_len_out (device) [batch], n_free_out
- *     (device) [1]: after it.  They may be the table's own and n_free (update in place).  Entries
- *     past a row's pages are -1 in another table; in place, where the row had pages before.
+ *     (device) [1]: after it.  They may be the table's own and n_free (update in place), and
+ *     seq_len_out may be source, length or finished.  Entries past a row's pages are -1 in
+ *     another table; in place, where the row had pages before.
  *   free_blocks, n_free: the free list.  Pages that no row holds any more are put on its end, in
  *     order of their first row and position; then the copies' pages are taken from its end, in
  *     order of the rows.  The first n_free entries stay as they are.

@@ -203,6 +203,9 @@ __global__ void __launch_bounds__(kTableThreads) page_fork_kernel(const __grid_c
   }
   bad = __syncthreads_or(bad);
   if (bad) {
+    // every CTA has read source and length before one writes seq_len_out, which may be one of
+    // them: all see the same call and refuse it (one that went on would wait for CTAs that ended)
+    cluster_sync(ctas);
     fork_refused(p, RKV_FLAG_BAD_INDEX, n_free);
     return;
   }

@@ -1,0 +1,58 @@
+"""GPU calls of the operators around the paged cache whose buffers share memory, and those that the
+library's own loop makes seldom: each against the same call on buffers of its own."""
+import numpy as np
+import pytest
+import torch
+
+import residual_kv_cache_gb300 as rkv
+
+pytestmark = pytest.mark.gpu
+cuda = pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def rows_of_pages(batch, width, block, seed):
+    """(table, lengths, free list, free count): rows of pages of their own, in random order."""
+    g = np.random.default_rng(seed)
+    lens = g.integers(1, width * block + 1, size=batch)
+    have = -(-lens // block)
+    ids = g.permutation(int(have.sum()) + 2 * batch)
+    table, at = np.full((batch, width), -1), 0
+    for b, n in enumerate(have):
+        table[b, :n] = ids[at:at + n]
+        at += n
+    free = np.zeros(len(ids), np.int64)
+    free[:2 * batch] = ids[at:]
+    return table, lens, free, 2 * batch
+
+
+@cuda
+@pytest.mark.parametrize("batch,width", [(9, 40), (256, 40), (700, 20), (8192, 5)])      # 1, 8, 16 and 16 CTAs
+@pytest.mark.parametrize("shared", ["source", "length"])
+@pytest.mark.parametrize("inplace", [False, True])
+def test_fork_whose_lengths_go_where_its_arguments_are(batch, width, shared, inplace):
+    """seq_len_out may be source or length: every CTA reads those before one writes, also where the
+    call is refused."""
+    table, lens, free, nf = rows_of_pages(batch, width, 16, batch)
+    g = np.random.default_rng(1)
+    source = g.integers(-1, batch, size=batch)
+    length = np.array([g.integers(0, lens[s] + 1) if s >= 0 else 3 for s in source])
+    for bad in (False, True):
+        src, cut = source.copy(), length.copy()
+        if bad:
+            src[-1], cut[-1] = batch - 1, lens[-1] + 1
+
+        def call(alias):
+            t, ln, f, n, a, b, flags = i32(table), i32(lens), i32(free), i32([nf]), i32(src), i32(cut), i32([0])
+            to = t if inplace else torch.empty_like(t)
+            out = {"source": a, "length": b}[shared] if alias else torch.empty_like(ln)
+            c = rkv.page_fork(a, ln, t, f, n, 16, length=b, block_table_out=to, seq_len_out=out, flags=flags)
+            return [to, out, f, n, flags, *c[:3]]
+        want = [x.tolist() for x in call(False)]
+        assert want[4] == [rkv.FLAG_BAD_INDEX if bad else 0]
+        assert (want[1] == lens.tolist() and want[0] == table.tolist()) == bad
+        for _ in range(20):
+            assert [x.tolist() for x in call(True)] == want
