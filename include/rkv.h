@@ -560,8 +560,9 @@ rkv_status rkv_prompt_attention_workspace(const rkv_prompt* prompt, size_t* byte
  *   q, k, q_out, k_out (device) [n_rows, heads, D]: row r, head h at r * strides[0] + h *
  *     strides[1] elements; 16-byte aligned rows.  Inputs of dtype, outputs of out_dtype: the
  *     same, or RKV_BF16.  An output may be its input itself (same address, strides and type);
- *     rows of an output must not overlap.  Either head count may be 0 (its pointers are not
- *     looked at).
+ *     beside that its rows must not overlap one another, the other output's or an input's
+ *     (RKV_EINVAL; parts of one buffer that lie side by side in each row are apart).  Either
+ *     head count may be 0 (its pointers are not looked at).
  *   q_weight, k_weight (device, dtype) [D] or NULL (all 1).
  *   positions (device, int32) [n_rows]; rows at negative ones are left as they are in the
  *     outputs (row_pos of rkv_page_plan is -1 past a step's rows).

@@ -322,6 +322,17 @@ extern "C" rkv_status rkv_head_norm_rotate(const rkv_head_rows* hr, void* stream
       return fail_with(RKV_EINVAL, "rows of an output overlap");
   }
   if (r.rotary_dim && !is_aligned(r.freq, 8)) return fail_with(RKV_EALIGN, "freq must be 8-byte aligned");
+  // other warps read rows while one writes: an output is its own input, or apart from both inputs
+  RowBytes from[2], to[2];
+  for (int i = 0; i < 2; ++i)
+    if (heads[i] && (!row_bytes(x[i], r.n_rows, heads[i], r.head_dim, st[i], r.dtype == RKV_F32 ? 4 : 2, from[i]) ||
+                     !row_bytes(out[i], r.n_rows, heads[i], r.head_dim, ost[i], r.out_dtype == RKV_F32 ? 4 : 2, to[i])))
+      return fail_with(RKV_EINVAL, "strides pass the address space");
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2; ++j)
+      if (heads[i] && heads[j] && !(i == j && from[j] == to[i]) && rows_meet(from[j], to[i]))
+        return fail_with(RKV_EINVAL, "an output overlaps an input and is not that input's own");
+  if (heads[0] && heads[1] && rows_meet(to[0], to[1])) return fail_with(RKV_EINVAL, "q_out and k_out overlap");
   a.positions = r.positions;
   a.freq = r.freq;
   a.n_rows = r.n_rows, a.rotary = r.rotary_dim, a.adjacent = r.adjacent != 0;

@@ -44,6 +44,91 @@ inline bool rows_apart(int rows, int heads, int D, const int64_t strides[2]) {
          (rows1 || heads1 || row >= (heads - 1) * head + Dl || head >= (rows - 1) * row + Dl);
 }
 
+// The bytes of a strided [rows, heads, D] tensor: n_outer blocks of n_inner runs of `width` bytes.
+// (Strides that are never used are 0.)
+struct RowBytes {
+  int64_t base, outer, inner, n_outer, n_inner, width;
+  int64_t block() const { return (n_inner - 1) * inner + width; }
+  int64_t end() const { return base + (n_outer - 1) * outer + block(); }
+  bool operator==(const RowBytes& o) const {
+    return base == o.base && outer == o.outer && inner == o.inner && n_outer == o.n_outer && n_inner == o.n_inner &&
+           width == o.width;
+  }
+};
+
+// false: the tensor does not fit an address space.
+inline bool row_bytes(const void* p, int rows, int heads, int D, const int64_t strides[2], int size, RowBytes& r) {
+  const double extent = ((double)(rows - 1) * (double)strides[0] + (double)(heads - 1) * (double)strides[1] + D) * size;
+  if (!(extent < 4611686018427387904.0)) return false;                // 2^62
+  int64_t s[2] = {rows > 1 ? strides[0] * size : 0, heads > 1 ? strides[1] * size : 0};
+  const int big = s[1] > s[0];
+  r.base = (int64_t)reinterpret_cast<uintptr_t>(p);
+  r.outer = s[big], r.inner = s[!big];
+  r.n_outer = r.outer ? (big ? heads : rows) : 1, r.n_inner = r.inner ? (big ? rows : heads) : 1;
+  r.width = (int64_t)D * size;
+  return true;
+}
+
+inline int64_t gcd_of(int64_t a, int64_t b) {
+  while (b) {
+    const int64_t t = a % b;
+    a = b, b = t;
+  }
+  return a;
+}
+inline int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b < 0); }
+
+// Whether bytes [x, x + w) meet a run of b, whose runs are apart (rows_apart).
+inline bool run_meets(const RowBytes& b, int64_t x, int64_t w) {
+  x -= b.base;
+  int64_t lo = 0, hi = 0;                        // blocks that begin before x + w and end after x
+  if (b.n_outer > 1) {
+    lo = floor_div(x - b.block(), b.outer) + 1, hi = floor_div(x + w - 1, b.outer);
+    lo = lo < 0 ? 0 : lo, hi = hi > b.n_outer - 1 ? b.n_outer - 1 : hi;
+  }
+  for (int64_t i = lo; i <= hi; ++i) {
+    const int64_t y = x - i * b.outer;
+    int64_t first = 0, last = 0;                 // the same of the block's runs
+    if (b.n_inner > 1) {
+      first = floor_div(y - b.width, b.inner) + 1, last = floor_div(y + w - 1, b.inner);
+      first = first < 0 ? 0 : first, last = last > b.n_inner - 1 ? b.n_inner - 1 : last;
+    } else if (y + w <= 0 || y >= b.width) {
+      continue;
+    }
+    if (first <= last) return true;
+  }
+  return false;
+}
+
+// Whether a and b share a byte; b's runs are apart.  Most pairs are apart as a whole, or lie side
+// by side in each row (parts of one projection): a division then.  Others are looked through run
+// by run; of more than 2^20 runs without an answer it is yes.
+inline bool rows_meet(const RowBytes& a, const RowBytes& b) {
+  if (a.end() <= b.base || b.end() <= a.base) return false;
+  // places within a period of both: blocks of the outer strides, runs of all strides
+  const int64_t outer = gcd_of(a.outer, b.outer), all = gcd_of(outer, gcd_of(a.inner, b.inner));
+  if (outer) {
+    const int64_t at = b.base - a.base - floor_div(b.base - a.base, outer) * outer;
+    if (at >= a.block() && at + b.block() <= outer) return false;
+  }
+  if (all) {
+    const int64_t at = b.base - a.base - floor_div(b.base - a.base, all) * all;
+    if (at >= a.width && at + b.width <= all) return false;
+  }
+  RowBytes to = b;
+  int64_t blocks = a.n_outer;
+  if (a.outer == b.outer) {                      // only the distance of two blocks matters
+    to.base -= (a.n_outer - 1) * a.outer;
+    to.n_outer += a.n_outer - 1;
+    blocks = 1;
+  }
+  int64_t left = 1 << 20;
+  for (int64_t i = 0; i < blocks; ++i)
+    for (int64_t j = 0; j < a.n_inner; ++j)
+      if (left-- == 0 || run_meets(to, a.base + i * a.outer + j * a.inner, a.width)) return true;
+  return false;
+}
+
 // Row r, head h of a strided [rows, heads, D] tensor.
 struct Strides {
   int64_t row, head;

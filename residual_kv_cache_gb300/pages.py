@@ -129,8 +129,9 @@ def head_norm_rotate(q, k, positions, freq, q_weight=None, k_weight=None, eps=No
     the same type, then its rotation: pair j of the first 2 len(freq) values turns by
     positions[r] * freq[j] (int32 [rows]; float64 radians, see rotation_freq).  Pairs are values
     j and j + len(freq), or 2 j and 2 j + 1 where `adjacent`.  eps None leaves the norm out.
-    Returns (q, k) of the same type; q_out and k_out may be given (q and k themselves among
-    them, and bf16 for fp32 rows), and rows at negative positions are not written."""
+    Returns (q, k) of the same type; q_out and k_out may be given (q_out may be q itself, k_out
+    k, else they are apart from both inputs and from each other; bf16 for fp32 rows), and rows
+    at negative positions are not written."""
     return _ext().head_norm_rotate(q, k, positions, freq, q_weight, k_weight, eps, adjacent, q_out, k_out, stream)
 
 

@@ -56,3 +56,46 @@ def test_fork_whose_lengths_go_where_its_arguments_are(batch, width, shared, inp
         assert (want[1] == lens.tolist() and want[0] == table.tolist()) == bad
         for _ in range(20):
             assert [x.tolist() for x in call(True)] == want
+
+
+@cuda
+@pytest.mark.parametrize("n", [1, 7, 3000])
+@pytest.mark.parametrize("layout", ["parts of rows", "heads in turn", "rows in turn", "heads outer", "rows in turn, heads outer"])
+@pytest.mark.parametrize("inplace", [False, True])
+def test_head_rows_side_by_side_in_one_buffer(n, layout, inplace):
+    """Queries and keys that lie in one buffer without sharing a value, in every order of rows and
+    heads: the bits of buffers of their own."""
+    H, D = 3, 64
+    buf = torch.randn((6, n * H * D), generator=torch.Generator().manual_seed(n)).to(torch.bfloat16).cuda().view(-1)
+    view = lambda *s: buf[:int(np.prod(s))].view(*s)  # noqa: E731
+    if layout == "parts of rows":
+        b = view(n, 2 * H, D)
+        q, k = b[:, :H], b[:, H:]
+    elif layout == "heads in turn":
+        b = view(n, H, 2, D)
+        q, k = b[:, :, 0], b[:, :, 1]
+    elif layout == "rows in turn":
+        b = view(n, 2, H, D)
+        q, k = b[:, 0], b[:, 1]
+    elif layout == "heads outer":
+        b = view(2, H, n, D)
+        q, k = b[0].transpose(0, 1), b[1].transpose(0, 1)
+    else:
+        b = view(H, n, 2, D)
+        q, k = b[:, :, 0].transpose(0, 1), b[:, :, 1].transpose(0, 1)
+    pos, freq = torch.arange(n, dtype=torch.int32, device="cuda"), rkv.rotation_freq(D)
+    want = rkv.head_norm_rotate(q.contiguous(), k.contiguous(), pos, freq, eps=1e-6)
+    before = buf.clone()
+    if inplace:
+        qo, ko = q, k
+    else:
+        other = torch.zeros_like(buf)
+        qo, ko = (other.as_strided(x.shape, x.stride(), x.storage_offset()) for x in (q, k))
+    a, c = rkv.head_norm_rotate(q, k, pos, freq, eps=1e-6, q_out=qo, k_out=ko)
+    assert torch.equal(a, want[0]) and torch.equal(c, want[1])
+    assert inplace or torch.equal(buf, before)
+    # one for the other: read while it is written
+    if n > 1:
+        for bad in (dict(q_out=qo, k_out=qo), dict(q_out=k, k_out=ko), dict(q_out=q, k_out=q)):
+            with pytest.raises(rkv.RkvError, match="overlap"):
+                rkv.head_norm_rotate(q, k, pos, freq, eps=1e-6, **bad)

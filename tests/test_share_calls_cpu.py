@@ -1,0 +1,51 @@
+"""What the calls around the paged cache refuse because of what their buffers share, without a GPU."""
+import ctypes
+
+import pytest
+
+import residual_kv_cache_gb300 as rkv
+
+from test_share_cpu import A, Rows, S
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from residual_kv_cache_gb300 import build
+    build.build()
+    return rkv.lib()
+
+
+def refused(lib, status, text):
+    assert status == -1 and text in lib.rkv_last_error().decode(), (status, lib.rkv_last_error())
+
+
+def test_head_rows_that_overlap(lib):
+    """Outputs on each other or on an input that is not their own.  (1000 rows of 4 and of 2 heads
+    of 64 bf16 values, at addresses that are only looked at.)"""
+    far = 1 << 24
+
+    def call(**kw):
+        d = dict(q=A, k=A + far, q_out=A + 2 * far, k_out=A + 3 * far, q_strides=S(256, 64), k_strides=S(128, 64),
+                 q_out_strides=S(256, 64), k_out_strides=S(128, 64), q_weight=None, k_weight=None, positions=A, freq=A,
+                 n_rows=1000, n_q_heads=4, n_k_heads=2, head_dim=64, rotary_dim=64, adjacent=0, norm=0, dtype=1,
+                 out_dtype=1, eps=0.0)
+        return lib.rkv_head_norm_rotate(ctypes.byref(Rows(**{**d, **kw})), None)
+    both = "q_out and k_out overlap"
+    wide = dict(q_out_strides=S(512, 64), k_out_strides=S(512, 64))            # parts of rows of 512 values
+    apart = dict(q_out_strides=S(512, 128), k_out_strides=S(512, 128))         # heads with room between them
+    heads = dict(q_out_strides=S(64, 64000), k_out_strides=S(64, 64000))       # heads outermost
+    for bad in (dict(k_out=A + 2 * far), dict(k_out=A + 2 * far + 1000 * 512 - 16), dict(k_out=A + 2 * far - 256000 + 16),
+                dict(k_out=A + 2 * far + 3 * 128, **wide), dict(k_out=A + 2 * far - 2 * 128 + 16, **wide),
+                dict(k_out=A + 2 * far + 64, **apart), dict(k_out=A + 2 * far + 3 * 256 + 112, **apart),
+                dict(k_out=A + 2 * far + 999 * 128, **heads), dict(k_out=A + 2 * far, q_out_strides=S(64, 64000)),
+                dict(k_out=A + 2 * far + 16, n_rows=1)):
+        refused(lib, call(**bad), both)
+    own = "overlaps an input"
+    for bad in (dict(q_out=A + 512), dict(q_out=A, q_out_strides=S(512, 64)), dict(q_out=A + far),
+                dict(k_out=A + far + 128), dict(k_out=A + 512 * 999),
+                dict(q_out=A, k=A),                                                        # in place, and read as k
+                dict(q=A, q_out=A, dtype=0, q_strides=S(256, 64)),                         # bf16 over fp32
+                dict(q=A, q_out=A, q_strides=S(0, 64)),                                    # one row for all, and in place
+                dict(q=A + 128, q_out=A, q_strides=S(512, 64), q_out_strides=S(512, 64))):
+        refused(lib, call(**bad), own)
+    refused(lib, call(q_strides=S(1 << 60, 64)), "address space")
