@@ -682,7 +682,8 @@ rkv_status rkv_page_copy(const rkv_pages* layers, int32_t n_layers, const int32_
  * takes as k, v and cu_k).
  *   length (device, int32) [batch] or NULL (all): 0 leaves a sequence out.
  *   k, v (device, bf16) [max_rows, N, D], row r, head h at r * strides[0] + h * strides[1]
- *     elements, 16-byte aligned; rows must not overlap.  Rows past the total stay as they are.
+ *     elements, 16-byte aligned; no row of k or v may overlap another of either (RKV_EINVAL; the
+ *     two may be parts of one buffer).  Rows past the total stay as they are.
  *   cu_rows (device, int32) [batch + 1]: first row of each sequence, and the total.
  * A value is its code times its page's scale, which bf16 holds exactly (from 2^128 on it is
  * infinite).  Positions whose page is out of range give zero rows (RKV_FLAG_BAD_INDEX).  Where a

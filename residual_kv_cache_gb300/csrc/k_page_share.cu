@@ -904,6 +904,11 @@ extern "C" rkv_status rkv_page_gather(const rkv_pages* pages, const rkv_page_tab
   if (max_rows > 0 && (!rows_apart(max_rows, pages->n_kv_heads, pages->head_dim, k_strides) ||
                        !rows_apart(max_rows, pages->n_kv_heads, pages->head_dim, v_strides)))
     return fail_with(RKV_EINVAL, "rows of k or v overlap");
+  RowBytes kb, vb;
+  if (max_rows > 0 && (!row_bytes(k, max_rows, pages->n_kv_heads, pages->head_dim, k_strides, 2, kb) ||
+                       !row_bytes(v, max_rows, pages->n_kv_heads, pages->head_dim, v_strides, 2, vb)))
+    return fail_with(RKV_EINVAL, "strides pass the address space");
+  if (max_rows > 0 && rows_meet(kb, vb)) return fail_with(RKV_EINVAL, "k and v overlap");
   GatherArgs a;
   a.codes[0] = static_cast<const uint8_t*>(pages->k), a.codes[1] = static_cast<const uint8_t*>(pages->v);
   a.scale[0] = pages->k_scale, a.scale[1] = pages->v_scale;

@@ -178,8 +178,8 @@ def page_copy(caches, src, dst, rows=None, count=None, flags=None, stream=None):
 def page_gather(k8, v8, k_scale, v_scale, block_table, seq_len, max_rows=None, length=None, k_out=None, v_out=None,
                 flags=None, stream=None):
     """The first length[b] (int32 [batch]; None: all) stored positions of each sequence as packed
-    rows: (k, v, cu_rows) with k, v [max_rows, N, D] bf16 (k_out and v_out, if given, whose
-    rows max_rows is by default) and int32 cu_rows [batch + 1].  Rows past cu_rows[-1] are not
+    rows: (k, v, cu_rows) with k, v [max_rows, N, D] bf16 (k_out and v_out, if given, which must
+    not overlap and whose rows max_rows is by default) and int32 cu_rows [batch + 1].  Rows past cu_rows[-1] are not
     written.  More than max_rows rows: none, cu_rows all 0 and FLAG_NO_SPACE in `flags`."""
     return _ext().page_gather(k8, v8, k_scale, v_scale, block_table, seq_len, max_rows, length, k_out, v_out, flags,
                               stream)

@@ -99,3 +99,34 @@ def test_head_rows_side_by_side_in_one_buffer(n, layout, inplace):
         for bad in (dict(q_out=qo, k_out=qo), dict(q_out=k, k_out=ko), dict(q_out=q, k_out=q)):
             with pytest.raises(rkv.RkvError, match="overlap"):
                 rkv.head_norm_rotate(q, k, pos, freq, eps=1e-6, **bad)
+
+
+@cuda
+@pytest.mark.parametrize("layout", ["parts of rows", "heads in turn", "rows in turn", "heads outer"])
+def test_gather_into_one_buffer(layout):
+    N, D, P, lens = 3, 64, 16, [37, 0, 50]
+    table, _, _, _ = rows_of_pages(3, 4, P, 1)
+    table[:] = np.arange(12).reshape(3, 4)
+    g = torch.Generator().manual_seed(1)
+    k8, v8 = torch.randint(0, 127, (2, 12, N, P, D), generator=g, dtype=torch.uint8).cuda()
+    ks, vs = torch.exp2(torch.randint(-9, 9, (2, 12, N), generator=g).float()).cuda()
+    n = sum(lens)
+    call = lambda **kw: rkv.page_gather(k8, v8, ks, vs, i32(table), i32(lens), **kw)  # noqa: E731
+    want = call(max_rows=n)
+    buf = lambda *s: torch.full(s, 7, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    if layout == "parts of rows":
+        b = buf(n, 2 * N, D)
+        k, v = b[:, :N], b[:, N:]
+    elif layout == "heads in turn":
+        b = buf(n, N, 2, D)
+        k, v = b[:, :, 0], b[:, :, 1]
+    elif layout == "rows in turn":
+        b = buf(n, 2, N, D)
+        k, v = b[:, 0], b[:, 1]
+    else:
+        b = buf(2, N, n, D)
+        k, v = b[0].transpose(0, 1), b[1].transpose(0, 1)
+    got = call(k_out=k, v_out=v)
+    assert got[0] is k and got[1] is v and all(torch.equal(x, y) for x, y in zip(got, want))
+    with pytest.raises(rkv.RkvError, match="k and v overlap"):
+        call(k_out=k, v_out=k)

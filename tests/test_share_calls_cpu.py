@@ -5,7 +5,7 @@ import pytest
 
 import residual_kv_cache_gb300 as rkv
 
-from test_share_cpu import A, Rows, S
+from test_share_cpu import A, Rows, S, pages, table
 
 
 @pytest.fixture(scope="module")
@@ -49,3 +49,16 @@ def test_head_rows_that_overlap(lib):
                 dict(q=A + 128, q_out=A, q_strides=S(512, 64), q_out_strides=S(512, 64))):
         refused(lib, call(**bad), own)
     refused(lib, call(q_strides=S(1 << 60, 64)), "address space")
+
+
+def test_gathered_rows_that_overlap(lib):
+    """(1000 rows of 8 heads of 128, at addresses that are only looked at.)"""
+    far = 1 << 24
+
+    def call(k=A, ks=S(1024, 128), v=A + far, vs=S(1024, 128), rows=1000):
+        return lib.rkv_page_gather(ctypes.byref(pages()), table(), None, k, ks, v, vs, rows, A, None, None)
+    for bad in (dict(v=A), dict(v=A + 1000 * 2048 - 16), dict(v=A - 1000 * 2048 + 16), dict(v=A + 2032, rows=1),
+                dict(ks=S(2048, 128), v=A + 7 * 256, vs=S(2048, 128)), dict(ks=S(128, 128000), v=A + 999 * 256, vs=S(128, 128000)),
+                dict(ks=S(2048, 256), v=A + 128, vs=S(2048, 256)), dict(ks=S(128, 128000))):
+        refused(lib, call(**{**dict(v=A), **bad}), "k and v overlap")
+    refused(lib, call(ks=S(1 << 60, 128)), "address space")
