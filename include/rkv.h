@@ -609,8 +609,9 @@ rkv_status rkv_head_norm_rotate(const rkv_head_rows* rows, void* stream);
  *   table: block_table and seq_len before the call.
  *   block_table_out (device, int32) [batch, max_blocks], seq_len_out (device) [batch], n_free_out
  *     (device) [1]: after it.  They may be the table's own and n_free (update in place), and
- *     seq_len_out may be source, length or finished.  Entries past a row's pages are -1 in
- *     another table; in place, where the row had pages before.
+ *     seq_len_out may be source, length or finished.  A table or lengths that overlap the
+ *     table's own and are not they are refused.  Entries past a row's pages are -1 in another
+ *     table; in place, where the row had pages before.
  *   free_blocks, n_free: the free list.  Pages that no row holds any more are put on its end, in
  *     order of their first row and position; then the copies' pages are taken from its end, in
  *     order of the rows.  The first n_free entries stay as they are.
@@ -643,7 +644,8 @@ rkv_status rkv_page_fork_workspace(const rkv_page_table* table, int32_t num_bloc
  * the pool's end is free.  The i-th held page from n_live on (ascending) goes to the i-th number
  * below n_live that no row holds.
  *   table: read; block_table_out (device, int32) [batch, max_blocks] receives the new ids and may
- *     be the table's own; entries past a row's pages are -1 in another table.
+ *     be the table's own (another that overlaps it is refused); entries past a row's pages are
+ *     -1 in another table.
  *   free_blocks, n_free: receive num_blocks - n_live pages, the last one first (a plan takes
  *     n_live first).  What the list held before is not read: pages that were lost are free again.
  *   src, dst (device, int32) [num_blocks / 2], count (device, int32) [1]: the moves, -1 past them;

@@ -797,6 +797,10 @@ extern "C" rkv_status rkv_page_fork(const rkv_page_table* table, const int32_t* 
   if (rkv_status st = check_fork_table(table, num_blocks, block_tokens)) return st;
   if (!free_blocks || !n_free || !block_table_out || !seq_len_out || !n_free_out || !copy_src || !copy_dst || !copy_rows)
     return fail_with(RKV_EINVAL, "NULL pointer");
+  const int64_t entries = (int64_t)table->batch * table->max_blocks;
+  if (half_shared(block_table_out, entries, table->block_table, entries) ||
+      half_shared(seq_len_out, table->batch, table->seq_len, table->batch))
+    return fail_with(RKV_EINVAL, "block_table_out or seq_len_out overlaps the table's and is not it");
   if (rkv_status st = check_workspace(workspace, workspace_bytes, fork_bytes(table, num_blocks))) return st;
   ForkArgs a;
   a.source = source, a.length = length, a.finished = finished;
@@ -836,6 +840,9 @@ extern "C" rkv_status rkv_page_compact(const rkv_page_table* table, int32_t* fre
   if (rkv_status st = check_fork_table(table, num_blocks, block_tokens)) return st;
   if (!free_blocks || !n_free || !block_table_out || !count || (num_blocks > 1 && (!src || !dst)))
     return fail_with(RKV_EINVAL, "NULL pointer");
+  const int64_t entries = (int64_t)table->batch * table->max_blocks;
+  if (half_shared(block_table_out, entries, table->block_table, entries))
+    return fail_with(RKV_EINVAL, "block_table_out overlaps the table's and is not it");
   if (rkv_status st = check_workspace(workspace, workspace_bytes, compact_bytes(num_blocks))) return st;
   CompactArgs a;
   a.table = table->block_table, a.seq_len = table->seq_len, a.table_out = block_table_out;

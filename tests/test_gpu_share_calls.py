@@ -130,3 +130,27 @@ def test_gather_into_one_buffer(layout):
     assert got[0] is k and got[1] is v and all(torch.equal(x, y) for x, y in zip(got, want))
     with pytest.raises(rkv.RkvError, match="k and v overlap"):
         call(k_out=k, v_out=k)
+
+
+@cuda
+def test_tables_that_overlap_without_being_one():
+    """A table that lies a row further in the same buffer is refused; one right behind the other is
+    another table, in one buffer or not."""
+    table, lens, free, nf = rows_of_pages(6, 4, 16, 3)
+    source = [1, 2, 3, 4, 5, -1]
+
+    def call(at):
+        buf = torch.full((12, 4), -9, dtype=torch.int32, device="cuda")
+        buf[:6] = i32(table)
+        ln, f, n = i32(lens), i32(free), i32([nf])
+        rkv.page_fork(i32(source), ln, buf[:6], f, n, 16, block_table_out=buf[at:at + 6])
+        c = rkv.page_compact(ln, buf[at:at + 6], f, n, 16)
+        return buf[at:at + 6].tolist(), ln.tolist(), f[:n.item()].tolist(), c.count.item()
+    want = call(6)
+    assert call(0) == want
+    t = torch.full((12, 4), -1, dtype=torch.int32, device="cuda")
+    for at in (1, 5):
+        with pytest.raises(rkv.RkvError, match="overlaps"):
+            call(at)
+        with pytest.raises(rkv.RkvError, match="overlaps"):
+            rkv.page_compact(i32(lens), t[:6], i32(free), i32([nf]), 16, block_table_out=t[at:at + 6])

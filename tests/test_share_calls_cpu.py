@@ -62,3 +62,16 @@ def test_gathered_rows_that_overlap(lib):
                 dict(ks=S(2048, 256), v=A + 128, vs=S(2048, 256)), dict(ks=S(128, 128000))):
         refused(lib, call(**{**dict(v=A), **bad}), "k and v overlap")
     refused(lib, call(ks=S(1 << 60, 128)), "address space")
+
+
+def test_tables_that_overlap_without_being_one(lib):
+    """Entries would be read after others were written over them: 4 rows of 50, at A."""
+    n, m, more = ctypes.c_size_t(), ctypes.c_size_t(), 1 << 16
+    lib.rkv_page_fork_workspace(table(), 100, 64, ctypes.byref(n))
+    lib.rkv_page_compact_workspace(100, ctypes.byref(m))
+    t = table(seq_len=A + more)
+    for out, lens in ((A + 4, A + more), (A - 4, A + more), (A + 199 * 4, A + more), (A, A + more + 4), (A, A + more - 12)):
+        refused(lib, lib.rkv_page_fork(t, None, None, None, A, A, 100, 64, out, lens, A, A, A, A, A, n.value, None, None),
+                "overlaps the table's")
+    for out in (A + 4, A - 4, A + 199 * 4, A - 199 * 4):
+        refused(lib, lib.rkv_page_compact(t, A, A, 100, 64, out, A, A, A, A, m.value, None, None), "overlaps the table's")
