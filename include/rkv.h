@@ -686,7 +686,8 @@ rkv_status rkv_page_copy(const rkv_pages* layers, int32_t n_layers, const int32_
  *   k, v (device, bf16) [max_rows, N, D], row r, head h at r * strides[0] + h * strides[1]
  *     elements, 16-byte aligned; no row of k or v may overlap another of either (RKV_EINVAL; the
  *     two may be parts of one buffer).  Rows past the total stay as they are.
- *   cu_rows (device, int32) [batch + 1]: first row of each sequence, and the total.
+ *   cu_rows (device, int32) [batch + 1]: first row of each sequence, and the total; apart from
+ *     seq_len and length (RKV_EINVAL).
  * A value is its code times its page's scale, which bf16 holds exactly (from 2^128 on it is
  * infinite).  Positions whose page is out of range give zero rows (RKV_FLAG_BAD_INDEX).  Where a
  * length is negative, above seq_len or past the table (RKV_FLAG_BAD_INDEX), or the rows pass

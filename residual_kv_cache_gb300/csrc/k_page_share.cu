@@ -916,6 +916,10 @@ extern "C" rkv_status rkv_page_gather(const rkv_pages* pages, const rkv_page_tab
                        !row_bytes(v, max_rows, pages->n_kv_heads, pages->head_dim, v_strides, 2, vb)))
     return fail_with(RKV_EINVAL, "strides pass the address space");
   if (max_rows > 0 && rows_meet(kb, vb)) return fail_with(RKV_EINVAL, "k and v overlap");
+  // (every block reads the lengths, one writes cu_rows)
+  if (shared(cu_rows, (int64_t)table->batch + 1, table->seq_len, table->batch) ||
+      (length && shared(cu_rows, (int64_t)table->batch + 1, length, table->batch)))
+    return fail_with(RKV_EINVAL, "cu_rows overlaps seq_len or length");
   GatherArgs a;
   a.codes[0] = static_cast<const uint8_t*>(pages->k), a.codes[1] = static_cast<const uint8_t*>(pages->v);
   a.scale[0] = pages->k_scale, a.scale[1] = pages->v_scale;

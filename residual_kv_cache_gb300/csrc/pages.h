@@ -44,10 +44,13 @@ inline bool rows_apart(int rows, int heads, int D, const int64_t strides[2]) {
          (rows1 || heads1 || row >= (heads - 1) * head + Dl || head >= (rows - 1) * row + Dl);
 }
 
-// Whether two int32 arrays share memory without being the same one.
-inline bool half_shared(const int32_t* p, int64_t np, const int32_t* q, int64_t nq) {
+// Whether two int32 arrays share memory, and whether they do without being the same one.
+inline bool shared(const int32_t* p, int64_t np, const int32_t* q, int64_t nq) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return a != b && a < b + 4 * (uint64_t)nq && b < a + 4 * (uint64_t)np;
+  return a < b + 4 * (uint64_t)nq && b < a + 4 * (uint64_t)np;
+}
+inline bool half_shared(const int32_t* p, int64_t np, const int32_t* q, int64_t nq) {
+  return p != q && shared(p, np, q, nq);
 }
 
 // The bytes of a strided [rows, heads, D] tensor: n_outer blocks of n_inner runs of `width` bytes.

@@ -75,3 +75,10 @@ def test_tables_that_overlap_without_being_one(lib):
                 "overlaps the table's")
     for out in (A + 4, A - 4, A + 199 * 4, A - 199 * 4):
         refused(lib, lib.rkv_page_compact(t, A, A, 100, 64, out, A, A, A, A, m.value, None, None), "overlaps the table's")
+
+
+def test_gathered_offsets_on_the_lengths(lib):
+    far = 1 << 24
+    for lens, length, cu in ((A, None, A), (A, None, A - 16), (A, None, A + 12), (A, A + far, A + far), (A, A + far, A + far - 4)):
+        refused(lib, lib.rkv_page_gather(ctypes.byref(pages()), table(seq_len=lens), length, A + 2 * far, S(1024, 128),
+                                         A + 3 * far, S(1024, 128), 9, cu, None, None), "cu_rows overlaps")
