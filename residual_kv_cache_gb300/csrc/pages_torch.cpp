@@ -475,24 +475,32 @@ inline void* one_of(PyObject* o, const char* what, at::IntArrayRef shape, int de
 //  dst, rows, count, flags, stream)
 PyObject* page_copy(PyObject* const* a) {
   if (!PyList_Check(a[0]) && !PyTuple_Check(a[0])) throw Refused("caches must be a list or tuple");
-  const Py_ssize_t layers = PySequence_Fast_GET_SIZE(a[0]);
+  // arrays() may be any code: what it makes and the caches themselves live until the launch, whatever
+  // becomes of the list meanwhile
+  struct Held {
+    PyObject* o[1 + 128];
+    int n = 0;
+    PyObject* add(PyObject* x) { return o[n++] = x; }
+    ~Held() {
+      while (n) Py_DECREF(o[--n]);
+    }
+  } held;
+  PyObject* all = PySequence_Tuple(a[0]);
+  if (!all) throw PythonError();
+  held.add(all);
+  const Py_ssize_t layers = PyTuple_GET_SIZE(all);
   if (layers < 1 || layers > 128) throw Refused("caches must be 1 to 128");
   rkv_pages pg[128];
   int dev = 0;
   for (Py_ssize_t i = 0; i < layers; ++i) {
-    PyObject* l = PySequence_Fast_GET_ITEM(a[0], i);
-    // a tuple that arrays() makes; its tensors are the object's, which outlives the call
+    PyObject* l = PyTuple_GET_ITEM(all, i);
     PyObject* made = PyTuple_Check(l) ? nullptr : PyObject_CallMethod(l, "arrays", nullptr);
     if (made) {
-      l = made;
+      l = held.add(made);
     } else if (PyErr_Occurred()) {
       if (!PyErr_ExceptionMatches(PyExc_AttributeError)) throw PythonError();
       PyErr_Clear();
     }
-    struct Drop {
-      PyObject* o;
-      ~Drop() { Py_XDECREF(o); }
-    } drop{made};
     if (!PyTuple_Check(l) || PyTuple_GET_SIZE(l) != 4) throw Refused("a cache must be (k8, v8, k_scale, v_scale)");
     PyObject* const* t = &PyTuple_GET_ITEM(l, 0);
     if (i == 0) {

@@ -1,5 +1,7 @@
 """GPU calls of the operators around the paged cache whose buffers share memory, and those that the
 library's own loop makes seldom: each against the same call on buffers of its own."""
+import weakref
+
 import numpy as np
 import pytest
 import torch
@@ -154,3 +156,35 @@ def test_tables_that_overlap_without_being_one():
             call(at)
         with pytest.raises(rkv.RkvError, match="overlaps"):
             rkv.page_compact(i32(lens), t[:6], i32(free), i32([nf]), 16, block_table_out=t[at:at + 6])
+
+
+@cuda
+def test_copy_keeps_its_caches_until_the_launch():
+    """arrays() of a cache that makes its tensors, and that empties the list: all caches are copied,
+    and what was made lives until then."""
+    k8 = torch.randint(0, 127, (3, 4, 1, 16, 64), generator=torch.Generator().manual_seed(1), dtype=torch.uint8).cuda()
+    ks = torch.arange(12.0, device="cuda").view(3, 4, 1)
+    seen = []
+
+    class Cache:
+        def __init__(self, layer):
+            self.layer = layer
+
+        def arrays(self):
+            caches.clear()
+            assert all(ref() is not None for ref in seen)
+            made = tuple(x[self.layer].view(x[self.layer].shape) for x in (k8, k8, ks, ks))
+            seen.extend(weakref.ref(x) for x in made)
+            return made
+    caches = [Cache(layer) for layer in range(3)]
+    rkv.page_copy(caches, i32([1]), i32([3]))
+    assert caches == [] and len(seen) == 12 and all(ref() is None for ref in seen)
+    assert torch.equal(k8[:, 3], k8[:, 1]) and ks[:, 3].flatten().tolist() == [1, 5, 9]
+
+    seen.clear()
+
+    class Fails:
+        def arrays(self):
+            raise KeyError("no arrays")
+    with pytest.raises(KeyError):
+        rkv.page_copy([Cache(0), Fails()], i32([1]), i32([3]))
