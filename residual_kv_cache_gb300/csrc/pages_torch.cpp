@@ -490,11 +490,14 @@ PyObject* page_copy(PyObject* const* a) {
   held.add(all);
   const Py_ssize_t layers = PyTuple_GET_SIZE(all);
   if (layers < 1 || layers > 128) throw Refused("caches must be 1 to 128");
+  // (made once: a call's host time is mostly this loop's)
+  static PyObject* const arrays = PyUnicode_InternFromString("arrays");
+  if (!arrays) throw PythonError();
   rkv_pages pg[128];
   int dev = 0;
   for (Py_ssize_t i = 0; i < layers; ++i) {
     PyObject* l = PyTuple_GET_ITEM(all, i);
-    PyObject* made = PyTuple_Check(l) ? nullptr : PyObject_CallMethod(l, "arrays", nullptr);
+    PyObject* made = PyTuple_Check(l) ? nullptr : PyObject_CallMethodNoArgs(l, arrays);
     if (made) {
       l = held.add(made);
     } else if (PyErr_Occurred()) {
