@@ -32,6 +32,7 @@ differentiable: results carry no gradient.
 from __future__ import annotations
 
 import importlib
+import math
 import os
 from typing import NamedTuple
 
@@ -118,6 +119,10 @@ def prompt_attention(q, k, v, cu_q, cu_k=None, scale=None, out=None, lse=None, f
 def rotation_freq(rotary_dim: int, base: float = 10000.0, device=None):
     """base^(-2 j / rotary_dim) radians a position, j < rotary_dim / 2, as head_norm_rotate takes
     them (float64; the codec's restore rotates K by the same angles)."""
+    if rotary_dim < 0 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even and >= 0")
+    if not 0 < base < math.inf:
+        raise ValueError("base must be finite and > 0")
     j = torch.arange(0, rotary_dim, 2, dtype=torch.float64)
     return torch.pow(torch.tensor(base, dtype=torch.float64), -j / max(1, rotary_dim)).to(device or "cuda")
 

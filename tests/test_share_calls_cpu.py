@@ -1,5 +1,6 @@
 """What the calls around the paged cache refuse because of what their buffers share, without a GPU."""
 import ctypes
+import math
 
 import pytest
 
@@ -82,3 +83,14 @@ def test_gathered_offsets_on_the_lengths(lib):
     for lens, length, cu in ((A, None, A), (A, None, A - 16), (A, None, A + 12), (A, A + far, A + far), (A, A + far, A + far - 4)):
         refused(lib, lib.rkv_page_gather(ctypes.byref(pages()), table(seq_len=lens), length, A + 2 * far, S(1024, 128),
                                          A + 3 * far, S(1024, 128), 9, cu, None, None), "cu_rows overlaps")
+
+
+def test_rotation_freq_refusals():
+    """15 values are no pairs (they made the frequencies of 8), and powers of these are not."""
+    for dim in (15, 1, -2):
+        with pytest.raises(ValueError, match="rotary_dim"):
+            rkv.rotation_freq(dim, device="cpu")
+    for base in (0.0, -1e4, math.inf, math.nan):
+        with pytest.raises(ValueError, match="base"):
+            rkv.rotation_freq(16, base, device="cpu")
+    assert rkv.rotation_freq(2, 5e5, device="cpu").tolist() == [1.0]
