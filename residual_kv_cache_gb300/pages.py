@@ -124,7 +124,7 @@ def rotation_freq(rotary_dim: int, base: float = 10000.0, device=None):
     if not 0 < base < math.inf:
         raise ValueError("base must be finite and > 0")
     j = torch.arange(0, rotary_dim, 2, dtype=torch.float64)
-    return torch.pow(torch.tensor(base, dtype=torch.float64), -j / max(1, rotary_dim)).to(device or "cuda")
+    return torch.pow(torch.tensor(base, dtype=torch.float64), -j / max(1, rotary_dim)).to("cuda" if device is None else device)
 
 
 def head_norm_rotate(q, k, positions, freq, q_weight=None, k_weight=None, eps=None, adjacent: bool = False,
@@ -197,7 +197,7 @@ class PageTable:
 
     def __init__(self, batch: int, max_blocks: int, num_blocks: int, block_tokens: int = 64, device=None,
                  sharing: bool = False):
-        dev = torch.device(device or "cuda")
+        dev = torch.device("cuda" if device is None else device)
         self.block_tokens = block_tokens
         self.sharing = sharing
         self.block_table = torch.full((batch, max_blocks), -1, dtype=torch.int32, device=dev)
@@ -239,7 +239,7 @@ class PagedCache:
     """One layer's K/V rows in 8-bit pages."""
 
     def __init__(self, n_kv_heads: int, head_dim: int, num_blocks: int, block_tokens: int = 64, device=None):
-        dev = torch.device(device or "cuda")
+        dev = torch.device("cuda" if device is None else device)
         shape = (num_blocks, n_kv_heads, block_tokens, head_dim)
         self.k8 = torch.empty(shape, dtype=torch.uint8, device=dev)
         self.v8 = torch.empty(shape, dtype=torch.uint8, device=dev)

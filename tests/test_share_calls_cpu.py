@@ -3,6 +3,7 @@ import ctypes
 import math
 
 import pytest
+import torch
 
 import residual_kv_cache_gb300 as rkv
 
@@ -94,3 +95,15 @@ def test_rotation_freq_refusals():
         with pytest.raises(ValueError, match="base"):
             rkv.rotation_freq(16, base, device="cpu")
     assert rkv.rotation_freq(2, 5e5, device="cpu").tolist() == [1.0]
+
+
+def test_device_zero_is_not_the_current_one(monkeypatch):
+    seen = []
+    for name in ("full", "zeros", "empty", "arange"):
+        make = getattr(torch, name)
+        monkeypatch.setattr(torch, name, lambda *a, _make=make, device=None, **kw: seen.append(device) or _make(*a, **kw))
+    monkeypatch.setattr(torch.Tensor, "to", lambda t, where: seen.append(torch.device(where)) or t)
+    rkv.PageTable(2, 3, 4, 16, device=0)
+    rkv.PagedCache(2, 64, 4, 16, device=0)
+    rkv.rotation_freq(16, device=0)
+    assert len(seen) > 9 and {x for x in seen if x is not None} == {torch.device("cuda", 0)}
