@@ -619,12 +619,14 @@ rkv_status rkv_head_norm_rotate(const rkv_head_rows* rows, void* stream);
  *     where it needs none.
  *   workspace (device, 16-byte aligned): rkv_page_fork_workspace bytes, this call's alone while
  *     it runs; needs no initialisation.
- * All or nothing: where a source is past the table, a length is out of range or above its
- * source's (RKV_FLAG_BAD_INDEX), or the list would overflow or the copies' pages run out
- * (RKV_FLAG_NO_SPACE), everything stays (other outputs than in place receive it as it was) and
- * there are no copies.  Entries of the table that are no page are kept as they are and never reach
- * the list, and one of the list that is taken for a copy is handed out as it is
+ * All or nothing: where a source is past the table, a length (of any row, finished or not: what
+ * a row of unknown length holds cannot be told from what is free) or n_free is out of range, or
+ * a length above its source's (RKV_FLAG_BAD_INDEX), or the list would overflow or the copies'
+ * pages run out (RKV_FLAG_NO_SPACE), everything stays (other outputs than in place receive it as
+ * it was) and there are no copies.  Entries of the table that are no page are kept as they are and
+ * never reach the list, and one of the list that is taken for a copy is handed out as it is
  * (RKV_FLAG_BAD_INDEX).
+ * Outputs must not overlap each other or the inputs, but for those named.
  * batch * max_blocks below 2^31.
  * Errors (nothing launched): RKV_EINVAL, RKV_EALIGN, RKV_ECAPACITY (workspace), RKV_ECUDA.
  */
@@ -652,7 +654,8 @@ rkv_status rkv_page_fork_workspace(const rkv_page_table* table, int32_t num_bloc
  *     rkv_page_copy has to follow in every layer before anything reads the pages.
  *   workspace (device, 16-byte aligned): rkv_page_compact_workspace bytes, this call's alone
  *     while it runs; needs no initialisation.
- * Where a length is out of range, nothing moves, list and count stay (RKV_FLAG_BAD_INDEX).
+ * Where a length is out of range, nothing moves, list and n_free stay (RKV_FLAG_BAD_INDEX).
+ * Outputs must not overlap each other or the inputs, but for that named.
  * Entries that are no page are left as they are (RKV_FLAG_BAD_INDEX).
  * Errors (nothing launched): RKV_EINVAL, RKV_EALIGN, RKV_ECAPACITY (workspace), RKV_ECUDA.
  */

@@ -212,7 +212,9 @@ class PageTable:
                          self.block_tokens, max_rows, flags=self.flags, stream=stream)
 
     def release(self, finished, stream=None):
-        """Give back the pages of the sequences marked in `finished` (int32 [batch])."""
+        """Give back the pages of the sequences marked in `finished` (int32 [batch]).  With `sharing`
+        all or nothing, as page_fork: a length out of range in any row, finished or not, leaves the
+        table as it is (FLAG_BAD_INDEX), since the pages which that row holds are not known."""
         if self.sharing:                             # (a release shortens no row: there are no copies)
             page_fork(None, self.seq_len, self.block_table, self.free_blocks, self.n_free, self.block_tokens,
                       finished=finished, flags=self.flags, stream=stream)

@@ -188,3 +188,22 @@ def test_copy_keeps_its_caches_until_the_launch():
             raise KeyError("no arrays")
     with pytest.raises(KeyError):
         rkv.page_copy([Cache(0), Fails()], i32([1]), i32([3]))
+
+
+@cuda
+@pytest.mark.parametrize("batch", [5, 300])
+def test_release_of_a_sharing_table_with_a_bad_length_is_refused_until_it_is_mended(batch):
+    table, lens, free, nf = rows_of_pages(batch, 40, 16, 9)
+    pt = rkv.PageTable(batch, 40, len(free), 16, sharing=True)
+    for x, y in ((pt.block_table, table), (pt.seq_len, lens), (pt.free_blocks, free), (pt.n_free, [nf])):
+        x.copy_(i32(y))
+    pt.seq_len[2] = 40 * 16 + 1                                # a row that does not finish
+    before = [x.clone() for x in (pt.block_table, pt.seq_len, pt.free_blocks, pt.n_free)]
+    fin = i32([b != 2 for b in range(batch)])
+    pt.release(fin)
+    assert pt.flags.item() == rkv.FLAG_BAD_INDEX
+    assert all(torch.equal(x, y) for x, y in zip(before, (pt.block_table, pt.seq_len, pt.free_blocks, pt.n_free)))
+    pt.seq_len[2], pt.flags[0] = int(lens[2]), 0
+    pt.release(fin)
+    assert pt.flags.item() == 0 and pt.seq_len.tolist() == [int(lens[2]) if b == 2 else 0 for b in range(batch)]
+    assert pt.n_free.item() == len(free) - -(-int(lens[2]) // 16)
