@@ -563,7 +563,7 @@ rkv_status rkv_prompt_attention_workspace(const rkv_prompt* prompt, size_t* byte
  *     beside that its rows must not overlap one another, the other output's or an input's
  *     (RKV_EINVAL; parts of one buffer that lie side by side in each row are apart).  Either
  *     head count may be 0 (its pointers are not looked at).
- *   q_weight, k_weight (device, dtype) [D] or NULL (all 1).
+ *   q_weight, k_weight (device, dtype, 4-byte aligned) [D] or NULL (all 1).
  *   positions (device, int32) [n_rows]; rows at negative ones are left as they are in the
  *     outputs (row_pos of rkv_page_plan is -1 past a step's rows).
  *   freq (device, binary64) [rotary_dim / 2]: radians a position.

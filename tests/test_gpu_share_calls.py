@@ -207,3 +207,14 @@ def test_release_of_a_sharing_table_with_a_bad_length_is_refused_until_it_is_men
     pt.release(fin)
     assert pt.flags.item() == 0 and pt.seq_len.tolist() == [int(lens[2]) if b == 2 else 0 for b in range(batch)]
     assert pt.n_free.item() == len(free) - -(-int(lens[2]) // 16)
+
+
+@cuda
+def test_weights_that_do_not_start_on_four_bytes_are_refused():
+    q, pos, freq = torch.ones((4, 2, 64), dtype=torch.bfloat16, device="cuda"), i32([0, 1, 2, 3]), rkv.rotation_freq(64)
+    packed = torch.randn(129, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    with pytest.raises(rkv.RkvError, match="weights 4-byte"):
+        rkv.head_norm_rotate(q, None, pos, freq, q_weight=packed[65:], eps=1e-6)
+    a, _ = rkv.head_norm_rotate(q, None, pos, freq, q_weight=packed[64:128], eps=1e-6)
+    b, _ = rkv.head_norm_rotate(q, None, pos, freq, q_weight=packed[64:128].clone(), eps=1e-6)
+    assert torch.equal(a, b)
