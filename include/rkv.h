@@ -566,11 +566,12 @@ rkv_status rkv_prompt_attention_workspace(const rkv_prompt* prompt, size_t* byte
  *   q_weight, k_weight (device, dtype, 4-byte aligned) [D] or NULL (all 1).
  *   positions (device, int32) [n_rows]; rows at negative ones are left as they are in the
  *     outputs (row_pos of rkv_page_plan is -1 past a step's rows).
- *   freq (device, binary64) [rotary_dim / 2]: radians a position.
+ *   freq (device, binary64) [rotary_dim / 2]: radians a position, finite.
  *   head_dim 64 or 128; rotary_dim a multiple of 16 from 0 (no rotation) to head_dim; n_rows at
  *   most 2^30; eps in [1e-30, 1e30].
- * Sums and products are fp32 with one rounding to out_dtype at the end; the angle is kept to
- * 2^-32 of a turn, beside the 2^-54 of freq[j] in it for each position.
+ * Sums and products are fp32 with one rounding to out_dtype at the end.  The angle is reduced to
+ * a turn with an error of 2^-32 of one, beside 1.5 2^-53 of positions[r] * freq[j] (the frequency
+ * in turns), and then rounded to fp32: up to 2^-26 of a turn near half of one.
  * Errors (nothing launched): RKV_EINVAL, RKV_EALIGN, RKV_ECUDA.
  */
 typedef struct {

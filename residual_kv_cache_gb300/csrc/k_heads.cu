@@ -6,7 +6,8 @@
 // The angle of a far position needs more bits than fp32 has, and only its place within a turn
 // matters: freq_j / 2 pi is kept as a 64-bit binary fraction of a turn, an integer product with
 // the position drops the whole turns by overflow, and the upper 32 bits, taken as a signed
-// number, are the angle in (-pi, pi] to 2^-32 of a turn.
+// number, are the angle in [-pi, pi) to 2^-32 of a turn.  fp32 takes them to 24 bits, up to
+// 2^-26 of a turn (1.6 2^-24 radians) near half of one, next to the sine's and cosine's 2 ulp.
 //
 // Bandwidth bounds many rows, one chain of loads few (16 rows of 40 heads of 128 2.9 us).  A warp
 // takes a row: the sines are found once for its heads, a part of them in each lane.  The next

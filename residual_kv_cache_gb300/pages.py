@@ -131,9 +131,10 @@ def head_norm_rotate(q, k, positions, freq, q_weight=None, k_weight=None, eps=No
                      q_out=None, k_out=None, stream=None):
     """Root-mean-square norm of each head of q [rows, n_q_heads, D] and k [rows, N, D] (both bf16
     or both fp32, strided rows allowed; either may be None), times q_weight and k_weight [D] of
-    the same type (that start on 4 bytes: a bf16 slice from an even element on), then its rotation: pair j of the first 2 len(freq) values turns by
-    positions[r] * freq[j] (int32 [rows]; float64 radians, see rotation_freq).  Pairs are values
-    j and j + len(freq), or 2 j and 2 j + 1 where `adjacent`.  eps None leaves the norm out.
+    the same type (that start on 4 bytes: a bf16 slice from an even element on), then its
+    rotation: pair j of the first 2 len(freq) values turns by positions[r] * freq[j] (int32
+    [rows]; float64 radians, finite, see rotation_freq).  Pairs are values j and j + len(freq),
+    or 2 j and 2 j + 1 where `adjacent`.  eps None leaves the norm out.
     Returns (q, k) of the same type; q_out and k_out may be given (q_out may be q itself, k_out
     k, else they are apart from both inputs and from each other; bf16 for fp32 rows), and rows
     at negative positions are not written."""
