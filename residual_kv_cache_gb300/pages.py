@@ -11,7 +11,7 @@ CUDA tensors; ``PageTable`` and ``PagedCache`` hold the ones that a serving loop
     plan = table.plan(new_tokens, max_rows)          # once a step
     for cache in caches:                             # in each layer
         q, k = head_norm_rotate(q, k, plan.row_pos, freq)
-        o = prompt_attention(q, k, v, plan.cu_rows)  # prompts, from their raw K/V
+        o = prompt_attention(q, k, v, plan.cu_rows, flags=table.flags)   # prompts, from their raw K/V
         cache.append(k, v, table, plan)
         o = cache.attend(q, table)                   # decode: one query a sequence
     table.release(finished)
@@ -20,9 +20,13 @@ Requests that begin alike share the pages of what they have in common:
 
     table = PageTable(batch, max_blocks, num_blocks, block_tokens, sharing=True)
     copies = table.fork(source, length)              # rows become (prefixes of) other rows
-    page_copy(caches, *copies)                       # the pages that two of them have begun
+    page_copy(caches, *copies, flags=table.flags)    # the pages that two of them have begun
     k, v, cu_k = cache.gather(table, max_rows, length)     # a prompt's keys with its prefix's
-    page_copy(caches, *table.compact())              # all pages to the pool's low end
+    page_copy(caches, *table.compact(), flags=table.flags)     # all pages to the pool's low end
+
+What a call finds out of range, or has no space for, it leaves out or refuses on the GPU and
+notes in ``table.flags`` (FLAG_*), which a program reads where it waits for the GPU anyway: a
+copy without ``flags`` leaves no trace of it.
 
 Every tensor of a call must lie on one device, which need not be the current one.  Work goes
 to ``stream`` (a ``torch.cuda.Stream`` of that device), or to the device's current stream;
