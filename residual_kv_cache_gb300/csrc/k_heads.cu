@@ -15,7 +15,11 @@
 // heads of 128, normed and turned: 108 us, 6.2 TB/s (125 us with the sines found by every lane,
 // nothing loaded ahead and products one by one; 111 with the next row's values not loaded ahead).
 // Seven CTAs of 128 threads an SM: six are 112 us, eight spill (110); rows cut into two shares
-// 118, several waves of CTAs 112 to 120 (each sets the turns up again).
+// 118, several waves of CTAs 112 to 120 (each sets the turns up again).  That was chosen for bf16:
+// with fp32 rows seven spill too (20 bytes a thread stored, 12 loaded), and 16384 of them take
+// 124.5 us (5.4 TB/s) to fp32, 76.9 (6.5) to bf16.  Further from the copy's rate: adjacent pairs
+// 129 us, rotary 32 of 128 128 (both 5.2 TB/s), and heads that do not fill a warp's groups, which
+// leave lanes idle: 5 + 5 of 128 3.9 TB/s, 12 + 1 of 128 5.0, of 64 3.3.
 #include <cuda_bf16.h>
 
 #include "pages.h"
@@ -26,7 +30,7 @@ namespace {
 
 constexpr int kHeadThreads = 128;
 constexpr int kHeadWarps = kHeadThreads / 32;
-constexpr int kHeadCtas = 7;         // resident CTAs an SM that the registers allow
+constexpr int kHeadCtas = 7;         // resident CTAs an SM (fp32 rows spill a little)
 
 struct HeadRows {
   const void* x[2];                  // q, k
